@@ -108,6 +108,22 @@ def load_library():
     lib.topk_workspace_layout.restype = ctypes.c_int
     lib.topk_validate.argtypes = [I32, P, I64, P, P, I32, I32, P, P, SZ, I64]
     lib.topk_validate.restype = ctypes.c_int
+    U32 = ctypes.c_uint32
+    lib.topk_sample_workspace_bytes.argtypes = [I32, I32]
+    lib.topk_sample_workspace_bytes.restype = SZ
+    lib.topk_sample.argtypes = [P, I32, I64, I32, I32, P, P, P, P, P, P, P, U32, P, SZ, P]
+    lib.topk_sample.restype = ctypes.c_int
+    lib.topk_route.argtypes = [P, I32, I64, I32, I32, I32, P, I32, I32, U32, ctypes.c_float, P, P,
+                               P]
+    lib.topk_route.restype = ctypes.c_int
+    lib.topk_route_backward.argtypes = [P, I32, I64, I32, I32, I32, U32, ctypes.c_float, P, P, P,
+                                        I64, P]
+    lib.topk_route_backward.restype = ctypes.c_int
+    lib.topk_block_tables.argtypes = [P, I64, I32, I32, P, P, P, I64, P, I32, I64, P, P, P, P, I32,
+                                      P, P]
+    lib.topk_block_tables.restype = ctypes.c_int
+    lib.topk_slots.argtypes = [P, I64, I32, P, I64, I32, I32, P, I32, I32, P, I32, P]
+    lib.topk_slots.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -479,6 +495,17 @@ def new_workspace(num_rows: int, row_stride: int, k: int, device="cuda", stream=
     _check(load_library().topk_workspace_init(ws.data_ptr(), nbytes, _stream_ptr(stream, ws.device)))
     return ws
 
+
+def __getattr__(name):
+    # the row operators need torch, which this module imports only when called
+    if name in _ROW_OPS:
+        from . import row_ops
+        return getattr(row_ops, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+_ROW_OPS = ("sample_tokens", "route_experts", "route_experts_backward", "extend_block_tables",
+            "topk_slots")
 
 __all__ = ["topk_decode", "topk_prefill", "topk_decode_varlen", "block_max", "workspace_bytes",
            "new_workspace", "status", "plan_query",

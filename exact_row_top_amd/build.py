@@ -18,6 +18,7 @@ LIB = os.path.join(HERE, "libexact_row_top.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["gvr_kernels.hip", "blockskip.hip", "epilogue.hip", "state.hip", "calib.hip",
+           "sample.hip", "route.hip", "slots.hip", "rowops_abi.cpp",
            "topk_abi.cpp"]
 
 # -ffp-contract=off: the histogram bin is one definition evaluated in several

@@ -1,0 +1,191 @@
+// rowops.h -- launch parameters and small device helpers of the row operators
+// beside the top-K selection (sampling, expert routing, slot maps).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <stdint.h>
+
+namespace ert {
+
+// ---- sampling --------------------------------------------------------------
+
+constexpr int kSegment = 2048;    // scores one wave reads
+constexpr int kSegSlots = 64;     // candidates a segment can hand on
+constexpr int kMaxVocab = 1 << 20;
+
+// One segment's findings, written by the segment kernel for the row kernel.
+struct SegRecord {
+  float best;       // largest live score, -inf if none
+  int32_t first;    // greedy rows: the lowest position that holds it
+  float floor;      // every live score >= floor is among the candidates
+  int32_t count;    // candidates, -1 if they did not fit
+  uint64_t mass;    // rows that need it: sum of the weights against `best`
+  uint64_t pad;
+};
+
+struct Candidate {
+  float x;
+  int32_t i;
+};
+
+struct SampleParams {
+  const void* logits;
+  int64_t row_stride;  // elements
+  int32_t vocab;
+  int32_t rows;
+  int32_t segments;    // per row
+  const float* uniforms;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;
+  float* logprobs;
+  SegRecord* records;
+  Candidate* candidates;
+  int32_t whole_row;   // take the path that reads the row again
+};
+
+// ---- 16-byte score groups ----------------------------------------------------
+
+template <class T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int kVec = 4;
+  __device__ static __forceinline__ void unpack(const uint4& q, float (&x)[4]) {
+    x[0] = __uint_as_float(q.x);
+    x[1] = __uint_as_float(q.y);
+    x[2] = __uint_as_float(q.z);
+    x[3] = __uint_as_float(q.w);
+  }
+  __device__ static __forceinline__ void unpack_word(uint32_t w, float (&x)[1]) {
+    x[0] = __uint_as_float(w);
+  }
+  __device__ static __forceinline__ float load(const void* base, int64_t i) {
+    return static_cast<const float*>(base)[i];
+  }
+};
+template <>
+struct Elem<__hip_bfloat16> {
+  static constexpr int kVec = 8;
+  __device__ static __forceinline__ void unpack(const uint4& q, float (&x)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+  __device__ static __forceinline__ void unpack_word(uint32_t w, float (&x)[2]) {
+    x[0] = __uint_as_float(w << 16);
+    x[1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+  __device__ static __forceinline__ float load(const void* base, int64_t i) {
+    return __uint_as_float((uint32_t)static_cast<const unsigned short*>(base)[i] << 16);
+  }
+};
+template <>
+struct Elem<__half> {
+  static constexpr int kVec = 8;
+  __device__ static __forceinline__ void unpack(const uint4& q, float (&x)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __half2float(__ushort_as_half((unsigned short)(w[j] & 0xFFFFu)));
+      x[2 * j + 1] = __half2float(__ushort_as_half((unsigned short)(w[j] >> 16)));
+    }
+  }
+  __device__ static __forceinline__ void unpack_word(uint32_t w, float (&x)[2]) {
+    x[0] = __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
+    x[1] = __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+  }
+  __device__ static __forceinline__ float load(const void* base, int64_t i) {
+    return __half2float(static_cast<const __half*>(base)[i]);
+  }
+};
+
+}  // namespace ert
+
+namespace ert {
+
+// ---- routing to experts ----------------------------------------------------
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxGroups = 16;
+constexpr int kMaxRouteK = 64;
+
+struct RouteParams {
+  const void* logits;
+  int64_t row_stride;   // elements
+  int32_t tokens;
+  int32_t experts;
+  int32_t top_k;
+  int32_t sigmoid;      // else softmax
+  const float* bias;    // null: none
+  int32_t groups;
+  int32_t topk_groups;
+  int32_t top2;         // a group's score: its two largest summed, else its largest
+  int32_t renormalize;
+  float scale;
+  int32_t* indices;     // [tokens][top_k]
+  float* weights;
+};
+
+struct RouteGradParams {
+  const void* logits;
+  int64_t row_stride;
+  int32_t tokens;
+  int32_t experts;
+  int32_t top_k;
+  int32_t sigmoid;
+  int32_t renormalize;
+  float scale;
+  const int32_t* indices;
+  const float* grad_weights;
+  void* grad_logits;
+  int64_t grad_stride;
+};
+
+// ---- block tables and slots --------------------------------------------------
+
+constexpr int kMaxRequests = 4096;
+
+struct TableParams {
+  int32_t* tables;
+  int64_t table_stride;
+  int32_t max_blocks;
+  int32_t requests;
+  const int32_t* kv_lens;
+  const int32_t* new_tokens;
+  const int32_t* free_blocks;
+  int64_t num_free;
+  const int32_t* free_start;
+  int32_t block_size;
+  int64_t max_tokens;
+  int32_t* token_starts;
+  int32_t* token_requests;
+  int32_t* positions;
+  void* slots;
+  int32_t wide;         // slots are int64
+  int32_t* free_next;
+};
+
+struct SlotParams {
+  const int32_t* indices;
+  int64_t rows;
+  int32_t k;
+  const int32_t* tables;
+  int64_t table_stride;
+  int32_t max_blocks;
+  int32_t requests;
+  const int32_t* row_requests;
+  int32_t next_n;
+  int32_t block_size;
+  void* slots;
+  int32_t wide;
+};
+
+}  // namespace ert

@@ -1,0 +1,268 @@
+// rowops_abi.cpp -- C ABI of the row operators beside the selection: host-side
+// validation (no device reads) and the kernel launches.  The contract is
+// documented in include/exact_row_top.h.
+
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <string.h>
+
+#include "exact_row_top.h"
+#include "rowops.h"
+
+namespace ert {
+const void* sample_segment_kernel_ptr(int dtype);
+const void* sample_row_kernel_ptr(int dtype);
+const void* route_kernel_ptr(int dtype, int lanes);
+const void* route_grad_kernel_ptr(int dtype, int lanes);
+const void* block_table_kernel_ptr();
+const void* topk_slots_kernel_ptr();
+}  // namespace ert
+
+using namespace ert;
+
+namespace {
+
+bool at(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool dtype_ok(int32_t d) { return d >= TOPK_DT_F32 && d <= TOPK_DT_F16; }
+uintptr_t elem(int32_t d) { return d == TOPK_DT_F32 ? 4 : 2; }
+
+// Whether the current device is gfx950 (0 unknown, 1 yes, 2 no per device).
+constexpr int kMaxDev = 64;
+std::atomic<int> g_arch[kMaxDev];
+
+int device_ok() {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDev) return TOPK_EDEVICE;
+  int a = g_arch[dev].load(std::memory_order_relaxed);
+  if (a == 0) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return TOPK_EDEVICE;
+    a = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
+    g_arch[dev].store(a, std::memory_order_relaxed);
+  }
+  return a == 1 ? TOPK_OK : TOPK_EDEVICE;
+}
+
+int launch(const void* kernel, int64_t grid, int block, void* params, size_t lds, hipStream_t stream) {
+  if (!kernel || grid < 1 || grid >= ((int64_t)1 << 31)) return TOPK_EINVAL;
+  void* args[] = {params};
+  if (hipLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)block), args, lds, stream) !=
+      hipSuccess) {
+    (void)hipGetLastError();  // reported here, not by the caller's next call
+    return TOPK_ELAUNCH;
+  }
+  return TOPK_OK;
+}
+
+// Segments of a row whose first score may lie up to one 16-byte group past
+// an aligned boundary.
+int64_t segments_of(int32_t vocab) { return ((int64_t)vocab + 7 + kSegment - 1) / kSegment; }
+
+bool route_shape_ok(int32_t tokens, int32_t experts, int32_t top_k) {
+  return tokens >= 0 && experts >= 1 && experts <= kMaxExperts && top_k >= 1 && top_k <= kMaxRouteK &&
+         top_k <= experts;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t topk_sample_workspace_bytes(int32_t num_rows, int32_t vocab) {
+  if (num_rows < 1 || vocab < 1 || vocab > kMaxVocab) return 0;
+  return (size_t)num_rows * (size_t)segments_of(vocab) *
+         (sizeof(SegRecord) + kSegSlots * sizeof(Candidate));
+}
+
+int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t vocab,
+                int32_t num_rows, const float* uniforms, const float* temperature,
+                const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+                float* logprobs, uint32_t flags, void* workspace, size_t workspace_bytes,
+                hipStream_t stream) {
+  if (num_rows < 0 || !dtype_ok(dtype) || vocab < 1 || vocab > kMaxVocab || row_stride < vocab ||
+      (flags & ~(uint32_t)TOPK_SAMPLE_WHOLE_ROW))
+    return TOPK_EINVAL;
+  if (num_rows == 0) return TOPK_OK;
+  if (!logits || !uniforms || !tokens) return TOPK_EINVAL;
+  if (!at(logits, elem(dtype)) || !at(uniforms, 4) || !at(temperature, 4) || !at(top_k, 4) ||
+      !at(top_p, 4) || !at(min_p, 4) || !at(tokens, 4) || !at(logprobs, 4) || !at(workspace, 16))
+    return TOPK_ELAYOUT;
+  const int64_t segments = segments_of(vocab);
+  const int64_t waves = segments * num_rows;
+  if (waves >= ((int64_t)1 << 31)) return TOPK_EINVAL;
+  if (!workspace || workspace_bytes < topk_sample_workspace_bytes(num_rows, vocab))
+    return TOPK_EWORKSPACE;
+  int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  SampleParams p;
+  memset(&p, 0, sizeof(p));
+  p.logits = logits;
+  p.row_stride = row_stride;
+  p.vocab = vocab;
+  p.rows = num_rows;
+  p.segments = (int32_t)segments;
+  p.uniforms = uniforms;
+  p.temperature = temperature;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.tokens = tokens;
+  p.logprobs = logprobs;
+  p.records = static_cast<SegRecord*>(workspace);
+  p.candidates = reinterpret_cast<Candidate*>(p.records + waves);
+  p.whole_row = (flags & TOPK_SAMPLE_WHOLE_ROW) ? 1 : 0;
+  rc = launch(sample_segment_kernel_ptr(dtype), (waves + 3) / 4, 256, &p, 0, stream);
+  if (rc != TOPK_OK) return rc;
+  return launch(sample_row_kernel_ptr(dtype), num_rows, 1024, &p, 0, stream);
+}
+
+int topk_route(const void* logits, int32_t dtype, int64_t row_stride, int32_t num_tokens,
+               int32_t num_experts, int32_t top_k, const float* bias, int32_t num_groups,
+               int32_t topk_groups, uint32_t flags, float scale, int32_t* indices, float* weights,
+               hipStream_t stream) {
+  if (!route_shape_ok(num_tokens, num_experts, top_k) || !dtype_ok(dtype) ||
+      row_stride < num_experts || num_groups < 1 || num_groups > kMaxGroups ||
+      num_experts % num_groups || topk_groups < 1 || topk_groups > num_groups ||
+      (flags & ~(uint32_t)(TOPK_ROUTE_SIGMOID | TOPK_ROUTE_TOP2 | TOPK_ROUTE_RENORMALIZE)))
+    return TOPK_EINVAL;
+  if (num_tokens == 0) return TOPK_OK;
+  if (!logits || !indices || !weights) return TOPK_EINVAL;
+  if (!at(logits, elem(dtype)) || !at(bias, 4) || !at(indices, 4) || !at(weights, 4))
+    return TOPK_ELAYOUT;
+  const int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  RouteParams p;
+  memset(&p, 0, sizeof(p));
+  p.logits = logits;
+  p.row_stride = row_stride;
+  p.tokens = num_tokens;
+  p.experts = num_experts;
+  p.top_k = top_k;
+  p.sigmoid = (flags & TOPK_ROUTE_SIGMOID) ? 1 : 0;
+  p.bias = bias;
+  p.groups = num_groups;
+  p.topk_groups = topk_groups;
+  p.top2 = (flags & TOPK_ROUTE_TOP2) ? 1 : 0;
+  p.renormalize = (flags & TOPK_ROUTE_RENORMALIZE) ? 1 : 0;
+  p.scale = scale;
+  p.indices = indices;
+  p.weights = weights;
+  const int lanes = num_experts <= 256 ? 16 : 64;
+  const int per = 256 / lanes;
+  return launch(route_kernel_ptr(dtype, lanes), ((int64_t)num_tokens + per - 1) / per, 256, &p,
+                (size_t)per * num_experts * sizeof(double), stream);
+}
+
+int topk_route_backward(const void* logits, int32_t dtype, int64_t row_stride, int32_t num_tokens,
+                        int32_t num_experts, int32_t top_k, uint32_t flags, float scale,
+                        const int32_t* indices, const float* grad_weights, void* grad_logits,
+                        int64_t grad_row_stride, hipStream_t stream) {
+  if (!route_shape_ok(num_tokens, num_experts, top_k) || !dtype_ok(dtype) ||
+      row_stride < num_experts || grad_row_stride < num_experts ||
+      (flags & ~(uint32_t)(TOPK_ROUTE_SIGMOID | TOPK_ROUTE_TOP2 | TOPK_ROUTE_RENORMALIZE)))
+    return TOPK_EINVAL;
+  if (num_tokens == 0) return TOPK_OK;
+  if (!logits || !indices || !grad_weights || !grad_logits) return TOPK_EINVAL;
+  if (!at(logits, elem(dtype)) || !at(indices, 4) || !at(grad_weights, 4) ||
+      !at(grad_logits, elem(dtype)))
+    return TOPK_ELAYOUT;
+  const int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  RouteGradParams p;
+  memset(&p, 0, sizeof(p));
+  p.logits = logits;
+  p.row_stride = row_stride;
+  p.tokens = num_tokens;
+  p.experts = num_experts;
+  p.top_k = top_k;
+  p.sigmoid = (flags & TOPK_ROUTE_SIGMOID) ? 1 : 0;
+  p.renormalize = (flags & TOPK_ROUTE_RENORMALIZE) ? 1 : 0;
+  p.scale = scale;
+  p.indices = indices;
+  p.grad_weights = grad_weights;
+  p.grad_logits = grad_logits;
+  p.grad_stride = grad_row_stride;
+  const int lanes = num_experts <= 256 ? 16 : 64;
+  const int per = 256 / lanes;
+  return launch(route_grad_kernel_ptr(dtype, lanes), ((int64_t)num_tokens + per - 1) / per, 256, &p,
+                (size_t)per * num_experts * sizeof(float), stream);
+}
+
+int topk_block_tables(int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
+                      int32_t num_requests, const int32_t* kv_lens, const int32_t* new_tokens,
+                      const int32_t* free_blocks, int64_t num_free, const int32_t* free_start,
+                      int32_t block_size, int64_t max_tokens, int32_t* token_starts,
+                      int32_t* token_requests, int32_t* positions, void* slots, int32_t slots_64,
+                      int32_t* free_next, hipStream_t stream) {
+  if (num_requests < 0 || num_requests > kMaxRequests || max_blocks < 0 ||
+      table_stride < max_blocks || num_free < 0 || block_size < 1 || block_size > (1 << 30) ||
+      max_tokens < 0 || max_tokens >= ((int64_t)1 << 31) || (slots_64 != 0 && slots_64 != 1))
+    return TOPK_EINVAL;
+  if (!free_start || !free_next || free_start == free_next || !token_starts) return TOPK_EINVAL;
+  if (num_requests > 0 && (!kv_lens || !new_tokens || (max_blocks > 0 && !block_tables)))
+    return TOPK_EINVAL;
+  if (num_free > 0 && !free_blocks) return TOPK_EINVAL;
+  if (max_tokens > 0 && (!token_requests || !positions || !slots)) return TOPK_EINVAL;
+  if (!at(block_tables, 4) || !at(kv_lens, 4) || !at(new_tokens, 4) || !at(free_blocks, 4) ||
+      !at(free_start, 4) || !at(token_starts, 4) || !at(token_requests, 4) || !at(positions, 4) ||
+      !at(slots, slots_64 ? 8 : 4) || !at(free_next, 4))
+    return TOPK_ELAYOUT;
+  const int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  TableParams p;
+  memset(&p, 0, sizeof(p));
+  p.tables = block_tables;
+  p.table_stride = table_stride;
+  p.max_blocks = max_blocks;
+  p.requests = num_requests;
+  p.kv_lens = kv_lens;
+  p.new_tokens = new_tokens;
+  p.free_blocks = free_blocks;
+  p.num_free = num_free;
+  p.free_start = free_start;
+  p.block_size = block_size;
+  p.max_tokens = max_tokens;
+  p.token_starts = token_starts;
+  p.token_requests = token_requests;
+  p.positions = positions;
+  p.slots = slots;
+  p.wide = slots_64;
+  p.free_next = free_next;
+  int64_t grid = (max_tokens + 2047) / 2048;
+  grid = grid < 1 ? 1 : (grid > 2048 ? 2048 : grid);
+  return launch(block_table_kernel_ptr(), grid, 256, &p, (size_t)(2 * num_requests + 1) * 4, stream);
+}
+
+int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_t* block_tables,
+               int64_t table_stride, int32_t max_blocks, int32_t num_requests,
+               const int32_t* row_requests, int32_t next_n, int32_t block_size, void* slots,
+               int32_t slots_64, hipStream_t stream) {
+  if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || k < 1 || max_blocks < 0 ||
+      table_stride < max_blocks || num_requests < 0 || block_size < 1 || block_size > (1 << 30) ||
+      (slots_64 != 0 && slots_64 != 1) || (!row_requests && next_n < 1))
+    return TOPK_EINVAL;
+  if (num_rows == 0) return TOPK_OK;
+  if (!indices || !slots || (num_requests > 0 && max_blocks > 0 && !block_tables)) return TOPK_EINVAL;
+  if (slots_64 && slots == indices) return TOPK_EINVAL;
+  if (!at(indices, 4) || !at(block_tables, 4) || !at(row_requests, 4) || !at(slots, slots_64 ? 8 : 4))
+    return TOPK_ELAYOUT;
+  const int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  SlotParams p;
+  memset(&p, 0, sizeof(p));
+  p.indices = indices;
+  p.rows = num_rows;
+  p.k = k;
+  p.tables = block_tables;
+  p.table_stride = table_stride;
+  p.max_blocks = max_blocks;
+  p.requests = num_requests;
+  p.row_requests = row_requests;
+  p.next_n = row_requests ? 1 : next_n;
+  p.block_size = block_size;
+  p.slots = slots;
+  p.wide = slots_64;
+  return launch(topk_slots_kernel_ptr(), (num_rows * k + 255) / 256, 256, &p, 0, stream);
+}
+
+}  // extern "C"

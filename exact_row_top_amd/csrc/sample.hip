@@ -1,0 +1,828 @@
+// sample.hip -- one token per row from its logits: temperature, top-k, top-p,
+// min-p and a given uniform number.
+//
+// With m the row's largest live score (NaN and -inf are not live) and weights
+// w_i = exp((x_i - m) / T), all three cuts keep a prefix of one order (score
+// descending, then index ascending), and the token is the first index at
+// which the kept weights' running sum in INDEX order passes u times their
+// total.  So a row needs its maximum, one or two crossings in value order and
+// one crossing in index order; nothing is sorted.
+//
+// Weights are whole numbers: 2^43 times the value, rounded once, from an
+// exponential good to 46 bits in 64-bit arithmetic.  Their sums are exact in
+// 64 bits (at most 2^20 weights of at most 2^43) and the same in every order,
+// so atomics and splits never change a token; and a token differs from the
+// real-number definition only if u lies within about 1e-12 of a border.
+// Weights below 2^-44 of the largest count as zero.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "rowops.h"
+
+namespace ert {
+
+namespace {
+
+constexpr uint64_t kOne = 1ull << 43;   // the weight of a row's largest score
+constexpr double kLog2e = 1.4426950408889634;
+constexpr double kLn2 = 0.6931471805599453;
+constexpr double kTmax = 44.0;          // weights of 2^-44 and less are zero
+
+// 2^f on [-1/2, 1/2]: interpolation at the ten Chebyshev nodes, relative
+// error at most 2^-45.6.
+__device__ __forceinline__ double exp2_poly(double f) {
+  double p = 0x1.b6571de2f2351p-24;
+  p = __builtin_fma(p, f, 0x1.63ef969a64d3cp-20);
+  p = __builtin_fma(p, f, 0x1.ffcb76789860fp-17);
+  p = __builtin_fma(p, f, 0x1.43088e257f341p-13);
+  p = __builtin_fma(p, f, 0x1.5d87fe908f88ap-10);
+  p = __builtin_fma(p, f, 0x1.3b2ab72b175eep-7);
+  p = __builtin_fma(p, f, 0x1.c6b08d7044119p-5);
+  p = __builtin_fma(p, f, 0x1.ebfbdff8149f2p-3);
+  p = __builtin_fma(p, f, 0x1.62e42fefa39f7p-1);
+  return __builtin_fma(p, f, 0x1.000000000003dp+0);
+}
+
+// round(2^43 * 2^-t) for 0 <= t < 44.  Adding 1.5 * 2^52 rounds t to a whole
+// n in the sum's low word; adding 2^52 to the scaled value rounds it to a
+// whole number in the sum's low 52 bits.
+__device__ __forceinline__ uint64_t weight_of(double t) {
+  const double magic = 6755399441055744.0;
+  const double tm = t + magic;
+  const double n = tm - magic;
+  const double p = exp2_poly(n - t);
+  const uint32_t hi = (uint32_t)(1023 + 43 - (int)(uint32_t)__double_as_longlong(tm)) << 20;
+  const double scale = __hiloint2double((int)hi, 0);
+  const double r = __builtin_fma(p, scale, 4503599627370496.0);
+  return (uint64_t)__double_as_longlong(r) & 0xFFFFFFFFFFFFFull;
+}
+
+// 2^-t for t >= 0 (0 from t = 1000 on, and for NaN).
+__device__ __forceinline__ double exp2_neg(double t) {
+  if (!(t < 1000.0)) return 0.0;
+  const double n = __builtin_rint(t);
+  return __builtin_ldexp(exp2_poly(n - t), -(int)n);
+}
+
+// What a row asks for.
+struct RowAsk {
+  bool greedy;      // T is not > 0: the first of the order
+  bool cut_k;       // 0 < top_k < vocab
+  bool cut_p;       // top_p < 1
+  int k;
+  double p;
+  uint64_t min_w;   // weights below this are cut by min-p (0: none)
+  double c;         // log2(e) / T
+
+  __device__ __forceinline__ bool cuts() const { return cut_k || cut_p || min_w > 0; }
+};
+
+__device__ __forceinline__ RowAsk row_ask(const SampleParams& q, int row) {
+  RowAsk a;
+  const float T = q.temperature ? q.temperature[row] : 1.0f;
+  a.greedy = !(T > 0.0f);
+  a.c = a.greedy ? 0.0 : kLog2e / (double)T;
+  a.k = q.top_k ? q.top_k[row] : 0;
+  a.cut_k = a.k > 0 && a.k < q.vocab;
+  const float p = q.top_p ? q.top_p[row] : 1.0f;
+  a.cut_p = p < 1.0f;
+  a.p = (double)p;
+  const float mp = q.min_p ? q.min_p[row] : 0.0f;
+  a.min_w = mp > 0.0f ? (uint64_t)__builtin_ceil((mp < 1.0f ? (double)mp : 1.0) * (double)kOne) : 0ull;
+  return a;
+}
+
+// The weight of score x against the row's largest, m; zero for scores that
+// cannot be drawn.  x == m also covers m = +inf.
+__device__ __forceinline__ uint64_t weight(float x, float m, double c) {
+  if (x == m) return kOne;
+  const double t = ((double)m - (double)x) * c;
+  return t < kTmax ? weight_of(t) : 0ull;
+}
+__device__ __forceinline__ bool drawable(float x, float m, double c) {
+  return x == m || ((double)m - (double)x) * c < kTmax;
+}
+
+__device__ __forceinline__ uint32_t ordered(float x) {
+  uint32_t b = __float_as_uint(x);
+  b = (b == 0x80000000u) ? 0u : b;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// A row's scores as whole 16-byte groups from the boundary at or below its
+// first score; positions outside [0, vocab) read as -inf.
+template <class T>
+struct RowView {
+  const unsigned char* base;  // 16-byte aligned
+  int lead;                   // scores between base and the row's first
+  int vocab;
+
+  __device__ __forceinline__ RowView(const SampleParams& q, int row) {
+    const unsigned char* p =
+        static_cast<const unsigned char*>(q.logits) + (int64_t)row * q.row_stride * (int64_t)sizeof(T);
+    lead = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(T);
+    base = p - lead * (int)sizeof(T);
+    vocab = q.vocab;
+  }
+  // Group g: its scores, NaN as -inf, and the position of the first.
+  __device__ __forceinline__ int group(int g, float (&x)[Elem<T>::kVec]) const {
+    constexpr int V = Elem<T>::kVec;
+    const int pos = g * V - lead;
+    uint4 raw{0, 0, 0, 0};
+    if (pos < vocab && pos + V > 0) raw = *reinterpret_cast<const uint4*>(base + (int64_t)g * 16);
+    Elem<T>::unpack(raw, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      x[e] = ((unsigned)(pos + e) < (unsigned)vocab && x[e] > -__builtin_inff()) ? x[e]
+                                                                               : -__builtin_inff();
+    return pos;
+  }
+};
+
+template <class V>
+__device__ __forceinline__ V wave_sum(V v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+__device__ __forceinline__ int wave_min(int v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = min(v, __shfl_xor(v, d));
+  return v;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Segment kernel: one wave reads 2048 scores of a row into registers, once,
+// and writes what the row kernel needs of them: the largest, the weights'
+// sum against it (rows whose draw or top-p needs the whole row's), and the
+// candidates of a row with cuts.
+//
+// Candidates: the j-th largest of the 64 lanes' maxima is at most the
+// segment's j-th largest score, so at least j scores lie at or above it; an
+// 18-bit prefix of its key, found with ballots, is a floor that needs no
+// barrier and no atomics.  All live scores at or above the floor are handed
+// on.
+// ---------------------------------------------------------------------------
+template <class T>
+__global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams q) {
+  constexpr int V = Elem<T>::kVec;
+  constexpr int G = kSegment / (64 * V);
+  const int lane = threadIdx.x & 63;
+  const uint32_t id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6));
+  if (id >= (uint32_t)q.rows * (uint32_t)q.segments) return;
+  const int row = (int)(id / (uint32_t)q.segments);
+  const int seg = (int)(id - (uint32_t)row * (uint32_t)q.segments);
+  const RowAsk ask = row_ask(q, row);
+  const RowView<T> view(q, row);
+
+  float x[G][V];
+  const int g0 = seg * (kSegment / V);
+#pragma unroll
+  for (int g = 0; g < G; ++g) view.group(g0 + g * 64 + lane, x[g]);
+
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < V; ++e) top = fmaxf(top, x[g][e]);
+  const float best = wave_max(top);
+
+  SegRecord rec;
+  rec.best = best;
+  rec.first = 0x7FFFFFFF;
+  rec.floor = -__builtin_inff();
+  rec.count = 0;
+  rec.mass = 0;
+  rec.pad = 0;
+  if (best > -__builtin_inff()) {
+    if (ask.greedy) {
+      int first = 0x7FFFFFFF;
+#pragma unroll
+      for (int g = G - 1; g >= 0; --g)
+#pragma unroll
+        for (int e = V - 1; e >= 0; --e)
+          if (x[g][e] == best) first = (g0 + g * 64 + lane) * V + e - view.lead;
+      rec.first = wave_min(first);
+    } else {
+      if (!ask.cut_k) {
+        uint64_t mass = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int e = 0; e < V; ++e) mass += weight(x[g][e], best, ask.c);
+        rec.mass = wave_sum(mass);
+      }
+      if (ask.cuts()) {
+        // how many lane maxima the floor lies under: what a segment should
+        // hold of a row's best k, with room for an uneven spread; 16 where
+        // only the weights say how many are needed
+        int j = 16;
+        if (ask.cut_k) {
+          const float share = (float)ask.k / (float)q.segments;
+          j = min(48, (int)(share + 4.0f * __builtin_sqrtf(share)) + 4);
+        }
+        const uint32_t key = ordered(top);
+        uint32_t thr = 0;
+#pragma unroll
+        for (int b = 31; b >= 14; --b) {
+          const uint32_t t = thr | (1u << b);
+          if (__popcll(__ballot(key >= t)) >= j) thr = t;
+        }
+        const float floor = thr > ordered(-__builtin_inff()) ? from_ordered(thr) : -__builtin_inff();
+        Candidate* out = q.candidates + (int64_t)id * kSegSlots;
+        int n = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const bool in = x[g][e] >= floor && x[g][e] > -__builtin_inff();
+            const uint64_t mask = __ballot(in);
+            if (mask == 0) continue;
+            const int at = n + (int)__builtin_amdgcn_mbcnt_hi(
+                                   (uint32_t)(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+            if (in && at < kSegSlots)
+              out[at] = Candidate{x[g][e], (g0 + g * 64 + lane) * V + e - view.lead};
+            n += __popcll(mask);
+          }
+        rec.floor = floor;
+        rec.count = n <= kSegSlots ? n : -1;
+      }
+    }
+  }
+  if (lane == 0) q.records[id] = rec;
+}
+
+// ---------------------------------------------------------------------------
+// Row kernel: one workgroup per row.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+constexpr int kBinsS = 1024;   // histogram bins
+constexpr int kShort = 256;    // members of a bin that are ranked directly
+constexpr int kListS = 2048;   // candidates held in LDS
+
+struct RowShared {
+  uint32_t cnt[kBinsS];
+  uint64_t mass[kBinsS];
+  float sx[kShort];
+  int32_t si[kShort];
+  uint64_t sw[kShort];
+  uint64_t red[32];
+  double redd[32];
+  float redf[64];
+  uint32_t n;
+  int32_t bin;
+  int32_t found_i;
+  float found_x;
+  uint64_t before;
+  uint32_t list_n;
+  float lx[kListS];
+  int32_t li[kListS];
+};
+
+// Everything of the order up to and including (x, i).
+struct Cut {
+  float x;
+  int32_t i;
+  __device__ __forceinline__ bool holds(float y, int j) const { return y > x || (y == x && j <= i); }
+};
+
+// The candidates in LDS.
+struct ListSource {
+  const float* x;
+  const int32_t* i;
+  int n;
+  template <int BLOCK, class F>
+  __device__ __forceinline__ void visit(F&& f) const {
+    for (int t = threadIdx.x; t < n; t += BLOCK) f(x[t], i[t]);
+  }
+};
+
+// The live scores of groups [g0, g1) of a row in memory.
+template <class T>
+struct RowSource {
+  RowView<T> view;
+  int g0, g1;
+  template <int BLOCK, class F>
+  __device__ __forceinline__ void visit(F&& f) const {
+    constexpr int V = Elem<T>::kVec;
+    for (int g = g0 + (int)threadIdx.x; g < g1; g += BLOCK) {
+      const int pos = g * V - view.lead;
+      uint4 raw = *reinterpret_cast<const uint4*>(view.base + (int64_t)g * 16);
+      // one 32-bit word at a time: the callers' code appears once or twice,
+      // not once for each score of the group
+#pragma unroll 1
+      for (int w = 0; w < 4; ++w) {
+        float x[V / 4];
+        Elem<T>::unpack_word(raw.x, x);
+#pragma unroll
+        for (int e = 0; e < V / 4; ++e) {
+          const int i = pos + w * (V / 4) + e;
+          if ((unsigned)i < (unsigned)view.vocab && x[e] > -__builtin_inff()) f(x[e], i);
+        }
+        raw.x = raw.y;
+        raw.y = raw.z;
+        raw.z = raw.w;
+      }
+    }
+  }
+};
+
+template <int BLOCK, class V>
+__device__ __forceinline__ V block_sum(V v, V* red) {
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  V s = red[0];
+#pragma unroll
+  for (int w = 1; w < BLOCK / 64; ++w) s += red[w];
+  return s;
+}
+
+template <int BLOCK>
+__device__ __forceinline__ void block_min_max(float& lo, float& hi, float* red) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    lo = fminf(lo, __shfl_xor(lo, d));
+    hi = fmaxf(hi, __shfl_xor(hi, d));
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6] = lo;
+    red[32 + (threadIdx.x >> 6)] = hi;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < BLOCK / 64; ++w) {
+    lo = fminf(lo, red[w]);
+    hi = fmaxf(hi, red[32 + w]);
+  }
+}
+
+// Inclusive prefix sum over the workgroup in thread order.
+template <int BLOCK, class V>
+__device__ __forceinline__ V block_scan(V v, V* red) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const V o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();
+  if (lane == 63) red[wv] = v;
+  __syncthreads();
+  V off = 0;
+#pragma unroll
+  for (int w = 0; w < BLOCK / 64; ++w) off += w < wv ? red[w] : (V)0;
+  return off + v;
+}
+
+template <int BLOCK>
+__device__ __forceinline__ void clear_bins(RowShared& sh) {
+  __syncthreads();
+  for (int b = threadIdx.x; b < kBinsS; b += BLOCK) {
+    sh.cnt[b] = 0;
+    sh.mass[b] = 0;
+  }
+  if (threadIdx.x == 0) {
+    sh.n = 0;
+    sh.bin = -1;
+  }
+  __syncthreads();
+}
+
+// The first bin at which the running sum of the counts (or masses) reaches
+// `need`, and the sum before it; false if the total stays below.
+template <int BLOCK, bool MASS>
+__device__ __forceinline__ bool cross_bins(RowShared& sh, uint64_t need, int& bin, uint64_t& before) {
+  constexpr int PER = kBinsS / BLOCK;
+  __syncthreads();
+  uint64_t own = 0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int b = threadIdx.x * PER + e;
+    own += MASS ? sh.mass[b] : (uint64_t)sh.cnt[b];
+  }
+  const uint64_t incl = block_scan<BLOCK>(own, sh.red);
+  uint64_t run = incl - own;
+  if (run < need && need <= incl) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int b = threadIdx.x * PER + e;
+      const uint64_t v = MASS ? sh.mass[b] : (uint64_t)sh.cnt[b];
+      if (run < need && need <= run + v) {
+        sh.bin = b;
+        sh.before = run;
+      }
+      run += v;
+    }
+  }
+  __syncthreads();
+  bin = sh.bin;
+  before = sh.before;
+  return bin >= 0;
+}
+
+// The short list's member at which the running sum in the order (score
+// descending, index ascending) reaches `need`, left in found_x / found_i.
+template <bool MASS>
+__device__ __forceinline__ void rank_short(RowShared& sh, int m, uint64_t need) {
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < m) {
+    const float x = sh.sx[t];
+    const int i = sh.si[t];
+    uint64_t run = 0;
+    for (int o = 0; o < m; ++o) {
+      const float y = sh.sx[o];
+      if (y > x || (y == x && sh.si[o] < i)) run += MASS ? sh.sw[o] : 1ull;
+    }
+    const uint64_t own = MASS ? sh.sw[t] : 1ull;
+    if (run < need && need <= run + own) {
+      sh.found_x = x;
+      sh.found_i = i;
+    }
+  }
+  __syncthreads();
+}
+
+// The lowest index at which the running count (or mass) of the scores that
+// `pred` admits reaches `need`, in index order over [0, vocab); -1 if the
+// total stays below.
+template <int BLOCK, bool MASS, class Src, class Pred>
+__device__ int find_index(const Src& src, RowShared& sh, float m, double c, int from, int span,
+                          Pred&& pred, uint64_t need) {
+  int i0 = from, width = (span + kBinsS - 1) / kBinsS;
+  for (;;) {
+    clear_bins<BLOCK>(sh);
+    src.template visit<BLOCK>([&](float x, int i) {
+      const int d = i - i0;
+      if (d >= 0 && d < width * kBinsS && pred(x, i)) {
+        const int b = (int)((unsigned)d / (unsigned)width);
+        atomicAdd(&sh.cnt[b], 1u);
+        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)weight(x, m, c));
+      }
+    });
+    int bin;
+    uint64_t before;
+    if (!cross_bins<BLOCK, MASS>(sh, need, bin, before)) return -1;
+    need -= before;
+    i0 += bin * width;
+    const int members = (int)sh.cnt[bin];
+    if (width == 1 || members <= kShort) {
+      src.template visit<BLOCK>([&](float x, int i) {
+        const int d = i - i0;
+        if (d >= 0 && d < width && pred(x, i)) {
+          const uint32_t s = atomicAdd(&sh.n, 1u);
+          if (s < (uint32_t)kShort) {
+            sh.sx[s] = 0.0f;  // index order alone
+            sh.si[s] = i;
+            if (MASS) sh.sw[s] = weight(x, m, c);
+          }
+        }
+      });
+      rank_short<MASS>(sh, min(members, kShort), need);
+      return sh.found_i;
+    }
+    width = (width + kBinsS - 1) / kBinsS;
+  }
+}
+
+// The place in the order (score descending, index ascending) at which the
+// running count (or mass) of the drawable scores inside `within` reaches
+// `need` (>= 1); `within` itself if the total stays below.  Each round splits
+// the class's value range into equal bins, finds the crossing bin, and
+// narrows the range to that bin's own extremes, which land in different bins
+// next time; a class of one value is split by index.
+template <int BLOCK, bool MASS, class Src>
+__device__ Cut find_cut(const Src& src, RowShared& sh, float m, double c, float lo, const Cut& within,
+                        int vocab, uint64_t need) {
+  float hi = m;
+  for (;;) {
+    clear_bins<BLOCK>(sh);
+    const double range = (double)hi - (double)lo;
+    const double s = (range > 0.0 && range < 1e300) ? (double)kBinsS / range : 0.0;
+    auto bin_of = [&](float x) {
+      if (!(s > 0.0)) return 0;
+      const double b = ((double)hi - (double)x) * s;
+      return b < (double)(kBinsS - 1) ? (int)b : kBinsS - 1;
+    };
+    auto admitted = [&](float x, int i) {
+      return x <= hi && x >= lo && drawable(x, m, c) && within.holds(x, i);
+    };
+    src.template visit<BLOCK>([&](float x, int i) {
+      if (admitted(x, i)) {
+        const int b = bin_of(x);
+        atomicAdd(&sh.cnt[b], 1u);
+        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)weight(x, m, c));
+      }
+    });
+    int bin;
+    uint64_t before;
+    if (!cross_bins<BLOCK, MASS>(sh, need, bin, before)) return within;
+    need -= before;
+    const int members = (int)sh.cnt[bin];
+    float mn = __builtin_inff(), mx = -__builtin_inff();
+    src.template visit<BLOCK>([&](float x, int i) {
+      if (admitted(x, i) && bin_of(x) == bin) {
+        mn = fminf(mn, x);
+        mx = fmaxf(mx, x);
+        const uint32_t s = atomicAdd(&sh.n, 1u);
+        if (s < (uint32_t)kShort) {
+          sh.sx[s] = x;
+          sh.si[s] = i;
+          if (MASS) sh.sw[s] = weight(x, m, c);
+        }
+      }
+    });
+    if (members <= kShort) {
+      rank_short<MASS>(sh, members, need);
+      return Cut{sh.found_x, sh.found_i};
+    }
+    block_min_max<BLOCK>(mn, mx, sh.redf);
+    if (mn == mx) {
+      // one value: its first `count` indices
+      const uint64_t w = MASS ? weight(mn, m, c) : 1ull;
+      const uint64_t count = MASS ? (need + w - 1) / w : need;
+      const int at = find_index<BLOCK, false>(
+          src, sh, m, c, 0, vocab, [&](float x, int i) { return x == mn && within.holds(x, i); },
+          count);
+      return Cut{mn, at};
+    }
+    hi = mx;
+    lo = mn;
+  }
+}
+
+__device__ __forceinline__ uint64_t ceil_share(double p, double total) {
+  const double need = __builtin_ceil(p * total);
+  return need < 1.0 ? 1ull : (need >= total ? (uint64_t)total : (uint64_t)need);
+}
+
+__device__ __forceinline__ double clamp_uniform(float u) {
+  return u > 0.0f ? (u < 0.99999994f ? (double)u : 0.99999994039535522) : 0.0;
+}
+
+}  // namespace
+
+template <class T, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q) {
+  __shared__ RowShared sh;
+  constexpr int V = Elem<T>::kVec;
+  const int t = threadIdx.x;
+  const int row = blockIdx.x;
+  const RowAsk ask = row_ask(q, row);
+  const RowView<T> view(q, row);
+  const int nseg = q.segments;
+  const SegRecord* recs = q.records + (int64_t)row * nseg;
+  const float ninf = -__builtin_inff();
+
+  // The row's largest score, the candidates' common floor, and whether every
+  // segment's candidates fitted.
+  float m = ninf, floor = ninf;
+  bool fits = true;
+  int first = 0x7FFFFFFF;
+  for (int s = t; s < nseg; s += BLOCK) {
+    const SegRecord r = recs[s];
+    if (ask.greedy && (r.best > m || (r.best == m && r.first < first))) first = r.first;
+    m = fmaxf(m, r.best);
+    floor = fmaxf(floor, r.floor);
+    fits = fits && r.count >= 0;
+  }
+  const float own_best = m;
+  {
+    float nm = -m, f = floor;  // largest of both, through one reduction
+    block_min_max<BLOCK>(nm, f, sh.redf);
+    m = -nm;
+    floor = f;
+  }
+  fits = __syncthreads_and(fits);
+
+  if (m == ninf) {  // nothing to draw from
+    if (t == 0) {
+      q.tokens[row] = -1;
+      if (q.logprobs) q.logprobs[row] = ninf;
+    }
+    return;
+  }
+  if (ask.greedy) {
+    if (t == 0) sh.found_i = 0x7FFFFFFF;
+    __syncthreads();
+    if (own_best == m && first != 0x7FFFFFFF) atomicMin(&sh.found_i, first);
+    __syncthreads();
+    if (t == 0) {
+      q.tokens[row] = sh.found_i;
+      if (q.logprobs) q.logprobs[row] = 0.0f;
+    }
+    return;
+  }
+
+  const double u = clamp_uniform(q.uniforms[row]);
+  int token = -1;
+  double total = 0.0;  // the kept weights' sum, in units of 2^-43 of the largest
+
+  if (!ask.cuts() && !q.whole_row) {
+    // The whole vocabulary: the segment in which the running sum passes
+    // u * total, then the place inside it.
+    double* seg_m = reinterpret_cast<double*>(sh.mass);  // kBinsS entries >= segments
+    for (int s = t; s < nseg; s += BLOCK) {
+      const SegRecord r = recs[s];
+      seg_m[s] = r.best > ninf ? (r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * ask.c)) *
+                                     (double)r.mass
+                               : 0.0;
+    }
+    __syncthreads();
+    double own = 0.0;
+    const int per = (nseg + BLOCK - 1) / BLOCK;
+    for (int e = 0; e < per; ++e) {
+      const int s = t * per + e;
+      if (s < nseg) own += seg_m[s];
+    }
+    const double incl = block_scan<BLOCK>(own, sh.redd);
+    if (t == 0) sh.found_i = 0x7FFFFFFF;
+    if (t == BLOCK - 1) sh.redd[31] = incl;
+    __syncthreads();
+    total = sh.redd[31];
+    const double y = u * total;
+    double run = incl - own;
+    // u is at most 1 - 2^-24, far further below 1 than these sums' rounding,
+    // so some segment's running sum lies above y
+    int mine = 0x7FFFFFFF;
+    double mine_before = 0.0;
+    for (int e = 0; e < per; ++e) {
+      const int s = t * per + e;
+      if (s < nseg) {
+        if (mine == 0x7FFFFFFF && seg_m[s] > 0.0 && run + seg_m[s] > y) {
+          mine = s;
+          mine_before = run;
+        }
+        run += seg_m[s];
+      }
+    }
+    if (mine != 0x7FFFFFFF) atomicMin(&sh.found_i, mine);
+    __syncthreads();
+    const int seg = sh.found_i;
+    if (mine == seg) sh.redd[30] = mine_before;
+    __syncthreads();
+    const SegRecord r = recs[seg];
+    const double scale = r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * ask.c);
+    double rest = (y - sh.redd[30]) / scale;
+    if (!(rest > 0.0)) rest = 0.0;
+    uint64_t need = rest < (double)r.mass ? (uint64_t)rest + 1 : r.mass;
+    if (need > r.mass) need = r.mass;
+    const RowSource<T> src{view, seg * (kSegment / V),
+                           min((seg + 1) * (kSegment / V), (q.vocab + view.lead + V - 1) / V)};
+    token = find_index<BLOCK, true>(src, sh, r.best, ask.c, seg * kSegment - view.lead, kSegment,
+                                    [](float, int) { return true; }, need);
+  } else {
+    // Candidates at or above the common floor: every such score of the row.
+    bool covered = fits && !q.whole_row && ask.cuts();
+    ListSource list{sh.lx, sh.li, 0};
+    const Cut all{ninf, 0x7FFFFFFF};
+    if (covered) {
+      if (t == 0) sh.list_n = 0;
+      __syncthreads();
+      const int lane = t & 63;
+      for (int s = t >> 6; s < nseg; s += BLOCK / 64) {
+        const int n = recs[s].count;
+        Candidate cd{ninf, 0};
+        if (lane < n) cd = q.candidates[((int64_t)row * nseg + s) * kSegSlots + lane];
+        const bool in = lane < n && cd.x >= floor && drawable(cd.x, m, ask.c);
+        const uint64_t mask = __ballot(in);
+        if (mask) {
+          uint32_t b = 0;
+          if (lane == 0) b = atomicAdd(&sh.list_n, (uint32_t)__popcll(mask));
+          b = __builtin_amdgcn_readfirstlane(b);
+          const uint32_t at = b + __builtin_amdgcn_mbcnt_hi(
+                                      (uint32_t)(mask >> 32),
+                                      __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+          if (in && at < (uint32_t)kListS) {
+            sh.lx[at] = cd.x;
+            sh.li[at] = cd.i;
+          }
+        }
+      }
+      __syncthreads();
+      list.n = (int)sh.list_n;
+      covered = list.n <= kListS;
+    }
+    // no drawable score lies below the floor
+    const bool complete = floor == ninf || !drawable(floor, m, ask.c);
+    Cut cut = all;
+    auto mass_in = [&](const auto& src, const Cut& cc, uint64_t min_w) {
+      uint64_t s = 0;
+      src.template visit<BLOCK>([&](float x, int i) {
+        if (cc.holds(x, i)) {
+          const uint64_t w = weight(x, m, ask.c);
+          s += w >= min_w ? w : 0ull;
+        }
+      });
+      return block_sum<BLOCK>(s, sh.red);
+    };
+    if (covered) {
+      float low = m;
+      list.visit<BLOCK>([&](float x, int) { low = fminf(low, x); });
+      float high = m;
+      block_min_max<BLOCK>(low, high, sh.redf);
+      if (ask.cut_k) {
+        if (list.n >= ask.k)
+          cut = find_cut<BLOCK, false>(list, sh, m, ask.c, low, all, q.vocab, (uint64_t)ask.k);
+        else
+          covered = complete;
+      }
+      if (covered && ask.cut_p) {
+        const uint64_t have = mass_in(list, cut, 0);
+        double z = (double)have;
+        if (!ask.cut_k && !complete) {
+          double part = 0.0;
+          for (int s = t; s < nseg; s += BLOCK) {
+            const SegRecord r = recs[s];
+            if (r.best > ninf)
+              part += (r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * ask.c)) *
+                      (double)r.mass;
+          }
+          z = block_sum<BLOCK>(part, sh.redd);
+        }
+        const uint64_t need = ceil_share(ask.p, z);
+        if (have >= need)
+          cut = find_cut<BLOCK, true>(list, sh, m, ask.c, low, cut, q.vocab, need);
+        else
+          covered = complete || ask.cut_k;
+      }
+      if (covered && !ask.cut_k && !ask.cut_p)
+        covered = complete || weight(floor, m, ask.c) < ask.min_w;
+    }
+    auto draw = [&](const auto& src) {
+      const uint64_t z = mass_in(src, cut, ask.min_w);
+      total = (double)z;
+      const double y = u * total;
+      uint64_t need = (uint64_t)y + 1;
+      if (need > z) need = z;
+      token = find_index<BLOCK, true>(
+          src, sh, m, ask.c, 0, q.vocab,
+          [&](float x, int i) { return cut.holds(x, i) && weight(x, m, ask.c) >= (ask.min_w ? ask.min_w : 1ull); },
+          need);
+    };
+    if (covered) {
+      draw(list);
+    } else {
+      // The whole row again, from memory.
+      const RowSource<T> src{view, 0, (q.vocab + view.lead + V - 1) / V};
+      cut = all;
+      float low = m, high = m;
+      src.template visit<BLOCK>([&](float x, int) {
+        if (drawable(x, m, ask.c)) low = fminf(low, x);
+      });
+      block_min_max<BLOCK>(low, high, sh.redf);
+      if (ask.cut_k) cut = find_cut<BLOCK, false>(src, sh, m, ask.c, low, all, q.vocab, (uint64_t)ask.k);
+      if (ask.cut_p) {
+        const uint64_t z = mass_in(src, cut, 0);
+        cut = find_cut<BLOCK, true>(src, sh, m, ask.c, low, cut, q.vocab, ceil_share(ask.p, (double)z));
+      }
+      draw(src);
+    }
+  }
+
+  if (t == 0) {
+    q.tokens[row] = token;
+    if (q.logprobs && token >= 0) {
+      const float xt = Elem<T>::load(view.base, token + view.lead);
+      const double below = xt == m ? 0.0 : ((double)m - (double)xt) * ask.c;
+      q.logprobs[row] = (float)(-below * kLn2 - log(total * (1.0 / (double)kOne)));
+    }
+  }
+}
+
+const void* sample_segment_kernel_ptr(int dtype) {
+  switch (dtype) {
+    case 0: return reinterpret_cast<const void*>(&sample_segment_kernel<float>);
+    case 1: return reinterpret_cast<const void*>(&sample_segment_kernel<__hip_bfloat16>);
+    case 2: return reinterpret_cast<const void*>(&sample_segment_kernel<__half>);
+    default: return nullptr;
+  }
+}
+
+const void* sample_row_kernel_ptr(int dtype) {
+  switch (dtype) {
+    case 0: return reinterpret_cast<const void*>(&sample_row_kernel<float, 1024>);
+    case 1: return reinterpret_cast<const void*>(&sample_row_kernel<__hip_bfloat16, 1024>);
+    case 2: return reinterpret_cast<const void*>(&sample_row_kernel<__half, 1024>);
+    default: return nullptr;
+  }
+}
+
+}  // namespace ert

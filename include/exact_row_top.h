@@ -385,6 +385,131 @@ int topk_validate(int32_t mode, const void* logits, int64_t row_stride, const vo
                   const void* extents2, int32_t num_rows, int32_t k, const void* indices,
                   const void* workspace, size_t workspace_bytes, int64_t max_row_len);
 
+/* ---- Row operators beside the selection --------------------------------------
+ * What a serving or training step chooses next to the top-K: the cache slots
+ * behind the selected positions, the experts of a token, the token itself.
+ * The conventions above hold (device pointers, stream order, status codes, no
+ * host reads); none of these calls allocates, keeps state or uses the
+ * library's slab, so calls on different streams are independent as long as
+ * their outputs and workspaces are.  Equal scores go to the lower index.
+ * Scores come in float32, bfloat16 or float16 (a TOPK_DT_* value), rows
+ * row_stride elements apart with unit inner stride, aligned to their element;
+ * whole aligned 16-byte groups that hold a row's scores are read. */
+#define TOPK_DT_F32 0
+#define TOPK_DT_BF16 1
+#define TOPK_DT_F16 2
+
+/* One token per row of logits [num_rows][vocab].
+ *
+ * NaN and -inf logits are never drawn.  With m the row's largest logit and
+ * w_i = exp((x_i - m) / temperature), the kept tokens are a prefix of the
+ * order by logit descending, then index ascending, cut by each of
+ *   top_k: its first top_k tokens (<= 0 or >= vocab: all);
+ *   top_p: the shortest prefix of those that holds at least top_p of their
+ *          weight, never fewer than one (>= 1 or NaN: all);
+ *   min_p: the tokens of those with w_i >= min(min_p, 1) (<= 0 or NaN: all).
+ * The token is the lowest index at which the kept weights' running sum in
+ * index order exceeds uniforms[r] times their total; uniforms outside [0, 1)
+ * are clamped into it, NaN counts as 0.  A temperature that is not > 0 gives
+ * the first token of the order.  A row without a drawable token gives -1.
+ * Weights are held as whole multiples of 2^-43 of the largest, so results do
+ * not depend on the order of any sum; weights below 2^-44 count as zero.
+ *  temperature, top_p, min_p: device float[num_rows], top_k: device
+ *      int32[num_rows]; each may be NULL (temperature 1, no cut).
+ *  logprobs: optional device float[num_rows]: ln(w_token / kept total) (0 for
+ *      temperature <= 0, -inf beside token -1).
+ *  vocab: 1 .. 2^20.  row_stride >= vocab.
+ *  workspace: at least topk_sample_workspace_bytes(num_rows, vocab) bytes,
+ *      16-byte aligned; it needs no initialisation and holds nothing between
+ *      calls (TOPK_EWORKSPACE if NULL or too small).
+ *  flags: TOPK_SAMPLE_WHOLE_ROW reads every row again instead of using the
+ *      candidates of its first reading (same results; for tests). */
+#define TOPK_SAMPLE_WHOLE_ROW 1u
+
+size_t topk_sample_workspace_bytes(int32_t num_rows, int32_t vocab);
+
+int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t vocab,
+                int32_t num_rows, const float* uniforms, const float* temperature,
+                const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+                float* logprobs, uint32_t flags, void* workspace, size_t workspace_bytes,
+                hipStream_t stream);
+
+/* The top_k experts of each token and their weights.
+ *
+ * logits [num_tokens][num_experts]; s = sigmoid(x) (TOPK_ROUTE_SIGMOID) or
+ * softmax over the token's experts; c = s + bias (bias: device
+ * float[num_experts] or NULL; it takes part in the choice only, and without
+ * one the order is that of the logits).  With num_groups > 1 the experts lie
+ * in that many equal groups; the topk_groups groups with the largest score
+ * (largest c, or with TOPK_ROUTE_TOP2 the sum of the two largest, one where
+ * the group has one) stay.  The top_k largest c among them are chosen, in
+ * falling order.  Experts whose logit or c is -inf or NaN are never chosen.
+ *  indices, weights: device int32 / float [num_tokens][top_k].  weights are s
+ *      of the chosen, divided by their sum with TOPK_ROUTE_RENORMALIZE, times
+ *      scale; slots without an expert hold -1 and 0, and a sum of zero gives
+ *      weights of 0.  Scores are 64-bit numbers: a sigmoid below 1e-308
+ *      counts as zero.
+ *  num_experts 1 .. 1024, top_k 1 .. min(64, num_experts), num_groups 1 .. 16
+ *  dividing num_experts, topk_groups 1 .. num_groups. */
+#define TOPK_ROUTE_SIGMOID 1u
+#define TOPK_ROUTE_TOP2 2u
+#define TOPK_ROUTE_RENORMALIZE 4u
+
+int topk_route(const void* logits, int32_t dtype, int64_t row_stride, int32_t num_tokens,
+               int32_t num_experts, int32_t top_k, const float* bias, int32_t num_groups,
+               int32_t topk_groups, uint32_t flags, float scale, int32_t* indices, float* weights,
+               hipStream_t stream);
+
+/* Gradient of topk_route's weights in the logits: grad_weights [num_tokens]
+ * [top_k] -> grad_logits [num_tokens][num_experts] in the logits' type, every
+ * element written.  flags and scale as in the forward call (TOPK_ROUTE_TOP2
+ * has no effect); indices as it returned them (entries outside [0,
+ * num_experts) have no gradient; an expert named twice counts twice).  The
+ * choice itself, the bias and the groups have no gradient. */
+int topk_route_backward(const void* logits, int32_t dtype, int64_t row_stride, int32_t num_tokens,
+                        int32_t num_experts, int32_t top_k, uint32_t flags, float scale,
+                        const int32_t* indices, const float* grad_weights, void* grad_logits,
+                        int64_t grad_row_stride, hipStream_t stream);
+
+/* Block tables and slot maps of one step of a paged cache, from request
+ * lengths.  Request r holds kv_lens[r] tokens once the step is done, the last
+ * new_tokens[r] of them new (clamped to 0 <= new <= kv).  Its table row gets
+ * the blocks it lacks, entries [ceil((kv - new) / block_size), ceil(kv /
+ * block_size)), from free_blocks, taken in request order from place
+ * free_start[0] on; other entries are read or left as they are.  The step's
+ * new tokens, request after request, get
+ *  token_starts  int32[num_requests + 1]: first token of each request, total;
+ *  token_requests, positions  int32[max_tokens]: request, position in it;
+ *  slots  int32 or int64 (slots_64) [max_tokens]: table[pos / block_size] *
+ *      block_size + pos % block_size;
+ *  free_next  int32[1]: free_start plus the blocks taken.
+ * Entries behind the last token hold -1; tokens past max_tokens are counted
+ * but not written (their blocks are handed out all the same).  Blocks past
+ * the table's max_blocks are not taken and their tokens' slots are -1, as are
+ * slots of negative blocks, of blocks the free list (num_free entries) does
+ * not hold (free_next then exceeds num_free) and, in int32, slots over
+ * 2^31 - 1.  Sums saturate at 2^31 - 1.
+ * num_requests 0 .. 4096; block_size 1 .. 2^30; free_next must not be
+ * free_start. */
+int topk_block_tables(int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
+                      int32_t num_requests, const int32_t* kv_lens, const int32_t* new_tokens,
+                      const int32_t* free_blocks, int64_t num_free, const int32_t* free_start,
+                      int32_t block_size, int64_t max_tokens, int32_t* token_starts,
+                      int32_t* token_requests, int32_t* positions, void* slots, int32_t slots_64,
+                      int32_t* free_next, hipStream_t stream);
+
+/* Slots of selected positions (a selection's local indices): slots[r][j] =
+ * table[i / block_size] * block_size + i % block_size for i = indices[r][j],
+ * in the table row of request row_requests[r] (device int32[num_rows]) or,
+ * without it, r / next_n.  -1 where i is negative or past the table, the
+ * request is not in [0, num_requests), the block is negative, or an int32 slot
+ * would exceed 2^31 - 1.  k >= 1: any row length.  int32 slots may be written
+ * over indices. */
+int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_t* block_tables,
+               int64_t table_stride, int32_t max_blocks, int32_t num_requests,
+               const int32_t* row_requests, int32_t next_n, int32_t block_size, void* slots,
+               int32_t slots_64, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,664 @@
+"""The row operators on the GPU against their definitions in 64 bits: sampling,
+expert routing and its gradient, block tables and slot maps, slots of
+selected positions; alone, on other streams, in captured graphs, and together
+with the selection as a serving step uses them."""
+import itertools
+
+import numpy as np
+import pytest
+
+import row_reference as ref
+from gpu_helpers import log
+
+pytestmark = pytest.mark.gpu
+
+NINF = float("-inf")
+
+
+@pytest.fixture(scope="module")
+def ert():
+    import torch
+    import exact_row_top_amd as m
+    assert torch.cuda.is_available()
+    m.load_library()
+    return m
+
+
+def _dt(name):
+    import torch
+    return {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[name]
+
+
+def _cuda(a, dtype=None):
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+# ---------------------------------------------------------------------------
+# sampling
+# ---------------------------------------------------------------------------
+
+def _check_sample(ert, x, u, what, lp_abs=1e-11, **setting):
+    """Tokens equal the definition's, log-probabilities to one fp32 rounding
+    (2^-24 of the value) beside the weights' own 2^-45 a term (1e-11)."""
+    import torch
+    host = x.float().cpu().numpy()
+    rows = host.shape[0]
+    u = np.asarray(u, dtype=np.float32)
+    dev = {k: _cuda(np.asarray(v, dtype=np.int32 if k == "top_k" else np.float32))
+           for k, v in setting.items()}
+    want = [ref.sample_row(host[r], u[r], **{k: (int(v[r]) if k == "top_k" else np.float32(v[r]))
+                                             for k, v in setting.items()}) for r in range(rows)]
+    ud = _cuda(u)
+    for whole in (False, True):
+        log(f"[sample] {what} whole_row={whole}")
+        tok, lp = ert.sample_tokens(x, ud, return_logprobs=True, whole_row=whole, **dev)
+        torch.cuda.synchronize()
+        got = tok.cpu().numpy()
+        bad = [(r, int(got[r]), want[r][0]) for r in range(rows) if got[r] != want[r][0]]
+        assert not bad, (what, whole, bad[:5])
+        lp = lp.cpu().numpy().astype(np.float64)
+        for r in range(rows):
+            w = want[r][1]
+            if np.isinf(w):
+                assert lp[r] == w
+            else:
+                assert abs(lp[r] - w) <= 2.0 ** -24 * abs(w) * 1.001 + lp_abs, (what, whole, r, lp[r], w)
+
+
+def _settings(rng, rows, kind):
+    s = {"temperature": rng.uniform(0.4, 1.4, rows)}
+    if kind in ("k", "all", "mixed"):
+        s["top_k"] = rng.integers(1, 300, rows)
+    if kind in ("p", "all", "mixed"):
+        s["top_p"] = rng.uniform(0.05, 0.999, rows)
+    if kind in ("m", "all", "mixed"):
+        s["min_p"] = rng.uniform(0.0, 0.3, rows)
+    if kind == "mixed":
+        s["temperature"][rng.random(rows) < 0.2] = 0.0
+        s["top_k"][rng.random(rows) < 0.5] = 0
+        s["top_p"][rng.random(rows) < 0.4] = 1.0
+        s["min_p"][rng.random(rows) < 0.5] = 0.0
+    return s
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [1, 2, 7, 63, 65, 1000, 2047, 2048, 2049, 6150, 40001])
+def test_sample_sizes(ert, dtype, vocab):
+    rng = np.random.default_rng([vocab, 1])
+    for kind in ("none", "k", "p", "m", "all", "mixed"):
+        rows = 5
+        x = _cuda(rng.normal(0, 2.5, (rows, vocab)).astype(np.float32), _dt(dtype))
+        _check_sample(ert, x, rng.random(rows), f"{dtype} vocab={vocab} {kind}",
+                      **_settings(rng, rows, kind))
+
+
+@pytest.mark.parametrize("vocab,rows", [(131072, 3), (200003, 2), (1 << 20, 1)])
+def test_sample_long_rows(ert, vocab, rows):
+    rng = np.random.default_rng([vocab, 2])
+    for kind, spread in (("none", 2.0), ("p", 0.1), ("p", 2.5), ("all", 3.0), ("mixed", 1.0)):
+        x = _cuda(rng.normal(0, spread, (rows, vocab)).astype(np.float32))
+        _check_sample(ert, x, rng.random(rows), f"vocab={vocab} {kind} spread={spread}",
+                      **_settings(rng, rows, kind))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("offset,stride", [(0, 5007), (1, 5009), (3, 5006), (5, 5021), (7, 5008)])
+def test_sample_unaligned_rows_and_poisoned_neighbours(ert, dtype, offset, stride):
+    import torch
+    rng = np.random.default_rng([offset, stride])
+    rows, vocab = 4, 5001
+    buf = torch.full((rows * stride + 64,), float("inf"), device="cuda", dtype=_dt(dtype))
+    buf[::3] = float("nan")
+    x = buf.as_strided((rows, vocab), (stride, 1), offset)
+    x.copy_(_cuda(rng.normal(0, 2, (rows, vocab)).astype(np.float32), _dt(dtype)))
+    for kind in ("none", "all", "p"):
+        _check_sample(ert, x, rng.random(rows), f"{dtype} offset={offset} stride={stride} {kind}",
+                      **_settings(rng, rows, kind))
+
+
+def test_sample_masked_infinite_and_equal_rows(ert):
+    rng = np.random.default_rng(3)
+    vocab = 4500
+    rows = []
+    rows.append(np.full(vocab, NINF))                                # nothing left
+    rows.append(np.full(vocab, np.nan))                              # nothing left
+    one = np.full(vocab, NINF); one[4321] = -3.0e38; rows.append(one)  # one left
+    mix = rng.normal(0, 2, vocab); mix[::2] = np.nan; mix[1::4] = NINF; rows.append(mix)
+    inf = rng.normal(0, 2, vocab); inf[[77, 2050, 4400]] = np.inf; rows.append(inf)
+    rows.append(np.full(vocab, np.inf))                              # all +inf
+    rows.append(np.full(vocab, 1.25))                                # all equal
+    rows.append(np.full(vocab, np.finfo(np.float32).min))            # the type's lowest value
+    two = np.zeros(vocab); two[1000:4000] = 1.0; rows.append(two)    # two classes
+    low = rng.normal(0, 1, vocab); low[:4000] = np.finfo(np.float32).min; rows.append(low)
+    wide = np.concatenate([[3e38, -3e38], rng.normal(0, 1, vocab - 2)]); rows.append(wide)
+    zero = np.where(np.arange(vocab) % 2 == 0, 0.0, -0.0); rows.append(zero)
+    x = _cuda(np.array(rows, dtype=np.float32))
+    n = len(rows)
+    u = np.linspace(0.013, 0.987, n)
+    full = np.full(n, 1.0)
+    _check_sample(ert, x, u, "special rows, no cut")
+    for k in (1, 2, 3, 700, 4499, 4500, 9000):
+        _check_sample(ert, x, u, f"special rows top_k={k}", top_k=[k] * n)
+    for p in (0.0, 1e-9, 0.37, 0.999):
+        _check_sample(ert, x, u, f"special rows top_p={p}", top_p=[p] * n)
+    for m in (1e-20, 0.2, 1.0, 7.0):
+        _check_sample(ert, x, u, f"special rows min_p={m}", min_p=[m] * n)
+    _check_sample(ert, x, u, "special rows, all cuts", top_k=[1500] * n, top_p=[0.61] * n,
+                  min_p=[0.05] * n, temperature=0.7 * full)
+    for t in (0.0, -1.0, np.nan, np.inf, 1e-30, 1e30):
+        _check_sample(ert, x, u, f"special rows T={t}", temperature=[t] * n)
+        _check_sample(ert, x, u, f"special rows T={t} top_k", temperature=[t] * n, top_k=[1234] * n)
+
+
+def test_sample_uniform_ends_and_settings_that_cut_nothing(ert):
+    rng = np.random.default_rng(4)
+    u = np.array([0.0, 1e-30, 2.0 ** -24, 0.5, 1 - 2.0 ** -24, 1.0, 7.0, -1.0, np.nan, np.inf], dtype=np.float32)
+    n = u.size
+    x = _cuda(rng.normal(0, 2, (n, 3001)).astype(np.float32))
+    _check_sample(ert, x, u, "uniform ends")
+    _check_sample(ert, x, u, "uniform ends, cut", top_k=[40] * n, top_p=[0.9] * n)
+    _check_sample(ert, x, u, "nothing cut", top_k=[0, -5, 3001, 10 ** 9, 3002] * 2,
+                  top_p=[1.0, 1.5, np.nan, np.inf, 1.0] * 2, min_p=[0.0, -1.0, np.nan, 0.0, -0.0] * 2)
+
+
+def test_sample_crowded_candidates(ert):
+    # more equal scores than a segment or the row hands on, ties at the cut,
+    # the likely tokens side by side, and a flat row that needs most of it
+    rng = np.random.default_rng(5)
+    vocab, rows = 50000, 6
+    x = np.zeros((rows, vocab))
+    x[0] = np.round(rng.normal(0, 1, vocab))
+    x[1] = rng.integers(0, 3, vocab)
+    x[2] = rng.normal(0, 0.05, vocab)
+    x[3] = rng.normal(0, 1, vocab); x[3, 30000:31000] += 8
+    x[4] = -np.abs(np.arange(vocab) - 25000) / 3000.0
+    x[5] = rng.normal(0, 1, vocab); x[5, ::17] = 4.0
+    xd = _cuda(x.astype(np.float32))
+    u = rng.random(rows)
+    for k in (5, 64, 500, 3333, 20000):
+        _check_sample(ert, xd, u, f"crowded top_k={k}", top_k=[k] * rows)
+    for p in (0.1, 0.5, 0.95, 0.9999):
+        _check_sample(ert, xd, u, f"crowded top_p={p}", top_p=[p] * rows, top_k=[0, 9000] * 3)
+    _check_sample(ert, xd, u, "crowded min_p", min_p=[0.5, 1.0, 0.9, 0.1, 0.01, 0.9])
+
+
+def test_sample_outputs_given_and_empty_batch(ert):
+    import torch
+    x = torch.randn(4, 999, device="cuda")
+    u = torch.rand(4, device="cuda")
+    tok = torch.full((4,), -9, dtype=torch.int32, device="cuda")
+    lp = torch.full((4,), -9.0, device="cuda")
+    got = ert.sample_tokens(x, u, tokens=tok, logprobs=lp)
+    assert got[0] is tok and got[1] is lp
+    assert torch.equal(tok, ert.sample_tokens(x, u))
+    empty = ert.sample_tokens(x[:0], u[:0], return_logprobs=True)
+    assert empty[0].shape == (0,) and empty[1].shape == (0,)
+
+
+def test_sample_follows_the_distribution(ert):
+    # a grid of uniforms draws each token as often as its weight says, to one
+    # grid step
+    import torch
+    p = np.array([0.4, 0.1, 0.25, 0.05, 0.2])
+    n = 4000
+    x = _cuda(np.tile(np.log(p), (n, 1)).astype(np.float32))
+    u = (torch.arange(n, device="cuda") + 0.5) / n
+    tok = ert.sample_tokens(x, u).cpu().numpy()
+    assert np.all(np.abs(np.bincount(tok, minlength=5) - n * p) <= 1.0 + 1e-3)
+    assert np.all(np.diff(tok) >= 0)
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+
+def _check_route(ert, x, top_k, what, bias=None, **kw):
+    """Experts equal the definition's; weights to one fp32 rounding (2^-24)
+    beside 64-bit arithmetic (1e-12)."""
+    import torch
+    log(f"[route] {what}")
+    host = x.float().cpu().numpy()
+    names = {"num_groups": "groups"}
+    want = [ref.route_token(host[t], top_k, bias=bias,
+                            **{names.get(k, k): v for k, v in kw.items()})
+            for t in range(host.shape[0])]
+    b = _cuda(np.asarray(bias, dtype=np.float32)) if bias is not None else None
+    idx, w = ert.route_experts(x, top_k, bias=b, **kw)
+    torch.cuda.synchronize()
+    idx, w = idx.cpu().numpy(), w.cpu().numpy().astype(np.float64)
+    for t, (wi, ww) in enumerate(want):
+        assert np.array_equal(idx[t], wi), (what, t, idx[t], wi)
+        assert np.all(np.abs(w[t] - ww) <= np.abs(ww) * (2.0 ** -24 + 1e-12) + 2.0 ** -149), (what, t, w[t], ww)
+
+
+ROUTE_SHAPES = [(1, 1, 1, 1), (2, 2, 1, 1), (8, 2, 1, 1), (8, 3, 4, 2), (60, 6, 1, 1), (64, 8, 8, 3),
+                (63, 5, 3, 2), (128, 8, 1, 1), (160, 6, 8, 3), (255, 16, 5, 5), (256, 8, 8, 4),
+                (257, 4, 1, 1), (384, 8, 1, 1), (472, 13, 8, 7), (512, 10, 16, 2), (1024, 64, 2, 1)]
+
+
+@pytest.mark.parametrize("experts,top_k,groups,topk_groups", ROUTE_SHAPES)
+def test_route_shapes(ert, experts, top_k, groups, topk_groups):
+    rng = np.random.default_rng([experts, top_k])
+    for scoring, with_bias, renorm, dtype in itertools.product(
+            ("softmax", "sigmoid"), (False, True), (False, True), ("fp32", "bf16")):
+        tokens = int(rng.integers(1, 23))
+        x = _cuda(rng.normal(0, 1.5, (tokens, experts)).astype(np.float32), _dt(dtype))
+        bias = rng.normal(0, 0.1, experts).astype(np.float32) if with_bias else None
+        for gs in (("max", "top2") if groups > 1 else ("max",)):
+            _check_route(ert, x, top_k, f"E={experts} k={top_k} {scoring} bias={with_bias} "
+                         f"renorm={renorm} {dtype} {gs}", bias=bias, scoring=scoring,
+                         num_groups=groups, topk_groups=topk_groups, group_score=gs,
+                         renormalize=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_ties_masks_and_extremes(ert, scoring):
+    rng = np.random.default_rng(6)
+    E = 64
+    rows = [np.zeros(E), rng.integers(-2, 3, E).astype(float), np.full(E, NINF), np.full(E, np.nan)]
+    few = np.full(E, NINF); few[[3, 40, 41]] = [0.5, 2.0, 2.0]; rows.append(few)
+    half = rng.normal(0, 1, E); half[::2] = NINF; half[1] = np.nan; rows.append(half)
+    rows.append(np.full(E, -200.0)); rows.append(np.full(E, 90.0))
+    rows.append(np.linspace(-87, 88, E)); rows.append(np.full(E, np.finfo(np.float32).min))
+    inf = rng.normal(0, 1, E); inf[[5, 6]] = np.inf; rows.append(inf)
+    near = 1.0 + np.arange(E) * 2.0 ** -23; rows.append(near)
+    rows.append(near[::-1].copy())
+    x = _cuda(np.array(rows, dtype=np.float32))
+    equal = np.full(E, 0.25, dtype=np.float32)
+    masked = rng.normal(0, 0.1, E).astype(np.float32); masked[[0, 9]] = NINF; masked[11] = np.nan
+    for bias, (groups, tg), renorm in itertools.product((None, equal, masked),
+                                                        ((1, 1), (8, 2)), (False, True)):
+        for gs in (("max", "top2") if groups > 1 else ("max",)):
+            _check_route(ert, x, 8, f"special {scoring} bias={bias is not None} groups={groups} {gs} "
+                         f"renorm={renorm}", bias=bias, scoring=scoring, num_groups=groups,
+                         topk_groups=tg, group_score=gs, renormalize=renorm)
+
+
+def test_route_many_tokens_strided_and_tied(ert):
+    import torch
+    rng = np.random.default_rng(7)
+    for dtype, experts, pad in (("bf16", 256, 3), ("fp32", 128, 1), ("fp16", 320, 0)):
+        buf = torch.full((1111, experts + pad), float("inf"), device="cuda", dtype=_dt(dtype))
+        x = buf[:, :experts]
+        x.copy_(_cuda(rng.normal(0, 1, (1111, experts)).astype(np.float32), _dt(dtype)))
+        _check_route(ert, x, 8, f"many {dtype} zero bias", bias=np.zeros(experts, np.float32),
+                     scoring="sigmoid", num_groups=8, topk_groups=4, group_score="top2")
+        _check_route(ert, x, 6, f"many {dtype} no bias", scoring="softmax", renormalize=False)
+
+
+def _check_grad(ert, x, idx, g, what, **kw):
+    """One fp32 rounding of each of at most three terms (3 * 2^-24 of their
+    size), then one rounding to the output type (half a step, or half the
+    smallest subnormal)."""
+    import torch
+    log(f"[route grad] {what}")
+    host = x.float().cpu().numpy()
+    got = ert.route_experts_backward(_cuda(g.astype(np.float32)), x, _cuda(idx.astype(np.int32)), **kw)
+    torch.cuda.synchronize()
+    fi = torch.finfo(x.dtype)
+    got = got.double().cpu().numpy()
+    assert got.shape == host.shape
+    for t in range(host.shape[0]):
+        want, size = ref.route_grad_token(host[t], idx[t], g[t].astype(np.float32).astype(np.float64), **kw)
+        tol = size * (3 * 2.0 ** -24 + 1e-12) * (1 + fi.eps) + np.abs(want) * fi.eps / 2 \
+            + fi.smallest_normal * fi.eps / 2 + 2.0 ** -149
+        bad = np.flatnonzero(~(np.abs(got[t] - want) <= tol))
+        assert bad.size == 0, (what, t, bad[:4], got[t][bad[:4]], want[bad[:4]])
+
+
+@pytest.mark.parametrize("experts,top_k,groups,topk_groups", ROUTE_SHAPES)
+def test_route_gradient(ert, experts, top_k, groups, topk_groups):
+    rng = np.random.default_rng([experts, top_k, 1])
+    for scoring, renorm, dtype in itertools.product(("softmax", "sigmoid"), (False, True),
+                                                    ("fp32", "bf16", "fp16")):
+        tokens = int(rng.integers(1, 23))
+        x = _cuda(rng.normal(0, 1.5, (tokens, experts)).astype(np.float32), _dt(dtype))
+        idx = np.stack([rng.permutation(experts)[:top_k] for _ in range(tokens)])
+        _check_grad(ert, x, idx, rng.normal(0, 1, (tokens, top_k)), f"E={experts} k={top_k} "
+                    f"{scoring} renorm={renorm} {dtype}", scoring=scoring, renormalize=renorm, scale=1.5)
+
+
+def test_route_gradient_masks_repeats_and_extremes(ert):
+    rng = np.random.default_rng(8)
+    E, K = 48, 4
+    x = rng.normal(0, 1, (8, E)).astype(np.float32)
+    x[0] = NINF
+    x[1] = np.nan
+    x[2, 5:] = NINF
+    x[3] = -300.0
+    x[4] = 95.0
+    x[5] = np.linspace(-90, 90, E)
+    idx = np.array([[-1] * 4, [-1] * 4, [0, 3, -1, -1], [1, 2, 3, 4], [7, 6, 5, 4], [0, 47, 24, 10],
+                    [9, 9, 9, 2], [3, E, -7, 3]])
+    g = rng.normal(0, 1, (8, K))
+    for scoring, renorm, dtype in itertools.product(("softmax", "sigmoid"), (False, True), ("fp32", "bf16")):
+        _check_grad(ert, _cuda(x, _dt(dtype)), idx, g, f"special {scoring} {renorm} {dtype}",
+                    scoring=scoring, renormalize=renorm, scale=0.7)
+
+
+@pytest.mark.parametrize("scoring,renorm", itertools.product(("softmax", "sigmoid"), (False, True)))
+def test_route_gradient_against_differences(ert, scoring, renorm):
+    # central differences of the 64-bit definition: their own error is about
+    # h^2 = 1e-10 and 1e-16 / h = 1e-11
+    import torch
+    rng = np.random.default_rng(9)
+    x = rng.normal(0, 1, (3, 24)).astype(np.float32)
+    g = rng.normal(0, 1, (3, 5)).astype(np.float32)
+    xd = _cuda(x).requires_grad_()
+    idx, w = ert.route_experts(xd, 5, scoring=scoring, renormalize=renorm, scale=1.25)
+    assert w.requires_grad and not idx.requires_grad
+    w.backward(_cuda(g))
+    got = xd.grad.double().cpu().numpy()
+    idx = idx.cpu().numpy()
+    h = 1e-5
+    for t in range(3):
+        for e in range(24):
+            hi, lo = x[t].astype(np.float64), x[t].astype(np.float64)
+            hi[e] += h
+            lo[e] -= h
+            d = (ref.weights_of(hi, idx[t], scoring, renorm, 1.25) -
+                 ref.weights_of(lo, idx[t], scoring, renorm, 1.25)) / (2 * h)
+            assert abs((d * g[t]).sum() - got[t, e]) <= 1e-6
+
+
+def test_route_autograd_broadcast_gradient_and_refusals(ert):
+    import torch
+    x = torch.randn(33, 40, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    idx, w = ert.route_experts(x, 3, scoring="sigmoid", scale=2.0, renormalize=False)
+    w.sum().backward()                       # the gradient comes as a broadcast one
+    want = ert.route_experts_backward(torch.ones(33, 3, device="cuda"), x.detach(), idx,
+                                      scoring="sigmoid", scale=2.0, renormalize=False)
+    assert torch.equal(x.grad, want)
+    with torch.no_grad():
+        assert not ert.route_experts(x, 3)[1].requires_grad
+    with pytest.raises(ValueError):
+        ert.route_experts(x, 3, stream=torch.cuda.current_stream())
+    _, w = ert.route_experts(x, 3)
+    gx, = torch.autograd.grad(w.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        gx.float().sum().backward()          # no second derivative
+
+
+# ---------------------------------------------------------------------------
+# block tables and slots
+# ---------------------------------------------------------------------------
+
+def _check_tables(ert, kv, new, bs, what, width=None, num_free=None, start=0, max_tokens=None,
+                  wide=False, pad=0, block_base=0, seed=0):
+    import torch
+    log(f"[tables] {what}")
+    rng = np.random.default_rng([seed, len(kv), bs])
+    kv, new = np.asarray(kv, np.int32), np.asarray(new, np.int32)
+    R = kv.size
+    c = np.maximum(kv, 0).astype(np.int64)
+    a = np.minimum(np.maximum(new, 0), c)
+    need = -(-c // bs)
+    width = int(need.max(initial=0)) + 2 if width is None else width
+    total_new = int((need - (-(-(c - a) // bs))).sum())
+    num_free = total_new + start + 3 if num_free is None else num_free
+    ids = (rng.permutation(R * width + num_free) + block_base).astype(np.int32)
+    tables = np.full((R, width + pad), -77, np.int32)
+    tables[:, :width] = ids[:R * width].reshape(R, width)
+    free = ids[R * width:]
+    max_tokens = int(a.sum()) + 5 if max_tokens is None else max_tokens
+    td = _cuda(tables)
+    view = td[:, :width]
+    got = ert.extend_block_tables(view, _cuda(kv), _cuda(new), _cuda(free),
+                                  torch.tensor([start], dtype=torch.int32, device="cuda"), bs,
+                                  max_tokens, slot_dtype=torch.int64 if wide else None)
+    torch.cuda.synchronize()
+    want = ref.extend_tables(tables[:, :width], kv, new, free, start, bs, max_tokens, wide)
+    names = ("token_starts", "token_requests", "positions", "slots")
+    assert np.array_equal(view.cpu().numpy(), want[0]), what
+    if pad:
+        assert (td[:, width:] == -77).all(), "columns behind the table were written"
+    for name, g, w in zip(names, got[:4], want[1:5]):
+        assert np.array_equal(g.cpu().numpy(), w), (what, name)
+    assert int(got[4]) == want[5], what
+
+
+@pytest.mark.parametrize("bs", [1, 3, 16, 48, 64])
+def test_tables_lengths(ert, bs):
+    rng = np.random.default_rng(bs)
+    kv = [0, 1, bs, bs + 1, 2 * bs - 1, 2 * bs, 500, 513, 64, 0, 7]
+    _check_tables(ert, kv, kv, bs, f"whole prompts bs={bs}")
+    _check_tables(ert, kv, [1] * len(kv), bs, f"one new each bs={bs}", pad=3)
+    _check_tables(ert, kv, [0] * len(kv), bs, f"nothing new bs={bs}")
+    _check_tables(ert, kv, rng.integers(0, 9, len(kv)), bs, f"some new bs={bs}", start=4, wide=True)
+    _check_tables(ert, [-5, 10, 3], [4, 99, -2], bs, f"lengths out of range bs={bs}")
+
+
+@pytest.mark.parametrize("requests", [0, 1, 2, 255, 256, 257, 1000, 4096])
+def test_tables_request_counts(ert, requests):
+    rng = np.random.default_rng(requests)
+    kv = rng.integers(0, 90, requests)
+    _check_tables(ert, kv, np.minimum(kv, rng.integers(0, 60, requests)), 16,
+                  f"{requests} requests", start=11)
+
+
+def test_tables_long_short_lists_and_narrow_tables(ert):
+    _check_tables(ert, [70000, 3, 40001], [70000, 3, 20000], 16, "long prompts")
+    _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "free list too short", num_free=9)
+    _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "free list used up", num_free=9, start=20)
+    _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "no free list", num_free=0)
+    _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "table too narrow", width=5)
+    _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "more tokens than places", max_tokens=77)
+    _check_tables(ert, [100, 200], [100, 200], 16, "no places", max_tokens=0)
+    _check_tables(ert, [100, 200], [100, 200], 16, "padding behind", max_tokens=9000)
+    # slots on both sides of 2^31
+    for wide in (False, True):
+        _check_tables(ert, [300, 5000], [300, 4000], 64, f"far blocks wide={wide}",
+                      block_base=(1 << 25) - 60, wide=wide)
+
+
+@pytest.mark.parametrize("k,bs,next_n,wide", [(512, 64, 1, False), (1024, 16, 3, False), (2048, 48, 2, True),
+                                              (1, 1, 1, False), (7, 5, 4, True), (1000, 64, 1, False)])
+def test_slots(ert, k, bs, next_n, wide):
+    import torch
+    rng = np.random.default_rng([k, bs])
+    rows = 10
+    R, width = (rows + next_n - 1) // next_n, 40
+    tables = rng.permutation(R * width).reshape(R, width).astype(np.int32)
+    tables[0, 3] = -1
+    idx = rng.integers(-1, width * bs, (rows, k)).astype(np.int32)
+    idx[1, :] = -1
+    idx[2, 0] = width * bs            # past the table
+    idx[3, 0] = 2 ** 31 - 1
+    owner = np.arange(rows) // next_n
+    dt = torch.int64 if wide else torch.int32
+    got = ert.topk_slots(_cuda(idx), _cuda(tables), bs, next_n=next_n, slot_dtype=dt)
+    assert got.dtype == dt
+    assert np.array_equal(got.cpu().numpy(), ref.slots_of(idx, tables, bs, owner, wide))
+    owner = rng.integers(-1, R + 1, rows).astype(np.int32)   # requests outside the tables too
+    own = _cuda(idx)
+    got = ert.topk_slots(own, _cuda(tables), bs, row_requests=_cuda(owner), slot_dtype=dt,
+                         slots=None if wide else own)
+    assert np.array_equal(got.cpu().numpy(), ref.slots_of(idx, tables, bs, owner, wide))
+    if not wide:
+        assert got is own
+
+
+def test_slots_strided_tables_far_blocks_and_empty(ert):
+    import torch
+    tables = np.array([[1 << 25, (1 << 25) - 1, 5], [0, 2 ** 31 - 1, 7]], np.int32)
+    big = torch.full((2, 9), 3, dtype=torch.int32, device="cuda")
+    big[:, :3] = _cuda(tables)
+    idx = np.array([[0, 63, 64, 127, 128, -1], [1, 64, 70, 191, 192, 0]], np.int32)
+    for wide in (False, True):
+        got = ert.topk_slots(_cuda(idx), big[:, :3], 64, slot_dtype=torch.int64 if wide else torch.int32)
+        assert np.array_equal(got.cpu().numpy(), ref.slots_of(idx, tables, 64, [0, 1], wide))
+    none = ert.topk_slots(_cuda(idx)[:0], big, 64)
+    assert none.shape == (0, 6)
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, and the operators together
+# ---------------------------------------------------------------------------
+
+def _step(ert, s):
+    """A decode step's choices: slots for the new tokens, the selection, its
+    slots, the experts, the next token."""
+    starts, owner, pos, slots, nxt = ert.extend_block_tables(
+        s["tables"], s["kv"], s["new"], s["free"], s["start"], 64, s["kv"].shape[0] * s["next_n"])
+    sel = ert.topk_decode_varlen(s["scores"], s["kv"], 512, next_n=s["next_n"], workspace=s["ws"],
+                                 sorted=True, deterministic=True)
+    where = ert.topk_slots(sel, s["tables"], 64, next_n=s["next_n"])
+    experts, weights = ert.route_experts(s["router"], 4, scoring="sigmoid", bias=s["bias"],
+                                         num_groups=4, topk_groups=2, group_score="top2")
+    token, lp = ert.sample_tokens(s["logits"], s["u"], temperature=s["t"], top_k=s["k"],
+                                  top_p=s["p"], min_p=s["m"], return_logprobs=True)
+    return [starts, owner, pos, slots, nxt, sel, where, experts, weights, token, lp, s["tables"]]
+
+
+def _step_state(ert, seed, requests=6, next_n=2):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    rows = requests * next_n
+    def rand(*shape):
+        return torch.rand(*shape, device="cuda", generator=g)
+    kv = torch.tensor([3, 64, 640, 2047, 4000, 1000][:requests], dtype=torch.int32, device="cuda") + seed
+    ids = torch.randperm(requests * 70 + 64, device="cuda", generator=g).to(torch.int32)
+    tables = ids[:requests * 70].view(requests, 70).clone()
+    return {"kv": kv, "new": torch.full((requests,), next_n, dtype=torch.int32, device="cuda"),
+            "tables": tables, "free": ids[requests * 70:].clone(), "next_n": next_n,
+            "start": torch.tensor([seed % 5], dtype=torch.int32, device="cuda"),
+            "scores": torch.randn(rows, 4096, device="cuda", generator=g),
+            "ws": ert.new_workspace(rows, 4096, 512),
+            "router": torch.randn(rows, 64, device="cuda", generator=g).bfloat16(),
+            "bias": torch.randn(64, device="cuda", generator=g) * 0.05,
+            "logits": (torch.randn(rows, 9001, device="cuda", generator=g) * 2).half(),
+            "u": rand(rows), "t": rand(rows) + 0.3,
+            "k": torch.randint(0, 90, (rows,), device="cuda", generator=g, dtype=torch.int32),
+            "p": rand(rows) * 0.3 + 0.7, "m": rand(rows) * 0.05}
+
+
+def _check_step(s, out):
+    host = {k: v.float().cpu().numpy() if v.is_floating_point() else v.cpu().numpy()
+            for k, v in s.items() if hasattr(v, "cpu")}
+    o = [t.cpu().numpy() for t in out]
+    rows, n = host["scores"].shape[0], s["next_n"]
+    for r in range(rows):
+        kv = int(host["kv"][r // n])
+        nv = min(kv - n + r % n + 1, 4096) if kv >= n else 0
+        x = host["scores"][r, :nv]
+        want = np.argsort(-x, kind="stable")[:512] if nv > 512 else np.arange(nv)
+        assert np.array_equal(o[5][r, :want.size], want) and (o[5][r, want.size:] == -1).all()
+        assert np.array_equal(o[7][r], ref.route_token(host["router"][r], 4, "sigmoid", host["bias"],
+                                                       4, 2, "top2")[0])
+        assert o[9][r] == ref.sample_row(host["logits"][r], host["u"][r], host["t"][r],
+                                         int(host["k"][r]), host["p"][r], host["m"][r])[0]
+    assert np.array_equal(o[6], ref.slots_of(o[5], o[11], 64, np.arange(rows) // n))
+
+
+def test_a_decode_step_together(ert):
+    import torch
+    for seed in range(3):
+        s = _step_state(ert, seed)
+        before = s["tables"].cpu().numpy()
+        out = _step(ert, s)
+        torch.cuda.synchronize()
+        want = ref.extend_tables(before, s["kv"].cpu().numpy(), s["new"].cpu().numpy(),
+                                 s["free"].cpu().numpy(), int(s["start"]), 64, 12)
+        for got, w in zip([out[11], *out[:4]], want[:5]):
+            assert np.array_equal(got.cpu().numpy(), w)
+        assert int(out[4]) == want[5]
+        _check_step(s, out)
+
+
+def test_a_captured_step_replays(ert):
+    # captured once, replayed with new inputs copied in and eager work between
+    import torch
+    s = _step_state(ert, 0)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _step(ert, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _step(ert, s)
+    for seed in (1, 2, 3, 4):
+        n = _step_state(ert, seed)
+        for k, v in n.items():
+            if k not in ("next_n", "ws"):
+                s[k].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = _step(ert, n)
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b), seed
+        _check_step(n, eager)
+
+
+def test_two_captured_graphs_and_eager_calls_share_nothing(ert):
+    import torch
+    a, b = _step_state(ert, 5), _step_state(ert, 6)
+    want_a = [t.clone() for t in _step(ert, a)]
+    want_b = [t.clone() for t in _step(ert, b)]
+    torch.cuda.synchronize()
+    graphs = []
+    for s in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = _step(ert, s)
+        graphs.append((g, out))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for st, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        eager = ert.sample_tokens(a["logits"], a["u"], temperature=a["t"], top_k=a["k"], top_p=a["p"],
+                                  min_p=a["m"])
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want_a[9])
+        for (_, out), want in zip(graphs, (want_a, want_b)):
+            for x, y in zip(out, want):
+                assert torch.equal(x, y)
+
+
+def test_other_streams(ert):
+    import torch
+    st = torch.cuda.Stream()
+    x = torch.randn(8, 30000, device="cuda") * 2
+    u = torch.rand(8, device="cuda")
+    p = torch.full((8,), 0.9, device="cuda")
+    r = torch.randn(100, 64, device="cuda")
+    want = ert.sample_tokens(x, u, top_p=p), *ert.route_experts(r, 4)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = ert.sample_tokens(x, u, top_p=p, stream=st), *ert.route_experts(r, 4, stream=st)
+        other = ert.sample_tokens(x, u, top_p=p), *ert.route_experts(r, 4)
+        torch.cuda.synchronize()
+        for g, o, w in zip(got, other, want):
+            assert torch.equal(g, w) and torch.equal(o, w)
+
+
+def test_training_step_captured_beside_eager(ert):
+    # forward and backward captured on tensors of their own, with eager work on
+    # other leaves between the replays
+    import torch
+    x = torch.randn(50, 96, device="cuda", requires_grad=True)
+    g = torch.randn(50, 6, device="cuda")
+    def step(t):
+        _, w = ert.route_experts(t, 6, scoring="softmax", renormalize=True, scale=1.5)
+        return torch.autograd.grad(w, t, g)[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x)
+    for seed in range(3):
+        torch.manual_seed(seed)
+        new = torch.randn(50, 96, device="cuda")
+        with torch.no_grad():
+            x.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step(new.requires_grad_()))
