@@ -22,12 +22,29 @@ struct SegRecord {
   float floor;      // every live score >= floor is among the candidates
   int32_t count;    // candidates, -1 if they did not fit
   uint64_t mass;    // rows that need it: sum of the weights against `best`
-  uint64_t pad;
+  float low;        // rows with cuts: smallest live score
+  uint32_t pad;
 };
 
 struct Candidate {
   float x;
   int32_t i;
+};
+
+// A row's way through the kernels after the row kernel.
+constexpr int kRowBlock = 256;
+constexpr int kWideBlock = 512;   // a wave for each segment
+constexpr int kWideSegs = kWideBlock / 64;
+constexpr int kBinsS = 1024;      // histogram bins
+enum : uint32_t { kWideDone = 0, kWideBins = 1, kWideMembers = 2, kWideWhole = 3 };
+struct WideRow {
+  uint32_t state;
+  float m;              // the row's largest score
+  double scale;         // bins per unit of score below it
+  uint64_t need;        // count or mass at the cut; then what of it the crossing bin holds
+  int32_t bin;          // the crossing bin, kBinsS if nothing is cut
+  uint32_t members;     // scores listed from it
+  uint32_t arrived[2];  // workgroups done with the bins, with the members
 };
 
 struct SampleParams {
@@ -44,8 +61,12 @@ struct SampleParams {
   int32_t* tokens;
   float* logprobs;
   SegRecord* records;
-  Candidate* candidates;
-  int32_t whole_row;   // take the path that reads the row again
+  Candidate* candidates;  // [rows][segments][kSegSlots]; later the crossing bin's members
+  WideRow* wide;          // null where no row can have a cut
+  uint64_t* kept;         // [rows][segments]
+  uint64_t* slices;       // [rows][wide_wgs][kBinsS]
+  int32_t wide_wgs;       // workgroups of a row
+  int32_t whole_row;      // every row from memory
 };
 
 // ---- 16-byte score groups ----------------------------------------------------

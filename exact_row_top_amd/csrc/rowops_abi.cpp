@@ -13,6 +13,8 @@
 namespace ert {
 const void* sample_segment_kernel_ptr(int dtype);
 const void* sample_row_kernel_ptr(int dtype);
+const void* sample_bins_kernel_ptr(int dtype);
+const void* sample_wide_kernel_ptr(int dtype);
 const void* route_kernel_ptr(int dtype, int lanes);
 const void* route_grad_kernel_ptr(int dtype, int lanes);
 const void* block_table_kernel_ptr();
@@ -59,6 +61,8 @@ int launch(const void* kernel, int64_t grid, int block, void* params, size_t lds
 // an aligned boundary.
 int64_t segments_of(int32_t vocab) { return ((int64_t)vocab + 7 + kSegment - 1) / kSegment; }
 
+int64_t wide_wgs_of(int64_t segments) { return (segments + kWideSegs - 1) / kWideSegs; }
+
 bool route_shape_ok(int32_t tokens, int32_t experts, int32_t top_k) {
   return tokens >= 0 && experts >= 1 && experts <= kMaxExperts && top_k >= 1 && top_k <= kMaxRouteK &&
          top_k <= experts;
@@ -70,8 +74,9 @@ extern "C" {
 
 size_t topk_sample_workspace_bytes(int32_t num_rows, int32_t vocab) {
   if (num_rows < 1 || vocab < 1 || vocab > kMaxVocab) return 0;
-  return (size_t)num_rows * (size_t)segments_of(vocab) *
-         (sizeof(SegRecord) + kSegSlots * sizeof(Candidate));
+  const size_t seg = (size_t)segments_of(vocab);
+  return (size_t)num_rows * (seg * (sizeof(SegRecord) + kSegSlots * sizeof(Candidate) + 8) +
+                             wide_wgs_of(seg) * kBinsS * 8 + sizeof(WideRow));
 }
 
 int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t vocab,
@@ -108,12 +113,24 @@ int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t v
   p.min_p = min_p;
   p.tokens = tokens;
   p.logprobs = logprobs;
+  // the row's settings alone say whether it has a cut; without any, no row has
+  const bool cuts = top_k || top_p || min_p;
+  const bool whole = (flags & TOPK_SAMPLE_WHOLE_ROW) != 0;
+  const int64_t wgs = wide_wgs_of(segments);
   p.records = static_cast<SegRecord*>(workspace);
   p.candidates = reinterpret_cast<Candidate*>(p.records + waves);
-  p.whole_row = (flags & TOPK_SAMPLE_WHOLE_ROW) ? 1 : 0;
+  p.kept = reinterpret_cast<uint64_t*>(p.candidates + waves * kSegSlots);
+  p.slices = p.kept + waves;
+  p.wide = (cuts || whole) ? reinterpret_cast<WideRow*>(p.slices + num_rows * wgs * kBinsS) : nullptr;
+  p.wide_wgs = (int32_t)wgs;
+  p.whole_row = whole ? 1 : 0;
   rc = launch(sample_segment_kernel_ptr(dtype), (waves + 3) / 4, 256, &p, 0, stream);
-  if (rc != TOPK_OK) return rc;
-  return launch(sample_row_kernel_ptr(dtype), num_rows, 1024, &p, 0, stream);
+  if (rc == TOPK_OK) rc = launch(sample_row_kernel_ptr(dtype), num_rows, kRowBlock, &p, 0, stream);
+  if (rc == TOPK_OK && (top_k || top_p) && !whole)
+    rc = launch(sample_bins_kernel_ptr(dtype), num_rows * wgs, kWideBlock, &p, 0, stream);
+  if (rc == TOPK_OK && (cuts || whole))
+    rc = launch(sample_wide_kernel_ptr(dtype), num_rows * wgs, kWideBlock, &p, 0, stream);
+  return rc;
 }
 
 int topk_route(const void* logits, int32_t dtype, int64_t row_stride, int32_t num_tokens,

@@ -44,18 +44,20 @@ __device__ __forceinline__ double exp2_poly(double f) {
   return __builtin_fma(p, f, 0x1.000000000003dp+0);
 }
 
-// round(2^43 * 2^-t) for 0 <= t < 44.  Adding 1.5 * 2^52 rounds t to a whole
-// n in the sum's low word; adding 2^52 to the scaled value rounds it to a
-// whole number in the sum's low 52 bits.
-__device__ __forceinline__ uint64_t weight_of(double t) {
+// round(2^43 * 2^s) for s <= 0, under the exponent bits of 2^52: adding 1.5 *
+// 2^52 rounds s to a whole n, which then stands in the sum's low bits; adding
+// 2^52 to the scaled value rounds it to a whole number in the low 52 bits.  s
+// below -60 (or NaN) is taken as -60 and gives zero.  Callers that add many
+// of them up take the exponent bits out once, at the end.
+constexpr uint64_t kRaw = 0x4330000000000000ull;
+__device__ __forceinline__ uint64_t raw_weight(double s) {
   const double magic = 6755399441055744.0;
-  const double tm = t + magic;
-  const double n = tm - magic;
-  const double p = exp2_poly(n - t);
-  const uint32_t hi = (uint32_t)(1023 + 43 - (int)(uint32_t)__double_as_longlong(tm)) << 20;
-  const double scale = __hiloint2double((int)hi, 0);
-  const double r = __builtin_fma(p, scale, 4503599627370496.0);
-  return (uint64_t)__double_as_longlong(r) & 0xFFFFFFFFFFFFFull;
+  s = __builtin_fmax(s, -60.0);
+  const double sm = s + magic;
+  const double p = exp2_poly(s - (sm - magic));
+  const uint32_t hi = ((uint32_t)__double_as_longlong(sm) << 20) + ((1023u + 43u) << 20);
+  return (uint64_t)__double_as_longlong(
+      __builtin_fma(p, __hiloint2double((int)hi, 0), 4503599627370496.0));
 }
 
 // 2^-t for t >= 0 (0 from t = 1000 on, and for NaN).
@@ -93,15 +95,14 @@ __device__ __forceinline__ RowAsk row_ask(const SampleParams& q, int row) {
   return a;
 }
 
-// The weight of score x against the row's largest, m; zero for scores that
-// cannot be drawn.  x == m also covers m = +inf.
+// The weight of score x against m >= x.  x == m also covers m = +inf, beside
+// which nothing else weighs anything.
 __device__ __forceinline__ uint64_t weight(float x, float m, double c) {
-  if (x == m) return kOne;
-  const double t = ((double)m - (double)x) * c;
-  return t < kTmax ? weight_of(t) : 0ull;
+  return x == m ? kOne : raw_weight(((double)x - (double)m) * c) - kRaw;
 }
+// Scores that take part in cuts: weights above 2^-44.
 __device__ __forceinline__ bool drawable(float x, float m, double c) {
-  return x == m || ((double)m - (double)x) * c < kTmax;
+  return x == m || ((double)x - (double)m) * c > -kTmax;
 }
 
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
   rec.floor = -__builtin_inff();
   rec.count = 0;
   rec.mass = 0;
+  rec.low = best;
   rec.pad = 0;
   if (best > -__builtin_inff()) {
     if (ask.greedy) {
@@ -220,8 +222,10 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-          for (int e = 0; e < V; ++e) mass += weight(x[g][e], best, ask.c);
-        rec.mass = wave_sum(mass);
+          for (int e = 0; e < V; ++e)
+            mass += best < __builtin_inff() ? raw_weight(((double)x[g][e] - (double)best) * ask.c)
+                                            : (x[g][e] == best ? kOne + kRaw : kRaw);
+        rec.mass = wave_sum(mass - (uint64_t)(G * V) * kRaw);
       }
       if (ask.cuts()) {
         // how many lane maxima the floor lies under: what a segment should
@@ -258,6 +262,13 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
           }
         rec.floor = floor;
         rec.count = n <= kSegSlots ? n : -1;
+        float low = __builtin_inff();
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            low = fminf(low, x[g][e] > -__builtin_inff() ? x[g][e] : __builtin_inff());
+        rec.low = -wave_max(-low);
       }
     }
   }
@@ -270,7 +281,6 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 
 namespace {
 
-constexpr int kBinsS = 1024;   // histogram bins
 constexpr int kShort = 256;    // members of a bin that are ranked directly
 constexpr int kListS = 2048;   // candidates held in LDS
 
@@ -577,6 +587,52 @@ __device__ __forceinline__ double clamp_uniform(float u) {
   return u > 0.0f ? (u < 0.99999994f ? (double)u : 0.99999994039535522) : 0.0;
 }
 
+template <class T>
+__device__ __forceinline__ void put_token(const SampleParams& q, int row, const RowView<T>& view,
+                                          int token, float m, double c, double total) {
+  if (threadIdx.x != 0) return;
+  q.tokens[row] = token;
+  if (q.logprobs && token >= 0) {
+    const float xt = Elem<T>::load(view.base, token + view.lead);
+    const double below = xt == m ? 0.0 : ((double)m - (double)xt) * c;
+    q.logprobs[row] = (float)(-below * kLn2 - log(total * (1.0 / (double)kOne)));
+  }
+}
+
+// The sum of the weights of a source's scores inside a cut that min-p keeps.
+template <int BLOCK, class Src>
+__device__ __forceinline__ uint64_t mass_in(const Src& src, RowShared& sh, float m, double c,
+                                            const Cut& cut, uint64_t min_w) {
+  uint64_t s = 0;
+  src.template visit<BLOCK>([&](float x, int i) {
+    if (cut.holds(x, i) && drawable(x, m, c)) {
+      const uint64_t w = weight(x, m, c);
+      s += w >= min_w ? w : 0ull;
+    }
+  });
+  return block_sum<BLOCK>(s, sh.red);
+}
+
+// The draw over a source's kept scores.
+template <int BLOCK, class Src>
+__device__ int draw_from(const Src& src, RowShared& sh, float m, double c, const Cut& cut,
+                         uint64_t min_w, int vocab, double u, double& total) {
+  const uint64_t z = mass_in<BLOCK>(src, sh, m, c, cut, min_w);
+  total = (double)z;
+  uint64_t need = (uint64_t)(u * total) + 1;
+  if (need > z) need = z;
+  return find_index<BLOCK, true>(
+      src, sh, m, c, 0, vocab,
+      [&](float x, int i) {
+        return cut.holds(x, i) && drawable(x, m, c) && weight(x, m, c) >= min_w;
+      },
+      need);
+}
+
+__device__ __forceinline__ double below_best(const SegRecord& r, float m, double c) {
+  return r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * c);
+}
+
 }  // namespace
 
 template <class T, int BLOCK>
@@ -604,13 +660,11 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     fits = fits && r.count >= 0;
   }
   const float own_best = m;
-  {
-    float nm = -m, f = floor;  // largest of both, through one reduction
-    block_min_max<BLOCK>(nm, f, sh.redf);
-    m = -nm;
-    floor = f;
-  }
+  float nm = -m;  // the largest of both, through one reduction
+  block_min_max<BLOCK>(nm, floor, sh.redf);
+  m = -nm;
   fits = __syncthreads_and(fits);
+  if (t == 0 && q.wide) q.wide[row].state = kWideDone;
 
   if (m == ninf) {  // nothing to draw from
     if (t == 0) {
@@ -630,20 +684,22 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     }
     return;
   }
+  if (q.whole_row) {
+    if (t == 0) q.wide[row].state = kWideWhole;
+    return;
+  }
 
   const double u = clamp_uniform(q.uniforms[row]);
   int token = -1;
   double total = 0.0;  // the kept weights' sum, in units of 2^-43 of the largest
 
-  if (!ask.cuts() && !q.whole_row) {
+  if (!ask.cuts()) {
     // The whole vocabulary: the segment in which the running sum passes
     // u * total, then the place inside it.
     double* seg_m = reinterpret_cast<double*>(sh.mass);  // kBinsS entries >= segments
     for (int s = t; s < nseg; s += BLOCK) {
       const SegRecord r = recs[s];
-      seg_m[s] = r.best > ninf ? (r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * ask.c)) *
-                                     (double)r.mass
-                               : 0.0;
+      seg_m[s] = r.best > ninf ? below_best(r, m, ask.c) * (double)r.mass : 0.0;
     }
     __syncthreads();
     double own = 0.0;
@@ -679,8 +735,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     if (mine == seg) sh.redd[30] = mine_before;
     __syncthreads();
     const SegRecord r = recs[seg];
-    const double scale = r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * ask.c);
-    double rest = (y - sh.redd[30]) / scale;
+    double rest = (y - sh.redd[30]) / below_best(r, m, ask.c);
     if (!(rest > 0.0)) rest = 0.0;
     uint64_t need = rest < (double)r.mass ? (uint64_t)rest + 1 : r.mass;
     if (need > r.mass) need = r.mass;
@@ -688,141 +743,344 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
                            min((seg + 1) * (kSegment / V), (q.vocab + view.lead + V - 1) / V)};
     token = find_index<BLOCK, true>(src, sh, r.best, ask.c, seg * kSegment - view.lead, kSegment,
                                     [](float, int) { return true; }, need);
-  } else {
-    // Candidates at or above the common floor: every such score of the row.
-    bool covered = fits && !q.whole_row && ask.cuts();
-    ListSource list{sh.lx, sh.li, 0};
-    const Cut all{ninf, 0x7FFFFFFF};
-    if (covered) {
-      if (t == 0) sh.list_n = 0;
-      __syncthreads();
-      const int lane = t & 63;
-      for (int s = t >> 6; s < nseg; s += BLOCK / 64) {
-        const int n = recs[s].count;
-        Candidate cd{ninf, 0};
-        if (lane < n) cd = q.candidates[((int64_t)row * nseg + s) * kSegSlots + lane];
-        const bool in = lane < n && cd.x >= floor && drawable(cd.x, m, ask.c);
-        const uint64_t mask = __ballot(in);
-        if (mask) {
-          uint32_t b = 0;
-          if (lane == 0) b = atomicAdd(&sh.list_n, (uint32_t)__popcll(mask));
-          b = __builtin_amdgcn_readfirstlane(b);
-          const uint32_t at = b + __builtin_amdgcn_mbcnt_hi(
-                                      (uint32_t)(mask >> 32),
-                                      __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
-          if (in && at < (uint32_t)kListS) {
-            sh.lx[at] = cd.x;
-            sh.li[at] = cd.i;
-          }
+    put_token(q, row, view, token, m, ask.c, total);
+    return;
+  }
+
+  // Candidates at or above the common floor: every such score of the row.
+  bool covered = fits;
+  ListSource list{sh.lx, sh.li, 0};
+  if (covered) {
+    if (t == 0) sh.list_n = 0;
+    __syncthreads();
+    const int lane = t & 63;
+    for (int s = t >> 6; s < nseg; s += BLOCK / 64) {
+      const int n = recs[s].count;
+      Candidate cd{ninf, 0};
+      if (lane < n) cd = q.candidates[((int64_t)row * nseg + s) * kSegSlots + lane];
+      const bool in = lane < n && cd.x >= floor && drawable(cd.x, m, ask.c);
+      const uint64_t mask = __ballot(in);
+      if (mask) {
+        uint32_t b = 0;
+        if (lane == 0) b = atomicAdd(&sh.list_n, (uint32_t)__popcll(mask));
+        b = __builtin_amdgcn_readfirstlane(b);
+        const uint32_t at = b + __builtin_amdgcn_mbcnt_hi(
+                                    (uint32_t)(mask >> 32),
+                                    __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+        if (in && at < (uint32_t)kListS) {
+          sh.lx[at] = cd.x;
+          sh.li[at] = cd.i;
         }
       }
-      __syncthreads();
-      list.n = (int)sh.list_n;
-      covered = list.n <= kListS;
     }
-    // no drawable score lies below the floor
-    const bool complete = floor == ninf || !drawable(floor, m, ask.c);
-    Cut cut = all;
-    auto mass_in = [&](const auto& src, const Cut& cc, uint64_t min_w) {
-      uint64_t s = 0;
-      src.template visit<BLOCK>([&](float x, int i) {
-        if (cc.holds(x, i)) {
-          const uint64_t w = weight(x, m, ask.c);
-          s += w >= min_w ? w : 0ull;
-        }
-      });
-      return block_sum<BLOCK>(s, sh.red);
-    };
+    __syncthreads();
+    list.n = (int)sh.list_n;
+    covered = list.n <= kListS;
+  }
+  // no drawable score lies below the floor
+  const bool complete = floor == ninf || !drawable(floor, m, ask.c);
+  Cut cut{ninf, 0x7FFFFFFF};
+  uint64_t need_p = 0;
+  if (covered || (ask.cut_p && !ask.cut_k)) {
+    float low = m, high = m;
     if (covered) {
-      float low = m;
       list.visit<BLOCK>([&](float x, int) { low = fminf(low, x); });
-      float high = m;
       block_min_max<BLOCK>(low, high, sh.redf);
-      if (ask.cut_k) {
-        if (list.n >= ask.k)
-          cut = find_cut<BLOCK, false>(list, sh, m, ask.c, low, all, q.vocab, (uint64_t)ask.k);
-        else
-          covered = complete;
+    }
+    if (covered && ask.cut_k) {
+      if (list.n >= ask.k)
+        cut = find_cut<BLOCK, false>(list, sh, m, ask.c, low, cut, q.vocab, (uint64_t)ask.k);
+      else
+        covered = complete;
+    }
+    if (ask.cut_p && (covered || !ask.cut_k)) {
+      uint64_t have = 0;
+      double z = 0.0;
+      if (covered) {
+        have = mass_in<BLOCK>(list, sh, m, ask.c, cut, 0);
+        z = (double)have;
       }
-      if (covered && ask.cut_p) {
-        const uint64_t have = mass_in(list, cut, 0);
-        double z = (double)have;
-        if (!ask.cut_k && !complete) {
-          double part = 0.0;
-          for (int s = t; s < nseg; s += BLOCK) {
-            const SegRecord r = recs[s];
-            if (r.best > ninf)
-              part += (r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * ask.c)) *
-                      (double)r.mass;
-          }
-          z = block_sum<BLOCK>(part, sh.redd);
+      if (!ask.cut_k && !(covered && complete)) {
+        double part = 0.0;
+        for (int s = t; s < nseg; s += BLOCK) {
+          const SegRecord r = recs[s];
+          if (r.best > ninf) part += below_best(r, m, ask.c) * (double)r.mass;
         }
-        const uint64_t need = ceil_share(ask.p, z);
-        if (have >= need)
-          cut = find_cut<BLOCK, true>(list, sh, m, ask.c, low, cut, q.vocab, need);
-        else
-          covered = complete || ask.cut_k;
+        z = block_sum<BLOCK>(part, sh.redd);
       }
-      if (covered && !ask.cut_k && !ask.cut_p)
-        covered = complete || weight(floor, m, ask.c) < ask.min_w;
+      need_p = ceil_share(ask.p, z);
+      if (covered && have >= need_p)
+        cut = find_cut<BLOCK, true>(list, sh, m, ask.c, low, cut, q.vocab, need_p);
+      else
+        covered = covered && complete;
     }
-    auto draw = [&](const auto& src) {
-      const uint64_t z = mass_in(src, cut, ask.min_w);
-      total = (double)z;
-      const double y = u * total;
-      uint64_t need = (uint64_t)y + 1;
-      if (need > z) need = z;
-      token = find_index<BLOCK, true>(
-          src, sh, m, ask.c, 0, q.vocab,
-          [&](float x, int i) { return cut.holds(x, i) && weight(x, m, ask.c) >= (ask.min_w ? ask.min_w : 1ull); },
-          need);
-    };
-    if (covered) {
-      draw(list);
-    } else {
-      // The whole row again, from memory.
-      const RowSource<T> src{view, 0, (q.vocab + view.lead + V - 1) / V};
-      cut = all;
-      float low = m, high = m;
-      src.template visit<BLOCK>([&](float x, int) {
-        if (drawable(x, m, ask.c)) low = fminf(low, x);
-      });
-      block_min_max<BLOCK>(low, high, sh.redf);
-      if (ask.cut_k) cut = find_cut<BLOCK, false>(src, sh, m, ask.c, low, all, q.vocab, (uint64_t)ask.k);
-      if (ask.cut_p) {
-        const uint64_t z = mass_in(src, cut, 0);
-        cut = find_cut<BLOCK, true>(src, sh, m, ask.c, low, cut, q.vocab, ceil_share(ask.p, (double)z));
-      }
-      draw(src);
-    }
+    if (covered && !ask.cut_k && !ask.cut_p)
+      covered = complete || weight(floor, m, ask.c) < ask.min_w;
+  }
+  if (covered) {
+    token = draw_from<BLOCK>(list, sh, m, ask.c, cut, ask.min_w, q.vocab, u, total);
+    put_token(q, row, view, token, m, ask.c, total);
+    return;
   }
 
+  // The cut lies below the candidates: the kernels that follow find it.
+  float low = __builtin_inff(), high = m;
+  for (int s = t; s < nseg; s += BLOCK) {
+    const SegRecord r = recs[s];
+    if (r.best > ninf) low = fminf(low, r.low);
+  }
+  block_min_max<BLOCK>(low, high, sh.redf);
   if (t == 0) {
-    q.tokens[row] = token;
-    if (q.logprobs && token >= 0) {
-      const float xt = Elem<T>::load(view.base, token + view.lead);
-      const double below = xt == m ? 0.0 : ((double)m - (double)xt) * ask.c;
-      q.logprobs[row] = (float)(-below * kLn2 - log(total * (1.0 / (double)kOne)));
+    WideRow w;
+    const double least = (double)m - kTmax / ask.c;  // -inf at c = 0
+    const double range = (double)m - fmax(least, (double)low);
+    w.state = (ask.cut_k && ask.cut_p) ? kWideWhole : (ask.cut_k || ask.cut_p) ? kWideBins : kWideMembers;
+    w.m = m;
+    w.scale = (range > 0.0 && range < 1e300) ? (double)kBinsS / range : 0.0;
+    w.need = ask.cut_p ? need_p : (uint64_t)ask.k;
+    w.bin = kBinsS;
+    w.members = 0;
+    w.arrived[0] = 0;
+    w.arrived[1] = 0;
+    q.wide[row] = w;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows whose cut lies below the candidates (flat rows with a top-p, a large
+// top-k, a small min-p), kWideSegs segments a workgroup:
+//  1. sample_bins_kernel: the row's masses (top-p) or counts (top-k) in
+//     kBinsS equal bins of score from the largest down; the row's last
+//     workgroup adds the others' bins up and finds the crossing bin;
+//  2. sample_wide_kernel: each segment's kept mass above that bin, and the
+//     bin's members; the row's last workgroup finds the exact cut among the
+//     members, adds the kept ones to their segments, finds the segment in
+//     which the draw falls, and the token in it.
+// Sums are whole numbers, so which workgroup is last changes nothing.  What
+// crosses between workgroups goes through agent-scope atomics, complete
+// before their workgroup counts itself; nobody waits for anybody.
+// Rows with both a large top-k and a top-p, and bins with more members than
+// fit, are selected by one workgroup from memory, pass by pass.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+__device__ __forceinline__ int wide_bin(float x, float m, double scale) {
+  const double b = ((double)m - (double)x) * scale;
+  return b < (double)(kBinsS - 1) ? (int)b : kBinsS - 1;  // x == m = +inf: NaN, the last bin
+}
+
+template <class V>
+__device__ __forceinline__ V agent_load(const V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class V>
+__device__ __forceinline__ void agent_store(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Counts this workgroup in; true in the row's last one.
+__device__ __forceinline__ bool last_in(uint32_t* counter, int workgroups, RowShared& sh) {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's stores and atomics are done
+  __syncthreads();
+  if (threadIdx.x == 0)
+    sh.bin = (int)__hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const bool last = sh.bin == workgroups - 1;
+  __syncthreads();
+  return last;
+}
+
+// One wave's segment, as the segment kernel reads it.
+template <class T, class F>
+__device__ __forceinline__ void visit_segment(const RowView<T>& view, int seg, F&& f) {
+  constexpr int V = Elem<T>::kVec;
+  constexpr int G = kSegment / (64 * V);
+  const int lane = threadIdx.x & 63;
+#pragma unroll 2
+  for (int g = 0; g < G; ++g) {
+    float x[V];
+    const int pos = view.group(seg * (kSegment / V) + g * 64 + lane, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (x[e] > -__builtin_inff()) f(x[e], pos + e);
+  }
+}
+
+}  // namespace
+
+template <class T>
+__global__ void __launch_bounds__(kWideBlock) sample_bins_kernel(const SampleParams q) {
+  __shared__ RowShared sh;
+  const int t = threadIdx.x;
+  const int row = blockIdx.x / q.wide_wgs, part = blockIdx.x % q.wide_wgs;
+  WideRow* wr = q.wide + row;
+  if (wr->state != kWideBins) return;
+  const RowAsk ask = row_ask(q, row);
+  const RowView<T> view(q, row);
+  const float m = wr->m;
+  const double scale = wr->scale;
+  clear_bins<kWideBlock>(sh);
+  const int seg = part * kWideSegs + (t >> 6);
+  if (seg < q.segments)
+    visit_segment(view, seg, [&](float x, int) {
+      if (drawable(x, m, ask.c)) {
+        const unsigned long long v = ask.cut_p ? weight(x, m, ask.c) : 1ull;
+        atomicAdd((unsigned long long*)&sh.mass[wide_bin(x, m, scale)], v);
+      }
+    });
+  __syncthreads();
+  uint64_t* slices = q.slices + (int64_t)row * q.wide_wgs * kBinsS;
+  for (int b = t; b < kBinsS; b += kWideBlock) agent_store(&slices[part * kBinsS + b], sh.mass[b]);
+  if (!last_in(&wr->arrived[0], q.wide_wgs, sh)) return;
+  for (int b = t; b < kBinsS; b += kWideBlock) {
+    uint64_t s = 0;
+    for (int w = 0; w < q.wide_wgs; ++w) s += agent_load(&slices[w * kBinsS + b]);
+    sh.mass[b] = s;
+  }
+  if (t == 0) sh.bin = -1;
+  int bin;
+  uint64_t before;
+  const uint64_t need = wr->need;
+  const bool found = cross_bins<kWideBlock, true>(sh, need, bin, before);
+  if (t == 0) {
+    wr->state = kWideMembers;
+    wr->bin = found ? bin : kBinsS;  // not reached: nothing is cut
+    wr->need = need - (found ? before : 0);
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SampleParams q) {
+  __shared__ RowShared sh;
+  constexpr int V = Elem<T>::kVec;
+  const int t = threadIdx.x;
+  const int row = blockIdx.x / q.wide_wgs, part = blockIdx.x % q.wide_wgs;
+  WideRow* wr = q.wide + row;
+  const uint32_t state = wr->state;
+  if (state == kWideDone) return;
+  const RowAsk ask = row_ask(q, row);
+  const RowView<T> view(q, row);
+  const double u = clamp_uniform(q.uniforms[row]);
+  const int nseg = q.segments;
+  const int room = min(nseg * kSegSlots, kListS);
+  const Cut all{-__builtin_inff(), 0x7FFFFFFF};
+  Cut cut = all;
+  float m = wr->m;
+  bool fits = false;
+
+  if (state == kWideMembers) {
+    const double scale = wr->scale;
+    const int bin = wr->bin;
+    Candidate* members = q.candidates + (int64_t)row * nseg * kSegSlots;
+    uint64_t* kept = q.kept + (int64_t)row * nseg;
+    const int seg = part * kWideSegs + (t >> 6);
+    if (seg < nseg) {
+      uint64_t mass = 0;
+      visit_segment(view, seg, [&](float x, int i) {
+        if (!drawable(x, m, ask.c)) return;
+        const int b = wide_bin(x, m, scale);
+        if (b < bin) {
+          const uint64_t w = weight(x, m, ask.c);
+          mass += w >= ask.min_w ? w : 0ull;
+        } else if (b == bin) {
+          const uint32_t at = __hip_atomic_fetch_add(&wr->members, 1u, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT);
+          if (at < (uint32_t)room) {
+            const uint64_t both = ((uint64_t)(uint32_t)i << 32) | __float_as_uint(x);
+            agent_store(reinterpret_cast<uint64_t*>(members + at), both);
+          }
+        }
+      });
+      mass = wave_sum(mass);
+      if ((t & 63) == 0) agent_store(&kept[seg], mass);
     }
+    if (!last_in(&wr->arrived[1], q.wide_wgs, sh)) return;
+    const int n = (int)agent_load(&wr->members);
+    fits = n <= room;
+    if (fits) {
+      const ListSource list{sh.lx, sh.li, n};
+      float low = m, high = m;
+      for (int i = t; i < n; i += kWideBlock) {
+        const uint64_t both = agent_load(reinterpret_cast<const uint64_t*>(members + i));
+        const float x = __uint_as_float((uint32_t)both);
+        sh.lx[i] = x;
+        sh.li[i] = (int32_t)(both >> 32);
+        low = fminf(low, x);
+      }
+      block_min_max<kWideBlock>(low, high, sh.redf);
+      if (bin < kBinsS) {
+        if (ask.cut_p)
+          cut = find_cut<kWideBlock, true>(list, sh, m, ask.c, low, all, q.vocab, wr->need);
+        else
+          cut = find_cut<kWideBlock, false>(list, sh, m, ask.c, low, all, q.vocab, wr->need);
+      }
+      clear_bins<kWideBlock>(sh);
+      for (int s = t; s < nseg; s += kWideBlock) sh.mass[s] = agent_load(&kept[s]);
+      __syncthreads();
+      list.visit<kWideBlock>([&](float x, int i) {
+        const uint64_t w = weight(x, m, ask.c);
+        if (cut.holds(x, i) && w >= ask.min_w)
+          atomicAdd((unsigned long long*)&sh.mass[(i + view.lead) / kSegment], (unsigned long long)w);
+      });
+      __syncthreads();
+      uint64_t z = 0;
+      for (int s = t; s < nseg; s += kWideBlock) z += sh.mass[s];
+      z = block_sum<kWideBlock>(z, sh.red);
+      uint64_t need = (uint64_t)(u * (double)z) + 1, before;
+      if (need > z) need = z;
+      int at;
+      cross_bins<kWideBlock, true>(sh, need, at, before);
+      const RowSource<T> src{view, at * (kSegment / V),
+                             min((at + 1) * (kSegment / V), (q.vocab + view.lead + V - 1) / V)};
+      const int token = find_index<kWideBlock, true>(
+          src, sh, m, ask.c, at * kSegment - view.lead, kSegment,
+          [&](float x, int i) {
+            return cut.holds(x, i) && drawable(x, m, ask.c) && weight(x, m, ask.c) >= ask.min_w;
+          },
+          need - before);
+      put_token(q, row, view, token, m, ask.c, (double)z);
+      return;
+    }
+  } else if (part != 0 || state != kWideWhole) {
+    return;
   }
+
+  // The whole row from memory, by this workgroup alone.
+  const RowSource<T> src{view, 0, (q.vocab + view.lead + V - 1) / V};
+  float low = __builtin_inff(), high = -__builtin_inff();
+  src.template visit<kWideBlock>([&](float x, int) { high = fmaxf(high, x); });
+  block_min_max<kWideBlock>(low, high, sh.redf);
+  m = high;
+  low = m;
+  src.template visit<kWideBlock>([&](float x, int) {
+    if (drawable(x, m, ask.c)) low = fminf(low, x);
+  });
+  block_min_max<kWideBlock>(low, high, sh.redf);
+  cut = all;
+  if (ask.cut_k)
+    cut = find_cut<kWideBlock, false>(src, sh, m, ask.c, low, all, q.vocab, (uint64_t)ask.k);
+  if (ask.cut_p) {
+    const uint64_t z = mass_in<kWideBlock>(src, sh, m, ask.c, cut, 0);
+    cut = find_cut<kWideBlock, true>(src, sh, m, ask.c, low, cut, q.vocab, ceil_share(ask.p, (double)z));
+  }
+  double total;
+  const int token = draw_from<kWideBlock>(src, sh, m, ask.c, cut, ask.min_w, q.vocab, u, total);
+  put_token(q, row, view, token, m, ask.c, total);
 }
 
-const void* sample_segment_kernel_ptr(int dtype) {
-  switch (dtype) {
-    case 0: return reinterpret_cast<const void*>(&sample_segment_kernel<float>);
-    case 1: return reinterpret_cast<const void*>(&sample_segment_kernel<__hip_bfloat16>);
-    case 2: return reinterpret_cast<const void*>(&sample_segment_kernel<__half>);
-    default: return nullptr;
+#define ERT_SAMPLE_PTR(NAME, ...)                                                      \
+  const void* NAME##_ptr(int dtype) {                                                  \
+    switch (dtype) {                                                                   \
+      case 0: return reinterpret_cast<const void*>(&NAME<float __VA_ARGS__>);          \
+      case 1: return reinterpret_cast<const void*>(&NAME<__hip_bfloat16 __VA_ARGS__>); \
+      case 2: return reinterpret_cast<const void*>(&NAME<__half __VA_ARGS__>);         \
+      default: return nullptr;                                                         \
+    }                                                                                  \
   }
-}
-
-const void* sample_row_kernel_ptr(int dtype) {
-  switch (dtype) {
-    case 0: return reinterpret_cast<const void*>(&sample_row_kernel<float, 1024>);
-    case 1: return reinterpret_cast<const void*>(&sample_row_kernel<__hip_bfloat16, 1024>);
-    case 2: return reinterpret_cast<const void*>(&sample_row_kernel<__half, 1024>);
-    default: return nullptr;
-  }
-}
+ERT_SAMPLE_PTR(sample_segment_kernel)
+ERT_SAMPLE_PTR(sample_row_kernel, , kRowBlock)
+ERT_SAMPLE_PTR(sample_bins_kernel)
+ERT_SAMPLE_PTR(sample_wide_kernel)
 
 }  // namespace ert
