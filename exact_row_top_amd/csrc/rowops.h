@@ -42,8 +42,8 @@ struct WideRow {
   float m;              // the row's largest score
   double scale;         // bins per unit of score below it
   uint64_t need;        // count or mass at the cut; then what of it the crossing bin holds
-  int32_t bin;          // the crossing bin, kBinsS if nothing is cut
-  uint32_t members;     // scores listed from it
+  float above;          // scores at or above this lie above the crossing bin
+  float from;           // the bin's own begin here
   uint32_t arrived[2];  // workgroups done with the bins, with the members
 };
 
@@ -61,9 +61,9 @@ struct SampleParams {
   int32_t* tokens;
   float* logprobs;
   SegRecord* records;
-  Candidate* candidates;  // [rows][segments][kSegSlots]; later the crossing bin's members
+  Candidate* candidates;  // [rows][segments][kSegSlots]; later the crossing bins' members
   WideRow* wide;          // null where no row can have a cut
-  uint64_t* kept;         // [rows][segments]
+  uint64_t* kept;         // [rows][segments + wide_wgs]: kept masses, member counts
   uint64_t* slices;       // [rows][wide_wgs][kBinsS]
   int32_t wide_wgs;       // workgroups of a row
   int32_t whole_row;      // every row from memory

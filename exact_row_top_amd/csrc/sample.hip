@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gvr_device.h"
 #include "rowops.h"
 
 namespace ert {
@@ -30,41 +31,78 @@ constexpr double kLn2 = 0.6931471805599453;
 constexpr double kTmax = 44.0;          // weights of 2^-44 and less are zero
 
 // 2^f on [-1/2, 1/2]: interpolation at the ten Chebyshev nodes, relative
-// error at most 2^-45.6.
-__device__ __forceinline__ double exp2_poly(double f) {
-  double p = 0x1.b6571de2f2351p-24;
-  p = __builtin_fma(p, f, 0x1.63ef969a64d3cp-20);
-  p = __builtin_fma(p, f, 0x1.ffcb76789860fp-17);
-  p = __builtin_fma(p, f, 0x1.43088e257f341p-13);
-  p = __builtin_fma(p, f, 0x1.5d87fe908f88ap-10);
-  p = __builtin_fma(p, f, 0x1.3b2ab72b175eep-7);
-  p = __builtin_fma(p, f, 0x1.c6b08d7044119p-5);
-  p = __builtin_fma(p, f, 0x1.ebfbdff8149f2p-3);
-  p = __builtin_fma(p, f, 0x1.62e42fefa39f7p-1);
-  return __builtin_fma(p, f, 0x1.000000000003dp+0);
-}
+// error at most 2^-45.6.  The coefficients sit in scalar registers behind an
+// empty asm: as known constants each would be moved into a vector register
+// pair ahead of every multiply-add, two instructions to one.
+struct Exp2Poly {
+  double k0, k1, k2, k3, k4, k5, k6, k7, k8, k9;
+  __device__ __forceinline__ Exp2Poly()
+      : k0(0x1.000000000003dp+0), k1(0x1.62e42fefa39f7p-1), k2(0x1.ebfbdff8149f2p-3),
+        k3(0x1.c6b08d7044119p-5), k4(0x1.3b2ab72b175eep-7), k5(0x1.5d87fe908f88ap-10),
+        k6(0x1.43088e257f341p-13), k7(0x1.ffcb76789860fp-17), k8(0x1.63ef969a64d3cp-20),
+        k9(0x1.b6571de2f2351p-24) {
+    asm("" : "+s"(k0), "+s"(k1), "+s"(k2), "+s"(k3), "+s"(k4));
+    asm("" : "+s"(k5), "+s"(k6), "+s"(k7), "+s"(k8), "+s"(k9));
+  }
+  __device__ __forceinline__ double operator()(double f) const {
+    double p = __builtin_fma(f, k9, k8);
+    p = __builtin_fma(p, f, k7);
+    p = __builtin_fma(p, f, k6);
+    p = __builtin_fma(p, f, k5);
+    p = __builtin_fma(p, f, k4);
+    p = __builtin_fma(p, f, k3);
+    p = __builtin_fma(p, f, k2);
+    p = __builtin_fma(p, f, k1);
+    return __builtin_fma(p, f, k0);
+  }
+};
 
-// round(2^43 * 2^s) for s <= 0, under the exponent bits of 2^52: adding 1.5 *
-// 2^52 rounds s to a whole n, which then stands in the sum's low bits; adding
-// 2^52 to the scaled value rounds it to a whole number in the low 52 bits.  s
-// below -60 (or NaN) is taken as -60 and gives zero.  Callers that add many
-// of them up take the exponent bits out once, at the end.
+// The weights of a row's scores against m >= x.
+//
+// raw(x): round(2^43 * 2^s), s = (x - m) log2(e) / T <= 0, under the exponent
+// bits of 2^52: adding 1.5 * 2^52 rounds s to a whole n, which then stands in
+// the sum's low bits; adding 2^52 to the scaled value rounds it to a whole
+// number in the low 52 bits.  s below -60 (or NaN) is taken as -60 and gives
+// zero.  Callers that add many of them up take the exponent bits out once.
 constexpr uint64_t kRaw = 0x4330000000000000ull;
-__device__ __forceinline__ uint64_t raw_weight(double s) {
-  const double magic = 6755399441055744.0;
-  s = __builtin_fmax(s, -60.0);
-  const double sm = s + magic;
-  const double p = exp2_poly(s - (sm - magic));
-  const uint32_t hi = ((uint32_t)__double_as_longlong(sm) << 20) + ((1023u + 43u) << 20);
-  return (uint64_t)__double_as_longlong(
-      __builtin_fma(p, __hiloint2double((int)hi, 0), 4503599627370496.0));
-}
+struct Weigher {
+  Exp2Poly poly;
+  float m;
+  double md, c;
+  __device__ __forceinline__ Weigher(float m_, double c_) : m(m_), md((double)m_), c(c_) {}
+  __device__ __forceinline__ void against(float m_) {
+    m = m_;
+    md = (double)m_;
+  }
+  __device__ __forceinline__ double log2_of(float x) const { return ((double)x - md) * c; }
+  __device__ __forceinline__ uint64_t raw_of(double s) const {
+    const double magic = 6755399441055744.0;
+    s = __builtin_fmax(s, -60.0);
+    const double sm = s + magic;
+    const double p = poly(s - (sm - magic));
+    const uint32_t hi = ((uint32_t)__double_as_longlong(sm) << 20) + ((1023u + 43u) << 20);
+    return (uint64_t)__double_as_longlong(
+        __builtin_fma(p, __hiloint2double((int)hi, 0), 4503599627370496.0));
+  }
+  __device__ __forceinline__ uint64_t raw(float x) const { return raw_of(log2_of(x)); }
+  // x == m also covers m = +inf, beside which nothing else weighs anything
+  __device__ __forceinline__ uint64_t operator()(float x) const {
+    return x == m ? kOne : raw(x) - kRaw;
+  }
+  // scores that take part in cuts: weights above 2^-44
+  __device__ __forceinline__ bool drawable(float x) const { return x == m || log2_of(x) > -kTmax; }
+  // the weight of a drawable score, zero for others
+  __device__ __forceinline__ uint64_t drawn(float x) const {
+    const double s = log2_of(x);
+    return x == m ? kOne : s > -kTmax ? raw_of(s) - kRaw : 0ull;
+  }
+};
 
 // 2^-t for t >= 0 (0 from t = 1000 on, and for NaN).
-__device__ __forceinline__ double exp2_neg(double t) {
+__device__ __forceinline__ double exp2_neg(double t, const Exp2Poly& poly) {
   if (!(t < 1000.0)) return 0.0;
   const double n = __builtin_rint(t);
-  return __builtin_ldexp(exp2_poly(n - t), -(int)n);
+  return __builtin_ldexp(poly(n - t), -(int)n);
 }
 
 // What a row asks for.
@@ -95,25 +133,6 @@ __device__ __forceinline__ RowAsk row_ask(const SampleParams& q, int row) {
   return a;
 }
 
-// The weight of score x against m >= x.  x == m also covers m = +inf, beside
-// which nothing else weighs anything.
-__device__ __forceinline__ uint64_t weight(float x, float m, double c) {
-  return x == m ? kOne : raw_weight(((double)x - (double)m) * c) - kRaw;
-}
-// Scores that take part in cuts: weights above 2^-44.
-__device__ __forceinline__ bool drawable(float x, float m, double c) {
-  return x == m || ((double)x - (double)m) * c > -kTmax;
-}
-
-__device__ __forceinline__ uint32_t ordered(float x) {
-  uint32_t b = __float_as_uint(x);
-  b = (b == 0x80000000u) ? 0u : b;
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float from_ordered(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
 // A row's scores as whole 16-byte groups from the boundary at or below its
 // first score; positions outside [0, vocab) read as -inf.
 template <class T>
@@ -128,6 +147,29 @@ struct RowView {
     lead = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(T);
     base = p - lead * (int)sizeof(T);
     vocab = q.vocab;
+  }
+  // Group g of those that lie inside the row: its scores, NaN as -inf.
+  __device__ __forceinline__ void inner_group(int g, float (&x)[Elem<T>::kVec]) const {
+    Elem<T>::unpack(*reinterpret_cast<const uint4*>(base + (int64_t)g * 16), x);
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kVec; ++e)
+      x[e] = x[e] > -__builtin_inff() ? x[e] : -__builtin_inff();
+  }
+  // whether groups [g, g + n) lie inside the row
+  __device__ __forceinline__ bool inside(int g, int n) const {
+    return g * Elem<T>::kVec >= lead && (g + n) * Elem<T>::kVec - lead <= vocab;
+  }
+  // One wave's segment, all its loads at once.
+  static constexpr int kGroups = kSegment / (64 * Elem<T>::kVec);
+  __device__ __forceinline__ void segment(int seg, int lane, float (&x)[kGroups][Elem<T>::kVec]) const {
+    const int g0 = seg * (kSegment / Elem<T>::kVec);
+    if (inside(g0, kSegment / Elem<T>::kVec)) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) inner_group(g0 + g * 64 + lane, x[g]);
+    } else {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) group(g0 + g * 64 + lane, x[g]);
+    }
   }
   // Group g: its scores, NaN as -inf, and the position of the first.
   __device__ __forceinline__ int group(int g, float (&x)[Elem<T>::kVec]) const {
@@ -148,11 +190,6 @@ template <class V>
 __device__ __forceinline__ V wave_sum(V v) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
   return v;
 }
 __device__ __forceinline__ int wave_min(int v) {
@@ -189,15 +226,22 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 
   float x[G][V];
   const int g0 = seg * (kSegment / V);
-#pragma unroll
-  for (int g = 0; g < G; ++g) view.group(g0 + g * 64 + lane, x[g]);
+  view.segment(seg, lane, x);
 
   float top = -__builtin_inff();
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int e = 0; e < V; ++e) top = fmaxf(top, x[g][e]);
-  const float best = wave_max(top);
+  float best = top, low = __builtin_inff();
+  if (ask.cuts() && !ask.greedy) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        low = fminf(low, x[g][e] > -__builtin_inff() ? x[g][e] : __builtin_inff());
+  }
+  wave_minmax(low, best);
 
   SegRecord rec;
   rec.best = best;
@@ -205,7 +249,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
   rec.floor = -__builtin_inff();
   rec.count = 0;
   rec.mass = 0;
-  rec.low = best;
+  rec.low = low;
   rec.pad = 0;
   if (best > -__builtin_inff()) {
     if (ask.greedy) {
@@ -219,13 +263,32 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
     } else {
       if (!ask.cut_k) {
         uint64_t mass = 0;
+        if (best < __builtin_inff()) {
+          const Weigher w(best, ask.c);
+          // four scores at a time (the empty asm keeps the additions where
+          // they are): with all of them in flight, and added up at the end,
+          // the registers would leave room for three waves a SIMD
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+          for (int g = 0; g < G; ++g)
 #pragma unroll
-          for (int e = 0; e < V; ++e)
-            mass += best < __builtin_inff() ? raw_weight(((double)x[g][e] - (double)best) * ask.c)
-                                            : (x[g][e] == best ? kOne + kRaw : kRaw);
-        rec.mass = wave_sum(mass - (uint64_t)(G * V) * kRaw);
+            for (int e = 0; e < V; ++e) {
+              mass += w.raw(x[g][e]);
+              if (e % 4 == 3) {
+                asm("" : "+v"(mass));
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          mass -= (uint64_t)(G * V) * kRaw;
+        } else {
+          asm volatile("");  // not ahead of the branch
+          uint32_t n = 0;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < V; ++e) n += x[g][e] == best ? 1u : 0u;
+          mass = (uint64_t)n * kOne;
+        }
+        rec.mass = wave_sum(mass);
       }
       if (ask.cuts()) {
         // how many lane maxima the floor lies under: what a segment should
@@ -236,14 +299,14 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
           const float share = (float)ask.k / (float)q.segments;
           j = min(48, (int)(share + 4.0f * __builtin_sqrtf(share)) + 4);
         }
-        const uint32_t key = ordered(top);
+        const uint32_t key = fkey(top);
         uint32_t thr = 0;
 #pragma unroll
         for (int b = 31; b >= 14; --b) {
           const uint32_t t = thr | (1u << b);
           if (__popcll(__ballot(key >= t)) >= j) thr = t;
         }
-        const float floor = thr > ordered(-__builtin_inff()) ? from_ordered(thr) : -__builtin_inff();
+        const float floor = thr > fkey(-__builtin_inff()) ? from_key(thr) : -__builtin_inff();
         Candidate* out = q.candidates + (int64_t)id * kSegSlots;
         int n = 0;
 #pragma unroll
@@ -262,13 +325,6 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
           }
         rec.floor = floor;
         rec.count = n <= kSegSlots ? n : -1;
-        float low = __builtin_inff();
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int e = 0; e < V; ++e)
-            low = fminf(low, x[g][e] > -__builtin_inff() ? x[g][e] : __builtin_inff());
-        rec.low = -wave_max(-low);
       }
     }
   }
@@ -287,8 +343,7 @@ constexpr int kListS = 2048;   // candidates held in LDS
 struct RowShared {
   uint32_t cnt[kBinsS];
   uint64_t mass[kBinsS];
-  float sx[kShort];
-  int32_t si[kShort];
+  uint64_t sk[kShort];  // sort keys, larger first
   uint64_t sw[kShort];
   uint64_t red[32];
   double redd[32];
@@ -447,24 +502,34 @@ __device__ __forceinline__ bool cross_bins(RowShared& sh, uint64_t need, int& bi
   return bin >= 0;
 }
 
-// The short list's member at which the running sum in the order (score
-// descending, index ascending) reaches `need`, left in found_x / found_i.
-template <bool MASS>
+// Sort keys of the order (score descending, index ascending) and of index
+// order alone; the larger key comes first.
+__device__ __forceinline__ uint64_t order_key(float x, int i) {
+  return ((uint64_t)fkey(x) << 32) | (uint32_t)~i;
+}
+__device__ __forceinline__ uint64_t index_key(float x, int i) {
+  return ((uint64_t)(uint32_t)~i << 32) | fkey(x);
+}
+
+// The short list's member at which the running sum by falling key reaches
+// `need`, left in found_x / found_i.
+template <bool MASS, bool BY_INDEX = false>
 __device__ __forceinline__ void rank_short(RowShared& sh, int m, uint64_t need) {
   __syncthreads();
   const int t = threadIdx.x;
   if (t < m) {
-    const float x = sh.sx[t];
-    const int i = sh.si[t];
+    const uint64_t key = sh.sk[t];
     uint64_t run = 0;
+#pragma unroll 8
     for (int o = 0; o < m; ++o) {
-      const float y = sh.sx[o];
-      if (y > x || (y == x && sh.si[o] < i)) run += MASS ? sh.sw[o] : 1ull;
+      const uint64_t v = MASS ? sh.sw[o] : 1ull;
+      run += sh.sk[o] > key ? v : 0ull;
     }
     const uint64_t own = MASS ? sh.sw[t] : 1ull;
     if (run < need && need <= run + own) {
-      sh.found_x = x;
-      sh.found_i = i;
+      const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+      sh.found_x = from_key(BY_INDEX ? lo : hi);
+      sh.found_i = (int)~(BY_INDEX ? hi : lo);
     }
   }
   __syncthreads();
@@ -474,7 +539,7 @@ __device__ __forceinline__ void rank_short(RowShared& sh, int m, uint64_t need) 
 // `pred` admits reaches `need`, in index order over [0, vocab); -1 if the
 // total stays below.
 template <int BLOCK, bool MASS, class Src, class Pred>
-__device__ int find_index(const Src& src, RowShared& sh, float m, double c, int from, int span,
+__device__ int find_index(const Src& src, RowShared& sh, const Weigher& w, int from, int span,
                           Pred&& pred, uint64_t need) {
   int i0 = from, width = (span + kBinsS - 1) / kBinsS;
   for (;;) {
@@ -484,7 +549,7 @@ __device__ int find_index(const Src& src, RowShared& sh, float m, double c, int 
       if (d >= 0 && d < width * kBinsS && pred(x, i)) {
         const int b = (int)((unsigned)d / (unsigned)width);
         atomicAdd(&sh.cnt[b], 1u);
-        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)weight(x, m, c));
+        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)w(x));
       }
     });
     int bin;
@@ -499,17 +564,64 @@ __device__ int find_index(const Src& src, RowShared& sh, float m, double c, int 
         if (d >= 0 && d < width && pred(x, i)) {
           const uint32_t s = atomicAdd(&sh.n, 1u);
           if (s < (uint32_t)kShort) {
-            sh.sx[s] = 0.0f;  // index order alone
-            sh.si[s] = i;
-            if (MASS) sh.sw[s] = weight(x, m, c);
+            sh.sk[s] = index_key(x, i);
+            if (MASS) sh.sw[s] = w(x);
           }
         }
       });
-      rank_short<MASS>(sh, min(members, kShort), need);
+      rank_short<MASS, true>(sh, min(members, kShort), need);
       return sh.found_i;
     }
     width = (width + kBinsS - 1) / kBinsS;
   }
+}
+
+// The lowest index of a segment at which the running mass of the scores that
+// `pred` admits reaches `need` (at most their total), with its score: every
+// thread's scores lie side by side, so one prefix sum over the workgroup
+// finds the thread and a walk over its registers the score.
+template <int BLOCK, class T, class Pred>
+__device__ __forceinline__ void pick_in_segment(const RowView<T>& view, int seg, RowShared& sh,
+                                                const Weigher& w, Pred&& pred, uint64_t need) {
+  constexpr int V = Elem<T>::kVec;
+  constexpr int N = kSegment / V;  // groups
+  constexpr int PER = (N + BLOCK - 1) / BLOCK;
+  float x[PER][V];
+  uint64_t own = 0;
+  const int g0 = threadIdx.x * PER;
+#pragma unroll
+  for (int g = 0; g < PER; ++g) {
+    if (g0 + g < N) {
+      view.group(seg * N + g0 + g, x[g]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[g][e] = -__builtin_inff();
+    }
+  }
+  uint64_t v[PER][V];
+#pragma unroll
+  for (int g = 0; g < PER; ++g)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int i = (seg * N + g0 + g) * V + e - view.lead;
+      v[g][e] = pred(x[g][e], i) ? w(x[g][e]) : 0ull;
+      own += v[g][e];
+    }
+  const uint64_t incl = block_scan<BLOCK>(own, sh.red);
+  uint64_t run = incl - own;
+  if (run < need && need <= incl) {
+#pragma unroll
+    for (int g = 0; g < PER; ++g)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (run < need && need <= run + v[g][e]) {
+          sh.found_i = (seg * N + g0 + g) * V + e - view.lead;
+          sh.found_x = x[g][e];
+        }
+        run += v[g][e];
+      }
+  }
+  __syncthreads();
 }
 
 // The place in the order (score descending, index ascending) at which the
@@ -519,9 +631,9 @@ __device__ int find_index(const Src& src, RowShared& sh, float m, double c, int 
 // narrows the range to that bin's own extremes, which land in different bins
 // next time; a class of one value is split by index.
 template <int BLOCK, bool MASS, class Src>
-__device__ Cut find_cut(const Src& src, RowShared& sh, float m, double c, float lo, const Cut& within,
+__device__ Cut find_cut(const Src& src, RowShared& sh, const Weigher& w, float lo, float hi,
+                        const Cut& within,
                         int vocab, uint64_t need) {
-  float hi = m;
   for (;;) {
     clear_bins<BLOCK>(sh);
     const double range = (double)hi - (double)lo;
@@ -532,13 +644,13 @@ __device__ Cut find_cut(const Src& src, RowShared& sh, float m, double c, float 
       return b < (double)(kBinsS - 1) ? (int)b : kBinsS - 1;
     };
     auto admitted = [&](float x, int i) {
-      return x <= hi && x >= lo && drawable(x, m, c) && within.holds(x, i);
+      return x <= hi && x >= lo && w.drawable(x) && within.holds(x, i);
     };
     src.template visit<BLOCK>([&](float x, int i) {
       if (admitted(x, i)) {
         const int b = bin_of(x);
         atomicAdd(&sh.cnt[b], 1u);
-        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)weight(x, m, c));
+        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)w(x));
       }
     });
     int bin;
@@ -553,9 +665,8 @@ __device__ Cut find_cut(const Src& src, RowShared& sh, float m, double c, float 
         mx = fmaxf(mx, x);
         const uint32_t s = atomicAdd(&sh.n, 1u);
         if (s < (uint32_t)kShort) {
-          sh.sx[s] = x;
-          sh.si[s] = i;
-          if (MASS) sh.sw[s] = weight(x, m, c);
+          sh.sk[s] = order_key(x, i);
+          if (MASS) sh.sw[s] = w(x);
         }
       }
     });
@@ -566,10 +677,10 @@ __device__ Cut find_cut(const Src& src, RowShared& sh, float m, double c, float 
     block_min_max<BLOCK>(mn, mx, sh.redf);
     if (mn == mx) {
       // one value: its first `count` indices
-      const uint64_t w = MASS ? weight(mn, m, c) : 1ull;
-      const uint64_t count = MASS ? (need + w - 1) / w : need;
+      const uint64_t one = MASS ? w(mn) : 1ull;
+      const uint64_t count = MASS ? (need + one - 1) / one : need;
       const int at = find_index<BLOCK, false>(
-          src, sh, m, c, 0, vocab, [&](float x, int i) { return x == mn && within.holds(x, i); },
+          src, sh, w, 0, vocab, [&](float x, int i) { return x == mn && within.holds(x, i); },
           count);
       return Cut{mn, at};
     }
@@ -587,50 +698,76 @@ __device__ __forceinline__ double clamp_uniform(float u) {
   return u > 0.0f ? (u < 0.99999994f ? (double)u : 0.99999994039535522) : 0.0;
 }
 
-template <class T>
-__device__ __forceinline__ void put_token(const SampleParams& q, int row, const RowView<T>& view,
-                                          int token, float m, double c, double total) {
+// The drawn token, its score in the row, and the kept total.
+__device__ __forceinline__ void put_token(const SampleParams& q, int row, int token, float x,
+                                          const Weigher& w, double total) {
   if (threadIdx.x != 0) return;
   q.tokens[row] = token;
-  if (q.logprobs && token >= 0) {
-    const float xt = Elem<T>::load(view.base, token + view.lead);
-    const double below = xt == m ? 0.0 : ((double)m - (double)xt) * c;
-    q.logprobs[row] = (float)(-below * kLn2 - log(total * (1.0 / (double)kOne)));
-  }
+  if (q.logprobs)
+    q.logprobs[row] =
+        (float)((x == w.m ? 0.0 : w.log2_of(x) * kLn2) - log(total * (1.0 / (double)kOne)));
 }
 
 // The sum of the weights of a source's scores inside a cut that min-p keeps.
 template <int BLOCK, class Src>
-__device__ __forceinline__ uint64_t mass_in(const Src& src, RowShared& sh, float m, double c,
+__device__ __forceinline__ uint64_t mass_in(const Src& src, RowShared& sh, const Weigher& w,
                                             const Cut& cut, uint64_t min_w) {
   uint64_t s = 0;
   src.template visit<BLOCK>([&](float x, int i) {
-    if (cut.holds(x, i) && drawable(x, m, c)) {
-      const uint64_t w = weight(x, m, c);
-      s += w >= min_w ? w : 0ull;
+    if (cut.holds(x, i)) {
+      const uint64_t v = w.drawn(x);
+      s += v >= min_w ? v : 0ull;
     }
   });
   return block_sum<BLOCK>(s, sh.red);
 }
 
-// The draw over a source's kept scores.
+// The draw over a source's kept scores, left in found_i / found_x.
 template <int BLOCK, class Src>
-__device__ int draw_from(const Src& src, RowShared& sh, float m, double c, const Cut& cut,
-                         uint64_t min_w, int vocab, double u, double& total) {
-  const uint64_t z = mass_in<BLOCK>(src, sh, m, c, cut, min_w);
+__device__ void draw_from(const Src& src, RowShared& sh, const Weigher& w, const Cut& cut,
+                          uint64_t min_w, int vocab, double u, double& total) {
+  const uint64_t z = mass_in<BLOCK>(src, sh, w, cut, min_w);
   total = (double)z;
   uint64_t need = (uint64_t)(u * total) + 1;
   if (need > z) need = z;
-  return find_index<BLOCK, true>(
-      src, sh, m, c, 0, vocab,
-      [&](float x, int i) {
-        return cut.holds(x, i) && drawable(x, m, c) && weight(x, m, c) >= min_w;
-      },
-      need);
+  find_index<BLOCK, true>(
+      src, sh, w, 0, vocab,
+      [&](float x, int i) { return cut.holds(x, i) && w.drawn(x) >= (min_w ? min_w : 1ull); }, need);
 }
 
-__device__ __forceinline__ double below_best(const SegRecord& r, float m, double c) {
-  return r.best == m ? 1.0 : exp2_neg(((double)m - (double)r.best) * c);
+// The same over a list: a few kept scores are ranked by index directly.
+template <int BLOCK>
+__device__ void draw_from_list(const ListSource& list, RowShared& sh, const Weigher& w, const Cut& cut,
+                               uint64_t min_w, int vocab, double u, double& total) {
+  __syncthreads();
+  if (threadIdx.x == 0) sh.n = 0;
+  __syncthreads();
+  uint64_t s = 0;
+  list.visit<BLOCK>([&](float x, int i) {
+    if (!cut.holds(x, i)) return;
+    const uint64_t v = w(x);
+    if (v < min_w) return;
+    s += v;
+    const uint32_t at = atomicAdd(&sh.n, 1u);
+    if (at < (uint32_t)kShort) {
+      sh.sk[at] = index_key(x, i);
+      sh.sw[at] = v;
+    }
+  });
+  const uint64_t z = block_sum<BLOCK>(s, sh.red);
+  const int n = (int)sh.n;
+  if (n > kShort) {
+    draw_from<BLOCK>(list, sh, w, cut, min_w, vocab, u, total);
+    return;
+  }
+  total = (double)z;
+  uint64_t need = (uint64_t)(u * total) + 1;
+  if (need > z) need = z;
+  rank_short<true, true>(sh, n, need);
+}
+
+__device__ __forceinline__ double below_best(const SegRecord& r, const Weigher& w) {
+  return r.best == w.m ? 1.0 : exp2_neg(-w.log2_of(r.best), w.poly);
 }
 
 }  // namespace
@@ -689,8 +826,8 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     return;
   }
 
+  Weigher w(m, ask.c);
   const double u = clamp_uniform(q.uniforms[row]);
-  int token = -1;
   double total = 0.0;  // the kept weights' sum, in units of 2^-43 of the largest
 
   if (!ask.cuts()) {
@@ -699,7 +836,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     double* seg_m = reinterpret_cast<double*>(sh.mass);  // kBinsS entries >= segments
     for (int s = t; s < nseg; s += BLOCK) {
       const SegRecord r = recs[s];
-      seg_m[s] = r.best > ninf ? below_best(r, m, ask.c) * (double)r.mass : 0.0;
+      seg_m[s] = r.best > ninf ? below_best(r, w) * (double)r.mass : 0.0;
     }
     __syncthreads();
     double own = 0.0;
@@ -735,15 +872,14 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     if (mine == seg) sh.redd[30] = mine_before;
     __syncthreads();
     const SegRecord r = recs[seg];
-    double rest = (y - sh.redd[30]) / below_best(r, m, ask.c);
+    double rest = (y - sh.redd[30]) / below_best(r, w);
     if (!(rest > 0.0)) rest = 0.0;
     uint64_t need = rest < (double)r.mass ? (uint64_t)rest + 1 : r.mass;
     if (need > r.mass) need = r.mass;
-    const RowSource<T> src{view, seg * (kSegment / V),
-                           min((seg + 1) * (kSegment / V), (q.vocab + view.lead + V - 1) / V)};
-    token = find_index<BLOCK, true>(src, sh, r.best, ask.c, seg * kSegment - view.lead, kSegment,
-                                    [](float, int) { return true; }, need);
-    put_token(q, row, view, token, m, ask.c, total);
+    w.against(r.best);
+    pick_in_segment<BLOCK>(view, seg, sh, w, [](float, int) { return true; }, need);
+    w.against(m);
+    put_token(q, row, sh.found_i, sh.found_x, w, total);
     return;
   }
 
@@ -754,13 +890,21 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     if (t == 0) sh.list_n = 0;
     __syncthreads();
     const int lane = t & 63;
-    for (int s = t >> 6; s < nseg; s += BLOCK / 64) {
-      const int n = recs[s].count;
-      Candidate cd{ninf, 0};
-      if (lane < n) cd = q.candidates[((int64_t)row * nseg + s) * kSegSlots + lane];
-      const bool in = lane < n && cd.x >= floor && drawable(cd.x, m, ask.c);
-      const uint64_t mask = __ballot(in);
-      if (mask) {
+    constexpr int W = BLOCK / 64, FLY = 4;  // segments a wave has in flight
+    for (int s0 = t >> 6; s0 < nseg; s0 += W * FLY) {
+      Candidate cd[FLY];
+      int n[FLY];
+#pragma unroll
+      for (int f = 0; f < FLY; ++f) {
+        const int s = min(s0 + f * W, nseg - 1);
+        n[f] = s0 + f * W < nseg ? recs[s].count : 0;
+        cd[f] = q.candidates[((int64_t)row * nseg + s) * kSegSlots + lane];
+      }
+#pragma unroll
+      for (int f = 0; f < FLY; ++f) {
+        const bool in = lane < n[f] && cd[f].x >= floor && w.drawable(cd[f].x);
+        const uint64_t mask = __ballot(in);
+        if (mask == 0) continue;
         uint32_t b = 0;
         if (lane == 0) b = atomicAdd(&sh.list_n, (uint32_t)__popcll(mask));
         b = __builtin_amdgcn_readfirstlane(b);
@@ -768,8 +912,8 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
                                     (uint32_t)(mask >> 32),
                                     __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
         if (in && at < (uint32_t)kListS) {
-          sh.lx[at] = cd.x;
-          sh.li[at] = cd.i;
+          sh.lx[at] = cd[f].x;
+          sh.li[at] = cd[f].i;
         }
       }
     }
@@ -778,18 +922,16 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     covered = list.n <= kListS;
   }
   // no drawable score lies below the floor
-  const bool complete = floor == ninf || !drawable(floor, m, ask.c);
+  const bool complete = floor == ninf || !w.drawable(floor);
+  // at or below every drawable score
+  const float least = (float)fmax((double)m - 1.0001 * kTmax / ask.c, -(double)__FLT_MAX__);
   Cut cut{ninf, 0x7FFFFFFF};
   uint64_t need_p = 0;
   if (covered || (ask.cut_p && !ask.cut_k)) {
-    float low = m, high = m;
-    if (covered) {
-      list.visit<BLOCK>([&](float x, int) { low = fminf(low, x); });
-      block_min_max<BLOCK>(low, high, sh.redf);
-    }
+    const float low = complete ? least : floor;
     if (covered && ask.cut_k) {
       if (list.n >= ask.k)
-        cut = find_cut<BLOCK, false>(list, sh, m, ask.c, low, cut, q.vocab, (uint64_t)ask.k);
+        cut = find_cut<BLOCK, false>(list, sh, w, low, m, cut, q.vocab, (uint64_t)ask.k);
       else
         covered = complete;
     }
@@ -797,29 +939,29 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
       uint64_t have = 0;
       double z = 0.0;
       if (covered) {
-        have = mass_in<BLOCK>(list, sh, m, ask.c, cut, 0);
+        have = mass_in<BLOCK>(list, sh, w, cut, 0);
         z = (double)have;
       }
       if (!ask.cut_k && !(covered && complete)) {
         double part = 0.0;
         for (int s = t; s < nseg; s += BLOCK) {
           const SegRecord r = recs[s];
-          if (r.best > ninf) part += below_best(r, m, ask.c) * (double)r.mass;
+          if (r.best > ninf) part += below_best(r, w) * (double)r.mass;
         }
         z = block_sum<BLOCK>(part, sh.redd);
       }
       need_p = ceil_share(ask.p, z);
       if (covered && have >= need_p)
-        cut = find_cut<BLOCK, true>(list, sh, m, ask.c, low, cut, q.vocab, need_p);
+        cut = find_cut<BLOCK, true>(list, sh, w, low, m, cut, q.vocab, need_p);
       else
         covered = covered && complete;
     }
     if (covered && !ask.cut_k && !ask.cut_p)
-      covered = complete || weight(floor, m, ask.c) < ask.min_w;
+      covered = complete || w(floor) < ask.min_w;
   }
   if (covered) {
-    token = draw_from<BLOCK>(list, sh, m, ask.c, cut, ask.min_w, q.vocab, u, total);
-    put_token(q, row, view, token, m, ask.c, total);
+    draw_from_list<BLOCK>(list, sh, w, cut, ask.min_w, q.vocab, u, total);
+    put_token(q, row, sh.found_i, sh.found_x, w, total);
     return;
   }
 
@@ -831,18 +973,17 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   }
   block_min_max<BLOCK>(low, high, sh.redf);
   if (t == 0) {
-    WideRow w;
-    const double least = (double)m - kTmax / ask.c;  // -inf at c = 0
-    const double range = (double)m - fmax(least, (double)low);
-    w.state = (ask.cut_k && ask.cut_p) ? kWideWhole : (ask.cut_k || ask.cut_p) ? kWideBins : kWideMembers;
-    w.m = m;
-    w.scale = (range > 0.0 && range < 1e300) ? (double)kBinsS / range : 0.0;
-    w.need = ask.cut_p ? need_p : (uint64_t)ask.k;
-    w.bin = kBinsS;
-    w.members = 0;
-    w.arrived[0] = 0;
-    w.arrived[1] = 0;
-    q.wide[row] = w;
+    WideRow wr;
+    const double range = (double)m - (double)fmaxf(least, low);
+    wr.state = (ask.cut_k && ask.cut_p) ? kWideWhole : (ask.cut_k || ask.cut_p) ? kWideBins : kWideMembers;
+    wr.m = m;
+    wr.scale = (range > 0.0 && range < 1e300) ? (double)kBinsS / range : 0.0;
+    wr.need = ask.cut_p ? need_p : (uint64_t)ask.k;
+    wr.above = ninf;  // nothing is cut, unless the bins say so
+    wr.from = __builtin_inff();
+    wr.arrived[0] = 0;
+    wr.arrived[1] = 0;
+    q.wide[row] = wr;
   }
 }
 
@@ -891,20 +1032,21 @@ __device__ __forceinline__ bool last_in(uint32_t* counter, int workgroups, RowSh
   return last;
 }
 
-// One wave's segment, as the segment kernel reads it.
+// One wave's segment, as the segment kernel reads it; dead scores are -inf.
 template <class T, class F>
 __device__ __forceinline__ void visit_segment(const RowView<T>& view, int seg, F&& f) {
   constexpr int V = Elem<T>::kVec;
-  constexpr int G = kSegment / (64 * V);
+  constexpr int G = RowView<T>::kGroups;
   const int lane = threadIdx.x & 63;
-#pragma unroll 2
-  for (int g = 0; g < G; ++g) {
-    float x[V];
-    const int pos = view.group(seg * (kSegment / V) + g * 64 + lane, x);
+  float x[G][V];
+  view.segment(seg, lane, x);
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (x[e] > -__builtin_inff()) f(x[e], pos + e);
-  }
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      f(x[g][e], (seg * (kSegment / V) + g * 64 + lane) * V + e - view.lead);
+      if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 }  // namespace
@@ -920,14 +1062,13 @@ __global__ void __launch_bounds__(kWideBlock) sample_bins_kernel(const SamplePar
   const RowView<T> view(q, row);
   const float m = wr->m;
   const double scale = wr->scale;
+  const Weigher w(m, ask.c);
   clear_bins<kWideBlock>(sh);
   const int seg = part * kWideSegs + (t >> 6);
   if (seg < q.segments)
     visit_segment(view, seg, [&](float x, int) {
-      if (drawable(x, m, ask.c)) {
-        const unsigned long long v = ask.cut_p ? weight(x, m, ask.c) : 1ull;
-        atomicAdd((unsigned long long*)&sh.mass[wide_bin(x, m, scale)], v);
-      }
+      const unsigned long long v = ask.cut_p ? w.drawn(x) : w.drawable(x) ? 1ull : 0ull;
+      if (v) atomicAdd((unsigned long long*)&sh.mass[wide_bin(x, m, scale)], v);
     });
   __syncthreads();
   uint64_t* slices = q.slices + (int64_t)row * q.wide_wgs * kBinsS;
@@ -943,9 +1084,24 @@ __global__ void __launch_bounds__(kWideBlock) sample_bins_kernel(const SamplePar
   uint64_t before;
   const uint64_t need = wr->need;
   const bool found = cross_bins<kWideBlock, true>(sh, need, bin, before);
+  if (found && t < 2) {
+    // thread 0: where the bins above the crossing one end; thread 1: where it ends
+    const int last = t == 0 ? bin - 1 : bin;
+    float edge = t == 0 ? __builtin_nanf("") : -__builtin_inff();
+    if (scale > 0.0 && last >= 0 && last < kBinsS - 1) {
+      uint32_t lo = fkey(-__FLT_MAX__), hi = fkey(m);  // the lowest key of a bin <= last
+      while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (wide_bin(from_key(mid), m, scale) <= last) hi = mid;
+        else lo = mid + 1;
+      }
+      edge = from_key(lo);
+    }
+    if (t == 0) wr->above = edge;
+    else wr->from = edge;
+  }
   if (t == 0) {
     wr->state = kWideMembers;
-    wr->bin = found ? bin : kBinsS;  // not reached: nothing is cut
     wr->need = need - (found ? before : 0);
   }
 }
@@ -963,65 +1119,79 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   const RowView<T> view(q, row);
   const double u = clamp_uniform(q.uniforms[row]);
   const int nseg = q.segments;
-  const int room = min(nseg * kSegSlots, kListS);
   const Cut all{-__builtin_inff(), 0x7FFFFFFF};
   Cut cut = all;
   float m = wr->m;
-  bool fits = false;
+  Weigher w(m, ask.c);
 
   if (state == kWideMembers) {
-    const double scale = wr->scale;
-    const int bin = wr->bin;
-    Candidate* members = q.candidates + (int64_t)row * nseg * kSegSlots;
-    uint64_t* kept = q.kept + (int64_t)row * nseg;
+    const float above = wr->above, from = wr->from;
+    const uint64_t need_cut = wr->need;
+    // each part's members in the places of its segments' candidates, its count
+    // behind the segments' kept masses
+    const int room = kWideSegs * kSegSlots;
+    uint64_t* members = reinterpret_cast<uint64_t*>(q.candidates + (int64_t)row * nseg * kSegSlots);
+    uint64_t* kept = q.kept + (int64_t)row * (nseg + q.wide_wgs);
     const int seg = part * kWideSegs + (t >> 6);
+    const uint64_t least = ask.min_w ? ask.min_w : 1ull;
+    const int mine = min(nseg - part * kWideSegs, kWideSegs) * kSegSlots;  // places for this part's
+    if (t == 0) sh.list_n = 0;
+    __syncthreads();
     if (seg < nseg) {
       uint64_t mass = 0;
       visit_segment(view, seg, [&](float x, int i) {
-        if (!drawable(x, m, ask.c)) return;
-        const int b = wide_bin(x, m, scale);
-        if (b < bin) {
-          const uint64_t w = weight(x, m, ask.c);
-          mass += w >= ask.min_w ? w : 0ull;
-        } else if (b == bin) {
-          const uint32_t at = __hip_atomic_fetch_add(&wr->members, 1u, __ATOMIC_RELAXED,
-                                                     __HIP_MEMORY_SCOPE_AGENT);
-          if (at < (uint32_t)room) {
-            const uint64_t both = ((uint64_t)(uint32_t)i << 32) | __float_as_uint(x);
-            agent_store(reinterpret_cast<uint64_t*>(members + at), both);
-          }
+        const uint64_t v = w.drawn(x);
+        mass += x >= above && v >= least ? v : 0ull;
+        if (x >= from && !(x >= above) && w.drawable(x)) {
+          const int at = (int)atomicAdd(&sh.list_n, 1u);
+          if (at < mine)
+            agent_store(&members[part * room + at],
+                        ((uint64_t)(uint32_t)i << 32) | __float_as_uint(x));
         }
       });
       mass = wave_sum(mass);
       if ((t & 63) == 0) agent_store(&kept[seg], mass);
     }
+    __syncthreads();
+    if (t == 0) agent_store(&kept[nseg + part], (uint64_t)sh.list_n);
     if (!last_in(&wr->arrived[1], q.wide_wgs, sh)) return;
-    const int n = (int)agent_load(&wr->members);
-    fits = n <= room;
-    if (fits) {
+    // the parts' counts, and their members one behind the other
+    for (int p = t; p < q.wide_wgs; p += kWideBlock) sh.cnt[p] = (uint32_t)agent_load(&kept[nseg + p]);
+    __syncthreads();
+    int n = 0;
+    bool fits = true;
+    for (int p = 0; p < q.wide_wgs; ++p) {
+      const int c = (int)sh.cnt[p];
+      fits = fits && c <= min(nseg - p * kWideSegs, kWideSegs) * kSegSlots;
+      n += c;
+    }
+    if (fits && n <= kListS) {
       const ListSource list{sh.lx, sh.li, n};
-      float low = m, high = m;
+      float low = __builtin_inff(), high = -__builtin_inff();
+      int p = 0, base = 0;
       for (int i = t; i < n; i += kWideBlock) {
-        const uint64_t both = agent_load(reinterpret_cast<const uint64_t*>(members + i));
+        while (i - base >= (int)sh.cnt[p]) base += (int)sh.cnt[p++];
+        const uint64_t both = agent_load(&members[p * room + i - base]);
         const float x = __uint_as_float((uint32_t)both);
         sh.lx[i] = x;
         sh.li[i] = (int32_t)(both >> 32);
         low = fminf(low, x);
+        high = fmaxf(high, x);
       }
       block_min_max<kWideBlock>(low, high, sh.redf);
-      if (bin < kBinsS) {
+      if (n > 0) {
         if (ask.cut_p)
-          cut = find_cut<kWideBlock, true>(list, sh, m, ask.c, low, all, q.vocab, wr->need);
+          cut = find_cut<kWideBlock, true>(list, sh, w, low, high, all, q.vocab, need_cut);
         else
-          cut = find_cut<kWideBlock, false>(list, sh, m, ask.c, low, all, q.vocab, wr->need);
+          cut = find_cut<kWideBlock, false>(list, sh, w, low, high, all, q.vocab, need_cut);
       }
       clear_bins<kWideBlock>(sh);
       for (int s = t; s < nseg; s += kWideBlock) sh.mass[s] = agent_load(&kept[s]);
       __syncthreads();
       list.visit<kWideBlock>([&](float x, int i) {
-        const uint64_t w = weight(x, m, ask.c);
-        if (cut.holds(x, i) && w >= ask.min_w)
-          atomicAdd((unsigned long long*)&sh.mass[(i + view.lead) / kSegment], (unsigned long long)w);
+        const uint64_t v = w(x);
+        if (cut.holds(x, i) && v >= ask.min_w)
+          atomicAdd((unsigned long long*)&sh.mass[(i + view.lead) / kSegment], (unsigned long long)v);
       });
       __syncthreads();
       uint64_t z = 0;
@@ -1031,15 +1201,10 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
       if (need > z) need = z;
       int at;
       cross_bins<kWideBlock, true>(sh, need, at, before);
-      const RowSource<T> src{view, at * (kSegment / V),
-                             min((at + 1) * (kSegment / V), (q.vocab + view.lead + V - 1) / V)};
-      const int token = find_index<kWideBlock, true>(
-          src, sh, m, ask.c, at * kSegment - view.lead, kSegment,
-          [&](float x, int i) {
-            return cut.holds(x, i) && drawable(x, m, ask.c) && weight(x, m, ask.c) >= ask.min_w;
-          },
+      pick_in_segment<kWideBlock>(
+          view, at, sh, w, [&](float x, int i) { return cut.holds(x, i) && w.drawn(x) >= least; },
           need - before);
-      put_token(q, row, view, token, m, ask.c, (double)z);
+      put_token(q, row, sh.found_i, sh.found_x, w, (double)z);
       return;
     }
   } else if (part != 0 || state != kWideWhole) {
@@ -1053,20 +1218,21 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   block_min_max<kWideBlock>(low, high, sh.redf);
   m = high;
   low = m;
+  w.against(m);
   src.template visit<kWideBlock>([&](float x, int) {
-    if (drawable(x, m, ask.c)) low = fminf(low, x);
+    if (w.drawable(x)) low = fminf(low, x);
   });
   block_min_max<kWideBlock>(low, high, sh.redf);
   cut = all;
   if (ask.cut_k)
-    cut = find_cut<kWideBlock, false>(src, sh, m, ask.c, low, all, q.vocab, (uint64_t)ask.k);
+    cut = find_cut<kWideBlock, false>(src, sh, w, low, high, all, q.vocab, (uint64_t)ask.k);
   if (ask.cut_p) {
-    const uint64_t z = mass_in<kWideBlock>(src, sh, m, ask.c, cut, 0);
-    cut = find_cut<kWideBlock, true>(src, sh, m, ask.c, low, cut, q.vocab, ceil_share(ask.p, (double)z));
+    const uint64_t z = mass_in<kWideBlock>(src, sh, w, cut, 0);
+    cut = find_cut<kWideBlock, true>(src, sh, w, low, high, cut, q.vocab, ceil_share(ask.p, (double)z));
   }
   double total;
-  const int token = draw_from<kWideBlock>(src, sh, m, ask.c, cut, ask.min_w, q.vocab, u, total);
-  put_token(q, row, view, token, m, ask.c, total);
+  draw_from<kWideBlock>(src, sh, w, cut, ask.min_w, q.vocab, u, total);
+  put_token(q, row, sh.found_i, sh.found_x, w, total);
 }
 
 #define ERT_SAMPLE_PTR(NAME, ...)                                                      \
