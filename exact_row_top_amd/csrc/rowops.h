@@ -32,7 +32,7 @@ struct Candidate {
 };
 
 // A row's way through the kernels after the row kernel.
-constexpr int kRowBlock = 256;
+constexpr int kRowBlock = 512;
 constexpr int kWideBlock = 512;   // a wave for each segment
 constexpr int kWideSegs = kWideBlock / 64;
 constexpr int kBinsS = 1024;      // histogram bins

@@ -339,6 +339,8 @@ namespace {
 
 constexpr int kShort = 256;    // members of a bin that are ranked directly
 constexpr int kListS = 2048;   // candidates held in LDS
+constexpr int kMaxSegments = (kMaxVocab + 7 + kSegment - 1) / kSegment;
+static_assert(kMaxSegments <= kBinsS, "the bins hold a row's segments");
 
 struct RowShared {
   uint32_t cnt[kBinsS];
@@ -356,6 +358,10 @@ struct RowShared {
   uint32_t list_n;
   float lx[kListS];
   int32_t li[kListS];
+  uint64_t lw[kListS];
+  float seg_best[kMaxSegments];
+  uint64_t seg_mass[kMaxSegments];
+  int32_t seg_count[kMaxSegments];
 };
 
 // Everything of the order up to and including (x, i).
@@ -369,10 +375,11 @@ struct Cut {
 struct ListSource {
   const float* x;
   const int32_t* i;
+  const uint64_t* v;  // their weights
   int n;
   template <int BLOCK, class F>
   __device__ __forceinline__ void visit(F&& f) const {
-    for (int t = threadIdx.x; t < n; t += BLOCK) f(x[t], i[t]);
+    for (int t = threadIdx.x; t < n; t += BLOCK) f(x[t], i[t], [&] { return v[t]; });
   }
 };
 
@@ -380,6 +387,7 @@ struct ListSource {
 template <class T>
 struct RowSource {
   RowView<T> view;
+  const Weigher& weigh;
   int g0, g1;
   template <int BLOCK, class F>
   __device__ __forceinline__ void visit(F&& f) const {
@@ -396,7 +404,8 @@ struct RowSource {
 #pragma unroll
         for (int e = 0; e < V / 4; ++e) {
           const int i = pos + w * (V / 4) + e;
-          if ((unsigned)i < (unsigned)view.vocab && x[e] > -__builtin_inff()) f(x[e], i);
+          if ((unsigned)i < (unsigned)view.vocab && x[e] > -__builtin_inff())
+            f(x[e], i, [&] { return weigh(x[e]); });
         }
         raw.x = raw.y;
         raw.y = raw.z;
@@ -544,12 +553,12 @@ __device__ int find_index(const Src& src, RowShared& sh, const Weigher& w, int f
   int i0 = from, width = (span + kBinsS - 1) / kBinsS;
   for (;;) {
     clear_bins<BLOCK>(sh);
-    src.template visit<BLOCK>([&](float x, int i) {
+    src.template visit<BLOCK>([&](float x, int i, auto&& v) {
       const int d = i - i0;
       if (d >= 0 && d < width * kBinsS && pred(x, i)) {
         const int b = (int)((unsigned)d / (unsigned)width);
         atomicAdd(&sh.cnt[b], 1u);
-        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)w(x));
+        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)v());
       }
     });
     int bin;
@@ -559,13 +568,13 @@ __device__ int find_index(const Src& src, RowShared& sh, const Weigher& w, int f
     i0 += bin * width;
     const int members = (int)sh.cnt[bin];
     if (width == 1 || members <= kShort) {
-      src.template visit<BLOCK>([&](float x, int i) {
+      src.template visit<BLOCK>([&](float x, int i, auto&& v) {
         const int d = i - i0;
         if (d >= 0 && d < width && pred(x, i)) {
           const uint32_t s = atomicAdd(&sh.n, 1u);
           if (s < (uint32_t)kShort) {
             sh.sk[s] = index_key(x, i);
-            if (MASS) sh.sw[s] = w(x);
+            if (MASS) sh.sw[s] = v();
           }
         }
       });
@@ -646,11 +655,11 @@ __device__ Cut find_cut(const Src& src, RowShared& sh, const Weigher& w, float l
     auto admitted = [&](float x, int i) {
       return x <= hi && x >= lo && w.drawable(x) && within.holds(x, i);
     };
-    src.template visit<BLOCK>([&](float x, int i) {
+    src.template visit<BLOCK>([&](float x, int i, auto&& v) {
       if (admitted(x, i)) {
         const int b = bin_of(x);
         atomicAdd(&sh.cnt[b], 1u);
-        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)w(x));
+        if (MASS) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)v());
       }
     });
     int bin;
@@ -659,14 +668,14 @@ __device__ Cut find_cut(const Src& src, RowShared& sh, const Weigher& w, float l
     need -= before;
     const int members = (int)sh.cnt[bin];
     float mn = __builtin_inff(), mx = -__builtin_inff();
-    src.template visit<BLOCK>([&](float x, int i) {
+    src.template visit<BLOCK>([&](float x, int i, auto&& v) {
       if (admitted(x, i) && bin_of(x) == bin) {
         mn = fminf(mn, x);
         mx = fmaxf(mx, x);
         const uint32_t s = atomicAdd(&sh.n, 1u);
         if (s < (uint32_t)kShort) {
           sh.sk[s] = order_key(x, i);
-          if (MASS) sh.sw[s] = w(x);
+          if (MASS) sh.sw[s] = v();
         }
       }
     });
@@ -713,10 +722,10 @@ template <int BLOCK, class Src>
 __device__ __forceinline__ uint64_t mass_in(const Src& src, RowShared& sh, const Weigher& w,
                                             const Cut& cut, uint64_t min_w) {
   uint64_t s = 0;
-  src.template visit<BLOCK>([&](float x, int i) {
-    if (cut.holds(x, i)) {
-      const uint64_t v = w.drawn(x);
-      s += v >= min_w ? v : 0ull;
+  src.template visit<BLOCK>([&](float x, int i, auto&& v) {
+    if (cut.holds(x, i) && w.drawable(x)) {
+      const uint64_t own = v();
+      s += own >= min_w ? own : 0ull;
     }
   });
   return block_sum<BLOCK>(s, sh.red);
@@ -743,9 +752,9 @@ __device__ void draw_from_list(const ListSource& list, RowShared& sh, const Weig
   if (threadIdx.x == 0) sh.n = 0;
   __syncthreads();
   uint64_t s = 0;
-  list.visit<BLOCK>([&](float x, int i) {
+  list.visit<BLOCK>([&](float x, int i, auto&& weight) {
     if (!cut.holds(x, i)) return;
-    const uint64_t v = w(x);
+    const uint64_t v = weight();
     if (v < min_w) return;
     s += v;
     const uint32_t at = atomicAdd(&sh.n, 1u);
@@ -766,8 +775,9 @@ __device__ void draw_from_list(const ListSource& list, RowShared& sh, const Weig
   rank_short<true, true>(sh, n, need);
 }
 
-__device__ __forceinline__ double below_best(const SegRecord& r, const Weigher& w) {
-  return r.best == w.m ? 1.0 : exp2_neg(-w.log2_of(r.best), w.poly);
+// 2^(best - m), in the row's units.
+__device__ __forceinline__ double below_best(float best, const Weigher& w) {
+  return best == w.m ? 1.0 : exp2_neg(-w.log2_of(best), w.poly);
 }
 
 }  // namespace
@@ -786,7 +796,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
 
   // The row's largest score, the candidates' common floor, and whether every
   // segment's candidates fitted.
-  float m = ninf, floor = ninf;
+  float m = ninf, floor = ninf, low = __builtin_inff();
   bool fits = true;
   int first = 0x7FFFFFFF;
   for (int s = t; s < nseg; s += BLOCK) {
@@ -794,7 +804,11 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     if (ask.greedy && (r.best > m || (r.best == m && r.first < first))) first = r.first;
     m = fmaxf(m, r.best);
     floor = fmaxf(floor, r.floor);
+    low = r.best > ninf ? fminf(low, r.low) : low;
     fits = fits && r.count >= 0;
+    sh.seg_best[s] = r.best;
+    sh.seg_mass[s] = r.mass;
+    sh.seg_count[s] = r.count;
   }
   const float own_best = m;
   float nm = -m;  // the largest of both, through one reduction
@@ -834,10 +848,8 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     // The whole vocabulary: the segment in which the running sum passes
     // u * total, then the place inside it.
     double* seg_m = reinterpret_cast<double*>(sh.mass);  // kBinsS entries >= segments
-    for (int s = t; s < nseg; s += BLOCK) {
-      const SegRecord r = recs[s];
-      seg_m[s] = r.best > ninf ? below_best(r, w) * (double)r.mass : 0.0;
-    }
+    for (int s = t; s < nseg; s += BLOCK)
+      seg_m[s] = sh.seg_best[s] > ninf ? below_best(sh.seg_best[s], w) * (double)sh.seg_mass[s] : 0.0;
     __syncthreads();
     double own = 0.0;
     const int per = (nseg + BLOCK - 1) / BLOCK;
@@ -871,12 +883,13 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     const int seg = sh.found_i;
     if (mine == seg) sh.redd[30] = mine_before;
     __syncthreads();
-    const SegRecord r = recs[seg];
-    double rest = (y - sh.redd[30]) / below_best(r, w);
+    const float best = sh.seg_best[seg];
+    const uint64_t mass = sh.seg_mass[seg];
+    double rest = (y - sh.redd[30]) / below_best(best, w);
     if (!(rest > 0.0)) rest = 0.0;
-    uint64_t need = rest < (double)r.mass ? (uint64_t)rest + 1 : r.mass;
-    if (need > r.mass) need = r.mass;
-    w.against(r.best);
+    uint64_t need = rest < (double)mass ? (uint64_t)rest + 1 : mass;
+    if (need > mass) need = mass;
+    w.against(best);
     pick_in_segment<BLOCK>(view, seg, sh, w, [](float, int) { return true; }, need);
     w.against(m);
     put_token(q, row, sh.found_i, sh.found_x, w, total);
@@ -885,19 +898,19 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
 
   // Candidates at or above the common floor: every such score of the row.
   bool covered = fits;
-  ListSource list{sh.lx, sh.li, 0};
+  ListSource list{sh.lx, sh.li, sh.lw, 0};
   if (covered) {
     if (t == 0) sh.list_n = 0;
     __syncthreads();
     const int lane = t & 63;
-    constexpr int W = BLOCK / 64, FLY = 4;  // segments a wave has in flight
+    constexpr int W = BLOCK / 64, FLY = 8;  // segments a wave has in flight
     for (int s0 = t >> 6; s0 < nseg; s0 += W * FLY) {
       Candidate cd[FLY];
       int n[FLY];
 #pragma unroll
       for (int f = 0; f < FLY; ++f) {
         const int s = min(s0 + f * W, nseg - 1);
-        n[f] = s0 + f * W < nseg ? recs[s].count : 0;
+        n[f] = s0 + f * W < nseg ? sh.seg_count[s] : 0;
         cd[f] = q.candidates[((int64_t)row * nseg + s) * kSegSlots + lane];
       }
 #pragma unroll
@@ -914,6 +927,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
         if (in && at < (uint32_t)kListS) {
           sh.lx[at] = cd[f].x;
           sh.li[at] = cd[f].i;
+          sh.lw[at] = w(cd[f].x);
         }
       }
     }
@@ -928,10 +942,10 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   Cut cut{ninf, 0x7FFFFFFF};
   uint64_t need_p = 0;
   if (covered || (ask.cut_p && !ask.cut_k)) {
-    const float low = complete ? least : floor;
+    const float from = complete ? least : floor;
     if (covered && ask.cut_k) {
       if (list.n >= ask.k)
-        cut = find_cut<BLOCK, false>(list, sh, w, low, m, cut, q.vocab, (uint64_t)ask.k);
+        cut = find_cut<BLOCK, false>(list, sh, w, from, m, cut, q.vocab, (uint64_t)ask.k);
       else
         covered = complete;
     }
@@ -944,15 +958,13 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
       }
       if (!ask.cut_k && !(covered && complete)) {
         double part = 0.0;
-        for (int s = t; s < nseg; s += BLOCK) {
-          const SegRecord r = recs[s];
-          if (r.best > ninf) part += below_best(r, w) * (double)r.mass;
-        }
+        for (int s = t; s < nseg; s += BLOCK)
+          if (sh.seg_best[s] > ninf) part += below_best(sh.seg_best[s], w) * (double)sh.seg_mass[s];
         z = block_sum<BLOCK>(part, sh.redd);
       }
       need_p = ceil_share(ask.p, z);
       if (covered && have >= need_p)
-        cut = find_cut<BLOCK, true>(list, sh, w, low, m, cut, q.vocab, need_p);
+        cut = find_cut<BLOCK, true>(list, sh, w, from, m, cut, q.vocab, need_p);
       else
         covered = covered && complete;
     }
@@ -966,11 +978,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   }
 
   // The cut lies below the candidates: the kernels that follow find it.
-  float low = __builtin_inff(), high = m;
-  for (int s = t; s < nseg; s += BLOCK) {
-    const SegRecord r = recs[s];
-    if (r.best > ninf) low = fminf(low, r.low);
-  }
+  float high = m;
   block_min_max<BLOCK>(low, high, sh.redf);
   if (t == 0) {
     WideRow wr;
@@ -1166,7 +1174,7 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
       n += c;
     }
     if (fits && n <= kListS) {
-      const ListSource list{sh.lx, sh.li, n};
+      const ListSource list{sh.lx, sh.li, sh.lw, n};
       float low = __builtin_inff(), high = -__builtin_inff();
       int p = 0, base = 0;
       for (int i = t; i < n; i += kWideBlock) {
@@ -1175,6 +1183,7 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
         const float x = __uint_as_float((uint32_t)both);
         sh.lx[i] = x;
         sh.li[i] = (int32_t)(both >> 32);
+        sh.lw[i] = w(x);
         low = fminf(low, x);
         high = fmaxf(high, x);
       }
@@ -1188,8 +1197,8 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
       clear_bins<kWideBlock>(sh);
       for (int s = t; s < nseg; s += kWideBlock) sh.mass[s] = agent_load(&kept[s]);
       __syncthreads();
-      list.visit<kWideBlock>([&](float x, int i) {
-        const uint64_t v = w(x);
+      list.visit<kWideBlock>([&](float x, int i, auto&& weight) {
+        const uint64_t v = weight();
         if (cut.holds(x, i) && v >= ask.min_w)
           atomicAdd((unsigned long long*)&sh.mass[(i + view.lead) / kSegment], (unsigned long long)v);
       });
@@ -1212,14 +1221,14 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   }
 
   // The whole row from memory, by this workgroup alone.
-  const RowSource<T> src{view, 0, (q.vocab + view.lead + V - 1) / V};
+  const RowSource<T> src{view, w, 0, (q.vocab + view.lead + V - 1) / V};
   float low = __builtin_inff(), high = -__builtin_inff();
-  src.template visit<kWideBlock>([&](float x, int) { high = fmaxf(high, x); });
+  src.template visit<kWideBlock>([&](float x, int, auto&&) { high = fmaxf(high, x); });
   block_min_max<kWideBlock>(low, high, sh.redf);
   m = high;
   low = m;
   w.against(m);
-  src.template visit<kWideBlock>([&](float x, int) {
+  src.template visit<kWideBlock>([&](float x, int, auto&&) {
     if (w.drawable(x)) low = fminf(low, x);
   });
   block_min_max<kWideBlock>(low, high, sh.redf);
