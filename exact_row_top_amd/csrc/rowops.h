@@ -23,7 +23,7 @@ struct SegRecord {
   int32_t count;    // candidates, -1 if they did not fit
   uint64_t mass;    // rows that need it: sum of the weights against `best`
   float low;        // rows with cuts: smallest live score
-  uint32_t pad;
+  float upper;      // rows with a top-p alone: the candidates' mass, rounded up
 };
 
 struct Candidate {
@@ -32,16 +32,15 @@ struct Candidate {
 };
 
 // A row's way through the kernels after the row kernel.
-constexpr int kRowBlock = 512;
 constexpr int kWideBlock = 512;   // a wave for each segment
 constexpr int kWideSegs = kWideBlock / 64;
+constexpr int kRowBlock = kWideBlock;
 constexpr int kBinsS = 1024;      // histogram bins
-enum : uint32_t { kWideDone = 0, kWideBins = 1, kWideMembers = 2, kWideWhole = 3 };
+enum : uint32_t { kWideDone = 0, kWideMembers = 1, kWideWhole = 2 };
 struct WideRow {
   uint32_t state;
   float m;              // the row's largest score
-  double scale;         // bins per unit of score below it
-  uint64_t need;        // count or mass at the cut; then what of it the crossing bin holds
+  uint64_t need;        // count or mass that the cut leaves to the crossing bin
   float above;          // scores at or above this lie above the crossing bin
   float from;           // the bin's own begin here
   uint32_t arrived[2];  // workgroups done with the bins, with the members
@@ -65,7 +64,8 @@ struct SampleParams {
   WideRow* wide;          // null where no row can have a cut
   uint64_t* kept;         // [rows][segments + wide_wgs]: kept masses, member counts
   uint64_t* slices;       // [rows][wide_wgs][kBinsS]
-  int32_t wide_wgs;       // workgroups of a row
+  int32_t wide_wgs;       // workgroups of a row in the wide kernel
+  int32_t row_wgs;        // in the row kernel: as many if a top-k or top-p is given, else one
   int32_t whole_row;      // every row from memory
 };
 

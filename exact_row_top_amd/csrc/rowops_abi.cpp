@@ -13,7 +13,6 @@
 namespace ert {
 const void* sample_segment_kernel_ptr(int dtype);
 const void* sample_row_kernel_ptr(int dtype);
-const void* sample_bins_kernel_ptr(int dtype);
 const void* sample_wide_kernel_ptr(int dtype);
 const void* route_kernel_ptr(int dtype, int lanes);
 const void* route_grad_kernel_ptr(int dtype, int lanes);
@@ -123,11 +122,11 @@ int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t v
   p.slices = p.kept + waves + num_rows * wgs;
   p.wide = (cuts || whole) ? reinterpret_cast<WideRow*>(p.slices + num_rows * wgs * kBinsS) : nullptr;
   p.wide_wgs = (int32_t)wgs;
+  p.row_wgs = (top_k || top_p) && !whole ? (int32_t)wgs : 1;
   p.whole_row = whole ? 1 : 0;
   rc = launch(sample_segment_kernel_ptr(dtype), (waves + 3) / 4, 256, &p, 0, stream);
-  if (rc == TOPK_OK) rc = launch(sample_row_kernel_ptr(dtype), num_rows, kRowBlock, &p, 0, stream);
-  if (rc == TOPK_OK && (top_k || top_p) && !whole)
-    rc = launch(sample_bins_kernel_ptr(dtype), num_rows * wgs, kWideBlock, &p, 0, stream);
+  if (rc == TOPK_OK)
+    rc = launch(sample_row_kernel_ptr(dtype), num_rows * p.row_wgs, kRowBlock, &p, 0, stream);
   if (rc == TOPK_OK && (cuts || whole))
     rc = launch(sample_wide_kernel_ptr(dtype), num_rows * wgs, kWideBlock, &p, 0, stream);
   return rc;

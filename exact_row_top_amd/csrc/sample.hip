@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
   rec.count = 0;
   rec.mass = 0;
   rec.low = low;
-  rec.pad = 0;
+  rec.upper = 0.0f;
   if (best > -__builtin_inff()) {
     if (ask.greedy) {
       int first = 0x7FFFFFFF;
@@ -261,35 +261,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
           if (x[g][e] == best) first = (g0 + g * 64 + lane) * V + e - view.lead;
       rec.first = wave_min(first);
     } else {
-      if (!ask.cut_k) {
-        uint64_t mass = 0;
-        if (best < __builtin_inff()) {
-          const Weigher w(best, ask.c);
-          // four scores at a time (the empty asm keeps the additions where
-          // they are): with all of them in flight, and added up at the end,
-          // the registers would leave room for three waves a SIMD
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              mass += w.raw(x[g][e]);
-              if (e % 4 == 3) {
-                asm("" : "+v"(mass));
-                __builtin_amdgcn_sched_barrier(0);
-              }
-            }
-          mass -= (uint64_t)(G * V) * kRaw;
-        } else {
-          asm volatile("");  // not ahead of the branch
-          uint32_t n = 0;
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int e = 0; e < V; ++e) n += x[g][e] == best ? 1u : 0u;
-          mass = (uint64_t)n * kOne;
-        }
-        rec.mass = wave_sum(mass);
-      }
+      float floor = __builtin_inff();
       if (ask.cuts()) {
         // how many lane maxima the floor lies under: what a segment should
         // hold of a row's best k, with room for an uneven spread; 16 where
@@ -306,7 +278,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
           const uint32_t t = thr | (1u << b);
           if (__popcll(__ballot(key >= t)) >= j) thr = t;
         }
-        const float floor = thr > fkey(-__builtin_inff()) ? from_key(thr) : -__builtin_inff();
+        floor = thr > fkey(-__builtin_inff()) ? from_key(thr) : -__builtin_inff();
         Candidate* out = q.candidates + (int64_t)id * kSegSlots;
         int n = 0;
 #pragma unroll
@@ -326,9 +298,60 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
         rec.floor = floor;
         rec.count = n <= kSegSlots ? n : -1;
       }
+      if (!ask.cut_k) {
+        if (best == __builtin_inff()) {
+          uint32_t n = 0;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < V; ++e) n += x[g][e] == best ? 1u : 0u;
+          rec.mass = wave_sum((uint64_t)n * kOne);
+        } else if (ask.cut_p) {
+          uint64_t mass = 0, top_mass = 0;
+          const Weigher w(best, ask.c);
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const uint64_t v = w.raw(x[g][e]);
+              mass += v;
+              top_mass += x[g][e] >= floor ? v : kRaw;
+              if (e % 4 == 3) {
+                asm("" : "+v"(mass), "+v"(top_mass));
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          rec.mass = wave_sum(mass - (uint64_t)(G * V) * kRaw);
+          rec.upper = (float)wave_sum(top_mass - (uint64_t)(G * V) * kRaw) * 1.000001f;
+        } else {
+          // four scores at a time (the empty asm keeps the additions where
+          // they are): with all of them in flight, and added up at the end,
+          // the registers would leave room for three waves a SIMD
+          uint64_t mass = 0;
+          const Weigher w(best, ask.c);
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              mass += w.raw(x[g][e]);
+              if (e % 4 == 3) {
+                asm("" : "+v"(mass));
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          rec.mass = wave_sum(mass - (uint64_t)(G * V) * kRaw);
+        }
+      }
     }
   }
-  if (lane == 0) q.records[id] = rec;
+  if (lane == 0) {
+    q.records[id] = rec;
+    if (seg == 0 && q.wide) {
+      q.wide[row].state = kWideDone;
+      q.wide[row].arrived[0] = 0;
+      q.wide[row].arrived[1] = 0;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -361,6 +384,7 @@ struct RowShared {
   uint64_t lw[kListS];
   float seg_best[kMaxSegments];
   uint64_t seg_mass[kMaxSegments];
+  float seg_upper[kMaxSegments];
   int32_t seg_count[kMaxSegments];
 };
 
@@ -780,6 +804,138 @@ __device__ __forceinline__ double below_best(float best, const Weigher& w) {
   return best == w.m ? 1.0 : exp2_neg(-w.log2_of(best), w.poly);
 }
 
+// ---------------------------------------------------------------------------
+// Rows whose cut lies below the candidates (flat rows with a top-p, a large
+// top-k, a small min-p), kWideSegs segments a workgroup:
+//  1. in the row kernel, the row's masses (top-p) or counts (top-k) in kBinsS
+//     equal bins of score from the largest down; the row's last workgroup
+//     adds the others' bins up and finds the crossing bin;
+//  2. sample_wide_kernel: each segment's kept mass above that bin, and the
+//     bin's members; the row's last workgroup finds the exact cut among the
+//     members, adds the kept ones to their segments, finds the segment in
+//     which the draw falls, and the token in it.
+// Sums are whole numbers, so which workgroup is last changes nothing.  What
+// crosses between workgroups goes through agent-scope atomics, complete
+// before their workgroup counts itself; nobody waits for anybody.
+// Rows with both a large top-k and a top-p, rows with +inf scores, and bins
+// with more members than fit are selected by one workgroup from memory, pass
+// by pass.
+// ---------------------------------------------------------------------------
+
+
+// The bin of log2-weight s <= 0; `rate` bins an octave.
+__device__ __forceinline__ int wide_bin(double s, double rate) {
+  return min((int)(s * -rate), kBinsS - 1);
+}
+
+template <class V>
+__device__ __forceinline__ V agent_load(const V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class V>
+__device__ __forceinline__ void agent_store(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Counts this workgroup in; true in the row's last one.
+__device__ __forceinline__ bool last_in(uint32_t* counter, int workgroups, RowShared& sh) {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's stores and atomics are done
+  __syncthreads();
+  if (threadIdx.x == 0)
+    sh.bin = (int)__hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const bool last = sh.bin == workgroups - 1;
+  __syncthreads();
+  return last;
+}
+
+// One wave's segment, as the segment kernel reads it; dead scores are -inf.
+template <class T, class F>
+__device__ __forceinline__ void visit_segment(const RowView<T>& view, int seg, F&& f) {
+  constexpr int V = Elem<T>::kVec;
+  constexpr int G = RowView<T>::kGroups;
+  const int lane = threadIdx.x & 63;
+  float x[G][V];
+  view.segment(seg, lane, x);
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      f(x[g][e], (seg * (kSegment / V) + g * 64 + lane) * V + e - view.lead);
+      if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// A drawable score's weight, else 0, for finite m: what Weigher::drawn gives.
+__device__ __forceinline__ uint64_t drawn_at(const Weigher& w, double s) {
+  const uint64_t v = w.raw_of(s) - kRaw;
+  return s > -kTmax ? v : 0ull;
+}
+
+// This workgroup's waves add segments [s0, s1) to the bins.
+template <class T>
+__device__ __forceinline__ void fill_bins(const RowView<T>& view, int s0, int s1, RowShared& sh,
+                                          const Weigher& w, double rate, bool by_mass) {
+  clear_bins<kWideBlock>(sh);
+  for (int seg = s0 + (int)(threadIdx.x >> 6); seg < s1; seg += kWideSegs) {
+    if (by_mass)
+      visit_segment(view, seg, [&](float x, int) {
+        const double s = w.log2_of(x);
+        const unsigned long long v = drawn_at(w, s);
+        if (v) atomicAdd((unsigned long long*)&sh.mass[wide_bin(s, rate)], v);
+      });
+    else
+      visit_segment(view, seg, [&](float x, int) {
+        const double s = w.log2_of(x);
+        if (s > -kTmax) atomicAdd((unsigned long long*)&sh.mass[wide_bin(s, rate)], 1ull);
+      });
+  }
+  __syncthreads();
+}
+
+// The crossing bin of a row's whole bins, handed to the wide kernel as the
+// scores at which it begins and ends.
+__device__ __forceinline__ void cross_wide(RowShared& sh, const Weigher& w, double rate, uint64_t need,
+                                           WideRow* wr) {
+  if (threadIdx.x == 0) sh.bin = -1;
+  int bin;
+  uint64_t before;
+  const bool found = cross_bins<kWideBlock, true>(sh, need, bin, before);
+  // nothing is cut unless the bins say so
+  float edge = threadIdx.x < 64 ? -__builtin_inff() : __builtin_inff();
+  if (found && threadIdx.x < 128) {
+    // wave 0: the lowest score of the bins above the crossing one (NaN: there
+    // is none); wave 1: of the crossing bin itself
+    const int last = threadIdx.x < 64 ? bin - 1 : bin;
+    edge = last < 0 ? __builtin_nanf("") : -__builtin_inff();
+    if (rate > 0.0 && last >= 0 && last < kBinsS - 1) {
+      const uint32_t lane = threadIdx.x & 63;
+      uint32_t lo = fkey(-__FLT_MAX__), hi = fkey(w.m);  // hi lies in bin 0
+      while (lo < hi) {  // the lowest key whose bin is at most `last`, 64 probes a round
+        const uint32_t step = (hi - lo) / 64 + 1;
+        const uint32_t probe = min(lo + lane * step, hi);
+        const uint64_t ok = __ballot(wide_bin(w.log2_of(from_key(probe)), rate) <= last);
+        const uint32_t f = (uint32_t)__ffsll((unsigned long long)ok);  // 1-based, 0: none
+        const uint32_t old = lo;
+        if (f == 1) hi = old;
+        else if (f == 0) lo = min(old + 63 * step, hi) + 1;
+        else {
+          lo = old + (f - 2) * step + 1;
+          hi = min(old + (f - 1) * step, hi);
+        }
+      }
+      edge = from_key(hi);
+    }
+  }
+  if (threadIdx.x == 0) {
+    wr->above = edge;
+    wr->m = w.m;
+    wr->need = need - (found ? before : 0);
+    wr->state = kWideMembers;
+  }
+  if (threadIdx.x == 64) wr->from = edge;
+}
+
 }  // namespace
 
 template <class T, int BLOCK>
@@ -787,8 +943,11 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   __shared__ RowShared sh;
   constexpr int V = Elem<T>::kVec;
   const int t = threadIdx.x;
-  const int row = blockIdx.x;
+  const int row = blockIdx.x / q.row_wgs, part = blockIdx.x % q.row_wgs;
   const RowAsk ask = row_ask(q, row);
+  // only rows whose one cut may lie low need more than one workgroup
+  const bool one_cut = ask.cut_p != ask.cut_k && !ask.greedy && !q.whole_row;
+  if (part > 0 && !one_cut) return;
   const RowView<T> view(q, row);
   const int nseg = q.segments;
   const SegRecord* recs = q.records + (int64_t)row * nseg;
@@ -798,6 +957,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   // segment's candidates fitted.
   float m = ninf, floor = ninf, low = __builtin_inff();
   bool fits = true;
+  int listed = 0;
   int first = 0x7FFFFFFF;
   for (int s = t; s < nseg; s += BLOCK) {
     const SegRecord r = recs[s];
@@ -806,8 +966,10 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     floor = fmaxf(floor, r.floor);
     low = r.best > ninf ? fminf(low, r.low) : low;
     fits = fits && r.count >= 0;
+    listed += r.count;
     sh.seg_best[s] = r.best;
     sh.seg_mass[s] = r.mass;
+    sh.seg_upper[s] = r.upper;
     sh.seg_count[s] = r.count;
   }
   const float own_best = m;
@@ -815,10 +977,8 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   block_min_max<BLOCK>(nm, floor, sh.redf);
   m = -nm;
   fits = __syncthreads_and(fits);
-  if (t == 0 && q.wide) q.wide[row].state = kWideDone;
-
   if (m == ninf) {  // nothing to draw from
-    if (t == 0) {
+    if (t == 0 && part == 0) {
       q.tokens[row] = -1;
       if (q.logprobs) q.logprobs[row] = ninf;
     }
@@ -896,6 +1056,52 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     return;
   }
 
+  // no drawable score lies below the floor
+  const bool complete = floor == ninf || !w.drawable(floor);
+  // at or below every drawable score
+  const float least = (float)fmax((double)m - 1.0001 * kTmax / ask.c, -(double)__FLT_MAX__);
+  float high = m;
+  WideRow* wr = q.wide + row;
+  double rate = 0.0;
+  uint64_t need = (uint64_t)ask.k;
+  if (one_cut && m < __builtin_inff()) {
+    // The cut's count or mass, and whether the candidates can hold it at all.
+    block_min_max<BLOCK>(low, high, sh.redf);
+    const double span = fmax(w.log2_of(low), -kTmax);
+    rate = span < 0.0 ? (double)kBinsS / -span : 0.0;
+    bool low_cut;
+    if (ask.cut_p) {
+      double z = 0.0, top = 0.0;
+      for (int s = t; s < nseg; s += BLOCK)
+        if (sh.seg_best[s] > ninf) {
+          const double unit = below_best(sh.seg_best[s], w);
+          z += unit * (double)sh.seg_mass[s];
+          top += unit * (double)sh.seg_upper[s];
+        }
+      z = block_sum<BLOCK>(z, sh.redd);
+      top = block_sum<BLOCK>(top, sh.redd);
+      need = ceil_share(ask.p, z);
+      low_cut = top < (double)need;
+    } else {
+      low_cut = block_sum<BLOCK>(listed, reinterpret_cast<int*>(sh.redf)) < ask.k && !complete;
+    }
+    fits = fits && !low_cut;
+  }
+  // This workgroup's share of the bins; the row's last one finds the crossing.
+  auto bin_row = [&] {
+    fill_bins(view, part * kWideSegs, min((part + 1) * kWideSegs, nseg), sh, w, rate, ask.cut_p);
+    uint64_t* slices = q.slices + (int64_t)row * q.row_wgs * kBinsS;
+    for (int b = t; b < kBinsS; b += BLOCK) agent_store(&slices[part * kBinsS + b], sh.mass[b]);
+    if (!last_in(&wr->arrived[0], q.row_wgs, sh)) return;
+    for (int b = t; b < kBinsS; b += BLOCK) {
+      uint64_t sum = 0;
+#pragma unroll 8
+      for (int p = 0; p < q.row_wgs; ++p) sum += agent_load(&slices[p * kBinsS + b]);
+      sh.mass[b] = sum;
+    }
+    cross_wide(sh, w, rate, need, wr);
+  };
+
   // Candidates at or above the common floor: every such score of the row.
   bool covered = fits;
   ListSource list{sh.lx, sh.li, sh.lw, 0};
@@ -935,41 +1141,29 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     list.n = (int)sh.list_n;
     covered = list.n <= kListS;
   }
-  // no drawable score lies below the floor
-  const bool complete = floor == ninf || !w.drawable(floor);
-  // at or below every drawable score
-  const float least = (float)fmax((double)m - 1.0001 * kTmax / ask.c, -(double)__FLT_MAX__);
+  // Whether the cut lies among them; each of the row's workgroups comes to the
+  // same answer.
   Cut cut{ninf, 0x7FFFFFFF};
-  uint64_t need_p = 0;
-  if (covered || (ask.cut_p && !ask.cut_k)) {
-    const float from = complete ? least : floor;
-    if (covered && ask.cut_k) {
-      if (list.n >= ask.k)
-        cut = find_cut<BLOCK, false>(list, sh, w, from, m, cut, q.vocab, (uint64_t)ask.k);
-      else
-        covered = complete;
+  const float from = complete ? least : floor;
+  if (covered && ask.cut_k) covered = list.n >= ask.k || complete;
+  if (one_cut && covered && ask.cut_p) {
+    const uint64_t have = mass_in<BLOCK>(list, sh, w, cut, 0);
+    if (complete) need = ceil_share(ask.p, (double)have);
+    covered = have >= need;
+  }
+  if (one_cut && !covered && m < __builtin_inff()) {
+    bin_row();
+    return;
+  }
+  if (part > 0) return;
+  if (covered) {
+    if (ask.cut_k && list.n >= ask.k)
+      cut = find_cut<BLOCK, false>(list, sh, w, from, m, cut, q.vocab, (uint64_t)ask.k);
+    if (ask.cut_p) {
+      if (ask.cut_k) need = ceil_share(ask.p, (double)mass_in<BLOCK>(list, sh, w, cut, 0));
+      cut = find_cut<BLOCK, true>(list, sh, w, from, m, cut, q.vocab, need);
     }
-    if (ask.cut_p && (covered || !ask.cut_k)) {
-      uint64_t have = 0;
-      double z = 0.0;
-      if (covered) {
-        have = mass_in<BLOCK>(list, sh, w, cut, 0);
-        z = (double)have;
-      }
-      if (!ask.cut_k && !(covered && complete)) {
-        double part = 0.0;
-        for (int s = t; s < nseg; s += BLOCK)
-          if (sh.seg_best[s] > ninf) part += below_best(sh.seg_best[s], w) * (double)sh.seg_mass[s];
-        z = block_sum<BLOCK>(part, sh.redd);
-      }
-      need_p = ceil_share(ask.p, z);
-      if (covered && have >= need_p)
-        cut = find_cut<BLOCK, true>(list, sh, w, from, m, cut, q.vocab, need_p);
-      else
-        covered = covered && complete;
-    }
-    if (covered && !ask.cut_k && !ask.cut_p)
-      covered = complete || w(floor) < ask.min_w;
+    if (!ask.cut_k && !ask.cut_p) covered = complete || w(floor) < ask.min_w;
   }
   if (covered) {
     draw_from_list<BLOCK>(list, sh, w, cut, ask.min_w, q.vocab, u, total);
@@ -977,140 +1171,13 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     return;
   }
 
-  // The cut lies below the candidates: the kernels that follow find it.
-  float high = m;
-  block_min_max<BLOCK>(low, high, sh.redf);
+  // Two cuts below the candidates, +inf scores, or (needing no bins) min-p.
   if (t == 0) {
-    WideRow wr;
-    const double range = (double)m - (double)fmaxf(least, low);
-    wr.state = (ask.cut_k && ask.cut_p) ? kWideWhole : (ask.cut_k || ask.cut_p) ? kWideBins : kWideMembers;
-    wr.m = m;
-    wr.scale = (range > 0.0 && range < 1e300) ? (double)kBinsS / range : 0.0;
-    wr.need = ask.cut_p ? need_p : (uint64_t)ask.k;
-    wr.above = ninf;  // nothing is cut, unless the bins say so
-    wr.from = __builtin_inff();
-    wr.arrived[0] = 0;
-    wr.arrived[1] = 0;
-    q.wide[row] = wr;
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Rows whose cut lies below the candidates (flat rows with a top-p, a large
-// top-k, a small min-p), kWideSegs segments a workgroup:
-//  1. sample_bins_kernel: the row's masses (top-p) or counts (top-k) in
-//     kBinsS equal bins of score from the largest down; the row's last
-//     workgroup adds the others' bins up and finds the crossing bin;
-//  2. sample_wide_kernel: each segment's kept mass above that bin, and the
-//     bin's members; the row's last workgroup finds the exact cut among the
-//     members, adds the kept ones to their segments, finds the segment in
-//     which the draw falls, and the token in it.
-// Sums are whole numbers, so which workgroup is last changes nothing.  What
-// crosses between workgroups goes through agent-scope atomics, complete
-// before their workgroup counts itself; nobody waits for anybody.
-// Rows with both a large top-k and a top-p, and bins with more members than
-// fit, are selected by one workgroup from memory, pass by pass.
-// ---------------------------------------------------------------------------
-
-namespace {
-
-__device__ __forceinline__ int wide_bin(float x, float m, double scale) {
-  const double b = ((double)m - (double)x) * scale;
-  return b < (double)(kBinsS - 1) ? (int)b : kBinsS - 1;  // x == m = +inf: NaN, the last bin
-}
-
-template <class V>
-__device__ __forceinline__ V agent_load(const V* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <class V>
-__device__ __forceinline__ void agent_store(V* p, V v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// Counts this workgroup in; true in the row's last one.
-__device__ __forceinline__ bool last_in(uint32_t* counter, int workgroups, RowShared& sh) {
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's stores and atomics are done
-  __syncthreads();
-  if (threadIdx.x == 0)
-    sh.bin = (int)__hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  const bool last = sh.bin == workgroups - 1;
-  __syncthreads();
-  return last;
-}
-
-// One wave's segment, as the segment kernel reads it; dead scores are -inf.
-template <class T, class F>
-__device__ __forceinline__ void visit_segment(const RowView<T>& view, int seg, F&& f) {
-  constexpr int V = Elem<T>::kVec;
-  constexpr int G = RowView<T>::kGroups;
-  const int lane = threadIdx.x & 63;
-  float x[G][V];
-  view.segment(seg, lane, x);
-#pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      f(x[g][e], (seg * (kSegment / V) + g * 64 + lane) * V + e - view.lead);
-      if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-    }
-}
-
-}  // namespace
-
-template <class T>
-__global__ void __launch_bounds__(kWideBlock) sample_bins_kernel(const SampleParams q) {
-  __shared__ RowShared sh;
-  const int t = threadIdx.x;
-  const int row = blockIdx.x / q.wide_wgs, part = blockIdx.x % q.wide_wgs;
-  WideRow* wr = q.wide + row;
-  if (wr->state != kWideBins) return;
-  const RowAsk ask = row_ask(q, row);
-  const RowView<T> view(q, row);
-  const float m = wr->m;
-  const double scale = wr->scale;
-  const Weigher w(m, ask.c);
-  clear_bins<kWideBlock>(sh);
-  const int seg = part * kWideSegs + (t >> 6);
-  if (seg < q.segments)
-    visit_segment(view, seg, [&](float x, int) {
-      const unsigned long long v = ask.cut_p ? w.drawn(x) : w.drawable(x) ? 1ull : 0ull;
-      if (v) atomicAdd((unsigned long long*)&sh.mass[wide_bin(x, m, scale)], v);
-    });
-  __syncthreads();
-  uint64_t* slices = q.slices + (int64_t)row * q.wide_wgs * kBinsS;
-  for (int b = t; b < kBinsS; b += kWideBlock) agent_store(&slices[part * kBinsS + b], sh.mass[b]);
-  if (!last_in(&wr->arrived[0], q.wide_wgs, sh)) return;
-  for (int b = t; b < kBinsS; b += kWideBlock) {
-    uint64_t s = 0;
-    for (int w = 0; w < q.wide_wgs; ++w) s += agent_load(&slices[w * kBinsS + b]);
-    sh.mass[b] = s;
-  }
-  if (t == 0) sh.bin = -1;
-  int bin;
-  uint64_t before;
-  const uint64_t need = wr->need;
-  const bool found = cross_bins<kWideBlock, true>(sh, need, bin, before);
-  if (found && t < 2) {
-    // thread 0: where the bins above the crossing one end; thread 1: where it ends
-    const int last = t == 0 ? bin - 1 : bin;
-    float edge = t == 0 ? __builtin_nanf("") : -__builtin_inff();
-    if (scale > 0.0 && last >= 0 && last < kBinsS - 1) {
-      uint32_t lo = fkey(-__FLT_MAX__), hi = fkey(m);  // the lowest key of a bin <= last
-      while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (wide_bin(from_key(mid), m, scale) <= last) hi = mid;
-        else lo = mid + 1;
-      }
-      edge = from_key(lo);
-    }
-    if (t == 0) wr->above = edge;
-    else wr->from = edge;
-  }
-  if (t == 0) {
-    wr->state = kWideMembers;
-    wr->need = need - (found ? before : 0);
+    wr->above = ninf;
+    wr->from = __builtin_inff();
+    wr->m = m;
+    wr->need = 0;
+    wr->state = (m == __builtin_inff() || ask.cut_k || ask.cut_p) ? kWideWhole : kWideMembers;
   }
 }
 
@@ -1121,7 +1188,7 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   const int t = threadIdx.x;
   const int row = blockIdx.x / q.wide_wgs, part = blockIdx.x % q.wide_wgs;
   WideRow* wr = q.wide + row;
-  const uint32_t state = wr->state;
+  const uint32_t state = wr->state;  // kWideWhole rows: the first workgroup alone
   if (state == kWideDone) return;
   const RowAsk ask = row_ask(q, row);
   const RowView<T> view(q, row);
@@ -1148,9 +1215,10 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
     if (seg < nseg) {
       uint64_t mass = 0;
       visit_segment(view, seg, [&](float x, int i) {
-        const uint64_t v = w.drawn(x);
+        const double s = w.log2_of(x);
+        const uint64_t v = drawn_at(w, s);
         mass += x >= above && v >= least ? v : 0ull;
-        if (x >= from && !(x >= above) && w.drawable(x)) {
+        if (x >= from && !(x >= above) && s > -kTmax) {
           const int at = (int)atomicAdd(&sh.list_n, 1u);
           if (at < mine)
             agent_store(&members[part * room + at],
@@ -1255,7 +1323,6 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   }
 ERT_SAMPLE_PTR(sample_segment_kernel)
 ERT_SAMPLE_PTR(sample_row_kernel, , kRowBlock)
-ERT_SAMPLE_PTR(sample_bins_kernel)
 ERT_SAMPLE_PTR(sample_wide_kernel)
 
 }  // namespace ert
