@@ -10,13 +10,17 @@
 // divided by their sum if asked, times a scale.  Experts whose logit is -inf
 // or NaN are never chosen; slots without an expert hold -1 and weight 0.
 //
-// The choice is a whole number that has to be the same wherever it is made,
-// so it is made on 64-bit scores.
+// The choice is a whole number that has to come out the same wherever it is
+// made, so it is the choice on 64-bit scores.  It is made on 32-bit ones
+// first: where every score that was taken stands clear of the next one by
+// more than both can be off, the 64-bit order is the same; the few tokens
+// (and ties under a bias) where it does not are chosen again in 64 bits.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include "gvr_device.h"
 #include "rowops.h"
 
 namespace ert {
@@ -24,6 +28,7 @@ namespace ert {
 namespace {
 
 constexpr int kRouteBlock = 256;
+constexpr int kNear = 16;  // experts that are ranked one a lane
 
 // Sums and maxima over the L lanes that share a token.
 template <int L, class V>
@@ -48,6 +53,56 @@ __device__ __forceinline__ int lanes_min(int v) {
   return v;
 }
 
+// All-lane reductions of 32-bit values by rotations within rows of 16 lanes
+// (no LDS), and for L = 64 over the four rows' results.
+template <int N>
+__device__ __forceinline__ uint32_t ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 + N, 0xf, 0xf, false);
+}
+template <int L, class Op>
+__device__ __forceinline__ uint32_t lanes_fold(uint32_t v, Op&& op) {
+  v = op(v, ror<8>(v));
+  v = op(v, ror<4>(v));
+  v = op(v, ror<2>(v));
+  v = op(v, ror<1>(v));
+  if (L == 64) {
+    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
+    const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32);
+    const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+    v = op(op(a, b), op(c, d));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t fold_max(uint32_t v) {
+  return lanes_fold<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ float fold_maxf(float v) {
+  return __uint_as_float(lanes_fold<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+template <int L>
+__device__ __forceinline__ float fold_sumf(float v) {
+  return __uint_as_float(lanes_fold<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int L>
+__device__ __forceinline__ uint32_t fold_sum(uint32_t v) {
+  return lanes_fold<L>(v, [](uint32_t a, uint32_t b) { return a + b; });
+}
+
+// A wave's LDS operations are done in order: this only keeps the compiler
+// from moving them.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ bool live(float x) { return x > -__builtin_inff(); }
 
 __device__ __forceinline__ double sigmoid64(double x) {
@@ -55,11 +110,159 @@ __device__ __forceinline__ double sigmoid64(double x) {
   return (x < 0.0 ? e : 1.0) / (1.0 + e);
 }
 
+// The group of expert e < 1024.
+__device__ __forceinline__ uint32_t group_of(const RouteParams& q, int e) {
+  return q.group_size > 1 ? __umulhi((uint32_t)e, q.group_magic) : (uint32_t)e & 31u;
+}
+
+// Scores in 64 bits, to 2^-45 of themselves.
+struct Score64 {
+  Exp2Poly poly;
+  float top;      // softmax: the largest of the logits that share the mass
+  double inv_z;
+  bool sigmoid;
+  __device__ __forceinline__ double share(float x) const {
+    const double v = exp2_64(((double)x - (double)top) * kLog2e, poly);  // 0 at -inf
+    return x == top ? 1.0 : v;
+  }
+  __device__ __forceinline__ double operator()(float x) const {
+    if (!sigmoid) return share(x) * inv_z;
+    const double e = exp2_64(-__builtin_fabs((double)x) * kLog2e, poly);
+    return (x < 0.0f ? e : 1.0) / (1.0 + e);
+  }
+};
+
+__device__ __forceinline__ double ror64(double v, int n) {
+  const uint32_t lo = (uint32_t)__double2loint(v), hi = (uint32_t)__double2hiint(v);
+  uint32_t a, b;
+  switch (n) {
+    case 8: a = ror<8>(lo); b = ror<8>(hi); break;
+    case 4: a = ror<4>(lo); b = ror<4>(hi); break;
+    case 2: a = ror<2>(lo); b = ror<2>(hi); break;
+    default: a = ror<1>(lo); b = ror<1>(hi); break;
+  }
+  return __hiloint2double((int)b, (int)a);
+}
+template <int L>
+__device__ __forceinline__ double fold_max64(double v) {
+  v = fmax(v, ror64(v, 8));
+  v = fmax(v, ror64(v, 4));
+  v = fmax(v, ror64(v, 2));
+  v = fmax(v, ror64(v, 1));
+  if (L == 64) {
+    v = fmax(v, __shfl_xor(v, 16));
+    v = fmax(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+// One token's scores in 64 bits; -inf for experts that cannot be chosen.
+template <class T, int L, int EPL>
+__device__ __forceinline__ void scores64(const RouteParams& q, const float (&x)[EPL],
+                                         const Score64& score, int l, double (&d)[EPL]) {
+  constexpr int V = Elem<T>::kVec;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = (i / V * L + l) * V + i % V;
+    const double v = q.bias ? score(x[i]) + (double)q.bias[min(e, q.experts - 1)] : (double)x[i];
+    d[i] = (live(x[i]) && v > -__builtin_inf()) ? v : -__builtin_inf();
+  }
+}
+
+// The groups that stay, in 64 bits; `c` and `group_score` in LDS.
+template <class T, int L, int EPL>
+__device__ __forceinline__ uint32_t groups64(const RouteParams& q, const float (&x)[EPL],
+                                             const Score64& score, int l, double* c,
+                                             double* group_score) {
+  constexpr int V = Elem<T>::kVec;
+  const double ninf = -__builtin_inf();
+  double d[EPL];
+  scores64<T, L, EPL>(q, x, score, l, d);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = (i / V * L + l) * V + i % V;
+    if (e < q.experts) c[e] = d[i];
+  }
+  wave_sync();
+  if (l < q.groups) {
+    double a = ninf, b = ninf;
+#pragma unroll 4
+    for (int n = 0; n < q.group_size; ++n) {
+      const double v = c[l * q.group_size + n];
+      b = fmax(b, fmin(a, v));
+      a = fmax(a, v);
+    }
+    double v = a;
+    if (q.top2 && a > ninf) {
+      v = q.bias ? a : score((float)a);
+      if (b > ninf) v += q.bias ? b : score((float)b);
+    }
+    group_score[l] = v;
+  }
+  wave_sync();
+  bool stay = false;
+  if (l < q.groups) {
+    const double own = group_score[l];
+    int better = 0;
+    for (int h = 0; h < q.groups; ++h) {
+      const double o = group_score[h];
+      better += (o > own || (o == own && h < l)) ? 1 : 0;
+    }
+    stay = better < q.topk_groups;
+  }
+  wave_sync();
+  return (uint32_t)(__ballot(stay) >> ((threadIdx.x & 63) / L * L)) & 0xFFFFu;
+}
+
+// The choice of one token in 64 bits by its L lanes, among the groups kept.
+template <class T, int L, int EPL>
+__device__ __forceinline__ void choose64(const RouteParams& q, const float (&x)[EPL],
+                                         const Score64& score, int l, uint32_t keep, int32_t* chosen) {
+  constexpr int V = Elem<T>::kVec;
+  const double ninf = -__builtin_inf();
+  double d[EPL];
+  scores64<T, L, EPL>(q, x, score, l, d);
+  if (q.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (!((keep >> group_of(q, (i / V * L + l) * V + i % V)) & 1u)) d[i] = ninf;
+  }
+  for (int j = 0; j < q.top_k; ++j) {
+    double best = ninf;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) best = fmax(best, d[i]);
+    best = fold_max64<L>(best);
+    int i = EPL;
+#pragma unroll
+    for (int o = EPL - 1; o >= 0; --o) i = d[o] == best ? o : i;
+    if (!(best > ninf)) i = EPL;
+    const int own = i < EPL ? (i / V * L + l) * V + i % V : 0x7FFFFFFF;
+    const int at = lanes_min<L>(own);  // the lowest of equals
+    if (l == 0) chosen[j] = at == 0x7FFFFFFF ? -1 : at;
+    const int gone = at == own ? i : EPL;
+#pragma unroll
+    for (int o = 0; o < EPL; ++o) d[o] = o == gone ? ninf : d[o];
+  }
+}
+
 }  // namespace
 
-template <class T, int L>
+// L lanes a token, up to EPL experts a lane in 16-byte groups: group v of lane
+// l holds experts (v * L + l) * V ... of the token, so a token's loads are one
+// piece.  Waves work alone.
+//
+// The chosen scores come off in falling order as 31-bit keys: with M the last
+// key taken, key - M as an unsigned number is at least 2^31 exactly for the
+// keys below M and larger the nearer they are, so the next one is the largest
+// difference, and nothing needs marking.  16-bit logits without a bias carry
+// the expert's number in the key's low bits and are unique; other equal keys
+// are found by counting, at the end, the keys at or above the last.
+template <class T, int L, int EPL>
 __global__ void __launch_bounds__(kRouteBlock) route_kernel(const RouteParams q) {
   constexpr int TOKENS = kRouteBlock / L;
+  constexpr int V = Elem<T>::kVec;
+  constexpr int NV = EPL / V;
+  constexpr bool NARROW = V == 8;
   extern __shared__ double lds[];
   __shared__ double group_score[TOKENS][kMaxGroups];
   __shared__ int32_t chosen[TOKENS][kMaxRouteK];
@@ -67,111 +270,292 @@ __global__ void __launch_bounds__(kRouteBlock) route_kernel(const RouteParams q)
   const int slot = threadIdx.x / L;
   const int64_t token = (int64_t)blockIdx.x * TOKENS + slot;
   const bool on = token < q.tokens;
-  const int E = q.experts;
-  const double ninf = -__builtin_inf();
-  double* c = lds + (int64_t)slot * E;
-  const T* row = static_cast<const T*>(q.logits) + (on ? token : 0) * q.row_stride;
+  const int E = q.experts, K = q.top_k;
+  const float ninf = -__builtin_inff();
+  const T* row = static_cast<const T*>(q.logits) + (on ? token : (int64_t)q.tokens - 1) * q.row_stride;
+  int32_t* mine = chosen[slot];
 
-  // scores of the choice
-  float top = -__builtin_inff();
-  for (int e = l; e < E; e += L) {
-    const float x = Elem<T>::load(row, e);
-    if (live(x)) top = fmaxf(top, x);
-  }
-  top = lanes_max<L>(top);
-  auto share = [&](float x) { return x == top ? 1.0 : exp((double)x - (double)top); };
-  double z = 1.0;
-  const bool whole = !q.sigmoid && (q.bias || !q.renormalize);
-  if (whole) {
-    z = 0.0;
-    for (int e = l; e < E; e += L) {
-      const float x = Elem<T>::load(row, e);
-      if (live(x)) z += share(x);
+  float x[EPL];
+  if (q.vector) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e0 = (v * L + l) * V;
+      float y[V];
+      uint4 raw{0, 0, 0, 0};
+      if (e0 < E) raw = *reinterpret_cast<const uint4*>(row + e0);
+      Elem<T>::unpack(raw, y);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[v * V + i] = (e0 < E && live(y[i])) ? y[i] : ninf;
     }
-    z = lanes_sum<L>(z);
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = (v * L + l) * V + i;
+        const float y = e < E ? Elem<T>::load(row, e) : ninf;
+        x[v * V + i] = live(y) ? y : ninf;
+      }
   }
-  // without a bias the order is that of the logits
-  auto score = [&](float x) { return q.sigmoid ? sigmoid64((double)x) : share(x) / z; };
-  for (int e = l; e < E; e += L) {
-    const float x = Elem<T>::load(row, e);
-    double v = ninf;
-    if (live(x)) v = q.bias ? score(x) + (double)q.bias[e] : (double)x;
-    c[e] = v;
-  }
-  __syncthreads();
 
-  if (q.groups > 1) {
-    const int size = E / q.groups;
-    for (int g = l; g < q.groups; g += L) {
-      double a = ninf, b = ninf;
-      for (int i = 0; i < size; ++i) {
-        const double v = c[g * size + i];
-        if (v > a) {
-          b = a;
-          a = v;
-        } else if (v > b) {
-          b = v;
+  Score64 score;
+  score.sigmoid = q.sigmoid;
+  score.inv_z = 1.0;
+  float top = ninf;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) top = fmaxf(top, x[i]);
+  top = fold_maxf<L>(top);
+  score.top = top;
+  if (!q.sigmoid && (!q.renormalize || q.bias)) {
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) z += live(x[i]) ? score.share(x[i]) : 0.0;
+    z = lanes_sum<L>(z);
+    score.inv_z = z > 0.0 ? 1.0 / z : 0.0;
+  }
+
+  // 32-bit scores, how far two of them may be off against each other, and
+  // whether that bound does not hold
+  float c[EPL];
+  float eps = 0.0f;
+  bool hard = false;
+  if (q.bias) {
+    const float log2e = 1.44269504f;
+    float scale = (float)score.inv_z, best;
+    if (q.sigmoid) {
+      best = 1.0f / (1.0f + __builtin_amdgcn_exp2f(-top * log2e));
+      // below, the exponential's own error would no longer be small beside
+      // the largest score
+      hard = top < -16.0f;
+    } else {
+      best = scale;
+      hard = !(top < __builtin_inff());
+    }
+    // A sigmoid is off by at most (|x| + 4) 2^-24 of itself (the product with
+    // log2(e), one unit each of v_exp_f32 and v_rcp_f32, two sums) while |x|
+    // <= 16, and beyond by less than that of the largest; a softmax share by
+    // (1.5 |x - top| + 4) 2^-24 of itself.  Two of
+    // either differ by less than 2^-17 of the largest.  Adding the bias costs
+    // 2^-24 of the result, the bits that the key gives up 2^-18, each of two.
+    eps = best * 0x1p-17f;
+    float widest = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e0 = (v * L + l) * V;
+      float b[V];
+      if (q.vector_bias) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const f4 y = *reinterpret_cast<const f4*>(q.bias + min(e0 + i, E - 4));
+#pragma unroll
+          for (int o = 0; o < 4; ++o) b[i + o] = y[o];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = q.bias[min(e0 + i, E - 1)];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = v * V + i;
+        const float s = q.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[j] * log2e))
+                                  : __builtin_amdgcn_exp2f((x[j] - top) * log2e) * scale;
+        const float sum = s + b[i];
+        const bool in = live(x[j]) && sum > ninf;
+        c[j] = in ? sum : ninf;
+        widest = fmaxf(widest, in ? __builtin_fabsf(sum) : 0.0f);
+      }
+    }
+    eps += fold_maxf<L>(widest) * 0x1p-17f;
+    hard = hard || !(eps < 1e30f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = x[i];
+  }
+
+  uint32_t keep = 0xFFFFFFFFu;  // the groups that stay
+  bool unsure = hard || (!q.bias && q.top2);  // (sums of two logits are no scores)
+  if (q.groups > 1 && !unsure) {
+    float* cc = reinterpret_cast<float*>(lds + (int64_t)slot * E);
+    float* gs = reinterpret_cast<float*>(group_score[slot]);
+    const int size = q.group_size;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = (v * L + l) * V + i;
+        if (e < E) cc[e] = c[v * V + i];
+      }
+    wave_sync();
+    // `split` neighbouring lanes a group, each over every split-th part of it
+    const int split = 1 << q.group_lanes, g = l >> q.group_lanes, part = l & (split - 1);
+    float a = ninf, b = ninf;
+    if (g < q.groups) {
+      const float* own_c = cc + g * size;
+      if (size % 4 == 0) {
+        for (int n = part * 4; n < size; n += split * 4) {
+          const f4 y = *reinterpret_cast<const f4*>(own_c + n);
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {
+            b = fmaxf(b, fminf(a, y[o]));
+            a = fmaxf(a, y[o]);
+          }
+        }
+      } else {
+        for (int n = part; n < size; n += split) {
+          const float y = own_c[n];
+          b = fmaxf(b, fminf(a, y));
+          a = fmaxf(a, y);
         }
       }
-      double v = a;
-      if (q.top2 && a > ninf) {
-        v = q.bias ? a : score((float)a);
-        if (b > ninf) v += q.bias ? b : score((float)b);
-      }
-      group_score[slot][g] = v;
     }
-    __syncthreads();
-    for (int g = l; g < q.groups; g += L) {
-      const double own = group_score[slot][g];
+    for (int d = 1; d < split; d <<= 1) {
+      const float oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
+      b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+      a = fmaxf(a, oa);
+    }
+    if (g < q.groups && part == 0) gs[g] = (q.top2 && live(b)) ? a + b : a;
+    wave_sync();
+    const float own = l < q.groups ? gs[l] : ninf;
+    bool stay = false;
+    if (l < q.groups) {
       int better = 0;
       for (int h = 0; h < q.groups; ++h) {
-        const double o = group_score[slot][h];
-        better += (o > own || (o == own && h < g)) ? 1 : 0;
+        const float o = gs[h];
+        better += (o > own || (o == own && h < l)) ? 1 : 0;
       }
-      if (better >= q.topk_groups)
-        for (int i = 0; i < size; ++i) c[g * size + i] = ninf;
+      stay = better < q.topk_groups;
     }
-    __syncthreads();
+    const float last = -fold_maxf<L>(stay && live(own) ? -own : ninf);
+    const float next = fold_maxf<L>(l < q.groups && !stay ? own : ninf);
+    unsure = q.bias && live(next) && last - next <= 2.0f * eps;
+    const uint64_t all = __ballot(stay);
+    keep = (uint32_t)(all >> ((threadIdx.x & 63) / L * L)) & 0xFFFFu;
+    wave_sync();
+  }
+  if (q.groups > 1 && unsure)
+    keep = groups64<T, L, EPL>(q, x, score, l, lds + (int64_t)slot * E, group_score[slot]);
+
+  // Keys: a 16-bit logit's 19 leading bits (all a bfloat16 or float16 has) and
+  // the expert's number; under a bias 27 bits and the score's place in the
+  // lane; else 31 bits.
+  uint32_t key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = (i / V * L + l) * V + i % V;
+    uint32_t k = fkey(c[i]) >> 1;
+    if (q.bias) k = (k & ~15u) | (uint32_t)(EPL - 1 - i);
+    else if (NARROW) k = (k >> 12) << 10 | (uint32_t)(1023 - e);
+    bool in = live(c[i]);
+    if (q.groups > 1) in = in && ((keep >> group_of(q, e)) & 1u);
+    key[i] = in ? k : 0u;
   }
 
-  for (int j = 0; j < q.top_k; ++j) {
-    double best = ninf;
-    int at = 0x7FFFFFFF;
-    for (int e = l; e < E; e += L)
-      if (c[e] > best) {
-        best = c[e];
-        at = e;
-      }
-    const double all = lanes_max<L>(best);
-    at = lanes_min<L>(best == all && all > ninf ? at : 0x7FFFFFFF);
-    if (l == 0) {
-      chosen[slot][j] = at == 0x7FFFFFFF ? -1 : at;
-      if (at != 0x7FFFFFFF) c[at] = ninf;
+  // one more than asked for, to see that the last one stands clear
+  unsure = false;
+  uint32_t last = 0x80000000u;  // above every key
+  uint32_t lowest = 0x80000000u;
+  int taken = 0;
+  float before = 0.0f;
+  for (int j = 0; j <= K; ++j) {
+    uint32_t own = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) own = max(own, key[i] - last);
+    const uint32_t d = fold_max<L>(own);
+    const uint32_t now = last + d;
+    const bool any = d >= 0x80000000u && now > 0u;
+    if (q.bias) {
+      const float f = from_key((now & ~15u) << 1);
+      unsure = unsure || (any && j > 0 && before - f <= eps);
+      before = f;
     }
-    __syncthreads();
+    last = any ? now : 0u;
+    if (j == K) break;
+    if (!any) {
+      if (l == 0) mine[j] = -1;
+      continue;
+    }
+    lowest = last;
+    ++taken;
+    if (NARROW && !q.bias) {
+      if (l == 0) mine[j] = 1023 - (int)(now & 1023u);
+    } else if (own == d) {  // this lane's; two lanes with one key are found below
+      int i = EPL - 1 - (int)(now & 15u);
+      if (!q.bias) {
+        i = 0;
+#pragma unroll
+        for (int o = 1; o < EPL; ++o) i = key[o] == last ? o : i;
+      }
+      mine[j] = (i / V * L + l) * V + i % V;
+    }
   }
+  if (q.bias || !NARROW) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) n += key[i] >= lowest ? 1u : 0u;
+    unsure = unsure || fold_sum<L>(n) != (uint32_t)taken;
+  }
+  wave_sync();
 
-  // weights of the chosen
+  if (unsure || hard) {
+    // Every expert whose 32-bit score is within eps of the last one taken:
+    // one a lane, ranked by 64-bit scores.  More than kNear, or scores too
+    // far down for eps to hold: all of them in 64 bits.
+    int n = 0;
+    int32_t* near = reinterpret_cast<int32_t*>(group_score[slot]);
+    if (!hard) {
+      const float thr = taken ? (q.bias ? from_key((lowest & ~15u) << 1) - eps : from_key(lowest << 1))
+                              : __builtin_inff();
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const bool in = key[i] > 0u && (c[i] >= thr || key[i] >= lowest);
+        const uint64_t all = __ballot(in) >> ((threadIdx.x & 63) / L * L);
+        const uint64_t m = L == 64 ? all : all & ((1ull << (L & 63)) - 1);
+        const int at = n + __popcll(m & ((1ull << l) - 1));
+        if (in && at < kNear) near[at] = (i / V * L + l) * V + i % V;
+        n += __popcll(m);
+      }
+      wave_sync();
+    }
+    if (hard || n > kNear) {
+      choose64<T, L, EPL>(q, x, score, l, keep, mine);
+    } else {
+      const int e = l < n ? near[l] : 0x7FFFFFFF;
+      double d = -__builtin_inf();
+      if (l < n) {
+        const float v = Elem<T>::load(row, e);
+        d = q.bias ? score(v) + (double)q.bias[e] : (double)v;
+      }
+      int rank = 0;
+      for (int o = 0; o < n; ++o) {
+        const int from = (int)(threadIdx.x & 63) / L * L + o;
+        const double y = __shfl(d, from);
+        const int f = __shfl(e, from);
+        rank += (y > d || (y == d && f < e)) ? 1 : 0;
+      }
+      if (l < n && rank < K) mine[rank] = e;
+      for (int j = n + l; j < K; j += L) mine[j] = -1;
+    }
+  }
+  wave_sync();
+
+  // the weights, in 64 bits
   double sum = 0.0;
-  for (int j = l; j < q.top_k; j += L) {
-    const int e = chosen[slot][j];
-    if (e >= 0) {
-      const float x = Elem<T>::load(row, e);
-      sum += q.sigmoid ? sigmoid64((double)x) : share(x);
-    }
+  for (int j = l; j < K; j += L) {
+    const int e = mine[j];
+    if (e >= 0) sum += score(Elem<T>::load(row, e));
   }
-  sum = lanes_sum<L>(sum);
-  const double over = q.renormalize ? sum : (q.sigmoid ? 1.0 : z);
+  if (q.renormalize) sum = lanes_sum<L>(sum);
   if (on)
-    for (int j = l; j < q.top_k; j += L) {
-      const int e = chosen[slot][j];
+    for (int j = l; j < K; j += L) {
+      const int e = mine[j];
       double w = 0.0;
-      if (e >= 0 && over > 0.0) {
-        const float x = Elem<T>::load(row, e);
-        w = (q.sigmoid ? sigmoid64((double)x) : share(x)) / over * (double)q.scale;
+      if (e >= 0) {
+        w = score(Elem<T>::load(row, e));
+        if (q.renormalize) w = sum > 0.0 ? w / sum : 0.0;
+        w *= (double)q.scale;
       }
-      q.indices[token * q.top_k + j] = e;
-      q.weights[token * q.top_k + j] = (float)w;
+      q.indices[token * K + j] = e;
+      q.weights[token * K + j] = (float)w;
     }
 }
 
@@ -297,19 +681,36 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
   }
 }
 
-#define ERT_ROUTE_PTR(NAME)                                                              \
-  const void* NAME##_ptr(int dtype, int lanes) {                                         \
-    switch (dtype * 2 + (lanes == 64 ? 1 : 0)) {                                         \
-      case 0: return reinterpret_cast<const void*>(&NAME<float, 16>);                    \
-      case 1: return reinterpret_cast<const void*>(&NAME<float, 64>);                    \
-      case 2: return reinterpret_cast<const void*>(&NAME<__hip_bfloat16, 16>);           \
-      case 3: return reinterpret_cast<const void*>(&NAME<__hip_bfloat16, 64>);           \
-      case 4: return reinterpret_cast<const void*>(&NAME<__half, 16>);                   \
-      case 5: return reinterpret_cast<const void*>(&NAME<__half, 64>);                   \
-      default: return nullptr;                                                           \
-    }                                                                                    \
+const void* route_kernel_ptr(int dtype, int lanes, int per_lane) {
+#define ERT_ROUTE(T, L, N) \
+  if (lanes == L && per_lane == N) return reinterpret_cast<const void*>(&route_kernel<T, L, N>)
+  if (dtype == 0) {
+    ERT_ROUTE(float, 16, 4);
+    ERT_ROUTE(float, 16, 8);
+    ERT_ROUTE(float, 16, 16);
+    ERT_ROUTE(float, 64, 16);
+  } else if (dtype == 1) {
+    ERT_ROUTE(__hip_bfloat16, 16, 8);
+    ERT_ROUTE(__hip_bfloat16, 16, 16);
+    ERT_ROUTE(__hip_bfloat16, 64, 16);
+  } else {
+    ERT_ROUTE(__half, 16, 8);
+    ERT_ROUTE(__half, 16, 16);
+    ERT_ROUTE(__half, 64, 16);
   }
-ERT_ROUTE_PTR(route_kernel)
-ERT_ROUTE_PTR(route_grad_kernel)
+  return nullptr;
+}
+
+const void* route_grad_kernel_ptr(int dtype, int lanes) {
+  switch (dtype * 2 + (lanes == 64 ? 1 : 0)) {
+    case 0: return reinterpret_cast<const void*>(&route_grad_kernel<float, 16>);
+    case 1: return reinterpret_cast<const void*>(&route_grad_kernel<float, 64>);
+    case 2: return reinterpret_cast<const void*>(&route_grad_kernel<__hip_bfloat16, 16>);
+    case 3: return reinterpret_cast<const void*>(&route_grad_kernel<__hip_bfloat16, 64>);
+    case 4: return reinterpret_cast<const void*>(&route_grad_kernel<__half, 16>);
+    case 5: return reinterpret_cast<const void*>(&route_grad_kernel<__half, 64>);
+    default: return nullptr;
+  }
+}
 
 }  // namespace ert

@@ -69,6 +69,44 @@ struct SampleParams {
   int32_t whole_row;      // every row from memory
 };
 
+// ---- exponentials in 64 bits ---------------------------------------------------
+
+constexpr double kLog2e = 1.4426950408889634;
+
+// 2^f on [-1/2, 1/2]: interpolation at the ten Chebyshev nodes, relative
+// error at most 2^-45.6.  The coefficients sit in scalar registers behind an
+// empty asm: as known constants each would be moved into a vector register
+// pair ahead of every multiply-add, two instructions to one.
+struct Exp2Poly {
+  double k0, k1, k2, k3, k4, k5, k6, k7, k8, k9;
+  __device__ __forceinline__ Exp2Poly()
+      : k0(0x1.000000000003dp+0), k1(0x1.62e42fefa39f7p-1), k2(0x1.ebfbdff8149f2p-3),
+        k3(0x1.c6b08d7044119p-5), k4(0x1.3b2ab72b175eep-7), k5(0x1.5d87fe908f88ap-10),
+        k6(0x1.43088e257f341p-13), k7(0x1.ffcb76789860fp-17), k8(0x1.63ef969a64d3cp-20),
+        k9(0x1.b6571de2f2351p-24) {
+    asm("" : "+s"(k0), "+s"(k1), "+s"(k2), "+s"(k3), "+s"(k4));
+    asm("" : "+s"(k5), "+s"(k6), "+s"(k7), "+s"(k8), "+s"(k9));
+  }
+  __device__ __forceinline__ double operator()(double f) const {
+    double p = __builtin_fma(f, k9, k8);
+    p = __builtin_fma(p, f, k7);
+    p = __builtin_fma(p, f, k6);
+    p = __builtin_fma(p, f, k5);
+    p = __builtin_fma(p, f, k4);
+    p = __builtin_fma(p, f, k3);
+    p = __builtin_fma(p, f, k2);
+    p = __builtin_fma(p, f, k1);
+    return __builtin_fma(p, f, k0);
+  }
+};
+
+// 2^s for s <= 0; 0 for NaN.
+__device__ __forceinline__ double exp2_64(double s, const Exp2Poly& poly) {
+  s = __builtin_fmax(s, -1100.0);
+  const double n = __builtin_rint(s);
+  return __builtin_ldexp(poly(s - n), (int)n);
+}
+
 // ---- 16-byte score groups ----------------------------------------------------
 
 template <class T>
@@ -147,6 +185,11 @@ struct RouteParams {
   int32_t sigmoid;      // else softmax
   const float* bias;    // null: none
   int32_t groups;
+  int32_t group_size;
+  uint32_t group_magic;  // e / group_size = the high word of e * group_magic
+  int32_t group_lanes;   // log2 of the lanes that look at one group together
+  int32_t vector;        // every row starts on 16 bytes and holds whole groups
+  int32_t vector_bias;   // so does the bias, with groups of four
   int32_t topk_groups;
   int32_t top2;         // a group's score: its two largest summed, else its largest
   int32_t renormalize;

@@ -14,7 +14,7 @@ namespace ert {
 const void* sample_segment_kernel_ptr(int dtype);
 const void* sample_row_kernel_ptr(int dtype);
 const void* sample_wide_kernel_ptr(int dtype);
-const void* route_kernel_ptr(int dtype, int lanes);
+const void* route_kernel_ptr(int dtype, int lanes, int per_lane);
 const void* route_grad_kernel_ptr(int dtype, int lanes);
 const void* block_table_kernel_ptr();
 const void* topk_slots_kernel_ptr();
@@ -157,15 +157,25 @@ int topk_route(const void* logits, int32_t dtype, int64_t row_stride, int32_t nu
   p.sigmoid = (flags & TOPK_ROUTE_SIGMOID) ? 1 : 0;
   p.bias = bias;
   p.groups = num_groups;
+  p.group_size = num_experts / num_groups;
+  // exact for e < 1024 with sizes of 2 and more: the quotient's error, below
+  // e / 2^32, is less than the 1 / size to the next whole number
+  p.group_magic = p.group_size > 1 ? (uint32_t)((((uint64_t)1 << 32) + p.group_size - 1) / p.group_size) : 0;
   p.topk_groups = topk_groups;
   p.top2 = (flags & TOPK_ROUTE_TOP2) ? 1 : 0;
   p.renormalize = (flags & TOPK_ROUTE_RENORMALIZE) ? 1 : 0;
   p.scale = scale;
   p.indices = indices;
   p.weights = weights;
+  const int vec = dtype == TOPK_DT_F32 ? 4 : 8;
+  p.vector = at(logits, 16) && (num_tokens == 1 || row_stride % vec == 0) && num_experts % vec == 0;
+  p.vector_bias = bias && at(bias, 16) && num_experts % 4 == 0;
   const int lanes = num_experts <= 256 ? 16 : 64;
+  while ((num_groups << (p.group_lanes + 1)) <= lanes) ++p.group_lanes;
+  int per_lane = vec;
+  while (per_lane * lanes < num_experts || (lanes == 64 && per_lane < 16)) per_lane *= 2;
   const int per = 256 / lanes;
-  return launch(route_kernel_ptr(dtype, lanes), ((int64_t)num_tokens + per - 1) / per, 256, &p,
+  return launch(route_kernel_ptr(dtype, lanes, per_lane), ((int64_t)num_tokens + per - 1) / per, 256, &p,
                 (size_t)per * num_experts * sizeof(double), stream);
 }
 

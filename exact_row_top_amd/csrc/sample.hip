@@ -26,36 +26,8 @@ namespace ert {
 namespace {
 
 constexpr uint64_t kOne = 1ull << 43;   // the weight of a row's largest score
-constexpr double kLog2e = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
 constexpr double kTmax = 44.0;          // weights of 2^-44 and less are zero
-
-// 2^f on [-1/2, 1/2]: interpolation at the ten Chebyshev nodes, relative
-// error at most 2^-45.6.  The coefficients sit in scalar registers behind an
-// empty asm: as known constants each would be moved into a vector register
-// pair ahead of every multiply-add, two instructions to one.
-struct Exp2Poly {
-  double k0, k1, k2, k3, k4, k5, k6, k7, k8, k9;
-  __device__ __forceinline__ Exp2Poly()
-      : k0(0x1.000000000003dp+0), k1(0x1.62e42fefa39f7p-1), k2(0x1.ebfbdff8149f2p-3),
-        k3(0x1.c6b08d7044119p-5), k4(0x1.3b2ab72b175eep-7), k5(0x1.5d87fe908f88ap-10),
-        k6(0x1.43088e257f341p-13), k7(0x1.ffcb76789860fp-17), k8(0x1.63ef969a64d3cp-20),
-        k9(0x1.b6571de2f2351p-24) {
-    asm("" : "+s"(k0), "+s"(k1), "+s"(k2), "+s"(k3), "+s"(k4));
-    asm("" : "+s"(k5), "+s"(k6), "+s"(k7), "+s"(k8), "+s"(k9));
-  }
-  __device__ __forceinline__ double operator()(double f) const {
-    double p = __builtin_fma(f, k9, k8);
-    p = __builtin_fma(p, f, k7);
-    p = __builtin_fma(p, f, k6);
-    p = __builtin_fma(p, f, k5);
-    p = __builtin_fma(p, f, k4);
-    p = __builtin_fma(p, f, k3);
-    p = __builtin_fma(p, f, k2);
-    p = __builtin_fma(p, f, k1);
-    return __builtin_fma(p, f, k0);
-  }
-};
 
 // The weights of a row's scores against m >= x.
 //
@@ -97,13 +69,6 @@ struct Weigher {
     return x == m ? kOne : s > -kTmax ? raw_of(s) - kRaw : 0ull;
   }
 };
-
-// 2^-t for t >= 0 (0 from t = 1000 on, and for NaN).
-__device__ __forceinline__ double exp2_neg(double t, const Exp2Poly& poly) {
-  if (!(t < 1000.0)) return 0.0;
-  const double n = __builtin_rint(t);
-  return __builtin_ldexp(poly(n - t), -(int)n);
-}
 
 // What a row asks for.
 struct RowAsk {
@@ -801,7 +766,7 @@ __device__ void draw_from_list(const ListSource& list, RowShared& sh, const Weig
 
 // 2^(best - m), in the row's units.
 __device__ __forceinline__ double below_best(float best, const Weigher& w) {
-  return best == w.m ? 1.0 : exp2_neg(-w.log2_of(best), w.poly);
+  return best == w.m ? 1.0 : exp2_64(w.log2_of(best), w.poly);
 }
 
 // ---------------------------------------------------------------------------
