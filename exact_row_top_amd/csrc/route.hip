@@ -30,20 +30,11 @@ namespace {
 constexpr int kRouteBlock = 256;
 constexpr int kNear = 16;  // experts that are ranked one a lane
 
-// Sums and maxima over the L lanes that share a token.
+// Sums and least values over the L lanes that share a token.
 template <int L, class V>
 __device__ __forceinline__ V lanes_sum(V v) {
 #pragma unroll
   for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-template <int L, class V>
-__device__ __forceinline__ V lanes_max(V v) {
-#pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) {
-    const V o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
   return v;
 }
 template <int L>
@@ -85,12 +76,6 @@ __device__ __forceinline__ float fold_maxf(float v) {
   }));
 }
 template <int L>
-__device__ __forceinline__ float fold_sumf(float v) {
-  return __uint_as_float(lanes_fold<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
-template <int L>
 __device__ __forceinline__ uint32_t fold_sum(uint32_t v) {
   return lanes_fold<L>(v, [](uint32_t a, uint32_t b) { return a + b; });
 }
@@ -104,11 +89,6 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 __device__ __forceinline__ bool live(float x) { return x > -__builtin_inff(); }
-
-__device__ __forceinline__ double sigmoid64(double x) {
-  const double e = exp(-__builtin_fabs(x));
-  return (x < 0.0 ? e : 1.0) / (1.0 + e);
-}
 
 // The group of expert e < 1024.
 __device__ __forceinline__ uint32_t group_of(const RouteParams& q, int e) {
@@ -581,9 +561,12 @@ __device__ __forceinline__ void store_as<__half>(__half* p, float v) { *p = __fl
 
 }  // namespace
 
-template <class T, int L>
+// A token's row of changes is put together in LDS: zeros, the chosen
+// experts' changes (at most K), and out in 16-byte pieces.
+template <class T, int L, int EPL>
 __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGradParams q) {
   constexpr int TOKENS = kRouteBlock / L;
+  constexpr int V = Elem<T>::kVec;
   extern __shared__ float row_lds[];
   __shared__ float change[TOKENS][kMaxRouteK];
   const int l = threadIdx.x % L;
@@ -591,49 +574,65 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
   const int64_t token = (int64_t)blockIdx.x * TOKENS + slot;
   const bool on = token < q.tokens;
   const int E = q.experts, K = q.top_k;
-  float* d = row_lds + (int64_t)slot * E;
-  const int64_t tk = on ? token : 0;
+  const float ninf = -__builtin_inff();
+  float* d = row_lds + (int64_t)slot * (L * EPL);
+  const int64_t tk = on ? token : (int64_t)q.tokens - 1;
   const T* row = static_cast<const T*>(q.logits) + tk * q.row_stride;
   const int32_t* idx = q.indices + tk * K;
   const float* grad = q.grad_weights + tk * K;
 
-  for (int e = l; e < E; e += L) d[e] = 0.0f;
-  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < EPL; i += 4) *reinterpret_cast<f4*>(d + (i / 4 * L + l) * 4) = f4{0, 0, 0, 0};
 
   const bool whole = !q.sigmoid && !q.renormalize;
-  float top = -__builtin_inff();
-  double z = 1.0;
+  Score64 score;
+  score.sigmoid = q.sigmoid;
+  score.inv_z = 1.0;
+  float top = ninf;
+  float x[EPL];
   if (whole) {
-    for (int e = l; e < E; e += L) {
-      const float x = Elem<T>::load(row, e);
-      if (live(x)) top = fmaxf(top, x);
+#pragma unroll
+    for (int v = 0; v < EPL / V; ++v) {
+      const int e0 = (v * L + l) * V;
+      float y[V];
+      if (q.vector) {
+        uint4 raw{0, 0, 0, 0};
+        if (e0 < E) raw = *reinterpret_cast<const uint4*>(row + e0);
+        Elem<T>::unpack(raw, y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = e0 + i < E ? Elem<T>::load(row, e0 + i) : ninf;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        x[v * V + i] = (e0 + i < E && live(y[i])) ? y[i] : ninf;
+        top = fmaxf(top, x[v * V + i]);
+      }
     }
   } else if (!q.sigmoid) {
     for (int j = l; j < K; j += L) {
       const int e = idx[j];
       if ((unsigned)e < (unsigned)E) {
-        const float x = Elem<T>::load(row, e);
-        if (live(x)) top = fmaxf(top, x);
+        const float y = Elem<T>::load(row, e);
+        if (live(y)) top = fmaxf(top, y);
       }
     }
   }
-  top = lanes_max<L>(top);
-  auto share = [&](float x) { return x == top ? 1.0 : exp((double)x - (double)top); };
+  score.top = fold_maxf<L>(top);
   if (whole) {
-    z = 0.0;
-    for (int e = l; e < E; e += L) {
-      const float x = Elem<T>::load(row, e);
-      if (live(x)) z += share(x);
-    }
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) z += live(x[i]) ? score.share(x[i]) : 0.0;
     z = lanes_sum<L>(z);
+    score.inv_z = z > 0.0 ? 1.0 / z : 0.0;
   }
-  auto score = [&](float x) { return !live(x) ? 0.0 : q.sigmoid ? sigmoid64((double)x) : share(x) / z; };
 
   double sum = 0.0, dot = 0.0;
   for (int j = l; j < K; j += L) {
     const int e = idx[j];
     if ((unsigned)e < (unsigned)E) {
-      const double s = score(Elem<T>::load(row, e));
+      const float y = Elem<T>::load(row, e);
+      const double s = live(y) ? score(y) : 0.0;
       sum += s;
       dot += (double)grad[j] * s;
     }
@@ -646,16 +645,17 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
   const double mean = q.renormalize ? dot * inv : 0.0;
   for (int j = l; j < K; j += L) {
     const int e = idx[j];
-    change[slot][j] = 0.0f;
+    double v = 0.0;
     if ((unsigned)e < (unsigned)E) {
-      const float x = Elem<T>::load(row, e);
-      const double s = score(x);
-      double v = ((double)grad[j] - mean) * inv * scale * s;
-      if (q.sigmoid) v *= live(x) ? sigmoid64(-(double)x) : 0.0;
-      change[slot][j] = (float)v;
+      const float y = Elem<T>::load(row, e);
+      if (live(y)) {
+        v = ((double)grad[j] - mean) * inv * scale * score(y);
+        if (q.sigmoid) v *= score(-y);
+      }
     }
+    change[slot][j] = (float)v;
   }
-  __syncthreads();
+  wave_sync();
   // an expert that a caller names twice gets both changes, added in order by
   // the first slot that names it
   for (int j = l; j < K; j += L) {
@@ -670,47 +670,60 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
     }
     if (first) d[e] = v;
   }
-  __syncthreads();
-  if (on) {
-    T* out = static_cast<T*>(q.grad_logits) + token * q.grad_stride;
-    for (int e = l; e < E; e += L) {
-      float v = d[e];
-      if (whole) v -= (float)(score(Elem<T>::load(row, e)) * dot * scale);
-      store_as(out + e, v);
+  wave_sync();
+  if (!on) return;
+  T* out = static_cast<T*>(q.grad_logits) + token * q.grad_stride;
+  const double pull = dot * scale;
+#pragma unroll
+  for (int v = 0; v < EPL / V; ++v) {
+    const int e0 = (v * L + l) * V;
+    if (e0 >= E) continue;
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f4 part = *reinterpret_cast<const f4*>(d + e0 + i);
+#pragma unroll
+      for (int o = 0; o < 4; ++o) y[i + o] = part[o];
+    }
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        y[i] -= live(x[v * V + i]) ? (float)(score(x[v * V + i]) * pull) : 0.0f;
+    }
+    if (q.vector) {
+      T packed[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) store_as(packed + i, y[i]);
+      *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(packed);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < E) store_as(out + e0 + i, y[i]);
     }
   }
 }
 
-const void* route_kernel_ptr(int dtype, int lanes, int per_lane) {
-#define ERT_ROUTE(T, L, N) \
-  if (lanes == L && per_lane == N) return reinterpret_cast<const void*>(&route_kernel<T, L, N>)
-  if (dtype == 0) {
-    ERT_ROUTE(float, 16, 4);
-    ERT_ROUTE(float, 16, 8);
-    ERT_ROUTE(float, 16, 16);
-    ERT_ROUTE(float, 64, 16);
-  } else if (dtype == 1) {
-    ERT_ROUTE(__hip_bfloat16, 16, 8);
-    ERT_ROUTE(__hip_bfloat16, 16, 16);
-    ERT_ROUTE(__hip_bfloat16, 64, 16);
-  } else {
-    ERT_ROUTE(__half, 16, 8);
-    ERT_ROUTE(__half, 16, 16);
-    ERT_ROUTE(__half, 64, 16);
+#define ERT_ROUTE(NAME, T, L, N) \
+  if (lanes == L && per_lane == N) return reinterpret_cast<const void*>(&NAME<T, L, N>)
+#define ERT_ROUTE_PTR(NAME)                                              \
+  const void* NAME##_ptr(int dtype, int lanes, int per_lane) {           \
+    if (dtype == 0) {                                                    \
+      ERT_ROUTE(NAME, float, 16, 4);                                     \
+      ERT_ROUTE(NAME, float, 16, 8);                                     \
+      ERT_ROUTE(NAME, float, 16, 16);                                    \
+      ERT_ROUTE(NAME, float, 64, 16);                                    \
+    } else if (dtype == 1) {                                             \
+      ERT_ROUTE(NAME, __hip_bfloat16, 16, 8);                            \
+      ERT_ROUTE(NAME, __hip_bfloat16, 16, 16);                           \
+      ERT_ROUTE(NAME, __hip_bfloat16, 64, 16);                           \
+    } else {                                                             \
+      ERT_ROUTE(NAME, __half, 16, 8);                                    \
+      ERT_ROUTE(NAME, __half, 16, 16);                                   \
+      ERT_ROUTE(NAME, __half, 64, 16);                                   \
+    }                                                                    \
+    return nullptr;                                                      \
   }
-  return nullptr;
-}
-
-const void* route_grad_kernel_ptr(int dtype, int lanes) {
-  switch (dtype * 2 + (lanes == 64 ? 1 : 0)) {
-    case 0: return reinterpret_cast<const void*>(&route_grad_kernel<float, 16>);
-    case 1: return reinterpret_cast<const void*>(&route_grad_kernel<float, 64>);
-    case 2: return reinterpret_cast<const void*>(&route_grad_kernel<__hip_bfloat16, 16>);
-    case 3: return reinterpret_cast<const void*>(&route_grad_kernel<__hip_bfloat16, 64>);
-    case 4: return reinterpret_cast<const void*>(&route_grad_kernel<__half, 16>);
-    case 5: return reinterpret_cast<const void*>(&route_grad_kernel<__half, 64>);
-    default: return nullptr;
-  }
-}
+ERT_ROUTE_PTR(route_kernel)
+ERT_ROUTE_PTR(route_grad_kernel)
 
 }  // namespace ert

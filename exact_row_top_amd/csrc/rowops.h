@@ -211,6 +211,7 @@ struct RouteGradParams {
   const float* grad_weights;
   void* grad_logits;
   int64_t grad_stride;
+  int32_t vector;       // rows of both start on 16 bytes and hold whole groups
 };
 
 // ---- block tables and slots --------------------------------------------------

@@ -15,7 +15,7 @@ const void* sample_segment_kernel_ptr(int dtype);
 const void* sample_row_kernel_ptr(int dtype);
 const void* sample_wide_kernel_ptr(int dtype);
 const void* route_kernel_ptr(int dtype, int lanes, int per_lane);
-const void* route_grad_kernel_ptr(int dtype, int lanes);
+const void* route_grad_kernel_ptr(int dtype, int lanes, int per_lane);
 const void* block_table_kernel_ptr();
 const void* topk_slots_kernel_ptr();
 }  // namespace ert
@@ -65,6 +65,17 @@ int64_t wide_wgs_of(int64_t segments) { return (segments + kWideSegs - 1) / kWid
 bool route_shape_ok(int32_t tokens, int32_t experts, int32_t top_k) {
   return tokens >= 0 && experts >= 1 && experts <= kMaxExperts && top_k >= 1 && top_k <= kMaxRouteK &&
          top_k <= experts;
+}
+
+// How a token's experts are spread: 16 lanes up to 256 experts (four tokens a
+// wave share each step of the selection), a whole wave above.
+struct Spread {
+  int lanes, per_lane;
+};
+Spread route_spread(int experts, int vec) {
+  Spread s{experts <= 256 ? 16 : 64, vec};
+  while (s.per_lane * s.lanes < experts || (s.lanes == 64 && s.per_lane < 16)) s.per_lane *= 2;
+  return s;
 }
 
 }  // namespace
@@ -170,12 +181,10 @@ int topk_route(const void* logits, int32_t dtype, int64_t row_stride, int32_t nu
   const int vec = dtype == TOPK_DT_F32 ? 4 : 8;
   p.vector = at(logits, 16) && (num_tokens == 1 || row_stride % vec == 0) && num_experts % vec == 0;
   p.vector_bias = bias && at(bias, 16) && num_experts % 4 == 0;
-  const int lanes = num_experts <= 256 ? 16 : 64;
-  while ((num_groups << (p.group_lanes + 1)) <= lanes) ++p.group_lanes;
-  int per_lane = vec;
-  while (per_lane * lanes < num_experts || (lanes == 64 && per_lane < 16)) per_lane *= 2;
-  const int per = 256 / lanes;
-  return launch(route_kernel_ptr(dtype, lanes, per_lane), ((int64_t)num_tokens + per - 1) / per, 256, &p,
+  const Spread sp = route_spread(num_experts, vec);
+  while ((num_groups << (p.group_lanes + 1)) <= sp.lanes) ++p.group_lanes;
+  const int per = 256 / sp.lanes;
+  return launch(route_kernel_ptr(dtype, sp.lanes, sp.per_lane), ((int64_t)num_tokens + per - 1) / per, 256, &p,
                 (size_t)per * num_experts * sizeof(double), stream);
 }
 
@@ -208,10 +217,14 @@ int topk_route_backward(const void* logits, int32_t dtype, int64_t row_stride, i
   p.grad_weights = grad_weights;
   p.grad_logits = grad_logits;
   p.grad_stride = grad_row_stride;
-  const int lanes = num_experts <= 256 ? 16 : 64;
-  const int per = 256 / lanes;
-  return launch(route_grad_kernel_ptr(dtype, lanes), ((int64_t)num_tokens + per - 1) / per, 256, &p,
-                (size_t)per * num_experts * sizeof(float), stream);
+  const int vec = dtype == TOPK_DT_F32 ? 4 : 8;
+  p.vector = at(logits, 16) && at(grad_logits, 16) && num_experts % vec == 0 &&
+             (num_tokens == 1 || (row_stride % vec == 0 && grad_row_stride % vec == 0));
+  const Spread sp = route_spread(num_experts, vec);
+  const int per = 256 / sp.lanes;
+  return launch(route_grad_kernel_ptr(dtype, sp.lanes, sp.per_lane),
+                ((int64_t)num_tokens + per - 1) / per, 256, &p,
+                (size_t)256 * sp.per_lane * sizeof(float), stream);
 }
 
 int topk_block_tables(int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
