@@ -500,7 +500,8 @@ def __getattr__(name):
     # the row operators need torch, which this module imports only when called
     if name in _ROW_OPS:
         from . import row_ops
-        return getattr(row_ops, name)
+        globals().update({n: getattr(row_ops, n) for n in _ROW_OPS})
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

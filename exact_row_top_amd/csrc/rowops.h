@@ -217,6 +217,17 @@ struct RouteGradParams {
 // ---- block tables and slots --------------------------------------------------
 
 constexpr int kMaxRequests = 4096;
+constexpr int kSlotBlock = 256;
+constexpr int kSlotPart = 1024;    // entries of a row that a workgroup maps
+
+// Division by d of numbers below 2^31: a shift for powers of two (magic 0),
+// else the high word of the product with ceil(2^(31 + L) / d), L =
+// ceil(log2 d), shifted by L - 1: the rounding adds less than n 2^L / 2^(31 +
+// L) < 1 to n / d scaled by d, so the quotient is exact.
+struct Divisor {
+  uint32_t magic;
+  uint32_t shift;
+};
 
 struct TableParams {
   int32_t* tables;
@@ -229,6 +240,8 @@ struct TableParams {
   int64_t num_free;
   const int32_t* free_start;
   int32_t block_size;
+  Divisor by_block;
+  int32_t vector;       // the token arrays start on 16 bytes
   int64_t max_tokens;
   int32_t* token_starts;
   int32_t* token_requests;
@@ -249,6 +262,10 @@ struct SlotParams {
   const int32_t* row_requests;
   int32_t next_n;
   int32_t block_size;
+  Divisor by_block;
+  int32_t parts;        // workgroups of a row
+  int32_t vector;       // rows of both start on 16 bytes and hold whole groups of four
+  int32_t staged;       // the table goes through LDS
   void* slots;
   int32_t wide;
 };

@@ -16,7 +16,7 @@ const void* sample_row_kernel_ptr(int dtype);
 const void* sample_wide_kernel_ptr(int dtype);
 const void* route_kernel_ptr(int dtype, int lanes, int per_lane);
 const void* route_grad_kernel_ptr(int dtype, int lanes, int per_lane);
-const void* block_table_kernel_ptr();
+const void* block_table_kernel_ptr(int per_thread);
 const void* topk_slots_kernel_ptr();
 }  // namespace ert
 
@@ -65,6 +65,13 @@ int64_t wide_wgs_of(int64_t segments) { return (segments + kWideSegs - 1) / kWid
 bool route_shape_ok(int32_t tokens, int32_t experts, int32_t top_k) {
   return tokens >= 0 && experts >= 1 && experts <= kMaxExperts && top_k >= 1 && top_k <= kMaxRouteK &&
          top_k <= experts;
+}
+
+Divisor divisor(uint32_t d) {
+  uint32_t log = 0;
+  while (((uint64_t)1 << log) < d) ++log;
+  if (((uint64_t)1 << log) == d) return Divisor{0, log};
+  return Divisor{(uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), log - 1};
 }
 
 // How a token's experts are spread: 16 lanes up to 256 experts (four tokens a
@@ -267,9 +274,16 @@ int topk_block_tables(int32_t* block_tables, int64_t table_stride, int32_t max_b
   p.slots = slots;
   p.wide = slots_64;
   p.free_next = free_next;
-  int64_t grid = (max_tokens + 2047) / 2048;
-  grid = grid < 1 ? 1 : (grid > 2048 ? 2048 : grid);
-  return launch(block_table_kernel_ptr(), grid, 256, &p, (size_t)(2 * num_requests + 1) * 4, stream);
+  p.by_block = divisor((uint32_t)block_size);
+  p.vector = at(token_requests, 16) && at(positions, 16) && at(slots, 16);
+  // Four tokens a thread once 1024 workgroups of single ones are full; beyond
+  // 1024 workgroups another round costs less than another workgroup's sums
+  // over the requests.
+  const int per_thread = max_tokens > 1024 * kSlotBlock ? 4 : 1;
+  int64_t grid = (max_tokens + kSlotBlock * per_thread - 1) / (kSlotBlock * per_thread);
+  grid = grid < 1 ? 1 : (grid > 1024 ? 1024 : grid);
+  return launch(block_table_kernel_ptr(per_thread), grid, kSlotBlock, &p,
+                (size_t)(3 * num_requests + 1) * 4, stream);
 }
 
 int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_t* block_tables,
@@ -301,7 +315,14 @@ int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_
   p.block_size = block_size;
   p.slots = slots;
   p.wide = slots_64;
-  return launch(topk_slots_kernel_ptr(), (num_rows * k + 255) / 256, 256, &p, 0, stream);
+  p.by_block = divisor((uint32_t)block_size);
+  p.vector = k % 4 == 0 && at(indices, 16) && at(slots, 16);
+  p.parts = (k + kSlotPart - 1) / kSlotPart;
+  // a part reads no more table entries than it maps positions; with few
+  // workgroups the copy's latency is all that would be added
+  p.staged = max_blocks <= kSlotPart && max_blocks <= k && num_rows * p.parts >= 1024;
+  return launch(topk_slots_kernel_ptr(), num_rows * p.parts, kSlotBlock, &p,
+                p.staged ? (size_t)max_blocks * 4 : 0, stream);
 }
 
 }  // extern "C"

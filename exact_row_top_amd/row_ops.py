@@ -122,7 +122,7 @@ class _On:
 def _elsewhere(t, name, stream):
     """A guard if the call has to leave the current device or stream."""
     _tensor(t, name)
-    if stream is not None or t.device.index != torch.cuda.current_device():
+    if stream is not None or t.device.index != torch._C._cuda_getDevice():
         return _On(t.device, stream)
     return None
 
@@ -336,12 +336,14 @@ def extend_block_tables(block_tables, kv_lens, new_tokens, free_blocks, free_sta
     max_tokens = _int32(max_tokens, "max_tokens")
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    dt, wide = _slot_dtype(slot_dtype)
-    starts = torch.empty(requests + 1, dtype=torch.int32, device=dev)
-    owner = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-    positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
-    slots = torch.empty(max_tokens, dtype=dt, device=dev)
-    free_next = torch.empty(1, dtype=torch.int32, device=dev)
+    _, wide = _slot_dtype(slot_dtype)
+    # one allocation, each token array on a 16-byte boundary of it
+    pad = -max_tokens % 4
+    room = [max_tokens, pad, max_tokens, pad, max_tokens << wide, 2 * pad, requests + 1, 1]
+    owner, _, positions, _, slots, _, starts, free_next = torch.empty(
+        sum(room), dtype=torch.int32, device=dev).split_with_sizes(room)
+    if wide:
+        slots = slots.view(torch.int64)
     _check(_lib().topk_block_tables(
         block_tables.data_ptr(), stride, width, requests, kv, new, free, num_free, start,
         _int32(block_size, "block_size"), max_tokens, starts.data_ptr(), owner.data_ptr(),
