@@ -11,7 +11,7 @@
 #include "rowops.h"
 
 namespace ert {
-const void* sample_segment_kernel_ptr(int dtype);
+const void* sample_segment_kernel_ptr(int dtype, bool cuts);
 const void* sample_row_kernel_ptr(int dtype);
 const void* sample_wide_kernel_ptr(int dtype);
 const void* route_kernel_ptr(int dtype, int lanes, int per_lane);
@@ -142,7 +142,7 @@ int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t v
   p.wide_wgs = (int32_t)wgs;
   p.row_wgs = (top_k || top_p) && !whole ? (int32_t)wgs : 1;
   p.whole_row = whole ? 1 : 0;
-  rc = launch(sample_segment_kernel_ptr(dtype), (waves + 3) / 4, 256, &p, 0, stream);
+  rc = launch(sample_segment_kernel_ptr(dtype, cuts || whole), (waves + 3) / 4, 256, &p, 0, stream);
   if (rc == TOPK_OK)
     rc = launch(sample_row_kernel_ptr(dtype), num_rows * p.row_wgs, kRowBlock, &p, 0, stream);
   if (rc == TOPK_OK && (cuts || whole))

@@ -177,7 +177,7 @@ __device__ __forceinline__ int wave_min(int v) {
 // barrier and no atomics.  All live scores at or above the floor are handed
 // on.
 // ---------------------------------------------------------------------------
-template <class T>
+template <class T, bool CUTS>
 __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams q) {
   constexpr int V = Elem<T>::kVec;
   constexpr int G = kSegment / (64 * V);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 #pragma unroll
     for (int e = 0; e < V; ++e) top = fmaxf(top, x[g][e]);
   float best = top, low = __builtin_inff();
-  if (ask.cuts() && !ask.greedy) {
+  if (CUTS && ask.cuts() && !ask.greedy) {
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
       rec.first = wave_min(first);
     } else {
       float floor = __builtin_inff();
-      if (ask.cuts()) {
+      if (CUTS && ask.cuts()) {
         // how many lane maxima the floor lies under: what a segment should
         // hold of a row's best k, with room for an uneven spread; 16 where
         // only the weights say how many are needed
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
         rec.floor = floor;
         rec.count = n <= kSegSlots ? n : -1;
       }
-      if (!ask.cut_k) {
+      if (!CUTS || !ask.cut_k) {
         if (best == __builtin_inff()) {
           uint32_t n = 0;
 #pragma unroll
@@ -271,7 +271,12 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 #pragma unroll
             for (int e = 0; e < V; ++e) n += x[g][e] == best ? 1u : 0u;
           rec.mass = wave_sum((uint64_t)n * kOne);
-        } else if (ask.cut_p) {
+        } else {
+          // Four scores at a time (the empty asm keeps the additions where
+          // they are): with all of them in flight, and added up at the end,
+          // the registers would leave room for three waves a SIMD, not
+          // eight.  (One loop for all rows: of two, the compiler shares the
+          // conversions, which then stay in registers across both.)
           uint64_t mass = 0, top_mass = 0;
           const Weigher w(best, ask.c);
 #pragma unroll
@@ -280,38 +285,21 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
             for (int e = 0; e < V; ++e) {
               const uint64_t v = w.raw(x[g][e]);
               mass += v;
-              top_mass += x[g][e] >= floor ? v : kRaw;
+              if (CUTS) top_mass += x[g][e] >= floor ? v : kRaw;
               if (e % 4 == 3) {
                 asm("" : "+v"(mass), "+v"(top_mass));
                 __builtin_amdgcn_sched_barrier(0);
               }
             }
           rec.mass = wave_sum(mass - (uint64_t)(G * V) * kRaw);
-          rec.upper = (float)wave_sum(top_mass - (uint64_t)(G * V) * kRaw) * 1.000001f;
-        } else {
-          // four scores at a time (the empty asm keeps the additions where
-          // they are): with all of them in flight, and added up at the end,
-          // the registers would leave room for three waves a SIMD
-          uint64_t mass = 0;
-          const Weigher w(best, ask.c);
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              mass += w.raw(x[g][e]);
-              if (e % 4 == 3) {
-                asm("" : "+v"(mass));
-                __builtin_amdgcn_sched_barrier(0);
-              }
-            }
-          rec.mass = wave_sum(mass - (uint64_t)(G * V) * kRaw);
+          if (CUTS) rec.upper = (float)wave_sum(top_mass - (uint64_t)(G * V) * kRaw) * 1.000001f;
         }
       }
     }
   }
   if (lane == 0) {
     q.records[id] = rec;
-    if (seg == 0 && q.wide) {
+    if (CUTS && seg == 0) {
       q.wide[row].state = kWideDone;
       q.wide[row].arrived[0] = 0;
       q.wide[row].arrived[1] = 0;
@@ -1277,6 +1265,18 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   put_token(q, row, sh.found_i, sh.found_x, w, total);
 }
 
+const void* sample_segment_kernel_ptr(int dtype, bool cuts) {
+  switch (dtype * 2 + (cuts ? 1 : 0)) {
+    case 0: return reinterpret_cast<const void*>(&sample_segment_kernel<float, false>);
+    case 1: return reinterpret_cast<const void*>(&sample_segment_kernel<float, true>);
+    case 2: return reinterpret_cast<const void*>(&sample_segment_kernel<__hip_bfloat16, false>);
+    case 3: return reinterpret_cast<const void*>(&sample_segment_kernel<__hip_bfloat16, true>);
+    case 4: return reinterpret_cast<const void*>(&sample_segment_kernel<__half, false>);
+    case 5: return reinterpret_cast<const void*>(&sample_segment_kernel<__half, true>);
+    default: return nullptr;
+  }
+}
+
 #define ERT_SAMPLE_PTR(NAME, ...)                                                      \
   const void* NAME##_ptr(int dtype) {                                                  \
     switch (dtype) {                                                                   \
@@ -1286,7 +1286,6 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
       default: return nullptr;                                                         \
     }                                                                                  \
   }
-ERT_SAMPLE_PTR(sample_segment_kernel)
 ERT_SAMPLE_PTR(sample_row_kernel, , kRowBlock)
 ERT_SAMPLE_PTR(sample_wide_kernel)
 

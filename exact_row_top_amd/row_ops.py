@@ -51,13 +51,14 @@ def _tensor(t, name):
 
 def _scores(t, name):
     """(rows, width, row stride, dtype code) of a score matrix."""
-    _tensor(t, name)
     code = TOPK_DT.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, width = t.shape
+    if t.is_contiguous():
+        return rows, width, width, code
     stride = t.stride(0) if rows > 1 else width
     if rows and width > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit inner stride")
@@ -70,14 +71,18 @@ def _vector(t, name, dtype, length, device):
     """Pointer of a contiguous 1-D tensor of `length` values, or None."""
     if t is None:
         return None
+    try:
+        if (t.dtype is dtype and t.dim() == 1 and t.numel() == length and t.is_contiguous()
+                and t.get_device() == device.index):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _tensor(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != length or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} [{length}] tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be on {device}")
 
 
 def _matrix(t, name, dtype, shape, device):
