@@ -191,8 +191,10 @@ int topk_route(const void* logits, int32_t dtype, int64_t row_stride, int32_t nu
   const Spread sp = route_spread(num_experts, vec);
   while ((num_groups << (p.group_lanes + 1)) <= sp.lanes) ++p.group_lanes;
   const int per = 256 / sp.lanes;
-  return launch(route_kernel_ptr(dtype, sp.lanes, sp.per_lane), ((int64_t)num_tokens + per - 1) / per, 256, &p,
-                (size_t)per * num_experts * sizeof(double), stream);
+  // the groups' scores go through LDS
+  return launch(route_kernel_ptr(dtype, sp.lanes, sp.per_lane),
+                ((int64_t)num_tokens + per - 1) / per, 256, &p,
+                num_groups > 1 ? (size_t)per * num_experts * sizeof(double) : 0, stream);
 }
 
 int topk_route_backward(const void* logits, int32_t dtype, int64_t row_stride, int32_t num_tokens,

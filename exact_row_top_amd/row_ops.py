@@ -37,8 +37,9 @@ def _lib():
 
 def _check(status):
     if status != 0:
-        from . import TopKError, strerror
-        raise TopKError(status, strerror(status))
+        from . import TOPK_EINVAL, TopKError, strerror
+        raise TopKError(status, "a size, count or setting outside the call's range"
+                        if status == TOPK_EINVAL else strerror(status))
 
 
 def _tensor(t, name):

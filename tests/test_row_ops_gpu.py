@@ -184,6 +184,64 @@ def test_sample_crowded_candidates(ert):
     _check_sample(ert, xd, u, "crowded min_p", min_p=[0.5, 1.0, 0.9, 0.1, 0.01, 0.9])
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_sample_low_cuts(ert, dtype):
+    # cuts far below the likeliest tokens: each alone, min-p beside them, both
+    # at once, ties across the cut, rows with +inf scores
+    rng = np.random.default_rng(15)
+    vocab, rows = 30011, 6
+    x = rng.normal(0, 0.3, (rows, vocab))
+    x[1] = rng.normal(0, 1.5, vocab)
+    x[2] = np.round(rng.normal(0, 1, vocab) * 8) / 8
+    x[3, ::2] = NINF
+    x[4, [5, 20000]] = 30.0
+    x[5, [7, 8, 29000]] = np.inf
+    xd = _cuda(x.astype(np.float32), _dt(dtype))
+    u = rng.random(rows)
+    one = np.ones(rows)
+    _check_sample(ert, xd, u, f"{dtype} low top-p", top_p=0.9 * one, temperature=one)
+    _check_sample(ert, xd, u, f"{dtype} low top-p and min-p", top_p=0.9 * one, min_p=0.2 * one)
+    _check_sample(ert, xd, u, f"{dtype} low top-k", top_k=[12345] * rows)
+    _check_sample(ert, xd, u, f"{dtype} low top-k and min-p", top_k=[12345] * rows, min_p=0.3 * one)
+    _check_sample(ert, xd, u, f"{dtype} low min-p", min_p=0.05 * one)
+    _check_sample(ert, xd, u, f"{dtype} low top-k and top-p", top_k=[12345] * rows, top_p=0.7 * one)
+    _check_sample(ert, xd, u, f"{dtype} hot", temperature=40 * one, top_p=0.5 * one)
+    _check_sample(ert, xd, u, f"{dtype} no temperature at all", temperature=np.inf * one, top_p=0.5 * one)
+
+
+def test_sample_low_cuts_side_by_side(ert):
+    # rows that several workgroups share, in two graphs and eagerly on two
+    # streams at once, again and again
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    x = torch.randn(24, 60001, device="cuda", generator=g)
+    u = torch.rand(24, device="cuda", generator=g)
+    p = torch.full((24,), 0.9, device="cuda")
+    k = torch.randint(1, 30000, (24,), device="cuda", generator=g, dtype=torch.int32)
+    want_p, want_k = ert.sample_tokens(x, u, top_p=p).clone(), ert.sample_tokens(x, u, top_k=k).clone()
+    torch.cuda.synchronize()
+    graphs = []
+    for kw in (dict(top_p=p), dict(top_k=k)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = ert.sample_tokens(x, u, **kw)
+        graphs.append((graph, out))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            graphs[0][0].replay()
+            one = ert.sample_tokens(x, u, top_p=p)
+        with torch.cuda.stream(b):
+            graphs[1][0].replay()
+            two = ert.sample_tokens(x, u, top_k=k)
+        three = ert.sample_tokens(x, u, top_p=p)
+        torch.cuda.synchronize()
+        for got, want in ((one, want_p), (three, want_p), (graphs[0][1], want_p), (two, want_k),
+                          (graphs[1][1], want_k)):
+            assert torch.equal(got, want)
+
+
 def test_sample_outputs_given_and_empty_batch(ert):
     import torch
     x = torch.randn(4, 999, device="cuda")
@@ -286,6 +344,31 @@ def test_route_many_tokens_strided_and_tied(ert):
         _check_route(ert, x, 8, f"many {dtype} zero bias", bias=np.zeros(experts, np.float32),
                      scoring="sigmoid", num_groups=8, topk_groups=4, group_score="top2")
         _check_route(ert, x, 6, f"many {dtype} no bias", scoring="softmax", renormalize=False)
+
+
+def test_route_fewer_experts_than_asked_for(ert):
+    # the groups that stay hold fewer experts than top_k
+    rng = np.random.default_rng(17)
+    x = _cuda(rng.normal(0, 1, (9, 64)).astype(np.float32))
+    bias = rng.normal(0, 0.1, 64).astype(np.float32)
+    for b in (None, bias):
+        _check_route(ert, x, 16, "two groups of four for sixteen", bias=b, scoring="sigmoid",
+                     num_groups=16, topk_groups=2, group_score="top2")
+        _check_route(ert, x, 64, "all of them", bias=b, scoring="softmax")
+
+
+def test_route_near_ties(ert):
+    # scores a few 2^-24 apart, and sigmoids that 32 bits cannot tell apart
+    rng = np.random.default_rng(18)
+    E = 256
+    base = rng.normal(0, 1, (40, E)).astype(np.float32)
+    base[:, 100:160] = (np.float32(2.0) + np.arange(60, dtype=np.float32) * 2.0 ** -22)[rng.permutation(60)]
+    base[20:, 30:60] = 17.0 + rng.random((20, 30)).astype(np.float32) * 12
+    for scoring, b in itertools.product(("sigmoid", "softmax"),
+                                        (np.zeros(E, np.float32), np.full(E, -3.0, np.float32))):
+        _check_route(ert, _cuda(base), 12, f"near ties {scoring}", bias=b, scoring=scoring,
+                     num_groups=8, topk_groups=5, group_score="top2")
+        _check_route(ert, _cuda(base), 12, f"near ties {scoring}, one group", bias=b, scoring=scoring)
 
 
 def _check_grad(ert, x, idx, g, what, **kw):
@@ -440,6 +523,9 @@ def test_tables_request_counts(ert, requests):
 
 def test_tables_long_short_lists_and_narrow_tables(ert):
     _check_tables(ert, [70000, 3, 40001], [70000, 3, 20000], 16, "long prompts")
+    _check_tables(ert, [300001, 0, 5, 70002], [300001, 0, 5, 70002], 48, "four tokens a thread")
+    _check_tables(ert, [300001, 7, 5, 70002], [300001, 7, 0, 70002], 64, "four tokens a thread, wide",
+                  wide=True, max_tokens=370003)
     _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "free list too short", num_free=9)
     _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "free list used up", num_free=9, start=20)
     _check_tables(ert, [100, 200, 300], [100, 50, 300], 16, "no free list", num_free=0)
@@ -478,6 +564,34 @@ def test_slots(ert, k, bs, next_n, wide):
     assert np.array_equal(got.cpu().numpy(), ref.slots_of(idx, tables, bs, owner, wide))
     if not wide:
         assert got is own
+
+
+@pytest.mark.parametrize("bs", [1, 2, 3, 5, 7, 48, 100, 641, 65537, 1 << 20, (1 << 30) - 1, 1 << 30])
+def test_slots_block_sizes(ert, bs):
+    # quotients over the whole range of positions, in and out of the table
+    import torch
+    rng = np.random.default_rng(bs)
+    width = 37
+    edge = np.array([q * bs + o for q in range(width + 1) for o in (-1, 0, 1)], dtype=np.int64)
+    far = np.concatenate([edge, rng.integers(0, 2 ** 31, 500), [2 ** 31 - 1, 0]])
+    idx = far[(far >= 0) & (far < 2 ** 31)].astype(np.int32)[None, :]
+    tables = rng.permutation(width).astype(np.int32)[None, :]
+    got = ert.topk_slots(_cuda(idx), _cuda(tables), bs, slot_dtype=torch.int64)
+    assert np.array_equal(got.cpu().numpy(), ref.slots_of(idx, tables, bs, [0], True))
+
+
+def test_slots_many_rows(ert):
+    # enough rows for the staged tables, rows over several workgroups
+    rng = np.random.default_rng(19)
+    for rows, k, width in ((1200, 512, 300), (700, 2048, 64), (1030, 1001, 900)):
+        tables = rng.permutation(20 * width).reshape(20, width).astype(np.int32)
+        idx = rng.integers(-1, width * 16 + 5, (rows, k)).astype(np.int32)
+        owner = rng.integers(0, 20, rows).astype(np.int32)
+        got = ert.topk_slots(_cuda(idx), _cuda(tables), 16, row_requests=_cuda(owner)).cpu().numpy()
+        at = idx.astype(np.int64)
+        ok = (at >= 0) & (at < width * 16)
+        want = np.where(ok, tables[owner[:, None], np.where(ok, at // 16, 0)].astype(np.int64) * 16 + at % 16, -1)
+        assert np.array_equal(got, want)
 
 
 def test_slots_strided_tables_far_blocks_and_empty(ert):
