@@ -80,14 +80,6 @@ __device__ __forceinline__ uint32_t fold_sum(uint32_t v) {
   return lanes_fold<L>(v, [](uint32_t a, uint32_t b) { return a + b; });
 }
 
-// A wave's LDS operations are done in order: this only keeps the compiler
-// from moving them.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 __device__ __forceinline__ bool live(float x) { return x > -__builtin_inff(); }
 
 // The group of expert e < 1024.

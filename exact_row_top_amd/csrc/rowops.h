@@ -107,6 +107,14 @@ __device__ __forceinline__ double exp2_64(double s, const Exp2Poly& poly) {
   return __builtin_ldexp(poly(s - n), (int)n);
 }
 
+// A wave's LDS operations are done in order: this only keeps the compiler
+// from moving them.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---- 16-byte score groups ----------------------------------------------------
 
 template <class T>

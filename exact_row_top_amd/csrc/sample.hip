@@ -151,10 +151,38 @@ struct RowView {
   }
 };
 
+// Prefix sums over a wave of 4- and 8-byte values with DPP row shifts and
+// broadcasts (no LDS: a 64-bit scan by ds_bpermute takes six times as long).
+template <int CTL, int ROWS, class V>
+__device__ __forceinline__ V dpp_from(V v) {  // 0 where there is no source lane
+  uint32_t w[sizeof(V) / 4];
+  __builtin_memcpy(w, &v, sizeof(V));
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i)
+    w[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[i], CTL, ROWS, 0xf, false);
+  __builtin_memcpy(&v, w, sizeof(V));
+  return v;
+}
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {
+  v += dpp_from<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+  v += dpp_from<0x112, 0xf>(v);
+  v += dpp_from<0x114, 0xf>(v);
+  v += dpp_from<0x118, 0xf>(v);
+  v += dpp_from<0x142, 0xa>(v);  // row_bcast 15, 31
+  v += dpp_from<0x143, 0xc>(v);
+  return v;
+}
+// The sum, in every lane.
 template <class V>
 __device__ __forceinline__ V wave_sum(V v) {
+  v = wave_scan(v);
+  uint32_t w[sizeof(V) / 4];
+  __builtin_memcpy(w, &v, sizeof(V));
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i)
+    w[i] = (uint32_t)__builtin_amdgcn_readlane((int)w[i], 63);
+  __builtin_memcpy(&v, w, sizeof(V));
   return v;
 }
 __device__ __forceinline__ int wave_min(int v) {
@@ -332,9 +360,14 @@ struct RowShared {
   float found_x;
   uint64_t before;
   uint32_t list_n;
-  float lx[kListS];
-  int32_t li[kListS];
-  uint64_t lw[kListS];
+  union {
+    struct {
+      float lx[kListS];
+      int32_t li[kListS];
+      uint64_t lw[kListS];
+    };
+    float dense[kWideSegs][64 + 256];  // each wave's scores on their way to a weight
+  };
   float seg_best[kMaxSegments];
   uint64_t seg_mass[kMaxSegments];
   float seg_upper[kMaxSegments];
@@ -406,11 +439,7 @@ __device__ __forceinline__ V block_sum(V v, V* red) {
 
 template <int BLOCK>
 __device__ __forceinline__ void block_min_max(float& lo, float& hi, float* red) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    lo = fminf(lo, __shfl_xor(lo, d));
-    hi = fmaxf(hi, __shfl_xor(hi, d));
-  }
+  wave_minmax(lo, hi);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) {
     red[threadIdx.x >> 6] = lo;
@@ -428,11 +457,7 @@ __device__ __forceinline__ void block_min_max(float& lo, float& hi, float* red) 
 template <int BLOCK, class V>
 __device__ __forceinline__ V block_scan(V v, V* red) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const V o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+  v = wave_scan(v);
   __syncthreads();
   if (lane == 63) red[wv] = v;
   __syncthreads();
@@ -819,24 +844,64 @@ __device__ __forceinline__ void visit_segment(const RowView<T>& view, int seg, F
     }
 }
 
+// One wave's segment again: f(x) for the scores that `take` admits, 64 at a
+// time (-inf in the lanes behind the last), so that the exponentials run on
+// full waves however few scores pass.  `buf` holds what is left over and four
+// scores of every lane.
+template <class T, class Take, class F>
+__device__ __forceinline__ void visit_dense(const RowView<T>& view, int seg, float* buf, Take&& take,
+                                            F&& f) {
+  constexpr int V = Elem<T>::kVec;
+  constexpr int G = RowView<T>::kGroups;
+  const int lane = threadIdx.x & 63;
+  float x[G][V];
+  view.segment(seg, lane, x);
+  int n = 0;
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e0 = 0; e0 < V; e0 += 4) {
+#pragma unroll
+      for (int e = e0; e < e0 + 4; ++e) {
+        const bool in = take(x[g][e], (seg * (kSegment / V) + g * 64 + lane) * V + e - view.lead);
+        const uint64_t mask = __ballot(in);
+        const int at = n + (int)__builtin_amdgcn_mbcnt_hi(
+                               (uint32_t)(mask >> 32),
+                               __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+        if (in) buf[at] = x[g][e];
+        n += __popcll(mask);
+      }
+      wave_sync();
+      while (n >= 64) {
+        n -= 64;
+        f(buf[n + lane]);
+      }
+      wave_sync();
+    }
+  if (n > 0) f(lane < n ? buf[lane] : -__builtin_inff());
+}
+
 // A drawable score's weight, else 0, for finite m: what Weigher::drawn gives.
 __device__ __forceinline__ uint64_t drawn_at(const Weigher& w, double s) {
   const uint64_t v = w.raw_of(s) - kRaw;
   return s > -kTmax ? v : 0ull;
 }
 
-// This workgroup's waves add segments [s0, s1) to the bins.
+// This workgroup's wave adds its segment to the bins: masses of the scores at
+// or above `from`, or counts.
 template <class T>
-__device__ __forceinline__ void fill_bins(const RowView<T>& view, int s0, int s1, RowShared& sh,
-                                          const Weigher& w, double rate, bool by_mass) {
+__device__ __forceinline__ void fill_bins(const RowView<T>& view, int seg, int nseg, RowShared& sh,
+                                          const Weigher& w, double rate, float from, bool by_mass) {
   clear_bins<kWideBlock>(sh);
-  for (int seg = s0 + (int)(threadIdx.x >> 6); seg < s1; seg += kWideSegs) {
+  if (seg < nseg) {
     if (by_mass)
-      visit_segment(view, seg, [&](float x, int) {
-        const double s = w.log2_of(x);
-        const unsigned long long v = drawn_at(w, s);
-        if (v) atomicAdd((unsigned long long*)&sh.mass[wide_bin(s, rate)], v);
-      });
+      visit_dense(
+          view, seg, sh.dense[threadIdx.x >> 6], [&](float x, int) { return x >= from; },
+          [&](float x) {
+            const double s = w.log2_of(x);
+            const unsigned long long v = drawn_at(w, s);
+            if (v) atomicAdd((unsigned long long*)&sh.mass[wide_bin(s, rate)], v);
+          });
     else
       visit_segment(view, seg, [&](float x, int) {
         const double s = w.log2_of(x);
@@ -926,9 +991,9 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     sh.seg_count[s] = r.count;
   }
   const float own_best = m;
-  float nm = -m;  // the largest of both, through one reduction
-  block_min_max<BLOCK>(nm, floor, sh.redf);
-  m = -nm;
+  block_min_max<BLOCK>(low, m, sh.redf);
+  float unused = 0.0f;
+  block_min_max<BLOCK>(unused, floor, sh.redf);
   fits = __syncthreads_and(fits);
   if (m == ninf) {  // nothing to draw from
     if (t == 0 && part == 0) {
@@ -1013,15 +1078,13 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   const bool complete = floor == ninf || !w.drawable(floor);
   // at or below every drawable score
   const float least = (float)fmax((double)m - 1.0001 * kTmax / ask.c, -(double)__FLT_MAX__);
-  float high = m;
   WideRow* wr = q.wide + row;
   double rate = 0.0;
+  float lowest = ninf;
   uint64_t need = (uint64_t)ask.k;
   if (one_cut && m < __builtin_inff()) {
     // The cut's count or mass, and whether the candidates can hold it at all.
-    block_min_max<BLOCK>(low, high, sh.redf);
-    const double span = fmax(w.log2_of(low), -kTmax);
-    rate = span < 0.0 ? (double)kBinsS / -span : 0.0;
+    double span = fmax(w.log2_of(low), -kTmax);
     bool low_cut;
     if (ask.cut_p) {
       double z = 0.0, top = 0.0;
@@ -1035,14 +1098,23 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
       top = block_sum<BLOCK>(top, sh.redd);
       need = ceil_share(ask.p, z);
       low_cut = top < (double)need;
+      // All scores whose weight is below (1 - p) / vocab of the total weigh
+      // less than 1 - p of it together: the cut lies above them (by 0.02
+      // octaves, so that no sum's rounding matters).
+      const double t = log2((1.0 - ask.p) * z * (1.0 / (double)kOne) / (double)q.vocab) - 0.02;
+      if (t > span) {
+        span = fmin(t, 0.0);
+        lowest = (float)((double)m + span / ask.c);
+      }
     } else {
       low_cut = block_sum<BLOCK>(listed, reinterpret_cast<int*>(sh.redf)) < ask.k && !complete;
     }
     fits = fits && !low_cut;
+    rate = span < 0.0 ? (double)kBinsS / -span : 0.0;
   }
   // This workgroup's share of the bins; the row's last one finds the crossing.
   auto bin_row = [&] {
-    fill_bins(view, part * kWideSegs, min((part + 1) * kWideSegs, nseg), sh, w, rate, ask.cut_p);
+    fill_bins(view, part * kWideSegs + (t >> 6), nseg, sh, w, rate, lowest, ask.cut_p);
     uint64_t* slices = q.slices + (int64_t)row * q.row_wgs * kBinsS;
     for (int b = t; b < kBinsS; b += BLOCK) agent_store(&slices[part * kBinsS + b], sh.mass[b]);
     if (!last_in(&wr->arrived[0], q.row_wgs, sh)) return;
@@ -1167,17 +1239,22 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
     __syncthreads();
     if (seg < nseg) {
       uint64_t mass = 0;
-      visit_segment(view, seg, [&](float x, int i) {
-        const double s = w.log2_of(x);
-        const uint64_t v = drawn_at(w, s);
-        mass += x >= above && v >= least ? v : 0ull;
-        if (x >= from && !(x >= above) && s > -kTmax) {
-          const int at = (int)atomicAdd(&sh.list_n, 1u);
-          if (at < mine)
-            agent_store(&members[part * room + at],
-                        ((uint64_t)(uint32_t)i << 32) | __float_as_uint(x));
-        }
-      });
+      visit_dense(
+          view, seg, sh.dense[t >> 6],
+          [&](float x, int i) {
+            const bool kept_above = x >= above;
+            if (x >= from && !kept_above && w.drawable(x)) {
+              const int at = (int)atomicAdd(&sh.list_n, 1u);
+              if (at < mine)
+                agent_store(&members[part * room + at],
+                            ((uint64_t)(uint32_t)i << 32) | __float_as_uint(x));
+            }
+            return kept_above;
+          },
+          [&](float x) {
+            const uint64_t v = drawn_at(w, w.log2_of(x));
+            mass += v >= least ? v : 0ull;
+          });
       mass = wave_sum(mass);
       if ((t & 63) == 0) agent_store(&kept[seg], mass);
     }
