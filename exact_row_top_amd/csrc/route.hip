@@ -13,8 +13,9 @@
 // The choice is a whole number that has to come out the same wherever it is
 // made, so it is the choice on 64-bit scores.  It is made on 32-bit ones
 // first: where every score that was taken stands clear of the next one by
-// more than both can be off, the 64-bit order is the same; the few tokens
-// (and ties under a bias) where it does not are chosen again in 64 bits.
+// more than both can be off, the 64-bit order is the same; the experts near
+// the last one of the few tokens (and ties under a bias) where it does not
+// are ranked again by 64-bit scores.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -554,13 +555,15 @@ __device__ __forceinline__ void store_as<__half>(__half* p, float v) { *p = __fl
 }  // namespace
 
 // A token's row of changes is put together in LDS: zeros, the chosen
-// experts' changes (at most K), and out in 16-byte pieces.
+// experts' changes (at most K), and out in 16-byte pieces.  Bound by the
+// chain of dependent steps at few tokens and by writing at many: NUMBERS
 template <class T, int L, int EPL>
 __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGradParams q) {
   constexpr int TOKENS = kRouteBlock / L;
   constexpr int V = Elem<T>::kVec;
   extern __shared__ float row_lds[];
   __shared__ float change[TOKENS][kMaxRouteK];
+  __shared__ int32_t names[TOKENS][kMaxRouteK];
   const int l = threadIdx.x % L;
   const int slot = threadIdx.x / L;
   const int64_t token = (int64_t)blockIdx.x * TOKENS + slot;
@@ -601,14 +604,29 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
         top = fmaxf(top, x[v * V + i]);
       }
     }
-  } else if (!q.sigmoid) {
-    for (int j = l; j < K; j += L) {
+  }
+
+  // this lane's share of the chosen: expert (-1 for none), logit, gradient
+  constexpr int R = kMaxRouteK / L;
+  int named[R];
+  float logit[R], g[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = r * L + l;
+    named[r] = -1;
+    logit[r] = ninf;
+    g[r] = 0.0f;
+    if (j < K) {
       const int e = idx[j];
       if ((unsigned)e < (unsigned)E) {
+        named[r] = e;
+        g[r] = grad[j];
         const float y = Elem<T>::load(row, e);
-        if (live(y)) top = fmaxf(top, y);
+        logit[r] = live(y) ? y : ninf;
       }
+      names[slot][j] = named[r];
     }
+    if (!whole && !q.sigmoid) top = fmaxf(top, logit[r]);
   }
   score.top = fold_maxf<L>(top);
   if (whole) {
@@ -619,15 +637,14 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
     score.inv_z = z > 0.0 ? 1.0 / z : 0.0;
   }
 
-  double sum = 0.0, dot = 0.0;
-  for (int j = l; j < K; j += L) {
-    const int e = idx[j];
-    if ((unsigned)e < (unsigned)E) {
-      const float y = Elem<T>::load(row, e);
-      const double s = live(y) ? score(y) : 0.0;
-      sum += s;
-      dot += (double)grad[j] * s;
-    }
+  double s[R], sum = 0.0, dot = 0.0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    s[r] = 0.0;
+    if (r * L >= K) continue;
+    if (live(logit[r])) s[r] = score(logit[r]);
+    sum += s[r];
+    dot += (double)g[r] * s[r];
   }
   sum = lanes_sum<L>(sum);
   dot = lanes_sum<L>(dot);
@@ -635,32 +652,29 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
   // a token whose chosen scores sum to zero has no weights to change
   const double inv = q.renormalize ? (sum > 0.0 ? 1.0 / sum : 0.0) : 1.0;
   const double mean = q.renormalize ? dot * inv : 0.0;
-  for (int j = l; j < K; j += L) {
-    const int e = idx[j];
-    double v = 0.0;
-    if ((unsigned)e < (unsigned)E) {
-      const float y = Elem<T>::load(row, e);
-      if (live(y)) {
-        v = ((double)grad[j] - mean) * inv * scale * score(y);
-        if (q.sigmoid) v *= score(-y);
-      }
-    }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = r * L + l;
+    if (j >= K) continue;
+    double v = ((double)g[r] - mean) * inv * scale * s[r];
+    if (q.sigmoid) v *= live(logit[r]) ? score(-logit[r]) : 0.0;
     change[slot][j] = (float)v;
   }
   wave_sync();
   // an expert that a caller names twice gets both changes, added in order by
   // the first slot that names it
-  for (int j = l; j < K; j += L) {
-    const int e = idx[j];
-    if ((unsigned)e >= (unsigned)E) continue;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = r * L + l;
+    if (j >= K || named[r] < 0) continue;
     float v = 0.0f;
     bool first = true;
     for (int o = 0; o < K; ++o) {
-      if (idx[o] != e) continue;
-      first = first && o >= j;
-      v += change[slot][o];
+      const bool same = names[slot][o] == named[r];
+      first = first && !(same && o < j);
+      v += same ? change[slot][o] : 0.0f;
     }
-    if (first) d[e] = v;
+    if (first) d[named[r]] = v;
   }
   wave_sync();
   if (!on) return;
