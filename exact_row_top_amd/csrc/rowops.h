@@ -12,7 +12,7 @@ namespace ert {
 // ---- sampling --------------------------------------------------------------
 
 constexpr int kSegment = 2048;    // scores one wave reads
-constexpr int kSegSlots = 64;     // candidates a segment can hand on
+constexpr int kSegSlots = 128;    // candidates a segment can hand on
 constexpr int kMaxVocab = 1 << 20;
 
 // One segment's findings, written by the segment kernel for the row kernel.
@@ -40,9 +40,14 @@ enum : uint32_t { kWideDone = 0, kWideMembers = 1, kWideWhole = 2 };
 struct WideRow {
   uint32_t state;
   float m;              // the row's largest score
-  uint64_t need;        // count or mass that the cut leaves to the crossing bin
-  float above;          // scores at or above this lie above the crossing bin
-  float from;           // the bin's own begin here
+  uint64_t need;        // mass that top-p leaves to its crossing bins
+  // Scores: the lowest above all crossing bins, the lowest in top-p's, and
+  // the same two of top-k's.  NaN: none.
+  float edge[4];
+  uint32_t need_k;      // count that top-k leaves to its crossing bin
+  uint32_t pad;
+  uint64_t mass_k;      // with both: the mass above that bin
+  uint64_t before;      // the mass above top-p's crossing bins
   uint32_t arrived[2];  // workgroups done with the bins, with the members
 };
 
@@ -63,7 +68,8 @@ struct SampleParams {
   Candidate* candidates;  // [rows][segments][kSegSlots]; later the crossing bins' members
   WideRow* wide;          // null where no row can have a cut
   uint64_t* kept;         // [rows][segments + wide_wgs]: kept masses, member counts
-  uint64_t* slices;       // [rows][wide_wgs][kBinsS]
+  uint64_t* masses;       // [rows][wide_wgs][kBinsS]
+  uint32_t* counts;       // the same
   int32_t wide_wgs;       // workgroups of a row in the wide kernel
   int32_t row_wgs;        // in the row kernel: as many if a top-k or top-p is given, else one
   int32_t whole_row;      // every row from memory

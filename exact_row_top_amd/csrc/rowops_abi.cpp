@@ -93,7 +93,7 @@ size_t topk_sample_workspace_bytes(int32_t num_rows, int32_t vocab) {
   if (num_rows < 1 || vocab < 1 || vocab > kMaxVocab) return 0;
   const size_t seg = (size_t)segments_of(vocab);
   return (size_t)num_rows * (seg * (sizeof(SegRecord) + kSegSlots * sizeof(Candidate) + 8) +
-                             wide_wgs_of(seg) * (kBinsS + 1) * 8 + sizeof(WideRow));
+                             wide_wgs_of(seg) * (kBinsS * 12 + 8) + sizeof(WideRow));
 }
 
 int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t vocab,
@@ -137,8 +137,9 @@ int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t v
   p.records = static_cast<SegRecord*>(workspace);
   p.candidates = reinterpret_cast<Candidate*>(p.records + waves);
   p.kept = reinterpret_cast<uint64_t*>(p.candidates + waves * kSegSlots);
-  p.slices = p.kept + waves + num_rows * wgs;
-  p.wide = (cuts || whole) ? reinterpret_cast<WideRow*>(p.slices + num_rows * wgs * kBinsS) : nullptr;
+  p.masses = p.kept + waves + num_rows * wgs;
+  p.counts = reinterpret_cast<uint32_t*>(p.masses + num_rows * wgs * kBinsS);
+  p.wide = (cuts || whole) ? reinterpret_cast<WideRow*>(p.counts + num_rows * wgs * kBinsS) : nullptr;
   p.wide_wgs = (int32_t)wgs;
   p.row_wgs = (top_k || top_p) && !whole ? (int32_t)wgs : 1;
   p.whole_row = whole ? 1 : 0;

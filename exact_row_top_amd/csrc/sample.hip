@@ -215,8 +215,8 @@ __device__ __forceinline__ int wave_min(int v) {
 // MB, 34 us, where a copy of as much runs at 5.2 TB/s (26 us) and the
 // instructions alone take about 24; with weights in flight for all of a
 // lane's 32 scores and constants in vector registers it took 54.  CUTS false
-// leaves the candidates' code out where no row of the call can have a cut (58
-// registers instead of 102).
+// leaves the candidates' code out where no row of the call can have a cut (74
+// registers instead of 108).
 // ---------------------------------------------------------------------------
 template <class T, bool CUTS>
 __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams q) {
@@ -269,14 +269,16 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
     } else {
       float floor = __builtin_inff();
       if (CUTS && ask.cuts()) {
-        // how many lane maxima the floor lies under: what a segment should
-        // hold of a row's best k, with room for an uneven spread; 16 where
-        // only the weights say how many are needed
-        int j = 16;
+        // How many candidates a segment should hand on: its share of a row's
+        // best k and room for an uneven spread, within what fits; 16 where
+        // only the weights say how many are needed.  With j of the 64 lane
+        // maxima at or above the floor, about -64 ln(1 - j / 64) scores are.
+        float want = 16.0f;
         if (ask.cut_k) {
           const float share = (float)ask.k / (float)q.segments;
-          j = min(48, (int)(share + 4.0f * __builtin_sqrtf(share)) + 4);
+          want = fminf(share + 4.0f * __builtin_sqrtf(share) + 4.0f, 88.0f);
         }
+        const int j = 1 + (int)(64.0f * (1.0f - __expf(want * (-1.0f / 64.0f))));
         const uint32_t key = fkey(top);
         uint32_t thr = 0;
 #pragma unroll
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 
 // ---------------------------------------------------------------------------
 // Row kernel: one workgroup per row, or one per kWideSegs segments for rows
-// whose only cut, a top-k or a top-p, may lie below the candidates.
+// whose top-k or top-p may lie below the candidates.
 //
 // Bound by its own chain of scans and barriers, not by work: one row of 32768
 // with all cuts takes 11 us, of which reading the records is 1.4, the
@@ -803,24 +805,24 @@ __device__ __forceinline__ double below_best(float best, const Weigher& w) {
 // ---------------------------------------------------------------------------
 // Rows whose cut lies below the candidates (flat rows with a top-p, a large
 // top-k, a small min-p), kWideSegs segments a workgroup:
-//  1. in the row kernel, the row's masses (top-p) or counts (top-k) in kBinsS
+//  1. in the row kernel, the row's masses (top-p) and counts (top-k) in kBinsS
 //     equal bins of score from the largest down; the row's last workgroup
-//     adds the others' bins up and finds the crossing bin;
-//  2. sample_wide_kernel: each segment's kept mass above that bin, and the
-//     bin's members; the row's last workgroup finds the exact cut among the
+//     adds the others' bins up and finds the crossing bins;
+//  2. sample_wide_kernel: each segment's kept mass above those bins, and the
+//     bins' members; the row's last workgroup finds the exact cut among the
 //     members, adds the kept ones to their segments, finds the segment in
 //     which the draw falls, and the token in it.
 // Sums are whole numbers, so which workgroup is last changes nothing.  What
 // crosses between workgroups goes through agent-scope atomics, complete
 // before their workgroup counts itself; nobody waits for anybody.
-// Rows with both a large top-k and a top-p, rows with +inf scores, and bins
-// with more members than fit are selected by one workgroup from memory, pass
-// by pass.
+// Rows with cuts and +inf scores, and bins with more members than fit, are
+// selected by one workgroup from memory, pass by pass.
 //
 // Both steps are bound by the exponentials (64 x 131072 with mixed cuts: row
-// kernel 19 us, wide kernel 18 us, of which 8 each are the waves' work and
+// kernel 19 us, wide kernel 19 us, of which 8 each are the waves' work and
 // the rest the last workgroup's chain of scans and look-ups).  One workgroup
-// a row, from memory, took 395 us for the same rows.
+// a row, from memory, took 395 us for the same rows, and 480 to 670 where
+// both cuts lie low (now 78 to 88, the whole call).
 // ---------------------------------------------------------------------------
 
 
@@ -910,14 +912,15 @@ __device__ __forceinline__ uint64_t drawn_at(const Weigher& w, double s) {
   return s > -kTmax ? v : 0ull;
 }
 
-// This workgroup's wave adds its segment to the bins: masses of the scores at
-// or above `from`, or counts.
+// This workgroup's wave adds its segment to the bins: the masses of the scores
+// at or above `from` (top-p), counts (top-k), or both.
 template <class T>
 __device__ __forceinline__ void fill_bins(const RowView<T>& view, int seg, int nseg, RowShared& sh,
-                                          const Weigher& w, double rate, float from, bool by_mass) {
+                                          const Weigher& w, double rate, float from, bool by_count,
+                                          bool by_mass) {
   clear_bins<kWideBlock>(sh);
   if (seg < nseg) {
-    if (by_mass)
+    if (!by_count)
       visit_dense(
           view, seg, sh.dense[threadIdx.x >> 6], [&](float x, int) { return x >= from; },
           [&](float x) {
@@ -928,53 +931,97 @@ __device__ __forceinline__ void fill_bins(const RowView<T>& view, int seg, int n
     else
       visit_segment(view, seg, [&](float x, int) {
         const double s = w.log2_of(x);
-        if (s > -kTmax) atomicAdd((unsigned long long*)&sh.mass[wide_bin(s, rate)], 1ull);
+        if (s > -kTmax) {
+          const int b = wide_bin(s, rate);
+          atomicAdd(&sh.cnt[b], 1u);
+          if (by_mass) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)drawn_at(w, s));
+        }
       });
   }
   __syncthreads();
 }
 
-// The crossing bin of a row's whole bins, handed to the wide kernel as the
-// scores at which it begins and ends.
-__device__ __forceinline__ void cross_wide(RowShared& sh, const Weigher& w, double rate, uint64_t need,
-                                           WideRow* wr) {
-  if (threadIdx.x == 0) sh.bin = -1;
-  int bin;
-  uint64_t before;
-  const bool found = cross_bins<kWideBlock, true>(sh, need, bin, before);
-  // nothing is cut unless the bins say so
-  float edge = threadIdx.x < 64 ? -__builtin_inff() : __builtin_inff();
-  if (found && threadIdx.x < 128) {
-    // wave 0: the lowest score of the bins above the crossing one (NaN: there
-    // is none); wave 1: of the crossing bin itself
-    const int last = threadIdx.x < 64 ? bin - 1 : bin;
-    edge = last < 0 ? __builtin_nanf("") : -__builtin_inff();
-    if (rate > 0.0 && last >= 0 && last < kBinsS - 1) {
-      const uint32_t lane = threadIdx.x & 63;
-      uint32_t lo = fkey(-__FLT_MAX__), hi = fkey(w.m);  // hi lies in bin 0
-      while (lo < hi) {  // the lowest key whose bin is at most `last`, 64 probes a round
-        const uint32_t step = (hi - lo) / 64 + 1;
-        const uint32_t probe = min(lo + lane * step, hi);
-        const uint64_t ok = __ballot(wide_bin(w.log2_of(from_key(probe)), rate) <= last);
-        const uint32_t f = (uint32_t)__ffsll((unsigned long long)ok);  // 1-based, 0: none
-        const uint32_t old = lo;
-        if (f == 1) hi = old;
-        else if (f == 0) lo = min(old + 63 * step, hi) + 1;
-        else {
-          lo = old + (f - 2) * step + 1;
-          hi = min(old + (f - 1) * step, hi);
-        }
-      }
-      edge = from_key(hi);
+// The lowest score of the bins up to `last`, by one wave: 64 probes a round
+// over the keys.  NaN if there is no such bin, -inf for the last one.
+__device__ __forceinline__ float bin_begin(int last, const Weigher& w, double rate) {
+  if (last < 0) return __builtin_nanf("");
+  if (!(rate > 0.0) || last >= kBinsS - 1) return -__builtin_inff();
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t lo = fkey(-__FLT_MAX__), hi = fkey(w.m);  // hi lies in bin 0
+  while (lo < hi) {
+    const uint32_t step = (hi - lo) / 64 + 1;
+    const uint32_t probe = min(lo + lane * step, hi);
+    const uint64_t ok = __ballot(wide_bin(w.log2_of(from_key(probe)), rate) <= last);
+    const uint32_t f = (uint32_t)__ffsll((unsigned long long)ok);  // 1-based, 0: none
+    const uint32_t old = lo;
+    if (f == 1) hi = old;
+    else if (f == 0) lo = min(old + 63 * step, hi) + 1;
+    else {
+      lo = old + (f - 2) * step + 1;
+      hi = min(old + (f - 1) * step, hi);
     }
   }
-  if (threadIdx.x == 0) {
-    wr->above = edge;
+  return from_key(hi);
+}
+
+// The crossing bins of a row's whole bins, handed to the wide kernel as the
+// scores at which they begin and end.
+//
+// With both cuts, top-p's share is of the top-k's mass, which is known but for
+// the count's crossing bin: the mass above it, and with all of it, bound the
+// share, and the mass's crossing lies in the bins from the one bound's to the
+// other's (mostly one bin).  The wide kernel lists the members of both and
+// settles the count first.
+__device__ __forceinline__ void cross_wide(RowShared& sh, const Weigher& w, double rate,
+                                           const RowAsk& ask, uint64_t need_p, WideRow* wr) {
+  const int t = threadIdx.x;
+  auto cross = [&](auto mass, uint64_t need, int& bin, uint64_t& before) {
+    __syncthreads();
+    if (t == 0) sh.bin = -1;
+    return cross_bins<kWideBlock, decltype(mass)::value>(sh, need, bin, before);
+  };
+  using Counts = std::false_type;
+  using Masses = std::true_type;
+  int bin_k = kBinsS, first = kBinsS, last = kBinsS;
+  uint64_t before_k = 0, before = 0, mass_k = 0, need = 0;
+  bool by_count = ask.cut_k && cross(Counts{}, (uint64_t)ask.k, bin_k, before_k);
+  if (!by_count) bin_k = kBinsS;
+  bool by_mass = ask.cut_p;
+  if (by_mass) {
+    uint64_t lo = need_p, hi = need_p;
+    if (ask.cut_k) {
+      uint64_t above = 0;
+      __syncthreads();
+      for (int b = t; b < kBinsS; b += kWideBlock) above += b < bin_k ? sh.mass[b] : 0ull;
+      mass_k = block_sum<kWideBlock>(above, sh.red);
+      lo = ceil_share(ask.p, (double)mass_k);
+      hi = ceil_share(ask.p, (double)(mass_k + (by_count ? sh.mass[bin_k] : 0ull)));
+    }
+    uint64_t unused;
+    by_mass = cross(Masses{}, lo, first, before);
+    if (by_mass) {
+      need = lo - before;
+      if (!cross(Masses{}, hi, last, unused)) last = kBinsS - 1;
+    }
+  }
+  const int wave = t >> 6;
+  if (wave < 4) {
+    // what lies above all crossing bins, top-p's, above top-k's, top-k's;
+    // nothing is cut unless the bins say so
+    const int end = wave == 0 ? (by_mass ? first : bin_k) - 1 : wave == 1 ? last : wave == 2 ? bin_k - 1 : bin_k;
+    const bool known = wave == 0 ? by_mass || by_count : wave == 1 ? by_mass : by_count;
+    float edge = wave == 0 ? -__builtin_inff() : __builtin_nanf("");
+    if (known) edge = bin_begin(end, w, rate);
+    if ((t & 63) == 0) wr->edge[wave] = edge;
+  }
+  if (t == 0) {
     wr->m = w.m;
-    wr->need = need - (found ? before : 0);
+    wr->need = need;
+    wr->need_k = by_count ? (uint32_t)(ask.k - before_k) : 0u;
+    wr->mass_k = mass_k;
+    wr->before = before;
     wr->state = kWideMembers;
   }
-  if (threadIdx.x == 64) wr->from = edge;
 }
 
 }  // namespace
@@ -986,9 +1033,9 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   const int t = threadIdx.x;
   const int row = blockIdx.x / q.row_wgs, part = blockIdx.x % q.row_wgs;
   const RowAsk ask = row_ask(q, row);
-  // only rows whose one cut may lie low need more than one workgroup
-  const bool one_cut = ask.cut_p != ask.cut_k && !ask.greedy && !q.whole_row;
-  if (part > 0 && !one_cut) return;
+  // only rows whose cut may lie low need more than one workgroup
+  const bool binned = (ask.cut_p || ask.cut_k) && !ask.greedy && !q.whole_row;
+  if (part > 0 && !binned) return;
   const RowView<T> view(q, row);
   const int nseg = q.segments;
   const SegRecord* recs = q.records + (int64_t)row * nseg;
@@ -1104,12 +1151,12 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   WideRow* wr = q.wide + row;
   double rate = 0.0;
   float lowest = ninf;
-  uint64_t need = (uint64_t)ask.k;
-  if (one_cut && m < __builtin_inff()) {
+  uint64_t need = 0;  // top-p's mass
+  if (binned && m < __builtin_inff()) {
     // The cut's count or mass, and whether the candidates can hold it at all.
     double span = fmax(w.log2_of(low), -kTmax);
     bool low_cut;
-    if (ask.cut_p) {
+    if (!ask.cut_k) {
       double z = 0.0, top = 0.0;
       for (int s = t; s < nseg; s += BLOCK)
         if (sh.seg_best[s] > ninf) {
@@ -1137,17 +1184,29 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   }
   // This workgroup's share of the bins; the row's last one finds the crossing.
   auto bin_row = [&] {
-    fill_bins(view, part * kWideSegs + (t >> 6), nseg, sh, w, rate, lowest, ask.cut_p);
-    uint64_t* slices = q.slices + (int64_t)row * q.row_wgs * kBinsS;
-    for (int b = t; b < kBinsS; b += BLOCK) agent_store(&slices[part * kBinsS + b], sh.mass[b]);
+    fill_bins(view, part * kWideSegs + (t >> 6), nseg, sh, w, rate, lowest, ask.cut_k, ask.cut_p);
+    uint64_t* masses = q.masses + (int64_t)row * q.row_wgs * kBinsS;
+    uint32_t* counts = q.counts + (int64_t)row * q.row_wgs * kBinsS;
+    for (int b = t; b < kBinsS; b += BLOCK) {
+      if (ask.cut_p) agent_store(&masses[part * kBinsS + b], sh.mass[b]);
+      if (ask.cut_k) agent_store(&counts[part * kBinsS + b], sh.cnt[b]);
+    }
     if (!last_in(&wr->arrived[0], q.row_wgs, sh)) return;
     for (int b = t; b < kBinsS; b += BLOCK) {
-      uint64_t sum = 0;
+      uint64_t mass = 0;
+      uint32_t count = 0;
+      if (ask.cut_p) {
 #pragma unroll 8
-      for (int p = 0; p < q.row_wgs; ++p) sum += agent_load(&slices[p * kBinsS + b]);
-      sh.mass[b] = sum;
+        for (int p = 0; p < q.row_wgs; ++p) mass += agent_load(&masses[p * kBinsS + b]);
+      }
+      if (ask.cut_k) {
+#pragma unroll 8
+        for (int p = 0; p < q.row_wgs; ++p) count += agent_load(&counts[p * kBinsS + b]);
+      }
+      sh.mass[b] = mass;
+      sh.cnt[b] = count;
     }
-    cross_wide(sh, w, rate, need, wr);
+    cross_wide(sh, w, rate, ask, need, wr);
   };
 
   // Candidates at or above the common floor: every such score of the row.
@@ -1157,15 +1216,19 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     if (t == 0) sh.list_n = 0;
     __syncthreads();
     const int lane = t & 63;
+    static_assert(kSegSlots == 128, "two rounds");
     constexpr int W = BLOCK / 64, FLY = 8;  // segments a wave has in flight
-    for (int s0 = t >> 6; s0 < nseg; s0 += W * FLY) {
+    // a segment's first 64 places, and the rest if one of the wave's uses them
+    int more = 0;
+    for (int s0 = t >> 6, from = 0; s0 < nseg;) {
       Candidate cd[FLY];
       int n[FLY];
 #pragma unroll
       for (int f = 0; f < FLY; ++f) {
         const int s = min(s0 + f * W, nseg - 1);
-        n[f] = s0 + f * W < nseg ? sh.seg_count[s] : 0;
-        cd[f] = q.candidates[((int64_t)row * nseg + s) * kSegSlots + lane];
+        n[f] = s0 + f * W < nseg ? sh.seg_count[s] - from : 0;
+        more = max(more, n[f]);
+        cd[f] = q.candidates[((int64_t)row * nseg + s) * kSegSlots + from + lane];
       }
 #pragma unroll
       for (int f = 0; f < FLY; ++f) {
@@ -1184,6 +1247,11 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
           sh.lw[at] = w(cd[f].x);
         }
       }
+      s0 += W * FLY;
+      if (s0 >= nseg && more > 64 && from == 0) {
+        s0 = t >> 6;
+        from = 64;
+      }
     }
     __syncthreads();
     list.n = (int)sh.list_n;
@@ -1194,12 +1262,12 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   Cut cut{ninf, 0x7FFFFFFF};
   const float from = complete ? least : floor;
   if (covered && ask.cut_k) covered = list.n >= ask.k || complete;
-  if (one_cut && covered && ask.cut_p) {
+  if (covered && ask.cut_p && !ask.cut_k) {
     const uint64_t have = mass_in<BLOCK>(list, sh, w, cut, 0);
     if (complete) need = ceil_share(ask.p, (double)have);
     covered = have >= need;
   }
-  if (one_cut && !covered && m < __builtin_inff()) {
+  if (binned && !covered && m < __builtin_inff()) {
     bin_row();
     return;
   }
@@ -1219,13 +1287,14 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     return;
   }
 
-  // Two cuts below the candidates, +inf scores, or (needing no bins) min-p.
+  // +inf scores, or (needing no bins) min-p alone
   if (t == 0) {
-    wr->above = ninf;
-    wr->from = __builtin_inff();
+    wr->edge[0] = ninf;
+    wr->edge[1] = wr->edge[2] = wr->edge[3] = __builtin_nanf("");
     wr->m = m;
     wr->need = 0;
-    wr->state = (m == __builtin_inff() || ask.cut_k || ask.cut_p) ? kWideWhole : kWideMembers;
+    wr->need_k = 0;
+    wr->state = m == __builtin_inff() ? kWideWhole : kWideMembers;
   }
 }
 
@@ -1248,8 +1317,9 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   Weigher w(m, ask.c);
 
   if (state == kWideMembers) {
-    const float above = wr->above, from = wr->from;
-    const uint64_t need_cut = wr->need;
+    const float above = wr->edge[0], from = wr->edge[1], above_k = wr->edge[2], from_k = wr->edge[3];
+    const uint32_t need_k = wr->need_k;
+    uint64_t need_cut = wr->need;
     // each part's members in the places of its segments' candidates, its count
     // behind the segments' kept masses
     const int room = kWideSegs * kSegSlots;
@@ -1266,7 +1336,8 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
           view, seg, sh.dense[t >> 6],
           [&](float x, int i) {
             const bool kept_above = x >= above;
-            if (x >= from && !kept_above && w.drawable(x)) {
+            const bool member = (x >= from && !kept_above) || (x >= from_k && !(x >= above_k));
+            if (member && w.drawable(x)) {
               const int at = (int)atomicAdd(&sh.list_n, 1u);
               if (at < mine)
                 agent_store(&members[part * room + at],
@@ -1296,7 +1367,8 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
     }
     if (fits && n <= kListS) {
       const ListSource list{sh.lx, sh.li, sh.lw, n};
-      float low = __builtin_inff(), high = -__builtin_inff();
+      // the extremes of top-p's members and of top-k's
+      float low = __builtin_inff(), high = -__builtin_inff(), low_k = low, high_k = high;
       int p = 0, base = 0;
       for (int i = t; i < n; i += kWideBlock) {
         while (i - base >= (int)sh.cnt[p]) base += (int)sh.cnt[p++];
@@ -1305,15 +1377,30 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
         sh.lx[i] = x;
         sh.li[i] = (int32_t)(both >> 32);
         sh.lw[i] = w(x);
-        low = fminf(low, x);
-        high = fmaxf(high, x);
+        if (x >= from && !(x >= above)) {
+          low = fminf(low, x);
+          high = fmaxf(high, x);
+        }
+        if (x >= from_k && !(x >= above_k)) {
+          low_k = fminf(low_k, x);
+          high_k = fmaxf(high_k, x);
+        }
       }
-      block_min_max<kWideBlock>(low, high, sh.redf);
-      if (n > 0) {
-        if (ask.cut_p)
-          cut = find_cut<kWideBlock, true>(list, sh, w, low, high, all, q.vocab, need_cut);
-        else
-          cut = find_cut<kWideBlock, false>(list, sh, w, low, high, all, q.vocab, need_cut);
+      if (need_k > 0) {
+        block_min_max<kWideBlock>(low_k, high_k, sh.redf);
+        cut = find_cut<kWideBlock, false>(list, sh, w, low_k, high_k, all, q.vocab, need_k);
+        if (ask.cut_p) {
+          uint64_t mass = 0;
+          list.visit<kWideBlock>([&](float x, int i, auto&& weight) {
+            if (x <= high_k && cut.holds(x, i)) mass += weight();
+          });
+          mass = wr->mass_k + block_sum<kWideBlock>(mass, sh.red);
+          need_cut = ceil_share(ask.p, (double)mass) - wr->before;
+        }
+      }
+      if (need_cut > 0) {
+        block_min_max<kWideBlock>(low, high, sh.redf);
+        cut = find_cut<kWideBlock, true>(list, sh, w, low, high, cut, q.vocab, need_cut);
       }
       clear_bins<kWideBlock>(sh);
       for (int s = t; s < nseg; s += kWideBlock) sh.mass[s] = agent_load(&kept[s]);

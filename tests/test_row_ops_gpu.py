@@ -209,6 +209,35 @@ def test_sample_low_cuts(ert, dtype):
     _check_sample(ert, xd, u, f"{dtype} no temperature at all", temperature=np.inf * one, top_p=0.5 * one)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_sample_both_cuts_low(ert, dtype):
+    # top-p's share is of what top-k leaves: from small to nearly all of it, k
+    # on either side of what the candidates hold, past the row's end, min-p and
+    # temperatures beside them, ties on both cuts, few scores that count at all
+    rng = np.random.default_rng(16)
+    vocab, rows = 24007, 8
+    x = rng.normal(0, 0.5, (rows, vocab))
+    x[1] = rng.normal(0, 3, vocab)
+    x[2] = np.round(rng.normal(0, 1, vocab) * 4) / 4
+    x[3, 100:] = NINF
+    x[4] = 0.25
+    x[5] = rng.normal(0, 1, vocab) + 40 * (rng.random(vocab) < 0.2)
+    x[6] = -np.abs(rng.normal(0, 200, vocab))
+    x[7, 11] = 9.0
+    xd = _cuda(x.astype(np.float32), _dt(dtype))
+    u = rng.random(rows)
+    one = np.ones(rows)
+    for k in (40, 700, 2500, 11000, 24006, 30000):
+        for p in (0.05, 0.6, 0.999):
+            _check_sample(ert, xd, u, f"{dtype} k={k} p={p}", top_k=[k] * rows, top_p=p * one)
+    _check_sample(ert, xd, u, f"{dtype} with min-p", top_k=[9000] * rows, top_p=0.8 * one, min_p=0.4 * one)
+    _check_sample(ert, xd, u, f"{dtype} hot", top_k=[9000] * rows, top_p=0.8 * one, temperature=30 * one)
+    _check_sample(ert, xd, u, f"{dtype} flat", top_k=[9000] * rows, top_p=0.8 * one, temperature=np.inf * one)
+    _check_sample(ert, xd, u, f"{dtype} each row its own", top_k=[9000, 0, 1, 50, 12000, 24007, 300, 5000],
+                  top_p=np.array([0.9, 0.5, 0.3, 1.0, 0.01, 0.7, -1.0, 0.95]),
+                  temperature=np.array([1, 0.2, 3, 1, 1, 8, 0, 1.0]))
+
+
 def test_sample_low_cuts_side_by_side(ert):
     # rows that several workgroups share, in two graphs and eagerly on two
     # streams at once, again and again
