@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 //
 // Bound by its own chain of scans and barriers, not by work: one row of 32768
 // with all cuts takes 11 us, of which reading the records is 1.4, the
-// candidates 1.8, the two cuts 5 and the draw 1.5.
+// candidates 1.7, the two cuts 5 and the draw 1.5.
 // ---------------------------------------------------------------------------
 
 namespace {
@@ -455,6 +455,25 @@ __device__ __forceinline__ V block_sum(V v, V* red) {
 #pragma unroll
   for (int w = 1; w < BLOCK / 64; ++w) s += red[w];
   return s;
+}
+
+template <int BLOCK>
+__device__ __forceinline__ void block_sum2(double& a, double& b, double* red) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6] = a;
+    red[BLOCK / 64 + (threadIdx.x >> 6)] = b;
+  }
+  __syncthreads();
+  a = red[0];
+  b = red[BLOCK / 64];
+#pragma unroll
+  for (int w = 1; w < BLOCK / 64; ++w) {
+    a += red[w];
+    b += red[BLOCK / 64 + w];
+  }
 }
 
 template <int BLOCK>
@@ -947,11 +966,19 @@ __device__ __forceinline__ float bin_begin(int last, const Weigher& w, double ra
   if (last < 0) return __builtin_nanf("");
   if (!(rate > 0.0) || last >= kBinsS - 1) return -__builtin_inff();
   const uint32_t lane = threadIdx.x & 63;
+  auto inside = [&](uint32_t key) { return wide_bin(w.log2_of(from_key(key)), rate) <= last; };
   uint32_t lo = fkey(-__FLT_MAX__), hi = fkey(w.m);  // hi lies in bin 0
+  // mostly within 32 floats of where real arithmetic has it
+  const double guess = (double)w.m - (double)(last + 1) / (rate * w.c);
+  if (guess > -1e38) {
+    const uint32_t probe = min(fkey((float)guess) - 32 + lane, hi);
+    const uint64_t ok = __ballot(inside(probe));
+    if (!(ok & 1) && ok) return from_key(__shfl(probe, __ffsll((unsigned long long)ok) - 1));
+  }
   while (lo < hi) {
     const uint32_t step = (hi - lo) / 64 + 1;
     const uint32_t probe = min(lo + lane * step, hi);
-    const uint64_t ok = __ballot(wide_bin(w.log2_of(from_key(probe)), rate) <= last);
+    const uint64_t ok = __ballot(inside(probe));
     const uint32_t f = (uint32_t)__ffsll((unsigned long long)ok);  // 1-based, 0: none
     const uint32_t old = lo;
     if (f == 1) hi = old;
@@ -1164,14 +1191,14 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
           z += unit * (double)sh.seg_mass[s];
           top += unit * (double)sh.seg_upper[s];
         }
-      z = block_sum<BLOCK>(z, sh.redd);
-      top = block_sum<BLOCK>(top, sh.redd);
+      block_sum2<BLOCK>(z, top, sh.redd);
       need = ceil_share(ask.p, z);
       low_cut = top < (double)need;
       // All scores whose weight is below (1 - p) / vocab of the total weigh
       // less than 1 - p of it together: the cut lies above them (by 0.02
       // octaves, so that no sum's rounding matters).
-      const double t = log2((1.0 - ask.p) * z * (1.0 / (double)kOne) / (double)q.vocab) - 0.02;
+      const float share = (float)((1.0 - ask.p) * z * (1.0 / (double)kOne)) / (float)q.vocab;
+      const double t = (double)__log2f(share) - 0.02;
       if (t > span) {
         span = fmin(t, 0.0);
         lowest = (float)((double)m + span / ask.c);
@@ -1192,20 +1219,24 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
       if (ask.cut_k) agent_store(&counts[part * kBinsS + b], sh.cnt[b]);
     }
     if (!last_in(&wr->arrived[0], q.row_wgs, sh)) return;
-    for (int b = t; b < kBinsS; b += BLOCK) {
-      uint64_t mass = 0;
-      uint32_t count = 0;
-      if (ask.cut_p) {
-#pragma unroll 8
-        for (int p = 0; p < q.row_wgs; ++p) mass += agent_load(&masses[p * kBinsS + b]);
+    auto add_up = [&](const auto* slices, auto* to) {
+      constexpr int PER = kBinsS / BLOCK, FLY = 8 / PER;  // 8 loads in flight
+      uint64_t sum[PER] = {};
+      for (int p0 = 0; p0 < q.row_wgs; p0 += FLY) {
+#pragma unroll
+        for (int f = 0; f < FLY; ++f)
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            const int p = min(p0 + f, q.row_wgs - 1);
+            const uint64_t v = agent_load(&slices[p * kBinsS + e * BLOCK + t]);
+            sum[e] += p0 + f < q.row_wgs ? v : 0;
+          }
       }
-      if (ask.cut_k) {
-#pragma unroll 8
-        for (int p = 0; p < q.row_wgs; ++p) count += agent_load(&counts[p * kBinsS + b]);
-      }
-      sh.mass[b] = mass;
-      sh.cnt[b] = count;
-    }
+#pragma unroll
+      for (int e = 0; e < PER; ++e) to[e * BLOCK + t] = sum[e];
+    };
+    if (ask.cut_p) add_up(masses, sh.mass);
+    if (ask.cut_k) add_up(counts, sh.cnt);
     cross_wide(sh, w, rate, ask, need, wr);
   };
 
@@ -1230,21 +1261,27 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
         more = max(more, n[f]);
         cd[f] = q.candidates[((int64_t)row * nseg + s) * kSegSlots + from + lane];
       }
+      uint64_t in[FLY];
+      int all = 0;
 #pragma unroll
       for (int f = 0; f < FLY; ++f) {
-        const bool in = lane < n[f] && cd[f].x >= floor && w.drawable(cd[f].x);
-        const uint64_t mask = __ballot(in);
-        if (mask == 0) continue;
-        uint32_t b = 0;
-        if (lane == 0) b = atomicAdd(&sh.list_n, (uint32_t)__popcll(mask));
-        b = __builtin_amdgcn_readfirstlane(b);
-        const uint32_t at = b + __builtin_amdgcn_mbcnt_hi(
-                                    (uint32_t)(mask >> 32),
-                                    __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
-        if (in && at < (uint32_t)kListS) {
-          sh.lx[at] = cd[f].x;
-          sh.li[at] = cd[f].i;
-          sh.lw[at] = w(cd[f].x);
+        in[f] = __ballot(lane < n[f] && cd[f].x >= floor && w.drawable(cd[f].x));
+        all += __popcll(in[f]);
+      }
+      if (all > 0) {
+        uint32_t base = 0;
+        if (lane == 0) base = atomicAdd(&sh.list_n, (uint32_t)all);
+        base = __builtin_amdgcn_readfirstlane(base);
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) {
+          const uint32_t at = base + __builtin_amdgcn_mbcnt_hi(
+                                         (uint32_t)(in[f] >> 32),
+                                         __builtin_amdgcn_mbcnt_lo((uint32_t)in[f], 0u));
+          if ((in[f] >> lane & 1) && at < (uint32_t)kListS) {
+            sh.lx[at] = cd[f].x;
+            sh.li[at] = cd[f].i;
+          }
+          base += (uint32_t)__popcll(in[f]);
         }
       }
       s0 += W * FLY;
@@ -1262,6 +1299,9 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
   Cut cut{ninf, 0x7FFFFFFF};
   const float from = complete ? least : floor;
   if (covered && ask.cut_k) covered = list.n >= ask.k || complete;
+  if (covered)
+    for (int i = t; i < list.n; i += BLOCK) sh.lw[i] = w(sh.lx[i]);
+  __syncthreads();
   if (covered && ask.cut_p && !ask.cut_k) {
     const uint64_t have = mass_in<BLOCK>(list, sh, w, cut, 0);
     if (complete) need = ceil_share(ask.p, (double)have);
