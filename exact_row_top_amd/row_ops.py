@@ -18,6 +18,8 @@ also holds the returned tensors.
 """
 from __future__ import annotations
 
+import operator
+
 import torch
 
 TOPK_DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -101,7 +103,7 @@ def _matrix(t, name, dtype, shape, device):
 
 
 def _int32(v, name):
-    v = int(v)
+    v = operator.index(v)
     if not -(1 << 31) <= v < (1 << 31):
         raise ValueError(f"{name} must fit 32 bits")
     return v

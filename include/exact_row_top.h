@@ -391,7 +391,8 @@ int topk_validate(int32_t mode, const void* logits, int64_t row_stride, const vo
  * The conventions above hold (device pointers, stream order, status codes, no
  * host reads); none of these calls allocates, keeps state or uses the
  * library's slab, so calls on different streams are independent as long as
- * their outputs and workspaces are.  Equal scores go to the lower index.
+ * their outputs and workspaces are.  Outputs overlap neither each other nor an
+ * input, but where a call says so.  Equal scores go to the lower index.
  * Scores come in float32, bfloat16 or float16 (a TOPK_DT_* value), rows
  * row_stride elements apart with unit inner stride, aligned to their element;
  * whole aligned 16-byte groups that hold a row's scores are read. */

@@ -8,8 +8,8 @@ P = 1 << 20  # a fake, 16-byte aligned "device" address (never dereferenced)
 INT = 2 ** 31 - 1
 
 
-def _sample(logits=P, dtype=0, stride=100, vocab=100, rows=2, u=P, t=P, k=P, p=P, m=P, tokens=P,
-            logprobs=P, flags=0, ws=P, ws_bytes=1 << 20):
+def _sample(logits=P, dtype=0, stride=100, vocab=100, rows=2, u=P, t=P, k=P, p=P, m=P, tokens=2 * P,
+            logprobs=3 * P, flags=0, ws=P, ws_bytes=1 << 20):
     return ert.load_library().topk_sample(logits, dtype, stride, vocab, rows, u, t, k, p, m, tokens,
                                           logprobs, flags, ws, ws_bytes, None)
 
@@ -45,7 +45,8 @@ REFUSALS = [
     (_sample, EINVAL, [dict(rows=-1), dict(dtype=3), dict(dtype=-1), dict(vocab=0), dict(stride=99),
                        dict(vocab=(1 << 20) + 1, stride=1 << 21), dict(flags=2), dict(logits=None),
                        dict(u=None), dict(tokens=None),
-                       dict(rows=INT, vocab=1 << 20, stride=1 << 20)]),
+                       dict(rows=INT, vocab=1 << 20, stride=1 << 20), dict(tokens=P), dict(tokens=P + 4),
+                       dict(k=2 * P), dict(k=2 * P + 4), dict(logprobs=2 * P + 4), dict(p=3 * P)]),
     (_sample, ELAYOUT, [dict(logits=P + 2), dict(logits=P + 1, dtype=1), dict(u=P + 2), dict(t=P + 1),
                         dict(k=P + 2), dict(p=P + 2), dict(m=P + 3), dict(tokens=P + 2),
                         dict(logprobs=P + 2), dict(ws=P + 8)]),
@@ -107,6 +108,12 @@ def test_binding_refuses_host_tensors_and_wrong_arguments():
         ert.sample_tokens(x, torch.zeros(2))
     with pytest.raises(TypeError):
         ert.sample_tokens([[0.0]], torch.zeros(1))
+    from exact_row_top_amd import row_ops
+    assert row_ops._int32(-5, "n") == -5
+    with pytest.raises(TypeError):
+        row_ops._int32(2.0, "n")
+    with pytest.raises(ValueError):
+        row_ops._int32(1 << 31, "n")
     with pytest.raises(ValueError):
         ert.route_experts(x, 2)
     with pytest.raises(ValueError):
@@ -135,6 +142,8 @@ def test_binding_refusals_on_the_device():
                 lambda: ert.route_experts(x.long(), 2), lambda: ert.route_experts(x, 2, bias=z(100, dtype=i32)),
                 lambda: ert.route_experts_backward(z(4, 2).half(), x, z(4, 2, dtype=i32)),
                 lambda: ert.route_experts_backward(z(4, 2), x, z(4, 2, dtype=torch.int64)),
+                lambda: ert.route_experts(x, 2.0),
+                lambda: ert.topk_slots(z(4, 4, dtype=i32), z(4, 4, dtype=i32), 16.0),
                 lambda: ert.topk_slots(x, z(4, 4, dtype=i32), 16),
                 lambda: ert.topk_slots(z(4, 4, dtype=i32), z(4, 4), 16),
                 lambda: ert.topk_slots(z(4, 4, dtype=i32), z(4, 4, dtype=i32), 16, slot_dtype=torch.int16),
