@@ -612,7 +612,8 @@ def test_slots_block_sizes(ert, bs):
 def test_slots_many_rows(ert):
     # enough rows for the staged tables, rows over several workgroups
     rng = np.random.default_rng(19)
-    for rows, k, width in ((1200, 512, 300), (700, 2048, 64), (1030, 1001, 900)):
+    for rows, k, width in ((1200, 512, 300), (700, 2048, 64), (1030, 1001, 900), (600, 1024, 512),
+                           (1030, 1001, 500), (512, 513, 256), (300, 5000, 77)):
         tables = rng.permutation(20 * width).reshape(20, width).astype(np.int32)
         idx = rng.integers(-1, width * 16 + 5, (rows, k)).astype(np.int32)
         owner = rng.integers(0, 20, rows).astype(np.int32)
