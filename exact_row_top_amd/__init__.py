@@ -511,4 +511,4 @@ _ROW_OPS = ("sample_tokens", "route_experts", "route_experts_backward", "extend_
 __all__ = ["topk_decode", "topk_prefill", "topk_decode_varlen", "block_max", "workspace_bytes",
            "new_workspace", "status", "plan_query",
            "strerror", "load_library", "TopKError", "STATS_WORDS", "VALID_K", "TOPK_SORTED",
-           "TOPK_DETERMINISTIC"]
+           "TOPK_DETERMINISTIC", *_ROW_OPS]
