@@ -52,6 +52,11 @@ def _tensor(t, name):
     return t
 
 
+def _fits(name, rows, width):
+    if rows >> 31 or width >> 31:
+        raise ValueError(f"{name} is too large: its sizes must fit 32 bits")
+
+
 def _scores(t, name):
     """(rows, width, row stride, dtype code) of a score matrix."""
     code = TOPK_DT.get(t.dtype)
@@ -60,6 +65,7 @@ def _scores(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, width = t.shape
+    _fits(name, rows, width)
     if t.is_contiguous():
         return rows, width, width, code
     stride = t.stride(0) if rows > 1 else width
@@ -174,10 +180,10 @@ def sample_tokens(logits, uniforms, *, temperature=None, top_k=None, top_p=None,
     tokens = _matrix(tokens, "tokens", torch.int32, (rows,), dev)
     if logprobs is not None or return_logprobs:
         logprobs = _matrix(logprobs, "logprobs", torch.float32, (rows,), dev)
-    nbytes = lib.topk_sample_workspace_bytes(rows, min(vocab, (1 << 31) - 1))
+    nbytes = lib.topk_sample_workspace_bytes(rows, vocab)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _check(lib.topk_sample(logits.data_ptr(), code, stride, min(vocab, (1 << 31) - 1), rows, *args,
-                           tokens.data_ptr(), logprobs.data_ptr() if logprobs is not None else None,
+    _check(lib.topk_sample(logits.data_ptr(), code, stride, vocab, rows, *args, tokens.data_ptr(),
+                           logprobs.data_ptr() if logprobs is not None else None,
                            TOPK_SAMPLE_WHOLE_ROW if whole_row else 0, ws.data_ptr(), nbytes,
                            _raw_stream(dev)))
     return tokens if logprobs is None else (tokens, logprobs)
@@ -242,7 +248,9 @@ def route_experts(logits, top_k, *, scoring="softmax", bias=None, num_groups=1, 
 
     Returns (indices, weights), int32 and float32 [tokens, top_k], best first;
     slots without an expert hold -1 and 0.  The weights are differentiable in
-    the logits (a call with stream, indices or weights given is not)."""
+    the logits (a call with stream, indices or weights given is not).  To
+    capture forward and backward into a graph, give it logits that no eager
+    autograd graph still refers to."""
     flags = _route_flags(scoring, group_score, renormalize)
     scale = float(scale)
     topk_groups = num_groups if topk_groups is None else topk_groups
@@ -300,6 +308,7 @@ def _tables_layout(t):
     if t.dim() != 2 or (t.numel() and t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("block_tables must be 2-D with unit inner stride")
     requests, width = t.shape
+    _fits("block_tables", requests, width)
     stride = t.stride(0) if requests > 1 else width
     if stride < width:
         raise ValueError("block_tables rows overlap")
@@ -376,6 +385,7 @@ def topk_slots(indices, block_tables, block_size, *, next_n=1, row_requests=None
     if indices.dim() != 2 or not indices.is_contiguous():
         raise ValueError("indices must be a contiguous int32 [rows, k] tensor")
     rows, k = indices.shape
+    _fits("indices", rows, k)
     dev = indices.device
     requests, width, stride = _tables_layout(block_tables)
     if block_tables.device != dev:

@@ -114,6 +114,9 @@ def test_binding_refuses_host_tensors_and_wrong_arguments():
         row_ops._int32(2.0, "n")
     with pytest.raises(ValueError):
         row_ops._int32(1 << 31, "n")
+    for shape in ((1 << 31, 1), (1, (1 << 32) + 5)):  # would be cut to 32 bits on the way to the C call
+        with pytest.raises(ValueError):
+            row_ops._scores(torch.empty(shape, dtype=torch.float16, device="meta"), "logits")
     with pytest.raises(ValueError):
         ert.route_experts(x, 2)
     with pytest.raises(ValueError):
