@@ -518,25 +518,46 @@ __global__ void __launch_bounds__(kRouteBlock) route_kernel(const RouteParams q)
   }
   wave_sync();
 
-  // the weights, in 64 bits
-  double sum = 0.0;
-  for (int j = l; j < K; j += L) {
-    const int e = mine[j];
-    if (e >= 0) sum += score(Elem<T>::load(row, e));
+  // The weights, in 64 bits.  Softmax scores that are divided by their sum are
+  // taken against the largest of the chosen, which a bias may have kept far
+  // below the token's largest.
+  constexpr int R = kMaxRouteK / L;
+  int named[R];
+  float logit[R];
+  float best = ninf;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = r * L + l;
+    named[r] = j < K ? mine[j] : -1;
+    logit[r] = named[r] >= 0 ? Elem<T>::load(row, named[r]) : ninf;
+    best = fmaxf(best, logit[r]);
   }
-  if (q.renormalize) sum = lanes_sum<L>(sum);
-  if (on)
-    for (int j = l; j < K; j += L) {
-      const int e = mine[j];
-      double w = 0.0;
-      if (e >= 0) {
-        w = score(Elem<T>::load(row, e));
-        if (q.renormalize) w = sum > 0.0 ? w / sum : 0.0;
-        w *= (double)q.scale;
-      }
-      q.indices[token * K + j] = e;
-      q.weights[token * K + j] = (float)w;
-    }
+  if (!q.sigmoid && q.renormalize) {
+    score.top = fold_maxf<L>(best);
+    score.inv_z = 1.0;
+  }
+  double s[R], sum = 0.0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    s[r] = 0.0;
+    if (r * L >= K) continue;
+    if (named[r] >= 0) s[r] = score(logit[r]);
+    sum += s[r];
+  }
+  if (q.renormalize) {
+    sum = lanes_sum<L>(sum);
+    sum = sum > 0.0 ? 1.0 / sum : 0.0;
+  } else {
+    sum = 1.0;
+  }
+  if (!on) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = r * L + l;
+    if (j >= K) continue;
+    q.indices[token * K + j] = named[r];
+    q.weights[token * K + j] = (float)(s[r] * sum * (double)q.scale);
+  }
 }
 
 // ---------------------------------------------------------------------------

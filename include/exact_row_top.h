@@ -449,7 +449,8 @@ int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t v
  *      of the chosen, divided by their sum with TOPK_ROUTE_RENORMALIZE, times
  *      scale; slots without an expert hold -1 and 0, and a sum of zero gives
  *      weights of 0.  Scores are 64-bit numbers: a sigmoid below 1e-308
- *      counts as zero.
+ *      counts as zero; softmax scores that are divided by their sum are taken
+ *      relative to the largest of the chosen.
  *  num_experts 1 .. 1024, top_k 1 .. min(64, num_experts), num_groups 1 .. 16
  *  dividing num_experts, topk_groups 1 .. num_groups. */
 #define TOPK_ROUTE_SIGMOID 1u

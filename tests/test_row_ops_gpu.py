@@ -363,6 +363,26 @@ def test_route_ties_masks_and_extremes(ert, scoring):
                          topk_groups=tg, group_score=gs, renormalize=renorm)
 
 
+def test_route_bias_keeps_the_largest_out(ert):
+    # the chosen lie so far below the token's largest logit that their shares
+    # of the whole softmax are zero in 64 bits; divided by their sum they are not
+    rng = np.random.default_rng(31)
+    x = rng.normal(0, 1, (40, 64)).astype(np.float32)
+    x[:, 5] = np.linspace(600, 3000, 40)
+    bias = np.zeros(64, dtype=np.float32)
+    bias[5] = -4.0
+    for renormalize in (True, False):
+        for top_k in (1, 6, 40):
+            idx, w = ert.route_experts(_cuda(x), top_k, bias=_cuda(bias), renormalize=renormalize)
+            for t in range(40):
+                want, ww = ref.route_token(x[t], top_k, "softmax", bias, renormalize=renormalize)
+                assert np.array_equal(idx[t].cpu().numpy(), want)
+                got = w[t].cpu().numpy()
+                # one rounding to float32 (of 64-bit shares good to 2^-44), half the least number below its normal range
+                assert np.all(np.abs(got - ww) <= 2.0 ** -24 * (1 + 1e-5) * np.abs(ww) + 2.0 ** -150)
+                assert not renormalize or abs(got.sum(dtype=np.float64) - 1) < 1e-5
+
+
 def test_route_many_tokens_strided_and_tied(ert):
     import torch
     rng = np.random.default_rng(7)
