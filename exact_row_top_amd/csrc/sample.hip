@@ -355,8 +355,9 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
 // whose top-k or top-p may lie below the candidates.
 //
 // Bound by its own chain of scans and barriers, not by work: one row of 32768
-// with all cuts takes 11 us, of which reading the records is 1.4, the
-// candidates 1.7, the two cuts 5 and the draw 1.5.
+// with all cuts takes 9.2 us, of which reading the records is 1.3, the
+// candidates 1.8, ranking them with both cuts 2.5 and the draw 1.5 (11 us with
+// a histogram for each cut, which longer lists take).
 // ---------------------------------------------------------------------------
 
 namespace {
@@ -814,6 +815,88 @@ __device__ void draw_from_list(const ListSource& list, RowShared& sh, const Weig
   uint64_t need = (uint64_t)(u * total) + 1;
   if (need > z) need = z;
   rank_short<true, true>(sh, n, need);
+}
+
+// Of n >= 1 distinct keys (at most kShort; one a thread, 0 in the threads
+// behind them, and equal zeros among them), how many are larger than this
+// thread's.  All waves share the comparisons: each takes 64 keys against a
+// part of the list.
+template <int BLOCK>
+__device__ __forceinline__ int rank_of(RowShared& sh, uint64_t key, int n) {
+  const int t = threadIdx.x, wave = t >> 6;
+  __syncthreads();
+  if (t < kShort) {
+    sh.sk[t] = key;
+    sh.cnt[t] = 0;
+  }
+  __syncthreads();
+  const int chunks = (n + 63) / 64;  // 1 .. 4
+  const int slices = chunks == 1 ? BLOCK / 64 : chunks == 2 ? BLOCK / 128 : BLOCK / 256;
+  const int slice = chunks == 1 ? wave : chunks == 2 ? wave >> 1 : wave >> 2;
+  const int e = (chunks == 1 ? 0 : chunks == 2 ? wave & 1 : wave & 3) * 64 + (t & 63);
+  const uint64_t own = sh.sk[e];
+  const int per = ((n + slices - 1) / slices + 7) & ~7;
+  uint32_t count = 0;
+  for (int s = slice * per; s < min((slice + 1) * per, n); s += 8) {
+#pragma unroll
+    for (int o = 0; o < 8; ++o) count += sh.sk[s + o] > own ? 1u : 0u;
+  }
+  if (e < n && count) atomicAdd(&sh.cnt[e], count);
+  __syncthreads();
+  return t < kShort ? (int)sh.cnt[t] : 0;
+}
+
+// Cuts and draw over a list of at most kShort candidates: ranked against each
+// other, one prefix sum of their weights gives the cuts; the kept ones ranked
+// by index, another one the token.  `need` is top-p's mass where no top-k
+// comes before it.
+template <int BLOCK>
+__device__ __forceinline__ void draw_ranked(const ListSource& list, RowShared& sh, const RowAsk& ask,
+                                            uint64_t need, double u, double& total) {
+  const int t = threadIdx.x, n = list.n;
+  uint64_t key = t < n ? order_key(list.x[t], list.i[t]) : 0ull;
+  uint64_t weight = t < n ? list.v[t] : 0ull;
+  int at = rank_of<BLOCK>(sh, key, n);
+  if (t < n) {
+    sh.sk[at] = key;
+    sh.mass[at] = weight;
+  }
+  __syncthreads();
+  // from here on thread t holds the t-th of the order
+  key = t < n ? sh.sk[t] : 0ull;
+  weight = t < n ? sh.mass[t] : 0ull;
+  int keep = ask.cut_k ? min(ask.k, n) : n;
+  const uint64_t to = block_scan<BLOCK>(weight, sh.red);
+  if (t == keep - 1) {
+    sh.before = to;
+    sh.bin = t;
+  }
+  __syncthreads();
+  if (ask.cut_p) {
+    if (ask.cut_k) need = ceil_share(ask.p, (double)sh.before);
+    if (t < keep && to >= need && to - weight < need) sh.bin = t;
+  }
+  __syncthreads();
+  keep = sh.bin + 1;
+  if (t >= keep || weight < ask.min_w) weight = 0;
+  at = rank_of<BLOCK>(sh, t < keep ? (uint64_t)(uint32_t)key : 0ull, keep);  // by ~index
+  if (t < keep) sh.mass[at] = weight;
+  __syncthreads();
+  const uint64_t part = t < keep ? sh.mass[t] : 0ull;
+  const uint64_t run = block_scan<BLOCK>(part, sh.red);
+  if (t == keep - 1) sh.before = run;
+  __syncthreads();
+  const uint64_t z = sh.before;
+  total = (double)z;
+  uint64_t pick = (uint64_t)(u * total) + 1;
+  if (pick > z) pick = z;
+  if (run >= pick && run - part < pick) sh.bin = t;
+  __syncthreads();
+  if (t < keep && at == sh.bin) {
+    sh.found_x = from_key((uint32_t)(key >> 32));
+    sh.found_i = (int)~(uint32_t)key;
+  }
+  __syncthreads();
 }
 
 // 2^(best - m), in the row's units.
@@ -1312,6 +1395,12 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     return;
   }
   if (part > 0) return;
+  if (covered && !ask.cut_k && !ask.cut_p) covered = complete || w(floor) < ask.min_w;
+  if (covered && list.n <= kShort) {
+    draw_ranked<BLOCK>(list, sh, ask, need, u, total);
+    put_token(q, row, sh.found_i, sh.found_x, w, total);
+    return;
+  }
   if (covered) {
     if (ask.cut_k && list.n >= ask.k)
       cut = find_cut<BLOCK, false>(list, sh, w, from, m, cut, q.vocab, (uint64_t)ask.k);
@@ -1319,9 +1408,6 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
       if (ask.cut_k) need = ceil_share(ask.p, (double)mass_in<BLOCK>(list, sh, w, cut, 0));
       cut = find_cut<BLOCK, true>(list, sh, w, from, m, cut, q.vocab, need);
     }
-    if (!ask.cut_k && !ask.cut_p) covered = complete || w(floor) < ask.min_w;
-  }
-  if (covered) {
     draw_from_list<BLOCK>(list, sh, w, cut, ask.min_w, q.vocab, u, total);
     put_token(q, row, sh.found_i, sh.found_x, w, total);
     return;

@@ -184,6 +184,28 @@ def test_sample_crowded_candidates(ert):
     _check_sample(ert, xd, u, "crowded min_p", min_p=[0.5, 1.0, 0.9, 0.1, 0.01, 0.9])
 
 
+def test_sample_candidate_counts(ert):
+    # rows of 1, 2, ... live scores, ties among them: one candidate more or less
+    # than the waves, and the workgroup, rank at once
+    rng = np.random.default_rng(23)
+    counts = [1, 2, 8, 9, 63, 64, 65, 127, 128, 129, 192, 193, 255, 256, 257, 300]
+    vocab, rows = 6 * 2048, len(counts)
+    x = np.full((rows, vocab), NINF)
+    for r, n in enumerate(counts):
+        x[r, rng.permutation(vocab)[:n]] = np.round(rng.normal(0, 2, n) * 8) / 8
+    xd = _cuda(x.astype(np.float32), _dt("bf16"))
+    u = rng.random(rows)
+    one = np.ones(rows)
+    for k in (1, 2, 64, 65, 200, 256, 257):
+        _check_sample(ert, xd, u, f"counts k={k}", top_k=[k] * rows)
+        _check_sample(ert, xd, u, f"counts k={k} and more", top_k=[k] * rows, top_p=0.8 * one, min_p=0.02 * one)
+    _check_sample(ert, xd, u, "counts top-p", top_p=0.7 * one)
+    _check_sample(ert, xd, u, "counts min-p", min_p=0.1 * one)
+    _check_sample(ert, xd, u, "counts cut to one", top_k=[300] * rows, top_p=0 * one)
+    _check_sample(ert, xd, 0 * u, "counts first", top_k=[300] * rows)
+    _check_sample(ert, xd, 0 * u + 0.99999994, "counts last", top_k=[300] * rows)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 def test_sample_low_cuts(ert, dtype):
     # cuts far below the likeliest tokens: each alone, min-p beside them, both
