@@ -15,7 +15,10 @@
 // first: where every score that was taken stands clear of the next one by
 // more than both can be off, the 64-bit order is the same; the experts near
 // the last one of the few tokens (and ties under a bias) where it does not
-// are ranked again by 64-bit scores.
+// are ranked again by 64-bit scores, and so are the groups near the last one
+// that stays, by the experts that can be their largest (a token's whole 64-bit
+// scores instead cost 2 us of the 16384 x 256 call, whose waves all run at
+// once and wait for the slowest).
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -233,7 +236,7 @@ __device__ __forceinline__ void choose64(const RouteParams& q, const float (&x)[
 //
 // Bound by the chain of top_k selections, each a maximum over the token's
 // lanes that the next one waits for (about 0.65 us of a token's time), not by
-// the 17.8 MB read: 16384 x 256 fp32, top 8, takes 11.4 us with softmax and 20
+// the 17.8 MB read: 16384 x 256 fp32, top 8, takes 11.4 us with softmax and 18
 // with sigmoid, bias and 4 of 8 groups; 64 x 128 bf16 5.4.  16 lanes a token
 // let four tokens share each step of a wave: with a wave a token the same
 // softmax calls take 35 and 7.1 us.
@@ -359,12 +362,21 @@ __global__ void __launch_bounds__(kRouteBlock) route_kernel(const RouteParams q)
     float* gs = reinterpret_cast<float*>(group_score[slot]);
     const int size = q.group_size;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      const int e0 = (v * L + l) * V;
+      if (E % V == 0) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = (v * L + l) * V + i;
-        if (e < E) cc[e] = c[v * V + i];
+        for (int i = 0; i < V; i += 4)
+          if (e0 < E)
+            *reinterpret_cast<f4*>(cc + e0 + i) =
+                f4{c[v * V + i], c[v * V + i + 1], c[v * V + i + 2], c[v * V + i + 3]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (e0 + i < E) cc[e0 + i] = c[v * V + i];
       }
+    }
+    if (l >= q.groups && l < kMaxGroups) gs[l] = ninf;  // read four at a time below
     wave_sync();
     // `split` neighbouring lanes a group, each over every split-th part of it
     const int split = 1 << q.group_lanes, g = l >> q.group_lanes, part = l & (split - 1);
@@ -393,24 +405,74 @@ __global__ void __launch_bounds__(kRouteBlock) route_kernel(const RouteParams q)
       b = fmaxf(fmaxf(b, ob), fminf(a, oa));
       a = fmaxf(a, oa);
     }
-    if (g < q.groups && part == 0) gs[g] = (q.top2 && live(b)) ? a + b : a;
+    float* lowest_in = gs + kMaxGroups;  // below these, no expert is one of its group's largest
+    if (g < q.groups && part == 0) {
+      gs[g] = (q.top2 && live(b)) ? a + b : a;
+      lowest_in[g] = (q.top2 ? b : a) - eps;
+    }
     wave_sync();
     const float own = l < q.groups ? gs[l] : ninf;
     bool stay = false;
     if (l < q.groups) {
       int better = 0;
-      for (int h = 0; h < q.groups; ++h) {
-        const float o = gs[h];
-        better += (o > own || (o == own && h < l)) ? 1 : 0;
+      for (int h = 0; h < q.groups; h += 4) {
+        const f4 y = *reinterpret_cast<const f4*>(gs + h);
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+          better += (y[o] > own || (y[o] == own && h + o < l)) ? 1 : 0;
       }
       stay = better < q.topk_groups;
     }
     const float last = -fold_maxf<L>(stay && live(own) ? -own : ninf);
     const float next = fold_maxf<L>(l < q.groups && !stay ? own : ninf);
     unsure = q.bias && live(next) && last - next <= 2.0f * eps;
-    const uint64_t all = __ballot(stay);
-    keep = (uint32_t)(all >> ((threadIdx.x & 63) / L * L)) & 0xFFFFu;
+    const int base = (int)(threadIdx.x & 63) / L * L;  // the token's first lane
+    auto token_mask = [&](bool p) { return (uint32_t)(__ballot(p) >> base) & 0xFFFFu; };
+    keep = token_mask(stay);
     wave_sync();
+    if (unsure) {
+      // Only groups as near to the border as two sums can be off are open, and
+      // of them only the experts that can be their largest: one a lane, in 64
+      // bits.  More of those than kNear: all of the token's, below.
+      const bool open = live(own) && own >= last - 2.0f * eps && own <= next + 2.0f * eps;
+      const uint32_t opened = token_mask(open), sure = token_mask(stay && !open);
+      int32_t* near = mine;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = (i / V * L + l) * V + i % V;
+        const uint32_t h = group_of(q, e) & 15u;
+        const bool in = live(c[i]) && ((opened >> h) & 1u) && c[i] >= lowest_in[h];
+        const uint64_t bits = __ballot(in) >> base;
+        const uint64_t m = L == 64 ? bits : bits & ((1ull << (L & 63)) - 1);
+        const int at = n + __popcll(m & ((1ull << l) - 1));
+        if (in && at < kNear) near[at] = e;
+        n += __popcll(m);
+      }
+      wave_sync();
+      if (n <= kNear) {
+        unsure = false;
+        const int e = l < n ? near[l] : 0;
+        const double d = l < n ? score(Elem<T>::load(row, e)) + (double)q.bias[e] : 0.0;
+        const int of = (int)group_of(q, e);
+        double first = -__builtin_inf(), second = -__builtin_inf();
+        for (int o = 0; o < n; ++o) {
+          const double y = __shfl(d, base + o);
+          if (__shfl(of, base + o) == l) {
+            second = fmax(second, fmin(first, y));
+            first = fmax(first, y);
+          }
+        }
+        if (q.top2 && second > -__builtin_inf()) first += second;
+        int better = 0;
+        for (int h = 0; h < q.groups; ++h) {
+          const double y = __shfl(first, base + h);
+          if ((opened >> h) & 1u) better += (y > first || (y == first && h < l)) ? 1 : 0;
+        }
+        keep = sure | token_mask(open && better < q.topk_groups - __popc(sure));
+      }
+      wave_sync();
+    }
   }
   if (q.groups > 1 && unsure)
     keep = groups64<T, L, EPL>(q, x, score, l, lds + (int64_t)slot * E, group_score[slot]);
@@ -425,9 +487,21 @@ __global__ void __launch_bounds__(kRouteBlock) route_kernel(const RouteParams q)
     uint32_t k = fkey(c[i]) >> 1;
     if (q.bias) k = (k & ~15u) | (uint32_t)(EPL - 1 - i);
     else if (NARROW) k = (k >> 12) << 10 | (uint32_t)(1023 - e);
-    bool in = live(c[i]);
-    if (q.groups > 1) in = in && ((keep >> group_of(q, e)) & 1u);
-    key[i] = in ? k : 0u;
+    key[i] = live(c[i]) ? k : 0u;
+  }
+  if (q.groups > 1) {
+    if (q.group_size % V == 0) {  // neighbours share their group
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const bool in = (keep >> group_of(q, (v * L + l) * V)) & 1u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[v * V + i] = in ? key[v * V + i] : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (!((keep >> group_of(q, (i / V * L + l) * V + i % V)) & 1u)) key[i] = 0u;
+    }
   }
 
   // one more than asked for, to see that the last one stands clear

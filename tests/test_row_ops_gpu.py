@@ -442,6 +442,36 @@ def test_route_near_ties(ert):
         _check_route(ert, _cuda(base), 12, f"near ties {scoring}, one group", bias=b, scoring=scoring)
 
 
+@pytest.mark.parametrize("experts,groups,topk_groups", [(256, 8, 4), (64, 4, 2), (60, 6, 3), (512, 16, 7), (48, 16, 5)])
+def test_route_near_group_borders(ert, experts, groups, topk_groups):
+    # group scores that are equal, a few 2^-24 apart, or clear; of two, several
+    # and all groups; groups with one live expert and with none
+    rng = np.random.default_rng([experts, groups])
+    size = experts // groups
+    T = 96
+    x = rng.normal(-2, 0.5, (T, experts)).astype(np.float32)
+    for t in range(T):
+        near = rng.permutation(groups)[:2 + t % groups] if t % 3 else np.arange(groups)
+        for g in range(groups):
+            lead = 1.5 if g in near else rng.choice([0.5, 1.0, 2.0, 2.5])
+            a, b = rng.permutation(size)[:2]
+            step = 2.0 ** -22 * rng.integers(0, 3, 2)
+            x[t, g * size + a] = np.float32(lead + step[0])
+            x[t, g * size + b] = np.float32(lead - 0.25 * (t % 2) + step[1])
+        if t % 5 == 0:
+            g = rng.integers(groups)
+            x[t, g * size:(g + 1) * size - 1] = NINF
+        if t % 7 == 0:
+            x[t, :size] = NINF
+    bias = (rng.integers(0, 2, experts) * 2.0 ** -23).astype(np.float32)
+    for scoring, how in itertools.product(("sigmoid", "softmax"), ("max", "top2")):
+        for b in (bias, np.zeros(experts, np.float32)):
+            _check_route(ert, _cuda(x), min(8, topk_groups * size), f"group borders {scoring} {how}", bias=b,
+                         scoring=scoring, num_groups=groups, topk_groups=topk_groups, group_score=how)
+    _check_route(ert, _cuda(x, _dt("bf16")), 4, "group borders bf16", bias=bias, scoring="sigmoid",
+                 num_groups=groups, topk_groups=topk_groups, group_score="top2")
+
+
 def _check_grad(ert, x, idx, g, what, **kw):
     """One fp32 rounding of each of at most three terms (3 * 2^-24 of their
     size), then one rounding to the output type (half a step, or half the
