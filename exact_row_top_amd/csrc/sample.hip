@@ -917,8 +917,10 @@ __device__ __forceinline__ double below_best(float best, const Weigher& w) {
 // Sums are whole numbers, so which workgroup is last changes nothing.  What
 // crosses between workgroups goes through agent-scope atomics, complete
 // before their workgroup counts itself; nobody waits for anybody.
-// Rows with cuts and +inf scores, and bins with more members than fit, are
-// selected by one workgroup from memory, pass by pass.
+// Of more members than fit, all of one value, the first so many are kept, found
+// by their counts in the segments.  Rows with cuts and +inf scores, and bins
+// with more members than fit of several values, are selected by one workgroup
+// from memory, pass by pass.
 //
 // Both steps are bound by the exponentials (64 x 131072 with mixed cuts: row
 // kernel 19 us, wide kernel 19 us, of which 8 each are the waves' work and
@@ -954,21 +956,25 @@ __device__ __forceinline__ bool last_in(uint32_t* counter, int workgroups, RowSh
   return last;
 }
 
-// One wave's segment, as the segment kernel reads it; dead scores are -inf.
+// One wave's segment, as the segment kernel reads it, dead scores as -inf: f
+// of four neighbouring scores of every lane and the first one's index, the
+// code once with the scores moving up (unrolled, the callers' conversions to
+// 64 bits are all made first and fill the registers; the times are the same).
 template <class T, class F>
-__device__ __forceinline__ void visit_segment(const RowView<T>& view, int seg, F&& f) {
+__device__ __forceinline__ void visit_fours(const RowView<T>& view, int seg, F&& f) {
   constexpr int V = Elem<T>::kVec;
   constexpr int G = RowView<T>::kGroups;
   const int lane = threadIdx.x & 63;
-  float x[G][V];
+  float x[G][V], y[G * V];
   view.segment(seg, lane, x);
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+  for (int i = 0; i < G * V; ++i) y[i] = x[i / V][i % V];
+#pragma unroll 1
+  for (int r = 0; r < G * V / 4; ++r) {
+    f(y, (seg * (kSegment / V) + r / (V / 4) * 64 + lane) * V + r % (V / 4) * 4 - view.lead);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      f(x[g][e], (seg * (kSegment / V) + g * 64 + lane) * V + e - view.lead);
-      if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int i = 0; i + 4 < G * V; ++i) y[i] = y[i + 4];
+  }
 }
 
 // One wave's segment again: f(x) for the scores that `take` admits, 64 at a
@@ -978,33 +984,26 @@ __device__ __forceinline__ void visit_segment(const RowView<T>& view, int seg, F
 template <class T, class Take, class F>
 __device__ __forceinline__ void visit_dense(const RowView<T>& view, int seg, float* buf, Take&& take,
                                             F&& f) {
-  constexpr int V = Elem<T>::kVec;
-  constexpr int G = RowView<T>::kGroups;
   const int lane = threadIdx.x & 63;
-  float x[G][V];
-  view.segment(seg, lane, x);
   int n = 0;
+  visit_fours(view, seg, [&](const float* y, int pos) {
 #pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int e0 = 0; e0 < V; e0 += 4) {
-#pragma unroll
-      for (int e = e0; e < e0 + 4; ++e) {
-        const bool in = take(x[g][e], (seg * (kSegment / V) + g * 64 + lane) * V + e - view.lead);
-        const uint64_t mask = __ballot(in);
-        const int at = n + (int)__builtin_amdgcn_mbcnt_hi(
-                               (uint32_t)(mask >> 32),
-                               __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
-        if (in) buf[at] = x[g][e];
-        n += __popcll(mask);
-      }
-      wave_sync();
-      while (n >= 64) {
-        n -= 64;
-        f(buf[n + lane]);
-      }
-      wave_sync();
+    for (int e = 0; e < 4; ++e) {
+      const bool in = take(y[e], pos + e);
+      const uint64_t mask = __ballot(in);
+      const int at = n + (int)__builtin_amdgcn_mbcnt_hi(
+                             (uint32_t)(mask >> 32),
+                             __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+      if (in) buf[at] = y[e];
+      n += __popcll(mask);
     }
+    wave_sync();
+    while (n >= 64) {
+      n -= 64;
+      f(buf[n + lane]);
+    }
+    wave_sync();
+  });
   if (n > 0) f(lane < n ? buf[lane] : -__builtin_inff());
 }
 
@@ -1031,12 +1030,16 @@ __device__ __forceinline__ void fill_bins(const RowView<T>& view, int seg, int n
             if (v) atomicAdd((unsigned long long*)&sh.mass[wide_bin(s, rate)], v);
           });
     else
-      visit_segment(view, seg, [&](float x, int) {
-        const double s = w.log2_of(x);
-        if (s > -kTmax) {
-          const int b = wide_bin(s, rate);
-          atomicAdd(&sh.cnt[b], 1u);
-          if (by_mass) atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)drawn_at(w, s));
+      visit_fours(view, seg, [&](const float* y, int) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const double s = w.log2_of(y[e]);
+          if (s > -kTmax) {
+            const int b = wide_bin(s, rate);
+            atomicAdd(&sh.cnt[b], 1u);
+            if (by_mass)
+              atomicAdd((unsigned long long*)&sh.mass[b], (unsigned long long)drawn_at(w, s));
+          }
         }
       });
   }
@@ -1456,14 +1459,20 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
     const int mine = min(nseg - part * kWideSegs, kWideSegs) * kSegSlots;  // places for this part's
     if (t == 0) sh.list_n = 0;
     __syncthreads();
+    SegRecord* recs = q.records + (int64_t)row * nseg;  // free again: the members' count and extremes
     if (seg < nseg) {
       uint64_t mass = 0;
+      int own = 0;
+      float lo = __builtin_inff(), hi = -__builtin_inff();
       visit_dense(
           view, seg, sh.dense[t >> 6],
           [&](float x, int i) {
             const bool kept_above = x >= above;
             const bool member = (x >= from && !kept_above) || (x >= from_k && !(x >= above_k));
             if (member && w.drawable(x)) {
+              ++own;
+              lo = fminf(lo, x);
+              hi = fmaxf(hi, x);
               const int at = (int)atomicAdd(&sh.list_n, 1u);
               if (at < mine)
                 agent_store(&members[part * room + at],
@@ -1476,7 +1485,14 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
             mass += v >= least ? v : 0ull;
           });
       mass = wave_sum(mass);
-      if ((t & 63) == 0) agent_store(&kept[seg], mass);
+      own = wave_sum(own);
+      wave_minmax(lo, hi);
+      if ((t & 63) == 0) {
+        agent_store(&kept[seg], mass);
+        agent_store(&recs[seg].count, own);
+        agent_store(&recs[seg].mass,
+                    ((uint64_t)__float_as_uint(hi) << 32) | (uint64_t)__float_as_uint(lo));
+      }
     }
     __syncthreads();
     if (t == 0) agent_store(&kept[nseg + part], (uint64_t)sh.list_n);
@@ -1491,7 +1507,8 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
       fits = fits && c <= min(nseg - p * kWideSegs, kWideSegs) * kSegSlots;
       n += c;
     }
-    if (fits && n <= kListS) {
+    bool ready = fits && n <= kListS;  // each segment's kept mass, in the bins
+    if (ready) {
       const ListSource list{sh.lx, sh.li, sh.lw, n};
       // the extremes of top-p's members and of top-k's
       float low = __builtin_inff(), high = -__builtin_inff(), low_k = low, high_k = high;
@@ -1536,6 +1553,43 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
         if (cut.holds(x, i) && v >= ask.min_w)
           atomicAdd((unsigned long long*)&sh.mass[(i + view.lead) / kSegment], (unsigned long long)v);
       });
+    } else {
+      // Too many to list, which mostly are equal scores (16-bit logits far
+      // from zero, or a constant row): of one value, the first so many.
+      float lo = __builtin_inff(), hi = -__builtin_inff();
+      clear_bins<kWideBlock>(sh);
+      for (int s = t; s < nseg; s += kWideBlock) {
+        const uint64_t ends = agent_load(&recs[s].mass);
+        sh.cnt[s] = (uint32_t)agent_load(&recs[s].count);
+        lo = fminf(lo, __uint_as_float((uint32_t)ends));
+        hi = fmaxf(hi, __uint_as_float((uint32_t)(ends >> 32)));
+      }
+      block_min_max<kWideBlock>(lo, hi, sh.redf);
+      ready = lo == hi;
+      if (ready) {
+        const uint64_t one = w.drawn(lo);
+        uint64_t take = (uint64_t)n, before;
+        if (need_k > 0) {
+          take = min(take, (uint64_t)need_k);
+          if (ask.cut_p) need_cut = ceil_share(ask.p, (double)(wr->mass_k + take * one)) - wr->before;
+        }
+        if (need_cut > 0 && one > 0) take = min(take, (need_cut + one - 1) / one);
+        int at;
+        cross_bins<kWideBlock, false>(sh, take, at, before);
+        take -= before;
+        cut.x = lo;
+        if (one > 0) {  // (else it makes no difference which of them are kept)
+          pick_in_segment<kWideBlock>(
+              view, at, sh, w, [&](float x, int) { return x == lo; }, take * one);
+          cut.i = sh.found_i;
+        }
+        for (int s = t; s < nseg; s += kWideBlock) {
+          const uint64_t count = s < at ? sh.cnt[s] : s == at ? take : 0ull;
+          sh.mass[s] = agent_load(&kept[s]) + (one >= least ? count * one : 0ull);
+        }
+      }
+    }
+    if (ready) {
       __syncthreads();
       uint64_t z = 0;
       for (int s = t; s < nseg; s += kWideBlock) z += sh.mass[s];

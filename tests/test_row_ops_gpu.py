@@ -260,6 +260,38 @@ def test_sample_both_cuts_low(ert, dtype):
                   temperature=np.array([1, 0.2, 3, 1, 1, 8, 0, 1.0]))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_sample_crowds_of_equal_scores(ert, dtype):
+    # more scores of the cut's own value than are listed: constant rows, two
+    # values, a crowd below a few others, masks between, crowds in some segments
+    # only, several crowded values
+    rng = np.random.default_rng(29)
+    vocab, rows = 20011, 9
+    x = np.zeros((rows, vocab))
+    x[1, :] = -3.5
+    x[1, rng.permutation(vocab)[:300]] = rng.normal(0, 0.5, 300)
+    x[2, ::3] = NINF
+    x[3] = np.where(rng.random(vocab) < 0.5, 1.0, 0.5)
+    x[4, :9000] = -30
+    x[5] = rng.normal(-8, 1, vocab)
+    x[5, 3000:9000] = -2.25
+    x[6] = rng.integers(0, 4, vocab) * 0.25
+    x[7, 1] = 2.0
+    x[8] = np.round(rng.normal(-20, 2, vocab))
+    xd = _cuda(x.astype(np.float32), _dt(dtype))
+    u = rng.random(rows)
+    one = np.ones(rows)
+    for p in (0.01, 0.5, 0.97):
+        _check_sample(ert, xd, u, f"{dtype} crowds p={p}", top_p=p * one)
+        _check_sample(ert, xd, u, f"{dtype} crowds p={p} and k", top_p=p * one, top_k=[6000] * rows)
+    for k in (250, 301, 2500, 8000, 20010):
+        _check_sample(ert, xd, u, f"{dtype} crowds k={k}", top_k=[k] * rows)
+    _check_sample(ert, xd, u, f"{dtype} crowds min-p", top_k=[8000] * rows, min_p=0.1 * one)
+    _check_sample(ert, xd, u, f"{dtype} crowds and min-p", top_p=0.9 * one, min_p=0.5 * one)
+    _check_sample(ert, xd, 0 * u, f"{dtype} crowds first", top_p=0.9 * one)
+    _check_sample(ert, xd, 0 * u + 0.99999994, f"{dtype} crowds last", top_p=0.9 * one)
+
+
 def test_sample_low_cuts_side_by_side(ert):
     # rows that several workgroups share, in two graphs and eagerly on two
     # streams at once, again and again
