@@ -325,6 +325,38 @@ def test_sample_low_cuts_side_by_side(ert):
             assert torch.equal(got, want)
 
 
+def test_sample_both_low_cuts_and_crowds_side_by_side(ert):
+    # the same with both cuts, and rows in which one value is crowded
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    x = (torch.randn(20, 50003, device="cuda", generator=g) * 2 - 25).bfloat16()
+    x[3] = 0.5
+    x[4, ::2] = 1.0
+    u = torch.rand(20, device="cuda", generator=g)
+    p = torch.full((20,), 0.9, device="cuda")
+    k = torch.randint(3, 30000, (20,), device="cuda", generator=g, dtype=torch.int32)
+    calls = [dict(top_p=p), dict(top_k=k), dict(top_k=k, top_p=p)]
+    want = [ert.sample_tokens(x, u, whole_row=True, **kw).clone() for kw in calls]
+    torch.cuda.synchronize()
+    graphs = []
+    for kw in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = ert.sample_tokens(x, u, **kw)
+        graphs.append((graph, out))
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(4):
+        eager = []
+        for stream, kw, (graph, _) in zip(streams, calls, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+                eager.append(ert.sample_tokens(x, u, **kw))
+        torch.cuda.synchronize()
+        for got, (_, out), right in zip(eager, graphs, want):
+            assert torch.equal(got, right) and torch.equal(out, right)
+
+
 def test_sample_outputs_given_and_empty_batch(ert):
     import torch
     x = torch.randn(4, 999, device="cuda")
