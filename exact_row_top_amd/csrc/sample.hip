@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
         // best k and room for an uneven spread, within what fits; 16 where
         // only the weights say how many are needed.  With j of the 64 lane
         // maxima at or above the floor, about -64 ln(1 - j / 64) scores are.
+        // (64 x 16000: top-k 300, whose candidates fit, takes 20 us, top-k
+        // 1000, whose do not, 33.)
         float want = 16.0f;
         if (ask.cut_k) {
           const float share = (float)ask.k / (float)q.segments;
