@@ -920,9 +920,9 @@ __device__ __forceinline__ double below_best(float best, const Weigher& w) {
 // crosses between workgroups goes through agent-scope atomics, complete
 // before their workgroup counts itself; nobody waits for anybody.
 // Of more members than fit, all of one value, the first so many are kept, found
-// by their counts in the segments.  Rows with cuts and +inf scores, and bins
-// with more members than fit of several values, are selected by one workgroup
-// from memory, pass by pass.
+// by their counts in the segments.  Rows with cuts and more +inf scores than
+// are handed on, and bins with more members than fit of several values, are
+// selected by one workgroup from memory, pass by pass.
 //
 // Both steps are bound by the exponentials (64 x 131072 with mixed cuts: row
 // kernel 19 us, wide kernel 19 us, of which 8 each are the waves' work and
@@ -1259,8 +1259,8 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     return;
   }
 
-  // no drawable score lies below the floor
-  const bool complete = floor == ninf || !w.drawable(floor);
+  // no drawable score lies below the floor (beside +inf nothing else is drawable)
+  const bool complete = floor == ninf || m == __builtin_inff() || !w.drawable(floor);
   // at or below every drawable score
   const float least = (float)fmax((double)m - 1.0001 * kTmax / ask.c, -(double)__FLT_MAX__);
   WideRow* wr = q.wide + row;
@@ -1418,7 +1418,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     return;
   }
 
-  // +inf scores, or (needing no bins) min-p alone
+  // +inf scores that were not all handed on, or (needing no bins) min-p alone
   if (t == 0) {
     wr->edge[0] = ninf;
     wr->edge[1] = wr->edge[2] = wr->edge[3] = __builtin_nanf("");

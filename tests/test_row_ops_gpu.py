@@ -292,6 +292,31 @@ def test_sample_crowds_of_equal_scores(ert, dtype):
     _check_sample(ert, xd, 0 * u + 0.99999994, f"{dtype} crowds last", top_p=0.9 * one)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_sample_infinities_that_are_candidates(ert, dtype):
+    # so many +inf scores in a segment that its floor is +inf, and all of them
+    # candidates: the cuts are of those scores alone
+    rng = np.random.default_rng(41)
+    vocab, counts = 4500, [1, 14, 15, 16, 40, 64, 100, 128]
+    x = rng.normal(0, 2, (len(counts) + 2, vocab))
+    for r, n in enumerate(counts):
+        x[r, np.arange(n) * 16 + r] = np.inf             # one a lane while there are lanes
+    x[-2, :4 * 40:4] = np.inf
+    x[-2, 2100:2100 + 3 * 60:3] = np.inf                 # in two segments
+    x[-1, :300] = np.inf                                 # more than a segment hands on
+    xd = _cuda(x.astype(np.float32), _dt(dtype))
+    short = _cuda(np.full((x.shape[0], 128), np.inf, dtype=np.float32), _dt(dtype))
+    u = rng.random(x.shape[0])
+    one = np.ones(x.shape[0])
+    for t, name in ((xd, "some"), (short, "all")):
+        for p in (0.0, 0.1, 0.5, 0.9):
+            _check_sample(ert, t, u, f"{dtype} {name} +inf p={p}", top_p=p * one)
+            _check_sample(ert, t, u, f"{dtype} {name} +inf p={p} and min-p", top_p=p * one, min_p=0.3 * one)
+            _check_sample(ert, t, u, f"{dtype} {name} +inf p={p} and k", top_p=p * one, top_k=[25] * len(u))
+        _check_sample(ert, t, u, f"{dtype} {name} +inf k", top_k=[12] * len(u))
+        _check_sample(ert, t, u, f"{dtype} {name} +inf min-p", min_p=0.3 * one)
+
+
 def test_sample_low_cuts_side_by_side(ert):
     # rows that several workgroups share, in two graphs and eagerly on two
     # streams at once, again and again
