@@ -11,9 +11,18 @@
 // Weights are whole numbers: 2^43 times the value, rounded once, from an
 // exponential good to 46 bits in 64-bit arithmetic.  Their sums are exact in
 // 64 bits (at most 2^20 weights of at most 2^43) and the same in every order,
-// so atomics and splits never change a token; and a token differs from the
-// real-number definition only if u lies within about 1e-12 of a border.
-// Weights below 2^-44 of the largest count as zero.
+// so atomics and splits never change a token.  Weights of 2^-44 of the largest
+// and less are zero, and such a token is never drawn.
+//
+// A weight is off by at most half a unit, 2^-44 of the largest (equal scores
+// all to the same side), so a token differs from the real-number definition
+// only if u Z lies within vocab * 2^-44 of a border: 6e-8 for 2^20 equal
+// scores at worst, about 1e-11 for ordinary rows.  Two sums are taken before
+// the row's largest score is known, each segment against its own and then
+// brought to the row's unit: the total of a row without a cut, and the total
+// that a top-p without a top-k takes its share of.  They are off by no more
+// than that either, but not by the same amount as a sum of the row's weights.
+// Segments whose largest score weighs nothing in the row add nothing to them.
 //
 // Three launches, the third only where a row may have a cut: the segment
 // kernel reads the logits once, a wave for each 2048 scores; the row kernel
@@ -630,9 +639,10 @@ __device__ int find_index(const Src& src, RowShared& sh, const Weigher& w, int f
 }
 
 // The lowest index of a segment at which the running mass of the scores that
-// `pred` admits reaches `need` (at most their total), with its score: every
-// thread's scores lie side by side, so one prefix sum over the workgroup
-// finds the thread and a walk over its registers the score.
+// `pred` admits reaches `need` (or their total, which is not zero, if that is
+// less), with its score: every thread's scores lie side by side, so one prefix
+// sum over the workgroup finds the thread and a walk over its registers the
+// score.
 template <int BLOCK, class T, class Pred>
 __device__ __forceinline__ void pick_in_segment(const RowView<T>& view, int seg, RowShared& sh,
                                                 const Weigher& w, Pred&& pred, uint64_t need) {
@@ -661,7 +671,10 @@ __device__ __forceinline__ void pick_in_segment(const RowView<T>& view, int seg,
       own += v[g][e];
     }
   const uint64_t incl = block_scan<BLOCK>(own, sh.red);
-  uint64_t run = incl - own;
+  uint64_t run = incl - own, total = 0;
+#pragma unroll
+  for (int o = 0; o < BLOCK / 64; ++o) total += sh.red[o];
+  need = need < total ? need : total;
   if (run < need && need <= incl) {
 #pragma unroll
     for (int g = 0; g < PER; ++g)
@@ -901,9 +914,10 @@ __device__ __forceinline__ void draw_ranked(const ListSource& list, RowShared& s
   __syncthreads();
 }
 
-// 2^(best - m), in the row's units.
+// What a segment's weights against its own best score come to against the
+// row's: 2^(best - m), or nothing if even that score's weight is zero.
 __device__ __forceinline__ double below_best(float best, const Weigher& w) {
-  return best == w.m ? 1.0 : exp2_64(w.log2_of(best), w.poly);
+  return best == w.m ? 1.0 : w(best) > 0 ? exp2_64(w.log2_of(best), w.poly) : 0.0;
 }
 
 // ---------------------------------------------------------------------------
@@ -1212,7 +1226,7 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     // u * total, then the place inside it.
     double* seg_m = reinterpret_cast<double*>(sh.mass);  // kBinsS entries >= segments
     for (int s = t; s < nseg; s += BLOCK)
-      seg_m[s] = sh.seg_best[s] > ninf ? below_best(sh.seg_best[s], w) * (double)sh.seg_mass[s] : 0.0;
+      seg_m[s] = below_best(sh.seg_best[s], w) * (double)sh.seg_mass[s];
     __syncthreads();
     double own = 0.0;
     const int per = (nseg + BLOCK - 1) / BLOCK;
@@ -1246,15 +1260,10 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     const int seg = sh.found_i;
     if (mine == seg) sh.redd[30] = mine_before;
     __syncthreads();
-    const float best = sh.seg_best[seg];
-    const uint64_t mass = sh.seg_mass[seg];
-    double rest = (y - sh.redd[30]) / below_best(best, w);
-    if (!(rest > 0.0)) rest = 0.0;
-    uint64_t need = rest < (double)mass ? (uint64_t)rest + 1 : mass;
-    if (need > mass) need = mass;
-    w.against(best);
-    pick_in_segment<BLOCK>(view, seg, sh, w, [](float, int) { return true; }, need);
-    w.against(m);
+    // inside it the weights are the row's again
+    const double rest = y - sh.redd[30];
+    pick_in_segment<BLOCK>(view, seg, sh, w, [](float, int) { return true; },
+                           rest > 0.0 ? (uint64_t)rest + 1 : 1ull);
     put_token(q, row, sh.found_i, sh.found_x, w, total);
     return;
   }
@@ -1273,12 +1282,11 @@ __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q)
     bool low_cut;
     if (!ask.cut_k) {
       double z = 0.0, top = 0.0;
-      for (int s = t; s < nseg; s += BLOCK)
-        if (sh.seg_best[s] > ninf) {
-          const double unit = below_best(sh.seg_best[s], w);
-          z += unit * (double)sh.seg_mass[s];
-          top += unit * (double)sh.seg_upper[s];
-        }
+      for (int s = t; s < nseg; s += BLOCK) {
+        const double unit = below_best(sh.seg_best[s], w);
+        z += unit * (double)sh.seg_mass[s];
+        top += unit * (double)sh.seg_upper[s];
+      }
       block_sum2<BLOCK>(z, top, sh.redd);
       need = ceil_share(ask.p, z);
       low_cut = top < (double)need;

@@ -414,7 +414,13 @@ int topk_validate(int32_t mode, const void* logits, int64_t row_stride, const vo
  * are clamped into it, NaN counts as 0.  A temperature that is not > 0 gives
  * the first token of the order.  A row without a drawable token gives -1.
  * Weights are held as whole multiples of 2^-43 of the largest, so results do
- * not depend on the order of any sum; weights below 2^-44 count as zero.
+ * not depend on the order of any sum; weights of 2^-44 and less count as zero
+ * and their tokens are never drawn.  A sum of weights is thus off by at most
+ * vocab * 2^-44 of the largest, and so are the borders between tokens, the
+ * cuts' and the total in logprobs.  (The total of a row without a cut, and the
+ * one that a top_p without a top_k takes its share of, are sums of weights
+ * rounded more finely: within the same bound, but not to the bit what the
+ * multiples add up to.)
  *  temperature, top_p, min_p: device float[num_rows], top_k: device
  *      int32[num_rows]; each may be NULL (temperature 1, no cut).
  *  logprobs: optional device float[num_rows]: ln(w_token / kept total) (0 for
@@ -424,7 +430,8 @@ int topk_validate(int32_t mode, const void* logits, int64_t row_stride, const vo
  *      16-byte aligned; it needs no initialisation and holds nothing between
  *      calls (TOPK_EWORKSPACE if NULL or too small).
  *  flags: TOPK_SAMPLE_WHOLE_ROW reads every row again instead of using the
- *      candidates of its first reading (same results; for tests). */
+ *      candidates and sums of its first reading (for tests; the same results
+ *      but for borders and totals within that bound of each other). */
 #define TOPK_SAMPLE_WHOLE_ROW 1u
 
 size_t topk_sample_workspace_bytes(int32_t num_rows, int32_t vocab);

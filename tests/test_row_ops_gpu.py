@@ -317,6 +317,72 @@ def test_sample_infinities_that_are_candidates(ert, dtype):
         _check_sample(ert, t, u, f"{dtype} {name} +inf min-p", min_p=0.3 * one)
 
 
+def _check_sample_near(ert, x, u, what, temperature=None, top_k=None, min_p=None):
+    """Scores so far down that their weights are a few units of 2^-43, each off
+    by up to half a unit, 2^-44: u Z may then lie in any token whose interval
+    of the weights' running sum is within vocab * 2^-44 of it, but only in one
+    that has a weight of 2^-44 or more, and u = 0 in the first of those alone."""
+    host = x.cpu().numpy().astype(np.longdouble)
+    rows, vocab = host.shape
+    off = np.longdouble(vocab) * np.longdouble(2) ** -44
+    kw = {k: _cuda(np.full(rows, v, np.int32 if k == "top_k" else np.float32))
+          for k, v in (("temperature", temperature), ("top_k", top_k), ("min_p", min_p)) if v is not None}
+    u = np.float32(u)
+    for whole in (False, True):
+        log(f"[sample] {what} whole_row={whole}")
+        tok, lp = ert.sample_tokens(x, _cuda(np.full(rows, u)), return_logprobs=True, whole_row=whole, **kw)
+        tok, lp = tok.cpu().numpy(), lp.cpu().numpy()
+        for r in range(rows):
+            w = np.exp((host[r] - host[r].max()) / np.longdouble(np.float32(temperature or 1.0)))
+            w = np.where(w < np.longdouble(2) ** -44, 0, w)
+            if top_k is not None:
+                w[np.argsort(-host[r], kind="stable")[top_k:]] = 0
+            run, t = np.cumsum(w), tok[r]
+            y = np.longdouble(u) * run[-1]
+            assert w[t] > 0 and run[t] - w[t] - off <= y <= run[t] + off, (what, whole, r, t)
+            assert u > 0 or t == np.flatnonzero(w)[0], (what, whole, r, t)
+            want = np.log(w[t] / run[-1])
+            assert abs(lp[r] - want) <= 2.0 ** -24 * abs(want) * 1.001 + off / run[-1], (what, whole, r, lp[r], want)
+
+
+@pytest.mark.parametrize("gap", [29.0, 30.0, 31.0, 37.5, 44.0, 60.0])
+def test_sample_segments_far_below_the_best(ert, gap):
+    # weights of 2^-44 and less are zero, whatever the other scores of their
+    # segment: small uniforms draw the first token that has a weight
+    vocab = 3 * 2048 + 777
+    x = np.zeros((6, vocab))
+    x[0, :2048] = -gap                        # a segment of them in front
+    x[1, :4096] = -gap                        # two
+    x[2, :-1] = -gap                          # all but the last token
+    x[3, :5000] = -gap                        # and a segment of both
+    x[3, 100] = -3.0
+    x[4, :2048] = -gap                        # one of them a little higher
+    x[4, 700] = 0.5 - gap
+    x[5, 2048:] = -gap                        # behind
+    xd = _cuda(x.astype(np.float32))
+    for u in (0.0, 2.0 ** -40, 2.0 ** -24, 0.5, 1 - 2.0 ** -24):
+        _check_sample_near(ert, xd, u, f"gap={gap} u={u}, no cut")
+        _check_sample_near(ert, xd, u, f"gap={gap} u={u}, cold", temperature=0.05)
+        _check_sample_near(ert, xd / 16, u, f"gap={gap} u={u}, colder scores", temperature=1 / 16)
+        _check_sample_near(ert, xd, u, f"gap={gap} u={u}, min-p that cuts nothing", min_p=1e-30)
+        _check_sample_near(ert, xd, u, f"gap={gap} u={u}, top-k of all but one", top_k=vocab - 1)
+
+
+def test_sample_top_p_beside_a_tail_without_weight(ert):
+    # 129024 scores of 2^-45 together weigh 3.7e-9 of the best, as much as one
+    # of the 64 tokens among which 1 - top_p = 2^-24 falls; they count nothing
+    vocab = 64 * 2048
+    x = np.full((2, vocab), -31.2)
+    x[:, 1:2048] = NINF
+    x[:, 0] = 0.0
+    x[:, 1:65] = -19.5
+    x[1] = x[1, ::-1]
+    p = np.full(2, 1 - 2.0 ** -24)
+    for u in (0.0, 0.5, 1 - 2.0 ** -23, 1 - 2.0 ** -24):
+        _check_sample(ert, _cuda(x.astype(np.float32)), np.full(2, u), f"tail u={u}", top_p=p)
+        _check_sample(ert, _cuda(x.astype(np.float32)), np.full(2, u), f"tail u={u}, no cut")
+
+
 def test_sample_low_cuts_side_by_side(ert):
     # rows that several workgroups share, in two graphs and eagerly on two
     # streams at once, again and again
