@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
   constexpr int TOKENS = kRouteBlock / L;
   constexpr int V = Elem<T>::kVec;
   extern __shared__ float row_lds[];
-  __shared__ float change[TOKENS][kMaxRouteK];
+  __shared__ double change[TOKENS][kMaxRouteK];
   __shared__ int32_t names[TOKENS][kMaxRouteK];
   const int l = threadIdx.x % L;
   const int slot = threadIdx.x / L;
@@ -757,34 +757,46 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
   // a token whose chosen scores sum to zero has no weights to change
   const double inv = q.renormalize ? (sum > 0.0 ? 1.0 / sum : 0.0) : 1.0;
   const double mean = q.renormalize ? dot * inv : 0.0;
+  double both[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int j = r * L + l;
+    both[r] = 0.0;
     if (j >= K) continue;
     double v = ((double)g[r] - mean) * inv * scale * s[r];
     if (q.sigmoid) v *= live(logit[r]) ? score(-logit[r]) : 0.0;
-    change[slot][j] = (float)v;
+    both[r] = whole ? (double)g[r] : v;
+    change[slot][j] = both[r];
   }
   wave_sync();
   // an expert that a caller names twice gets both changes, added in order by
   // the first slot that names it
+  bool first[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int j = r * L + l;
-    if (j >= K || named[r] < 0) continue;
-    float v = 0.0f;
-    bool first = true;
-    for (int o = 0; o < K; ++o) {
-      const bool same = names[slot][o] == named[r];
-      first = first && !(same && o < j);
-      v += same ? change[slot][o] : 0.0f;
-    }
-    if (first) d[named[r]] = v;
+    first[r] = j < K && named[r] >= 0;
+    if (!first[r]) continue;
+    for (int o = 0; o < K; ++o)
+      if (names[slot][o] == named[r] && o != j) {  // rarely any
+        first[r] = first[r] && o > j;
+        both[r] += change[slot][o];
+      }
+  }
+  wave_sync();
+  // Through the whole softmax a chosen expert's gradient less `dot` may be far
+  // smaller than either, so the row gets the chosen one's slot, from which the
+  // difference is taken in 64 bits below.
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (!first[r]) continue;
+    const int j = r * L + l;
+    if (whole) change[slot][j] = both[r];
+    d[named[r]] = whole ? __int_as_float(j + 1) : (float)both[r];
   }
   wave_sync();
   if (!on) return;
   T* out = static_cast<T*>(q.grad_logits) + token * q.grad_stride;
-  const double pull = dot * scale;
 #pragma unroll
   for (int v = 0; v < EPL / V; ++v) {
     const int e0 = (v * L + l) * V;
@@ -798,8 +810,11 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
     }
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        y[i] -= live(x[v * V + i]) ? (float)(score(x[v * V + i]) * pull) : 0.0f;
+      for (int i = 0; i < V; ++i) {
+        const int j = __float_as_int(y[i]);
+        const double own = j > 0 ? change[slot][j - 1] : 0.0;
+        y[i] = live(x[v * V + i]) ? (float)(score(x[v * V + i]) * (own - dot) * scale) : 0.0f;
+      }
     }
     if (q.vector) {
       T packed[V];

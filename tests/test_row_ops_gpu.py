@@ -677,6 +677,78 @@ def test_route_gradient_masks_repeats_and_extremes(ert):
                     scoring=scoring, renormalize=renorm, scale=0.7)
 
 
+def _sure_gradient(x, idx, g, scoring, renormalize, scale):
+    """One token's gradient in extended precision, the size of the terms that
+    cancel in it, and the size of what is left of them."""
+    LD = np.longdouble
+    x, g = x.astype(LD), g.astype(LD)
+    live = x > -np.inf
+    if scoring == "sigmoid":
+        s, other = np.where(live, 1 / (1 + np.exp(-x)), 0), 1 / (1 + np.exp(x))
+    else:
+        s = np.where(live, np.exp(x - x[live].max()), 0)
+        s = s / s.sum()
+    ok = [(j, e) for j, e in enumerate(idx) if e >= 0 and live[e]]
+    total = sum(s[e] for _, e in ok) if renormalize else LD(1)
+    out, terms, rest = (np.zeros(x.size, LD) for _ in range(3))
+    if scoring == "sigmoid" and not renormalize:
+        for j, e in ok:
+            out[e] += g[j] * s[e] * other[e]
+        return out * scale, abs(out) * 0, abs(out) * scale
+    share = {j: s[e] / total for j, e in ok}
+    mean = sum(g[j] * share[j] for j, _ in ok)
+    size = sum(abs(g[j]) * share[j] for j, _ in ok)
+    for j, e in ok:
+        out[e] += share[j] * (g[j] - mean * renormalize)
+        terms[e] += share[j] * (abs(g[j]) + size)
+        rest[e] += share[j] * (abs(g[j]) * (1 - share[j]) + size - share[j] * abs(g[j]))
+    if not renormalize:
+        out -= s * mean
+        chosen = np.isin(np.arange(x.size), [e for _, e in ok])
+        terms += np.where(chosen, 0, s * size)
+        rest += np.where(chosen, 0, s * size)
+    if scoring == "sigmoid":
+        out, terms, rest = (v * other for v in (out, terms, rest))
+    return out * scale, terms * scale, rest * scale
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_route_gradient_of_a_sure_choice(ert, dtype):
+    # s_e (g_e - sum_j g_j s_j) where the two nearly cancel: a chosen expert
+    # with nearly all of the mass, alone and beside others, with equal
+    # gradients, named twice.  Sums, products and quotients of 64 bits: at most
+    # 32 roundings of 2^-53 of the terms; exponentials good to 2^-45, four of
+    # them in what the terms leave; then a rounding to float32 and one to the
+    # output's type.
+    import torch
+    rng = np.random.default_rng(43)
+    E, rows = 40, 24
+    x = rng.normal(0, 1, (rows, E))
+    x[:, 7] += np.linspace(4, 30, rows)
+    x[0] = NINF
+    x[0, :5] = [20, 0, 0, 0, -1]
+    idx = np.tile(np.array([7, 3, 30, 12]), (rows, 1))
+    idx[0] = [0, 1, 2, 3]
+    idx[5:9, 1:] = -1                                      # the sure one alone
+    idx[9:12, 1] = 7                                       # named twice
+    g = rng.normal(0, 1, (rows, 4)).astype(np.float32)
+    g[12:15] = 1.2345
+    g[9:12, 1] = -g[9:12, 0] * np.float32(1 + 2.0 ** -20)
+    xd = _cuda(x.astype(np.float32), _dt(dtype))
+    host = xd.double().cpu().numpy()
+    fi = torch.finfo(xd.dtype)
+    for scoring, renorm in itertools.product(("softmax", "sigmoid"), (False, True)):
+        kw = dict(scoring=scoring, renormalize=renorm, scale=1.75)
+        log(f"[route grad] sure choice {dtype} {kw}")
+        got = ert.route_experts_backward(_cuda(g), xd, _cuda(idx.astype(np.int32)), **kw).double().cpu().numpy()
+        for t in range(rows):
+            want, terms, rest = _sure_gradient(host[t], idx[t], g[t], **kw)
+            tol = np.abs(want) * (2.0 ** -24 + fi.eps / 2 * (1 + 2.0 ** -23)) + terms * 2.0 ** -48 \
+                + rest * 2.0 ** -43 + fi.smallest_normal * fi.eps / 2 + 2.0 ** -149
+            bad = np.flatnonzero(~(np.abs(got[t] - want) <= tol))
+            assert bad.size == 0, (dtype, kw, t, bad[:4], got[t][bad[:4]], want[bad[:4]])
+
+
 @pytest.mark.parametrize("scoring,renorm", itertools.product(("softmax", "sigmoid"), (False, True)))
 def test_route_gradient_against_differences(ert, scoring, renorm):
     # central differences of the 64-bit definition: their own error is about
