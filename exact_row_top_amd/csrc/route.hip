@@ -103,7 +103,8 @@ struct Score64 {
   }
   __device__ __forceinline__ double operator()(float x) const {
     if (!sigmoid) return share(x) * inv_z;
-    const double e = exp2_64(-__builtin_fabs((double)x) * kLog2e, poly);
+    double e = exp2_64(-__builtin_fabs((double)x) * kLog2e, poly);
+    if (e < 0x1p-1022) e = 0.0;  // (a sum of subnormals has no reciprocal)
     return (x < 0.0f ? e : 1.0) / (1.0 + e);
   }
 };
@@ -731,7 +732,7 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
       }
       names[slot][j] = named[r];
     }
-    if (!whole && !q.sigmoid) top = fmaxf(top, logit[r]);
+    if (!whole) top = fmaxf(top, logit[r]);
   }
   score.top = fold_maxf<L>(top);
   if (whole) {
@@ -742,12 +743,15 @@ __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGrad
     score.inv_z = z > 0.0 ? 1.0 / z : 0.0;
   }
 
+  // sigmoids near the end of their range are raised, so that their products
+  // with small gradients and their sum's reciprocal stay inside it
+  const int raise = q.sigmoid && q.renormalize && score.top < -200.0f ? 500 : 0;
   double s[R], sum = 0.0, dot = 0.0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     s[r] = 0.0;
     if (r * L >= K) continue;
-    if (live(logit[r])) s[r] = score(logit[r]);
+    if (live(logit[r])) s[r] = __builtin_ldexp(score(logit[r]), raise);
     sum += s[r];
     dot += (double)g[r] * s[r];
   }

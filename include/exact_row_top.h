@@ -455,7 +455,7 @@ int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t v
  *  indices, weights: device int32 / float [num_tokens][top_k].  weights are s
  *      of the chosen, divided by their sum with TOPK_ROUTE_RENORMALIZE, times
  *      scale; slots without an expert hold -1 and 0, and a sum of zero gives
- *      weights of 0.  Scores are 64-bit numbers: a sigmoid below 1e-308
+ *      weights of 0.  Scores are 64-bit numbers: a sigmoid below 2^-1022
  *      counts as zero; softmax scores that are divided by their sum are taken
  *      relative to the largest of the chosen.
  *  num_experts 1 .. 1024, top_k 1 .. min(64, num_experts), num_groups 1 .. 16

@@ -774,6 +774,41 @@ def test_route_gradient_against_differences(ert, scoring, renorm):
             assert abs((d * g[t]).sum() - got[t, e]) <= 1e-6
 
 
+def test_route_sigmoids_at_the_end_of_64_bits(ert):
+    # scores on both sides of 2^-1022 (logits of -708.4), below which they
+    # count as zero: weights are shares of what is left, never inf or NaN
+    LD = np.longdouble
+    rng = np.random.default_rng(47)
+    E, K = 16, 4
+    at = [-700.0, -707.5, -708.0, -709.0, -709.8, -712.0, -730.0, -744.0, -746.0, -800.0]
+    x = np.array([a + rng.uniform(-0.2, 0.2, E) for a in at] +
+                 [np.linspace(-712, -704, E), np.linspace(-745, -708.6, E)]).astype(np.float32)
+    g = rng.normal(0, 1, (len(x), K)).astype(np.float32)
+    # an exponential of 64 bits is good to 2^-45, its argument to 2^-43 of 1022
+    rel = 2.0 ** -24 + 2.0 ** -32
+    for bias in (None, np.full(E, 0.5, np.float32)):
+        xd = _cuda(x).requires_grad_()
+        idx, w = ert.route_experts(xd, K, scoring="sigmoid", bias=None if bias is None else _cuda(bias))
+        w.backward(_cuda(g))
+        idx, w, dx = idx.cpu().numpy(), w.detach().cpu().numpy(), xd.grad.cpu().numpy()
+        assert np.isfinite(w).all() and np.isfinite(dx).all()
+        for t in range(len(x)):
+            s = np.exp(x[t].astype(LD))
+            s = np.where(s < LD(2.0) ** -1022, LD(0), s)
+            if bias is None:
+                assert np.array_equal(idx[t], np.argsort(-x[t], kind="stable")[:K])
+            own = s[idx[t]]
+            total = own.sum()
+            share = own / total if total > 0 else own
+            assert np.all(np.abs(w[t] - share) <= rel * share + 2.0 ** -149), (t, w[t], share)
+            want = np.zeros(E, LD)
+            mean = (g[t].astype(LD) * share).sum()
+            want[idx[t]] = share * (g[t] - mean)
+            size = np.zeros(E, LD)
+            size[idx[t]] = share * (np.abs(g[t]) + abs(mean))
+            assert np.all(np.abs(dx[t] - want) <= rel * np.abs(want) + 2.0 ** -32 * size + 2.0 ** -149), (t, dx[t], want)
+
+
 def test_route_autograd_broadcast_gradient_and_refusals(ert):
     import torch
     x = torch.randn(33, 40, device="cuda", dtype=torch.bfloat16, requires_grad=True)
