@@ -333,7 +333,7 @@ int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_
   p.wide = slots_64;
   p.by_block = divisor((uint32_t)block_size);
   p.vector = k % 4 == 0 && at(indices, 16) && at(slots, 16);
-  p.parts = (k + kSlotPart - 1) / kSlotPart;
+  p.parts = (int32_t)(((int64_t)k + kSlotPart - 1) / kSlotPart);
   // Where a part maps at least twice as many positions as its table has
   // entries, and workgroups hide the copy's latency: 4096 rows of 2048 over
   // 256 entries 13.4 us against 16.0, 4096 x 1024 over 512 8.7 against 9.1,

@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kSlotBlock) topk_slots_kernel(const SlotParams
   const int n = known ? q.max_blocks : 0;
   const int64_t base = (int64_t)row * q.k;
   const uint32_t bs = (uint32_t)q.block_size;
+  // (k < 2^31 and parts of a power of two: no position passes 2^31 - 1)
   int32_t i[kSlotPart / kSlotBlock / 4][4];
 #pragma unroll
   for (int g = 0; g < kSlotPart / kSlotBlock / 4; ++g) {

@@ -958,6 +958,24 @@ def test_slots_many_rows(ert):
         assert np.array_equal(got, want)
 
 
+def test_slots_of_the_longest_rows(ert):
+    # a row of nearly 2^31 positions, written over its indices
+    import torch
+    n = 2 ** 31 - 701
+    idx = torch.arange(n, dtype=torch.int32, device="cuda")
+    idx[5] = -1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    tables = torch.randperm(2048, device="cuda", generator=g).to(torch.int32)[None, :]
+    got = ert.topk_slots(idx[None, :], tables, 1 << 20, slots=idx[None, :])[0]
+    off = torch.arange(1 << 20, dtype=torch.int32, device="cuda")
+    assert int(got[5]) == -1
+    got[5] = (int(tables[0, 0]) << 20) + 5
+    for b in range(2048):
+        own = got[b << 20:(b + 1) << 20]
+        assert torch.equal(own, off[:own.numel()] + (int(tables[0, b]) << 20)), b
+
+
 def test_slots_strided_tables_far_blocks_and_empty(ert):
     import torch
     tables = np.array([[1 << 25, (1 << 25) - 1, 5], [0, 2 ** 31 - 1, 7]], np.int32)
