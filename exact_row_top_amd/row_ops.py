@@ -349,7 +349,7 @@ def extend_block_tables(block_tables, kv_lens, new_tokens, free_blocks, free_sta
     dev = block_tables.device
     kv = _vector(_tensor(kv_lens, "kv_lens"), "kv_lens", torch.int32, requests, dev)
     new = _vector(_tensor(new_tokens, "new_tokens"), "new_tokens", torch.int32, requests, dev)
-    num_free = _tensor(free_blocks, "free_blocks").shape[0] if free_blocks.dim() == 1 else -1
+    num_free = free_blocks.numel() if _tensor(free_blocks, "free_blocks").dim() == 1 else -1
     free = _vector(free_blocks, "free_blocks", torch.int32, num_free, dev)
     start = _vector(_tensor(free_start, "free_start"), "free_start", torch.int32, 1, dev)
     max_tokens = _int32(max_tokens, "max_tokens")

@@ -989,6 +989,25 @@ def test_slots_strided_tables_far_blocks_and_empty(ert):
     assert none.shape == (0, 6)
 
 
+def test_binding_names_what_is_missing(ert):
+    import torch
+    def z(*shape):
+        return torch.zeros(*shape, dtype=torch.int32, device="cuda")
+    given = [z(3, 4), z(3), z(3), z(5), z(1)]
+    for at, wrong in itertools.product(range(5), (None, [1, 2, 3], 7)):
+        args = list(given)
+        args[at] = wrong
+        with pytest.raises(TypeError):
+            ert.extend_block_tables(*args, 16, 4)
+    for wrong in (z(3, 4)[:, :1], z(2, 2), torch.zeros((), dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            ert.extend_block_tables(*given[:3], wrong, given[4], 16, 4)
+    with pytest.raises(TypeError):
+        ert.extend_block_tables(*given[:3], z(5).float(), given[4], 16, 4)
+    with pytest.raises(ValueError):
+        ert.extend_block_tables(*given[:3], z(5).cpu(), given[4], 16, 4)
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, and the operators together
 # ---------------------------------------------------------------------------
