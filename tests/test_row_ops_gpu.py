@@ -827,6 +827,32 @@ def test_route_autograd_broadcast_gradient_and_refusals(ert):
         gx.float().sum().backward()          # no second derivative
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_beyond_32_bit_offsets(ert, dtype):
+    # rows whose elements lie more than 2^31 apart from the first
+    import torch
+    rng = np.random.default_rng(53)
+    stride, rows = (1 << 30) + 24, 4
+    buf = torch.empty((rows - 1) * stride + 8192, dtype=_dt(dtype), device="cuda")
+    u = rng.random(rows)
+    x = buf.as_strided((rows, 5003), (stride, 1))
+    x.copy_(_cuda(rng.normal(0, 2, (rows, 5003)).astype(np.float32)))
+    one = np.ones(rows)
+    _check_sample(ert, x, u, f"{dtype} far rows")
+    _check_sample(ert, x, u, f"{dtype} far rows, cuts", top_k=[50, 0, 3000, 7], top_p=0.9 * one)
+    y = buf.as_strided((rows, 96), (stride, 1), 3)
+    bias = rng.normal(0, 0.1, 96).astype(np.float32)
+    near = y.contiguous()
+    assert all(torch.equal(a, b) for a, b in zip(
+        ert.route_experts(y, 6, scoring="sigmoid", bias=_cuda(bias), num_groups=4, topk_groups=2),
+        ert.route_experts(near, 6, scoring="sigmoid", bias=_cuda(bias), num_groups=4, topk_groups=2)))
+    idx = _cuda(np.stack([rng.permutation(96)[:6] for _ in range(rows)]).astype(np.int32))
+    g = _cuda(rng.normal(0, 1, (rows, 6)).astype(np.float32))
+    for renorm in (False, True):
+        assert torch.equal(ert.route_experts_backward(g, y, idx, renormalize=renorm),
+                           ert.route_experts_backward(g, near, idx, renormalize=renorm))
+
+
 # ---------------------------------------------------------------------------
 # block tables and slots
 # ---------------------------------------------------------------------------
