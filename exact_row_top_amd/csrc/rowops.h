@@ -45,7 +45,6 @@ struct WideRow {
   // the same two of top-k's.  NaN: none.
   float edge[4];
   uint32_t need_k;      // count that top-k leaves to its crossing bin
-  uint32_t pad;
   uint64_t mass_k;      // with both: the mass above that bin
   uint64_t before;      // the mass above top-p's crossing bins
   uint32_t arrived[2];  // workgroups done with the bins, with the members

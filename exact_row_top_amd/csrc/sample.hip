@@ -425,16 +425,16 @@ struct ListSource {
   }
 };
 
-// The live scores of groups [g0, g1) of a row in memory.
+// The live scores of a row in memory, of `groups` groups.
 template <class T>
 struct RowSource {
   RowView<T> view;
   const Weigher& weigh;
-  int g0, g1;
+  int groups;
   template <int BLOCK, class F>
   __device__ __forceinline__ void visit(F&& f) const {
     constexpr int V = Elem<T>::kVec;
-    for (int g = g0 + (int)threadIdx.x; g < g1; g += BLOCK) {
+    for (int g = threadIdx.x; g < groups; g += BLOCK) {
       const int pos = g * V - view.lead;
       uint4 raw = *reinterpret_cast<const uint4*>(view.base + (int64_t)g * 16);
       // one 32-bit word at a time: the callers' code appears once or twice,
@@ -601,9 +601,8 @@ __device__ __forceinline__ void rank_short(RowShared& sh, int m, uint64_t need) 
 // `pred` admits reaches `need`, in index order over [0, vocab); -1 if the
 // total stays below.
 template <int BLOCK, bool MASS, class Src, class Pred>
-__device__ int find_index(const Src& src, RowShared& sh, const Weigher& w, int from, int span,
-                          Pred&& pred, uint64_t need) {
-  int i0 = from, width = (span + kBinsS - 1) / kBinsS;
+__device__ int find_index(const Src& src, RowShared& sh, int vocab, Pred&& pred, uint64_t need) {
+  int i0 = 0, width = (vocab + kBinsS - 1) / kBinsS;
   for (;;) {
     clear_bins<BLOCK>(sh);
     src.template visit<BLOCK>([&](float x, int i, auto&& v) {
@@ -746,8 +745,7 @@ __device__ Cut find_cut(const Src& src, RowShared& sh, const Weigher& w, float l
       const uint64_t one = MASS ? w(mn) : 1ull;
       const uint64_t count = MASS ? (need + one - 1) / one : need;
       const int at = find_index<BLOCK, false>(
-          src, sh, w, 0, vocab, [&](float x, int i) { return x == mn && within.holds(x, i); },
-          count);
+          src, sh, vocab, [&](float x, int i) { return x == mn && within.holds(x, i); }, count);
       return Cut{mn, at};
     }
     hi = mx;
@@ -797,7 +795,7 @@ __device__ void draw_from(const Src& src, RowShared& sh, const Weigher& w, const
   uint64_t need = (uint64_t)(u * total) + 1;
   if (need > z) need = z;
   find_index<BLOCK, true>(
-      src, sh, w, 0, vocab,
+      src, sh, vocab,
       [&](float x, int i) { return cut.holds(x, i) && w.drawn(x) >= (min_w ? min_w : 1ull); }, need);
 }
 
@@ -1158,7 +1156,6 @@ __device__ __forceinline__ void cross_wide(RowShared& sh, const Weigher& w, doub
 template <class T, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) sample_row_kernel(const SampleParams q) {
   __shared__ RowShared sh;
-  constexpr int V = Elem<T>::kVec;
   const int t = threadIdx.x;
   const int row = blockIdx.x / q.row_wgs, part = blockIdx.x % q.row_wgs;
   const RowAsk ask = row_ask(q, row);
@@ -1619,7 +1616,7 @@ __global__ void __launch_bounds__(kWideBlock) sample_wide_kernel(const SamplePar
   }
 
   // The whole row from memory, by this workgroup alone.
-  const RowSource<T> src{view, w, 0, (q.vocab + view.lead + V - 1) / V};
+  const RowSource<T> src{view, w, (q.vocab + view.lead + V - 1) / V};
   float low = __builtin_inff(), high = -__builtin_inff();
   src.template visit<kWideBlock>([&](float x, int, auto&&) { high = fmaxf(high, x); });
   block_min_max<kWideBlock>(low, high, sh.redf);
