@@ -237,10 +237,15 @@ __device__ __forceinline__ void choose64(const RouteParams& q, const float (&x)[
 //
 // Bound by the chain of top_k selections, each a maximum over the token's
 // lanes that the next one waits for (about 0.65 us of a token's time), not by
-// the 17.8 MB read: 16384 x 256 fp32, top 8, takes 11.4 us with softmax and 18
-// with sigmoid, bias and 4 of 8 groups; 64 x 128 bf16 5.4.  16 lanes a token
+// the 17.8 MB read: 16384 x 256 fp32, top 8, takes 11 us with softmax and 18.4
+// with sigmoid, bias and 4 of 8 groups; 64 x 128 bf16 5.5.  16 lanes a token
 // let four tokens share each step of a wave: with a wave a token the same
 // softmax calls take 35 and 7.1 us.
+//
+// A group's two largest summed without a bias are sums of scores while the
+// order is that of the logits, and 32 bits would need a bound for each: such
+// calls settle the groups in 64 bits for every token (the 16384 x 256 call
+// with 4 of 8 groups 19.9 us, 13.4 by each group's largest).
 template <class T, int L, int EPL>
 __global__ void __launch_bounds__(kRouteBlock) route_kernel(const RouteParams q) {
   constexpr int TOKENS = kRouteBlock / L;
@@ -660,9 +665,9 @@ __device__ __forceinline__ void store_as<__half>(__half* p, float v) { *p = __fl
 // A token's row of changes is put together in LDS: zeros, the chosen
 // experts' changes (at most K), and out in 16-byte pieces.  Bound by the
 // chain of dependent steps at few tokens and by writing at many: 16384 x 256
-// fp32 sigmoid, whose 18.4 MB are written and hardly read, take 8.8 us (2.1
+// fp32 sigmoid, whose 18.4 MB are written and hardly read, take 8.9 us (2.1
 // TB/s; a store per chosen expert over rows of zeros took 11), 4097 x 64 bf16
-// with the whole softmax 6.0.
+// with the whole softmax 6.2.
 template <class T, int L, int EPL>
 __global__ void __launch_bounds__(kRouteBlock) route_grad_kernel(const RouteGradParams q) {
   constexpr int TOKENS = kRouteBlock / L;

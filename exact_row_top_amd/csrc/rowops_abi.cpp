@@ -291,10 +291,11 @@ int topk_block_tables(int32_t* block_tables, int64_t table_stride, int32_t max_b
   p.free_next = free_next;
   p.by_block = divisor((uint32_t)block_size);
   p.vector = at(token_requests, 16) && at(positions, 16) && at(slots, 16);
-  // Four tokens a thread once 1024 workgroups of single ones are full (a
-  // million tokens: 7.2 us against 9.4; 244000: 4.7 against 4.9; 32768: 4.2
-  // against 3.5; 64: 4.9 against 3.3); beyond 1024 workgroups another round
-  // costs less than another workgroup's sums over the requests.
+  // Four tokens a thread once 1024 workgroups of single ones are full (one
+  // behind the other in a graph, a million tokens: 7.2 us against 7.8; 244000:
+  // 5.3 either way; 32768: 4.8 against 3.9; 64: 5.0 against 3.6); beyond 1024
+  // workgroups another round costs less than another workgroup's sums over the
+  // requests.
   const int per_thread = max_tokens > 1024 * kSlotBlock ? 4 : 1;
   int64_t grid = (max_tokens + kSlotBlock * per_thread - 1) / (kSlotBlock * per_thread);
   grid = grid < 1 ? 1 : (grid > 1024 ? 1024 : grid);

@@ -15,14 +15,15 @@
 // and less are zero, and such a token is never drawn.
 //
 // A weight is off by at most half a unit, 2^-44 of the largest (equal scores
-// all to the same side), so a token differs from the real-number definition
-// only if u Z lies within vocab * 2^-44 of a border: 6e-8 for 2^20 equal
-// scores at worst, about 1e-11 for ordinary rows.  Two sums are taken before
-// the row's largest score is known, each segment against its own and then
-// brought to the row's unit: the total of a row without a cut, and the total
-// that a top-p without a top-k takes its share of.  They are off by no more
-// than that either, but not by the same amount as a sum of the row's weights.
-// Segments whose largest score weighs nothing in the row add nothing to them.
+// all to the same side), and 2^-45 of itself, so a token differs from the
+// real-number definition only if u Z lies within vocab * 2^-44 and 2^-44 Z of
+// a border: 6e-8 for 2^20 equal scores at worst, about 1e-11 for ordinary
+// rows.  Two sums are taken before the row's largest score is known, each
+// segment against its own and then brought to the row's unit: the total of a
+// row without a cut, and the total that a top-p without a top-k takes its
+// share of.  They are off by no more than that either, but not by the same
+// amount as a sum of the row's weights.  Segments whose largest score weighs
+// nothing in the row add nothing to them.
 //
 // Three launches, the third only where a row may have a cut: the segment
 // kernel reads the logits once, a wave for each 2048 scores; the row kernel
@@ -221,11 +222,11 @@ __device__ __forceinline__ int wave_min(int v) {
 //
 // Bound by 64-bit arithmetic where the weights are summed (about 20
 // instructions a score), close behind it by reading: 256 x 131072 fp32, 134
-// MB, 34 us, where a copy of as much runs at 5.2 TB/s (26 us) and the
-// instructions alone take about 24; with weights in flight for all of a
+// MB, 31.0 us, where a copy of as much runs at 5.2 TB/s (26 us) and the
+// instructions alone take about 22; with weights in flight for all of a
 // lane's 32 scores and constants in vector registers it took 54.  CUTS false
 // leaves the candidates' code out where no row of the call can have a cut (74
-// registers instead of 108).
+// registers, six waves a SIMD, instead of 108 and four).
 // ---------------------------------------------------------------------------
 template <class T, bool CUTS>
 __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams q) {
@@ -328,9 +329,10 @@ __global__ void __launch_bounds__(256) sample_segment_kernel(const SampleParams 
         } else {
           // Four scores at a time (the empty asm keeps the additions where
           // they are): with all of them in flight, and added up at the end,
-          // the registers would leave room for three waves a SIMD, not
-          // eight.  (One loop for all rows: of two, the compiler shares the
-          // conversions, which then stay in registers across both.)
+          // the registers would leave room for three waves a SIMD, not six
+          // (four with the cuts' code).  (One loop for all rows: of two, the
+          // compiler shares the conversions, which then stay in registers
+          // across both.)
           uint64_t mass = 0, top_mass = 0;
           const Weigher w(best, ask.c);
 #pragma unroll
@@ -937,7 +939,7 @@ __device__ __forceinline__ double below_best(float best, const Weigher& w) {
 // selected by one workgroup from memory, pass by pass.
 //
 // Both steps are bound by the exponentials (64 x 131072 with mixed cuts: row
-// kernel 19 us, wide kernel 19 us, of which 8 each are the waves' work and
+// kernel 18.2 us, wide kernel 19.6, of which 8 each are the waves' work and
 // the rest the last workgroup's chain of scans and look-ups).  One workgroup
 // a row, from memory, took 395 us for the same rows, and 480 to 670 where
 // both cuts lie low (now 78 to 88, the whole call).

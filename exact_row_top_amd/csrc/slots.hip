@@ -38,8 +38,8 @@ __device__ __forceinline__ int64_t slot_of(int32_t block, uint32_t bs, uint32_t 
 // table entry is written by the token that opens it.
 //
 // Bound by the sums over the requests, which every workgroup waits for, and
-// then by writing: a million tokens of 61 prompts, 12 MB, take 7.6 us; 64
-// decode tokens 3.2 with one token a thread and 4.5 with four.
+// then by writing: a million tokens of 61 prompts, 12 MB, take 7.7 us, 64
+// decode tokens 3.2.
 template <int N>
 __global__ void __launch_bounds__(kSlotBlock) block_table_kernel(const TableParams q) {
   extern __shared__ int32_t lds_i[];
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kSlotBlock) block_table_kernel(const TablePara
 // neighbours a thread.  The row's table goes through LDS where that pays:
 // its entries are then read once, side by side, and the scattered look-ups
 // stay on the compute unit.  Bound by reading and writing: 4096 rows of 1024
-// positions over 256 entries, 33.6 MB, take 7.6 us one behind the other (4.4
-// TB/s); 64 rows of 2048 take 2.6, which is the launch.
+// positions over 256 entries, 33.6 MB, take 8.4 us alone and 7.6 one behind
+// the other (4.4 TB/s); 64 rows of 2048 take 3.2, half of it the launch.
 __global__ void __launch_bounds__(kSlotBlock) topk_slots_kernel(const SlotParams q) {
   extern __shared__ int32_t table_lds[];
   const uint32_t row = blockIdx.x / (uint32_t)q.parts;

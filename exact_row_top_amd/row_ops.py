@@ -160,7 +160,8 @@ def sample_tokens(logits, uniforms, *, temperature=None, top_k=None, top_p=None,
     Returns the tokens, int32 [rows], or (tokens, logprobs) with the float32
     log-probability of each token among the kept ones.  Weights of 2^-44 of a
     row's largest and less count as zero; sums of weights, and with them the
-    borders between tokens, are good to vocab * 2^-44 of it.  whole_row reads
+    borders between tokens, are good to vocab * 2^-44 of it beside 2^-44 of
+    themselves.  whole_row reads
     every row a second time instead of using the candidates and sums of the
     first reading (for tests; the same results within that bound)."""
     guard = _elsewhere(logits, "logits", stream)

@@ -416,11 +416,11 @@ int topk_validate(int32_t mode, const void* logits, int64_t row_stride, const vo
  * Weights are held as whole multiples of 2^-43 of the largest, so results do
  * not depend on the order of any sum; weights of 2^-44 and less count as zero
  * and their tokens are never drawn.  A sum of weights is thus off by at most
- * vocab * 2^-44 of the largest, and so are the borders between tokens, the
- * cuts' and the total in logprobs.  (The total of a row without a cut, and the
- * one that a top_p without a top_k takes its share of, are sums of weights
- * rounded more finely: within the same bound, but not to the bit what the
- * multiples add up to.)
+ * vocab * 2^-44 of the largest and 2^-44 of itself, and so are the borders
+ * between tokens, the cuts' and the total in logprobs.  (The total of a row
+ * without a cut, and the one that a top_p without a top_k takes its share of,
+ * are sums of weights rounded more finely: within the same bound, but not to
+ * the bit what the multiples add up to.)
  *  temperature, top_p, min_p: device float[num_rows], top_k: device
  *      int32[num_rows]; each may be NULL (temperature 1, no cut).
  *  logprobs: optional device float[num_rows]: ln(w_token / kept total) (0 for
@@ -455,9 +455,11 @@ int topk_sample(const void* logits, int32_t dtype, int64_t row_stride, int32_t v
  *  indices, weights: device int32 / float [num_tokens][top_k].  weights are s
  *      of the chosen, divided by their sum with TOPK_ROUTE_RENORMALIZE, times
  *      scale; slots without an expert hold -1 and 0, and a sum of zero gives
- *      weights of 0.  Scores are 64-bit numbers: a sigmoid below 2^-1022
- *      counts as zero; softmax scores that are divided by their sum are taken
- *      relative to the largest of the chosen.
+ *      weights of 0.  Scores are 64-bit numbers, good to 2^-45 of themselves:
+ *      two c (or sums of two) of different logits that differ by less than
+ *      that may come in either order.  A sigmoid below 2^-1022 counts as zero;
+ *      softmax scores that are divided by their sum are taken relative to the
+ *      largest of the chosen.
  *  num_experts 1 .. 1024, top_k 1 .. min(64, num_experts), num_groups 1 .. 16
  *  dividing num_experts, topk_groups 1 .. num_groups. */
 #define TOPK_ROUTE_SIGMOID 1u
