@@ -124,6 +124,30 @@ def load_library():
     lib.topk_block_tables.restype = ctypes.c_int
     lib.topk_slots.argtypes = [P, I64, I32, P, I64, I32, I32, P, I32, I32, P, I32, P]
     lib.topk_slots.restype = ctypes.c_int
+    F32 = ctypes.c_float
+    lib.topk_beams_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    lib.topk_beams_workspace_bytes.restype = SZ
+    lib.topk_beams.argtypes = [P, I32, I64, I32, I32, I32, I32, P, P, I32, P, F32, P, P, P, P, SZ, P]
+    lib.topk_beams.restype = ctypes.c_int
+    lib.topk_reorder_rows.argtypes = [I32, P, P, P, P, P, P, I32, I32, I32, I32, P]
+    lib.topk_reorder_rows.restype = ctypes.c_int
+    lib.topk_reorder_blocks.argtypes = [P, I64, I32, P, P, I32, I32, I32, I32, P, P, I64, I32, P, I64,
+                                        I64, P]
+    lib.topk_reorder_blocks.restype = ctypes.c_int
+    lib.topk_attend_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32, I32, I64, I64]
+    lib.topk_attend_workspace_bytes.restype = SZ
+    heads = [P, I32, I64, I64, I32, I32, I32, I32, I32]
+    tables = [P, I64, I32, P, P, I32, P, I64, I32, P, F32]
+    lib.topk_attend.argtypes = (heads + [P, I64, I64, I64] * 2 + [I64, I32] + tables
+                                + [I64, I64, P, P, P, SZ, P])
+    lib.topk_attend.restype = ctypes.c_int
+    lib.topk_attend_mass.argtypes = (heads + [P, I64, I64, I64, I64, I32] + tables
+                                     + [P, F32, P, P, I32, P, P, I32, P])
+    lib.topk_attend_mass.restype = ctypes.c_int
+    lib.topk_evict_keep.argtypes = [P, I64, I64, I32, I32, I32, P, I32, I32, I32, P, P, I32, P, P]
+    lib.topk_evict_keep.restype = ctypes.c_int
+    lib.topk_evict_move.argtypes = [P, I32, I32, I32, P, I64, I32, P, I64, I32, I32, I32, P, I64, I64, P]
+    lib.topk_evict_move.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -497,18 +521,24 @@ def new_workspace(num_rows: int, row_stride: int, k: int, device="cuda", stream=
 
 
 def __getattr__(name):
-    # the row operators need torch, which this module imports only when called
+    # the row and search operators need torch, which this module imports only when called
     if name in _ROW_OPS:
         from . import row_ops
         globals().update({n: getattr(row_ops, n) for n in _ROW_OPS})
+        return globals()[name]
+    if name in _SEARCH_OPS:
+        from . import search_ops
+        globals().update({n: getattr(search_ops, n) for n in _SEARCH_OPS})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 _ROW_OPS = ("sample_tokens", "route_experts", "route_experts_backward", "extend_block_tables",
             "topk_slots")
+_SEARCH_OPS = ("select_beams", "reorder_beams", "reorder_block_tables", "prefix_attention",
+               "attention_mass", "evict_cache")
 
 __all__ = ["topk_decode", "topk_prefill", "topk_decode_varlen", "block_max", "workspace_bytes",
            "new_workspace", "status", "plan_query",
            "strerror", "load_library", "TopKError", "STATS_WORDS", "VALID_K", "TOPK_SORTED",
-           "TOPK_DETERMINISTIC", *_ROW_OPS]
+           "TOPK_DETERMINISTIC", *_ROW_OPS, *_SEARCH_OPS]

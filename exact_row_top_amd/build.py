@@ -19,6 +19,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["gvr_kernels.hip", "blockskip.hip", "epilogue.hip", "state.hip", "calib.hip",
            "sample.hip", "route.hip", "slots.hip", "rowops_abi.cpp",
+           "beams.hip", "reorder.hip", "attend.hip", "evict.hip", "search_abi.cpp",
            "topk_abi.cpp"]
 
 # -ffp-contract=off: the histogram bin is one definition evaluated in several

@@ -1,0 +1,238 @@
+// evict.hip -- eviction from a cache by accumulated attention mass: which
+// positions of each (request, head) stay, and the move of their rows to the
+// front of the cache.
+//
+// The positions that stay are the first `sinks`, the last `recent` and, of the
+// others, those with the largest mass (equal masses: the lower position; NaN
+// below all), listed in rising order.  So the j-th of them comes from position
+// kept[j] >= j, and rows can move in place from the front on.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gvr_device.h"
+#include "search.h"
+
+namespace ert {
+
+namespace {
+
+constexpr int kKeepWaves = kKeepBlock / 64;
+constexpr int kDigitBins = 2048;
+
+// n / d for n < 2^31.
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& d) {
+  return (d.magic ? __umulhi(n, d.magic) : n) >> d.shift;
+}
+
+struct KeepShared {
+  uint32_t count[kDigitBins];
+  uint32_t wave[kKeepWaves];
+  uint32_t wave2[kKeepWaves];
+  uint32_t digit;
+  uint32_t need;
+};
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// One workgroup a row: the key of the last position that stays, digit by
+// digit from the top (11, 11 and 10 bits, counted in LDS), then one pass that
+// writes what stays in order, each wave its own range.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams q) {
+  __shared__ KeepShared sh;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  const int req = blockIdx.x / q.heads, head = blockIdx.x - req * q.heads;
+  const float* mass = q.mass + req * q.request_stride + head * q.head_stride;
+  const int n = min(max(q.kv_lens[req], 0), q.positions);
+  const int stay = min(n, q.budget);
+  int32_t* kept = q.kept + (int64_t)blockIdx.x * q.budget;
+  float* out = q.mass_out ? q.mass_out + (int64_t)blockIdx.x * q.out_positions : nullptr;
+  if (head == 0 && t == 0) q.new_lens[req] = stay;
+  for (int j = stay + t; j < q.budget; j += kKeepBlock) kept[j] = -1;
+  if (out)
+    for (int j = stay + t; j < q.out_positions; j += kKeepBlock) out[j] = 0.0f;
+  if (n <= q.budget) {
+    for (int j = t; j < n; j += kKeepBlock) {
+      kept[j] = j;
+      if (out) out[j] = mass[j];
+    }
+    return;
+  }
+  const int lo = q.sinks, hi = n - q.recent;   // lo < hi: sinks + recent <= budget < n
+  uint32_t need = (uint32_t)(q.budget - q.sinks - q.recent);
+  // prefix: the digits found so far, of `bits` bits
+  uint32_t prefix = 0;
+  int bits = 0;
+  if (need > 0) {
+#pragma unroll 1
+    for (int level = 0; level < 3; ++level) {
+      const int width = level < 2 ? 11 : 10, shift = 32 - bits - width;
+      for (int b = t; b < kDigitBins; b += kKeepBlock) sh.count[b] = 0;
+      __syncthreads();
+      for (int i = lo + t; i < hi; i += kKeepBlock) {
+        const uint32_t key = rkey(mass[i]);
+        if (bits == 0 || (key >> (32 - bits)) == prefix)
+          atomicAdd(&sh.count[(key >> shift) & ((1u << width) - 1)], 1u);
+      }
+      __syncthreads();
+      // from the largest digit down: thread t holds digits 2047 - 2t and 2046 - 2t
+      const uint32_t a = sh.count[kDigitBins - 1 - 2 * t], b = sh.count[kDigitBins - 2 - 2 * t];
+      uint32_t sum = wave_scan(a + b);
+      if (lane == 63) sh.wave[wv] = sum;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kKeepWaves; ++w) sum += w < wv ? sh.wave[w] : 0u;
+      const uint32_t above = sum - a - b;
+      if (above < need && need <= above + a) {
+        sh.digit = (uint32_t)(kDigitBins - 1 - 2 * t);
+        sh.need = need - above;
+      } else if (above + a < need && need <= sum) {
+        sh.digit = (uint32_t)(kDigitBins - 2 - 2 * t);
+        sh.need = need - above - a;
+      }
+      __syncthreads();
+      prefix = (prefix << width) | sh.digit;
+      need = sh.need;
+      bits += width;
+    }
+  }
+  // Now `prefix` is the last key that stays, `need` how many of its positions.
+  const bool any = q.budget > q.sinks + q.recent;
+  const int span = ((n + kKeepBlock - 1) / kKeepBlock) * 64;  // a wave's positions
+  const int w0 = wv * span, w1 = min(w0 + span, n);
+  uint32_t larger = 0, even = 0;   // of this wave's
+  for (int i0 = w0; i0 < w1; i0 += 64) {
+    const int i = i0 + lane;
+    bool gt = false, eq = false;
+    if (i < w1) {
+      if (i < lo || i >= hi) {
+        gt = true;
+      } else if (any) {
+        const uint32_t key = rkey(mass[i]);
+        gt = key > prefix;
+        eq = key == prefix;
+      }
+    }
+    larger += (uint32_t)__popcll(__ballot(gt));
+    even += (uint32_t)__popcll(__ballot(eq));
+  }
+  if (lane == 0) {
+    sh.wave[wv] = larger;
+    sh.wave2[wv] = even;
+  }
+  __syncthreads();
+  uint32_t larger_before = 0, even_before = 0;
+  for (int w = 0; w < wv; ++w) {
+    larger_before += sh.wave[w];
+    even_before += sh.wave2[w];
+  }
+  uint32_t at = larger_before + min(even_before, need);
+  for (int i0 = w0; i0 < w1; i0 += 64) {
+    const int i = i0 + lane;
+    bool gt = false, eq = false;
+    float m = 0.0f;
+    if (i < w1) {
+      m = mass[i];
+      if (i < lo || i >= hi) {
+        gt = true;
+      } else if (any) {
+        const uint32_t key = rkey(m);
+        gt = key > prefix;
+        eq = key == prefix;
+      }
+    }
+    const uint64_t evens = __ballot(eq);
+    const uint32_t turn = even_before + __builtin_amdgcn_mbcnt_hi(
+                                            (uint32_t)(evens >> 32),
+                                            __builtin_amdgcn_mbcnt_lo((uint32_t)evens, 0u));
+    const bool in = gt || (eq && turn < need);
+    const uint64_t ins = __ballot(in);
+    const uint32_t j = at + __builtin_amdgcn_mbcnt_hi(
+                                (uint32_t)(ins >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)ins, 0u));
+    if (in) {
+      kept[j] = i;
+      if (out) out[j] = m;
+    }
+    at += (uint32_t)__popcll(ins);
+    even_before += (uint32_t)__popcll(evens);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Moves the kept rows, 16 bytes a thread, a step of rows at a time: all of a
+// step's loads are done before its first store, and a later step reads
+// positions behind everything that was stored (kept[j] >= j), so source and
+// target may be the same blocks.  parts > 1 only where they are not.
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kMoveRows = 8;   // rows in flight a thread
+}
+
+__global__ void __launch_bounds__(kMoveBlock) evict_move_kernel(const MoveParams q) {
+  uint32_t id = blockIdx.x;
+  const int part = (int)(id % (uint32_t)q.parts);
+  id /= (uint32_t)q.parts;
+  const int column = (int)(id % (uint32_t)q.columns);
+  id /= (uint32_t)q.columns;
+  const int head = (int)(id % (uint32_t)q.heads);
+  id /= (uint32_t)q.heads;
+  const int req = (int)(id % (uint32_t)q.requests);
+  unsigned char* cache = q.cache[id / (uint32_t)q.requests];
+  const int32_t* kept = q.kept + ((int64_t)req * q.heads + head) * q.budget;
+  const int32_t* from = q.tables + (int64_t)req * q.table_stride;
+  const int32_t* to = q.out_tables + (int64_t)req * q.out_stride;
+  const int64_t pieces = q.row_bytes / 16;
+  const int wide = (int)((pieces + q.columns - 1) / q.columns);   // this workgroup's pieces of a row
+  const int64_t c0 = (int64_t)column * wide;
+  const int mine = (int)(pieces - c0 < wide ? pieces - c0 : (int64_t)wide);
+  if (mine <= 0) return;
+  // threads side by side on a row's pieces, the rest on further rows
+  const int across = min(mine, kMoveBlock), down = kMoveBlock / across;
+  const int x = (int)threadIdx.x % across, y = (int)threadIdx.x / across;
+  const int step = down * kMoveRows;
+  const int span = (((q.budget + q.parts - 1) / q.parts + step - 1) / step) * step;
+  const int j1 = min(q.budget, (part + 1) * span);
+  auto address = [&](const int32_t* table, int width, int p) -> unsigned char* {
+    const uint32_t e = quotient((uint32_t)p, q.by_block);
+    if (e >= (uint32_t)width) return nullptr;
+    const int32_t b = table[e];
+    if (b < 0 || b >= q.num_blocks) return nullptr;
+    const int64_t slot = (int64_t)b * q.block_size + ((uint32_t)p - e * (uint32_t)q.block_size);
+    return cache + slot * q.slot_bytes + head * q.row_bytes + c0 * 16;
+  };
+  for (int j0 = part * span; j0 < j1; j0 += step) {
+    for (int x0 = 0; x0 < mine; x0 += across) {
+      uint4 v[kMoveRows];
+      unsigned char* dst[kMoveRows];
+#pragma unroll
+      for (int i = 0; i < kMoveRows; ++i) {
+        const int j = j0 + i * down + y;
+        dst[i] = nullptr;
+        v[i] = uint4{0, 0, 0, 0};
+        if (y < down && j < j1 && x0 + x < mine) {
+          const int p = kept[j];
+          const unsigned char* src = p >= 0 ? address(from, q.max_blocks, p) : nullptr;
+          dst[i] = src ? address(to, q.out_blocks, j) : nullptr;
+          if (dst[i] == src) dst[i] = nullptr;
+          if (dst[i]) {
+            v[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(x0 + x) * 16);
+            dst[i] += (int64_t)(x0 + x) * 16;
+          }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // the loads are done
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kMoveRows; ++i)
+        if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = v[i];
+      __syncthreads();
+    }
+  }
+}
+
+const void* evict_keep_kernel_ptr() { return reinterpret_cast<const void*>(&evict_keep_kernel); }
+const void* evict_move_kernel_ptr() { return reinterpret_cast<const void*>(&evict_move_kernel); }
+
+}  // namespace ert

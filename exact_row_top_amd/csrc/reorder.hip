@@ -1,0 +1,179 @@
+// reorder.hip -- after a beam search's choice: each child takes over what its
+// parent holds.
+//
+// Rows of any state move by gathering, out[child] = state[parent of child].  A
+// paged cache moves without its full blocks: children share them through
+// their table rows, and only the open block, which the next token is written
+// into, is copied to the block that the child's row owns.
+//
+// A thread owns 16 bytes of every row of a request: it loads its piece of all
+// parents' rows and stores its piece of all children's, so moving in place
+// needs no barrier and no second buffer, whatever the parents.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "search.h"
+
+namespace ert {
+
+namespace {
+
+// n / d for n < 2^31.
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& d) {
+  return (d.magic ? __umulhi(n, d.magic) : n) >> d.shift;
+}
+
+// The last bytes of a row, fewer than 16, in pieces of 8, 4, 2 and 1.
+__device__ __forceinline__ uint4 load_tail(const unsigned char* p, uint32_t n) {
+  unsigned char b[16] = {};
+  if (n & 8) __builtin_memcpy(b, p, 8), p += 8;
+  if (n & 4) __builtin_memcpy(b + 8, p, 4), p += 4;
+  if (n & 2) __builtin_memcpy(b + 12, p, 2), p += 2;
+  if (n & 1) b[14] = *p;
+  uint4 v;
+  __builtin_memcpy(&v, b, 16);
+  return v;
+}
+__device__ __forceinline__ void store_tail(unsigned char* p, uint32_t n, const uint4& v) {
+  unsigned char b[16];
+  __builtin_memcpy(b, &v, 16);
+  if (n & 8) __builtin_memcpy(p, b, 8), p += 8;
+  if (n & 4) __builtin_memcpy(p, b + 8, 4), p += 4;
+  if (n & 2) __builtin_memcpy(p, b + 12, 2), p += 2;
+  if (n & 1) *p = b[14];
+}
+
+// Moves this thread's piece of a request's rows: from(j) and to(j) are child
+// j's source and target (uniform; null: none), the loads of N children ahead
+// of their stores.  With k <= N everything is read before anything is
+// written.  A null source with a target clears.
+template <int N, class From, class To>
+__device__ __forceinline__ void move_rows(int k, int64_t bytes, int64_t off, From&& from, To&& to) {
+  const int64_t left = bytes - off;
+  if (left <= 0) return;
+  const uint32_t tail = left < 16 ? (uint32_t)left : 0u;
+  for (int j0 = 0; j0 < k; j0 += N) {
+    uint4 v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = uint4{0, 0, 0, 0};
+      const unsigned char* p = j0 + j < k ? from(j0 + j) : nullptr;
+      if (p) {
+        if (!tail) __builtin_memcpy(&v[j], p + off, 16);
+        else v[j] = load_tail(p + off, tail);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      unsigned char* p = j0 + j < k ? to(j0 + j) : nullptr;
+      if (p) {
+        if (!tail) __builtin_memcpy(p + off, &v[j], 16);
+        else store_tail(p + off, tail, v[j]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+// Rows of up to kMaxCopies arrays in one launch; a workgroup takes 4 KB of
+// every row of a request.
+template <int N>
+__global__ void __launch_bounds__(kCopyBlock) reorder_rows_kernel(const ReorderParams q) {
+  int a = 0;
+  while (a + 1 < q.copies && blockIdx.x >= q.copy[a + 1].first) ++a;
+  const RowCopy c = q.copy[a];
+  const uint32_t at = blockIdx.x - c.first;
+  const uint32_t req = at / c.tiles;
+  const int64_t off = ((int64_t)(at - req * c.tiles) * kCopyBlock + threadIdx.x) * 16;
+  const int32_t* parents = q.parents + (int64_t)req * q.k;
+  const unsigned char* src = c.src + (int64_t)req * q.beams * c.src_stride;
+  unsigned char* dst = c.dst + (int64_t)req * q.k * c.dst_stride;
+  auto from = [&](int j) -> const unsigned char* {
+    const int p = parents[j];
+    return (unsigned)p < (unsigned)q.beams ? src + p * c.src_stride : nullptr;
+  };
+  auto to = [&](int j) -> unsigned char* {
+    const bool has = (unsigned)parents[j] < (unsigned)q.beams;
+    unsigned char* d = dst + j * c.dst_stride;
+    // nothing to do for a row that stays where it is
+    if (!has ? !q.clear : d == src + parents[j] * c.src_stride) return nullptr;
+    return d;
+  };
+  move_rows<N>(q.k, c.row_bytes, off, from, to);
+}
+
+// Table rows and open blocks.  The launch's first workgroups copy: a request's
+// open blocks in one cache each, 4 KB of a block at a time; the others make
+// its table rows, a thread an entry of every row.
+template <int N>
+__global__ void __launch_bounds__(kCopyBlock) reorder_blocks_kernel(const ReorderBlocksParams q) {
+  const uint32_t copying = q.copying ? (uint32_t)q.caches * q.requests * q.tiles : 0u;
+  const uint32_t w = blockIdx.x;
+  const bool copy = w < copying;
+  const uint32_t per = copy ? q.tiles : q.table_tiles;
+  const uint32_t unit = (copy ? w : w - copying) / per;
+  const uint32_t tile = (copy ? w : w - copying) - unit * per;
+  const uint32_t req = copy ? unit % (uint32_t)q.requests : unit;
+  const int32_t* parents = q.parents + (int64_t)req * q.k;
+  const int32_t* tables = q.tables + (int64_t)req * q.beams * q.table_stride;
+  const int32_t* tail = q.tail ? q.tail + (int64_t)req * q.k : nullptr;
+  const uint32_t len = (uint32_t)max(q.kv_lens[req], 0);
+  const uint32_t full = quotient(len, q.by_block), part = len - full * (uint32_t)q.block_size;
+  const bool open = part > 0 && full < (uint32_t)q.max_blocks;
+  // the block that child j's open one becomes
+  auto own = [&](int j) { return tail ? tail[j] : tables[j * q.table_stride + full]; };
+  if (copy) {
+    if (!open) return;
+    unsigned char* cache = q.cache[unit / (uint32_t)q.requests];
+    auto block = [&](int32_t b) -> unsigned char* {
+      return b >= 0 && b < q.num_blocks ? cache + b * q.block_stride : nullptr;
+    };
+    auto from = [&](int j) -> const unsigned char* {
+      const int p = parents[j];
+      return (unsigned)p < (unsigned)q.beams ? block(tables[p * q.table_stride + full]) : nullptr;
+    };
+    auto to = [&](int j) -> unsigned char* {
+      const unsigned char* f = from(j);
+      unsigned char* d = f ? block(own(j)) : nullptr;
+      return d == f ? nullptr : d;
+    };
+    const int64_t bytes = (int64_t)part * q.slot_bytes;
+    for (int64_t off = ((int64_t)tile * kCopyBlock + threadIdx.x) * 16; off < bytes;
+         off += (int64_t)q.tiles * kCopyBlock * 16)
+      move_rows<N>(q.k, bytes, off, from, to);
+    return;
+  }
+  const uint32_t e = tile * kCopyBlock + threadIdx.x;
+  if (e >= (uint32_t)q.max_blocks) return;
+  int32_t* out = q.out + (int64_t)req * q.k * q.out_stride + e;
+  const bool rows_stay = q.beams == q.k;
+  for (int j0 = 0; j0 < q.k; j0 += N) {
+    int32_t v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = -1;
+      if (j0 + j >= q.k) continue;
+      const int p = parents[j0 + j];
+      const bool has = (unsigned)p < (unsigned)q.beams;
+      if (has && e < full) v[j] = tables[p * q.table_stride + e];
+      else if (has && open && e == full && tail) v[j] = tail[j0 + j];
+      else if (rows_stay) v[j] = tables[(j0 + j) * q.table_stride + e];
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j0 + j < q.k) out[(j0 + j) * q.out_stride] = v[j];
+  }
+}
+
+const void* reorder_rows_kernel_ptr(int n) {
+  return n == 8 ? reinterpret_cast<const void*>(&reorder_rows_kernel<8>)
+                : reinterpret_cast<const void*>(&reorder_rows_kernel<32>);
+}
+const void* reorder_blocks_kernel_ptr(int n) {
+  return n == 8 ? reinterpret_cast<const void*>(&reorder_blocks_kernel<8>)
+                : reinterpret_cast<const void*>(&reorder_blocks_kernel<32>);
+}
+
+}  // namespace ert

@@ -112,6 +112,99 @@ __device__ __forceinline__ double exp2_64(double s, const Exp2Poly& poly) {
   return __builtin_ldexp(poly(s - n), (int)n);
 }
 
+// ---- whole-number weights ---------------------------------------------------------
+
+constexpr uint64_t kOne = 1ull << 43;   // the weight of a row's largest score
+constexpr double kLn2 = 0.6931471805599453;
+constexpr double kTmax = 44.0;          // weights of 2^-44 and less are zero
+
+// The weights of a row's scores against m >= x.
+//
+// raw(x): round(2^43 * 2^s), s = (x - m) log2(e) / T <= 0, under the exponent
+// bits of 2^52: adding 1.5 * 2^52 rounds s to a whole n, which then stands in
+// the sum's low bits; adding 2^52 to the scaled value rounds it to a whole
+// number in the low 52 bits.  s below -60 (or NaN) is taken as -60 and gives
+// zero.  Callers that add many of them up take the exponent bits out once.
+constexpr uint64_t kRaw = 0x4330000000000000ull;
+struct Weigher {
+  Exp2Poly poly;
+  float m;
+  double md, c;
+  __device__ __forceinline__ Weigher(float m_, double c_) : m(m_), md((double)m_), c(c_) {}
+  __device__ __forceinline__ void against(float m_) {
+    m = m_;
+    md = (double)m_;
+  }
+  __device__ __forceinline__ double log2_of(float x) const { return ((double)x - md) * c; }
+  __device__ __forceinline__ uint64_t raw_of(double s) const {
+    const double magic = 6755399441055744.0;
+    s = __builtin_fmax(s, -60.0);
+    const double sm = s + magic;
+    const double p = poly(s - (sm - magic));
+    const uint32_t hi = ((uint32_t)__double_as_longlong(sm) << 20) + ((1023u + 43u) << 20);
+    return (uint64_t)__double_as_longlong(
+        __builtin_fma(p, __hiloint2double((int)hi, 0), 4503599627370496.0));
+  }
+  __device__ __forceinline__ uint64_t raw(float x) const { return raw_of(log2_of(x)); }
+  // x == m also covers m = +inf, beside which nothing else weighs anything
+  __device__ __forceinline__ uint64_t operator()(float x) const {
+    return x == m ? kOne : raw(x) - kRaw;
+  }
+  // scores that take part in cuts: weights above 2^-44
+  __device__ __forceinline__ bool drawable(float x) const { return x == m || log2_of(x) > -kTmax; }
+  // the weight of a drawable score, zero for others
+  __device__ __forceinline__ uint64_t drawn(float x) const {
+    const double s = log2_of(x);
+    return x == m ? kOne : s > -kTmax ? raw_of(s) - kRaw : 0ull;
+  }
+};
+
+// Prefix sums over a wave of 4- and 8-byte values with DPP row shifts and
+// broadcasts (no LDS: a 64-bit scan by ds_bpermute takes six times as long).
+template <int CTL, int ROWS, class V>
+__device__ __forceinline__ V dpp_from(V v) {  // 0 where there is no source lane
+  uint32_t w[sizeof(V) / 4];
+  __builtin_memcpy(w, &v, sizeof(V));
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i)
+    w[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[i], CTL, ROWS, 0xf, false);
+  __builtin_memcpy(&v, w, sizeof(V));
+  return v;
+}
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {
+  v += dpp_from<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+  v += dpp_from<0x112, 0xf>(v);
+  v += dpp_from<0x114, 0xf>(v);
+  v += dpp_from<0x118, 0xf>(v);
+  v += dpp_from<0x142, 0xa>(v);  // row_bcast 15, 31
+  v += dpp_from<0x143, 0xc>(v);
+  return v;
+}
+// The sum, in every lane.
+template <class V>
+__device__ __forceinline__ V wave_sum(V v) {
+  v = wave_scan(v);
+  uint32_t w[sizeof(V) / 4];
+  __builtin_memcpy(w, &v, sizeof(V));
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i)
+    w[i] = (uint32_t)__builtin_amdgcn_readlane((int)w[i], 63);
+  __builtin_memcpy(&v, w, sizeof(V));
+  return v;
+}
+
+// ---- between workgroups ------------------------------------------------------------
+
+template <class V>
+__device__ __forceinline__ V agent_load(const V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class V>
+__device__ __forceinline__ void agent_store(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // A wave's LDS operations are done in order: this only keeps the compiler
 // from moving them.
 __device__ __forceinline__ void wave_sync() {

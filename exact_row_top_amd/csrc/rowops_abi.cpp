@@ -4,11 +4,11 @@
 
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <string.h>
 
 #include "exact_row_top.h"
 #include "rowops.h"
+#include "rowops_host.h"
 
 namespace ert {
 const void* sample_segment_kernel_ptr(int dtype, bool cuts);
@@ -24,44 +24,6 @@ using namespace ert;
 
 namespace {
 
-bool at(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool dtype_ok(int32_t d) { return d >= TOPK_DT_F32 && d <= TOPK_DT_F16; }
-uintptr_t elem(int32_t d) { return d == TOPK_DT_F32 ? 4 : 2; }
-
-// Whether two arrays of `bytes` each (or one that is not given) lie apart.
-bool apart(const void* a, const void* b, uint64_t bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return !a || !b || (x < y ? y - x : x - y) >= bytes;
-}
-
-// Whether the current device is gfx950 (0 unknown, 1 yes, 2 no per device).
-constexpr int kMaxDev = 64;
-std::atomic<int> g_arch[kMaxDev];
-
-int device_ok() {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDev) return TOPK_EDEVICE;
-  int a = g_arch[dev].load(std::memory_order_relaxed);
-  if (a == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return TOPK_EDEVICE;
-    a = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-    g_arch[dev].store(a, std::memory_order_relaxed);
-  }
-  return a == 1 ? TOPK_OK : TOPK_EDEVICE;
-}
-
-int launch(const void* kernel, int64_t grid, int block, void* params, size_t lds, hipStream_t stream) {
-  if (!kernel || grid < 1 || grid >= ((int64_t)1 << 31)) return TOPK_EINVAL;
-  void* args[] = {params};
-  if (hipLaunchKernel(kernel, dim3((unsigned)grid), dim3((unsigned)block), args, lds, stream) !=
-      hipSuccess) {
-    (void)hipGetLastError();  // reported here, not by the caller's next call
-    return TOPK_ELAUNCH;
-  }
-  return TOPK_OK;
-}
-
 // Segments of a row whose first score may lie up to one 16-byte group past
 // an aligned boundary.
 int64_t segments_of(int32_t vocab) { return ((int64_t)vocab + 7 + kSegment - 1) / kSegment; }
@@ -71,13 +33,6 @@ int64_t wide_wgs_of(int64_t segments) { return (segments + kWideSegs - 1) / kWid
 bool route_shape_ok(int32_t tokens, int32_t experts, int32_t top_k) {
   return tokens >= 0 && experts >= 1 && experts <= kMaxExperts && top_k >= 1 && top_k <= kMaxRouteK &&
          top_k <= experts;
-}
-
-Divisor divisor(uint32_t d) {
-  uint32_t log = 0;
-  while (((uint64_t)1 << log) < d) ++log;
-  if (((uint64_t)1 << log) == d) return Divisor{0, log};
-  return Divisor{(uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), log - 1};
 }
 
 // How a token's experts are spread: 16 lanes up to 256 experts (four tokens a

@@ -1,0 +1,577 @@
+// search_abi.cpp -- C ABI of a beam search's operators over a paged cache:
+// host-side validation (no device reads) and the kernel launches.  The
+// contract is documented in include/exact_row_top.h.
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+
+#include "exact_row_top.h"
+#include "rowops_host.h"
+#include "search.h"
+
+namespace ert {
+const void* beam_segment_kernel_ptr(int dtype);
+const void* beam_row_kernel_ptr(int dtype);
+const void* reorder_rows_kernel_ptr(int n);
+const void* reorder_blocks_kernel_ptr(int n);
+const void* attend_kernel_ptr(int dtype, int dim, int nt);
+const void* attend_join_kernel_ptr(int dtype, int dim);
+const void* attend_mass_kernel_ptr(int dtype, int dim);
+const void* evict_keep_kernel_ptr();
+const void* evict_move_kernel_ptr();
+}  // namespace ert
+
+using namespace ert;
+
+namespace {
+
+constexpr int64_t kInt = ((int64_t)1 << 31) - 1;
+
+// Whether [a, a + na) and [b, b + nb) share no byte (or one is not given).
+bool clear_of(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return !a || !b || x + na <= y || y + nb <= x;
+}
+
+int64_t beam_segments(int32_t vocab) { return ((int64_t)vocab + kSegment - 1) / kSegment; }
+
+// Chunks that a row's threads can find above the k-th largest of their own
+// maxima (fewer than k threads hold any), and each wave's first k that equal it.
+int64_t beam_cap(int64_t segments, int32_t k) {
+  return (int64_t)(k - 1) * ((segments * 64 / (kBeamBlock / 64) + 63) / 64) + (int64_t)k * (kBeamBlock / 64);
+}
+
+struct AttendPlan {
+  int nt;
+  int64_t shared_keys, shared_splits, shared_tiles, own_keys, own_splits, own_tiles, shared_wgs, own_wgs;
+};
+
+// How the work is cut up.  32 or 64 query columns a workgroup; a split's keys
+// so that about 1024 workgroups share the longest rows there may be, but at
+// least one step of a workgroup.
+void plan_kind(int64_t units, int64_t longest, int64_t& keys, int64_t& splits) {
+  const int64_t steps = (longest + kAttendStep - 1) / kAttendStep;
+  int64_t want = units > 0 ? (1024 + units - 1) / units : 1;
+  want = want < 1 ? 1 : (want > steps ? steps : want);
+  const int64_t per = want > 0 ? (steps + want - 1) / want : 1;
+  keys = per * kAttendStep;
+  splits = longest > 0 ? (longest + keys - 1) / keys : 0;
+}
+
+bool attend_plan(int32_t groups, int32_t seqs, bool ragged, int32_t next_n, int32_t heads,
+                 int32_t kv_heads, int64_t max_shared, int64_t max_own, AttendPlan& p) {
+  const int64_t per = heads / kv_heads, rows = (int64_t)next_n * per;
+  const int64_t group_rows = groups > 0 ? (seqs + groups - 1) / groups * rows : 0;
+  p.nt = group_rows > 32 ? 2 : 1;
+  const int64_t cols = 32 * p.nt;
+  p.shared_tiles = ragged ? seqs * rows / cols + groups : groups * ((group_rows + cols - 1) / cols);
+  if (groups == 0 || max_shared == 0) p.shared_tiles = 0;
+  p.own_tiles = (rows + cols - 1) / cols;
+  plan_kind(p.shared_tiles * kv_heads, p.shared_tiles ? max_shared : 0, p.shared_keys, p.shared_splits);
+  plan_kind((int64_t)seqs * kv_heads * p.own_tiles, max_own, p.own_keys, p.own_splits);
+  p.shared_wgs = (p.shared_splits * kv_heads + 7) / 8 * 8 * p.shared_tiles;
+  p.own_wgs = (int64_t)seqs * p.own_splits * kv_heads * p.own_tiles;
+  return p.shared_wgs + p.own_wgs < kInt && p.shared_tiles < kInt;
+}
+
+size_t attend_bytes(const AttendPlan& p, int64_t rows, int32_t dim) {
+  return (size_t)((p.shared_splits + p.own_splits) * rows) * ((size_t)dim * 4 + 8);
+}
+
+// What attention and mass share.
+struct AttendShape {
+  int32_t dtype, groups, seqs, next_n, heads, kv_heads, dim, block_size;
+  int64_t num_blocks;
+};
+
+bool attend_shape_ok(const AttendShape& s, const int32_t* starts) {
+  return (s.dtype == TOPK_DT_BF16 || s.dtype == TOPK_DT_F16) && s.groups >= 0 && s.seqs >= 0 &&
+         s.next_n >= 1 && s.next_n <= 1024 && s.heads >= 1 && s.kv_heads >= 1 && s.heads % s.kv_heads == 0 &&
+         (s.dim == 64 || s.dim == 128) && s.block_size >= 1 && s.block_size <= (1 << 20) &&
+         s.num_blocks >= 0 && s.num_blocks < kInt &&
+         (int64_t)s.seqs * s.next_n * s.heads < kInt &&
+         (starts || s.groups == 0 || s.seqs % s.groups == 0);
+}
+
+bool pages_ok(const void* base, int64_t block, int64_t slot, int64_t head, int64_t num_blocks) {
+  return (base || num_blocks == 0) && block >= 0 && slot >= 0 && head >= 0;
+}
+
+bool pages_at(const void* base, int64_t block, int64_t slot, int64_t head) {
+  return at(base, 16) && block % 8 == 0 && slot % 8 == 0 && head % 8 == 0;
+}
+
+int tables_ok(const int32_t* tables, int64_t stride, int32_t width, const int32_t* lens, int32_t rows) {
+  if (width < 0 || stride < width || (rows > 0 && (!lens || (width > 0 && !tables)))) return TOPK_EINVAL;
+  return at(tables, 4) && at(lens, 4) ? TOPK_OK : TOPK_ELAYOUT;
+}
+
+void attend_params(AttendParams& p, const AttendShape& s, const void* q, int64_t q_stride,
+                   int64_t q_head_stride, const void* k, int64_t k_block, int64_t k_slot, int64_t k_head,
+                   const int32_t* shared_tables, int64_t shared_stride, int32_t shared_width,
+                   const int32_t* shared_lens, int64_t shared_limit, const int32_t* starts,
+                   const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                   const int32_t* own_lens, int64_t own_limit, float scale) {
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const unsigned char*>(q);
+  p.q_stride = q_stride * 2;
+  p.q_head_stride = q_head_stride * 2;
+  p.k = Pages{static_cast<const unsigned char*>(k), k_block * 2, k_slot * 2, k_head * 2};
+  p.num_blocks = s.num_blocks;
+  p.block_size = s.block_size;
+  p.by_block = divisor((uint32_t)s.block_size);
+  p.shared = PageTables{shared_tables, shared_stride, shared_width, (int32_t)shared_limit, shared_lens};
+  p.own = PageTables{own_tables, own_stride, own_width, (int32_t)own_limit, own_lens};
+  p.starts = starts;
+  p.groups = s.groups;
+  p.seqs = s.seqs;
+  p.members = s.groups > 0 ? s.seqs / s.groups : 1;
+  p.next_n = s.next_n;
+  p.heads = s.heads;
+  p.kv_heads = s.kv_heads;
+  p.per = s.heads / s.kv_heads;
+  // (a scale of zero, too, has to leave -inf where positions are masked)
+  p.scale = fmaxf(scale * 1.44269504f, 1e-30f);
+  p.rows = (int64_t)s.seqs * s.next_n * s.heads;
+}
+
+// The positions that rows of a table can hold, cut to the caller's bound; -1
+// if there are too many.
+constexpr int64_t kMaxPositions = (int64_t)1 << 30;
+int64_t longest_of(int32_t width, int64_t block_size, int64_t num_blocks, int64_t bound) {
+  const int64_t most = num_blocks > 0 ? (int64_t)width * block_size : 0;
+  if (most > kMaxPositions) return -1;
+  return bound > 0 && bound < most ? bound : most;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t topk_beams_workspace_bytes(int32_t num_requests, int32_t beams, int32_t k, int32_t vocab) {
+  if (num_requests < 1 || beams < 1 || beams > kMaxBeams || k < 1 || k > kMaxBeamK || vocab < 1 ||
+      vocab > kMaxVocab)
+    return 0;
+  const size_t rows = (size_t)num_requests * beams, seg = (size_t)beam_segments(vocab);
+  return rows * (seg * (8 + 4 + 64 * 4) + (size_t)k * sizeof(BeamCandidate)) + (size_t)num_requests * 4 + 16;
+}
+
+int topk_beams(const void* logits, int32_t dtype, int64_t row_stride, int32_t vocab, int32_t num_requests,
+               int32_t beams, int32_t k, const float* scores, const uint8_t* ended, int32_t end_token,
+               const int32_t* lengths, float length_penalty, float* out_scores, int32_t* parents,
+               int32_t* tokens, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (num_requests < 0 || beams < 1 || beams > kMaxBeams || k < 1 || k > kMaxBeamK || !dtype_ok(dtype) ||
+      vocab < 1 || vocab > kMaxVocab || row_stride < vocab || !isfinite(length_penalty) ||
+      (ended && (end_token < 0 || end_token >= vocab)))
+    return TOPK_EINVAL;
+  if (num_requests == 0) return TOPK_OK;
+  if (!logits || !scores || !out_scores || !parents || !tokens) return TOPK_EINVAL;
+  if (!at(logits, elem(dtype)) || !at(scores, 4) || !at(lengths, 4) || !at(out_scores, 4) ||
+      !at(parents, 4) || !at(tokens, 4) || !at(workspace, 16))
+    return TOPK_ELAYOUT;
+  const int64_t rows = (int64_t)num_requests * beams, segments = beam_segments(vocab);
+  if (rows * segments >= kInt) return TOPK_EINVAL;
+  // a request's workgroups read its settings while another's may be done
+  const uint64_t in = (uint64_t)rows * 4, out = (uint64_t)num_requests * k * 4;
+  const void* outs[] = {out_scores, parents, tokens};
+  for (int i = 0; i < 3; ++i) {
+    if (!clear_of(outs[i], out, scores, in) || !clear_of(outs[i], out, lengths, in) ||
+        !clear_of(outs[i], out, ended, (uint64_t)rows) || !clear_of(outs[i], out, outs[(i + 1) % 3], out))
+      return TOPK_EINVAL;
+  }
+  if (!workspace || workspace_bytes < topk_beams_workspace_bytes(num_requests, beams, k, vocab))
+    return TOPK_EWORKSPACE;
+  int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  BeamParams p;
+  memset(&p, 0, sizeof(p));
+  p.logits = logits;
+  p.row_stride = row_stride;
+  p.vocab = vocab;
+  p.rows = (int32_t)rows;
+  p.beams = beams;
+  p.k = k;
+  p.segments = (int32_t)segments;
+  p.scores = scores;
+  p.ended = ended;
+  p.end_token = end_token;
+  p.lengths = lengths;
+  p.penalty = (double)length_penalty;
+  p.out_scores = out_scores;
+  p.parents = parents;
+  p.tokens = tokens;
+  p.found = static_cast<BeamCandidate*>(workspace);
+  p.masses = reinterpret_cast<uint64_t*>(p.found + rows * k);
+  p.bests = reinterpret_cast<float*>(p.masses + rows * segments);
+  p.chunks = p.bests + rows * segments;
+  p.arrived = reinterpret_cast<uint32_t*>(p.chunks + rows * segments * 64);
+  p.cap = (int32_t)beam_cap(segments, k);
+  rc = launch(beam_segment_kernel_ptr(dtype), (rows * segments + 3) / 4, 256, &p, 0, stream);
+  if (rc != TOPK_OK) return rc;
+  size_t lds = (size_t)p.cap * 8;
+  const size_t gather = (size_t)k * kChunk * 8, merge = (size_t)beams * k * 16;
+  lds = lds > gather ? lds : gather;
+  lds = lds > merge ? lds : merge;
+  return launch(beam_row_kernel_ptr(dtype), rows, kBeamBlock, &p, lds, stream);
+}
+
+int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* const* targets,
+                      const int64_t* source_strides, const int64_t* target_strides,
+                      const int64_t* row_bytes, const int32_t* parents, int32_t num_requests,
+                      int32_t beams, int32_t k, int32_t clear, hipStream_t stream) {
+  if (num_arrays < 0 || num_requests < 0 || beams < 1 || k < 1 || k > kMaxBeams || beams > kMaxBeams ||
+      (clear != 0 && clear != 1))
+    return TOPK_EINVAL;
+  if (num_arrays == 0 || num_requests == 0) return TOPK_OK;
+  if (!sources || !targets || !source_strides || !target_strides || !row_bytes || !parents)
+    return TOPK_EINVAL;
+  if (!at(parents, 4)) return TOPK_ELAYOUT;
+  for (int32_t a = 0; a < num_arrays; ++a) {
+    const int64_t n = row_bytes[a], ss = source_strides[a], ts = target_strides[a];
+    const int64_t rows = (int64_t)num_requests * beams, outs = (int64_t)num_requests * k;
+    if (n < 0 || n > ((int64_t)1 << 40) || ss < n || ts < n || ss > ((int64_t)1 << 40) ||
+        ts > ((int64_t)1 << 40))
+      return TOPK_EINVAL;
+    if (n == 0) continue;
+    if (!sources[a] || !targets[a]) return TOPK_EINVAL;
+    const uint64_t sb = (uint64_t)((rows - 1) * ss + n), tb = (uint64_t)((outs - 1) * ts + n);
+    const bool in_place = sources[a] == targets[a] && ss == ts && beams == k;
+    if (!in_place && !clear_of(sources[a], sb, targets[a], tb)) return TOPK_EINVAL;
+    if (!clear_of(parents, (uint64_t)outs * 4, targets[a], tb)) return TOPK_EINVAL;
+    if ((n + 16 * kCopyBlock - 1) / (16 * kCopyBlock) * num_requests >= kInt) return TOPK_EINVAL;
+  }
+  int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  ReorderParams p;
+  memset(&p, 0, sizeof(p));
+  p.parents = parents;
+  p.requests = num_requests;
+  p.beams = beams;
+  p.k = k;
+  p.clear = clear;
+  int64_t grid = 0;
+  auto flush = [&]() -> int {
+    if (p.copies == 0) return TOPK_OK;
+    const int status = launch(reorder_rows_kernel_ptr(k <= 8 ? 8 : 32), grid, kCopyBlock, &p, 0, stream);
+    p.copies = 0;
+    grid = 0;
+    return status;
+  };
+  for (int32_t a = 0; a < num_arrays; ++a) {
+    if (row_bytes[a] == 0) continue;
+    const int64_t tiles = (row_bytes[a] + 16 * kCopyBlock - 1) / (16 * kCopyBlock);
+    if (p.copies == kMaxCopies || grid + tiles * num_requests >= kInt) {
+      rc = flush();
+      if (rc != TOPK_OK) return rc;
+    }
+    p.copy[p.copies++] = RowCopy{static_cast<const unsigned char*>(sources[a]),
+                                 static_cast<unsigned char*>(targets[a]), source_strides[a],
+                                 target_strides[a], row_bytes[a], (uint32_t)tiles, (uint32_t)grid};
+    grid += tiles * num_requests;
+  }
+  return flush();
+}
+
+int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
+                        const int32_t* kv_lens, const int32_t* parents, int32_t num_requests,
+                        int32_t beams, int32_t k, int32_t block_size, const int32_t* tail_blocks,
+                        int32_t* out_tables, int64_t out_stride, int32_t num_caches, void* const* caches,
+                        int64_t num_blocks, int64_t slot_bytes, hipStream_t stream) {
+  if (num_requests < 0 || beams < 1 || beams > kMaxBeams || k < 1 || k > kMaxBeams || max_blocks < 0 ||
+      table_stride < max_blocks || out_stride < max_blocks || block_size < 1 || block_size > (1 << 20) ||
+      num_caches < 0 || num_caches > kMaxCaches || num_blocks < 0 || num_blocks > kInt || slot_bytes < 0 ||
+      slot_bytes > ((int64_t)1 << 31) || (!tail_blocks && beams != k))
+    return TOPK_EINVAL;
+  if (num_requests == 0) return TOPK_OK;
+  if (!kv_lens || !parents || (max_blocks > 0 && (!block_tables || !out_tables)) ||
+      (num_caches > 0 && !caches))
+    return TOPK_EINVAL;
+  if (!at(block_tables, 4) || !at(kv_lens, 4) || !at(parents, 4) || !at(tail_blocks, 4) || !at(out_tables, 4))
+    return TOPK_ELAYOUT;
+  for (int32_t c = 0; c < num_caches; ++c)
+    if (!caches[c] && num_blocks > 0 && slot_bytes > 0) return TOPK_EINVAL;
+  const int64_t rows = (int64_t)num_requests * beams, outs = (int64_t)num_requests * k;
+  const bool in_place = block_tables == out_tables && table_stride == out_stride && beams == k;
+  const uint64_t out_bytes = max_blocks > 0 ? (uint64_t)((outs - 1) * out_stride + max_blocks) * 4 : 0;
+  if (!in_place && max_blocks > 0 &&
+      !clear_of(block_tables, (uint64_t)((rows - 1) * table_stride + max_blocks) * 4, out_tables, out_bytes))
+    return TOPK_EINVAL;
+  if (max_blocks > 0 && (!clear_of(out_tables, out_bytes, parents, (uint64_t)outs * 4) ||
+                         !clear_of(out_tables, out_bytes, kv_lens, (uint64_t)num_requests * 4) ||
+                         !clear_of(out_tables, out_bytes, tail_blocks, (uint64_t)outs * 4)))
+    return TOPK_EINVAL;
+  int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  if (max_blocks == 0) return TOPK_OK;
+  ReorderBlocksParams p;
+  memset(&p, 0, sizeof(p));
+  p.parents = parents;
+  p.requests = num_requests;
+  p.beams = beams;
+  p.k = k;
+  p.tables = block_tables;
+  p.table_stride = table_stride;
+  p.max_blocks = max_blocks;
+  p.out = out_tables;
+  p.out_stride = out_stride;
+  p.kv_lens = kv_lens;
+  p.tail = tail_blocks;
+  p.by_block = divisor((uint32_t)block_size);
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.slot_bytes = slot_bytes;
+  p.block_stride = slot_bytes * block_size;
+  p.caches = num_blocks > 0 && slot_bytes > 0 ? num_caches : 0;
+  const int64_t tiles = (p.block_stride + 16 * kCopyBlock - 1) / (16 * kCopyBlock);
+  p.tiles = (uint32_t)(tiles < 1 ? 1 : (tiles > 64 ? 64 : tiles));
+  p.table_tiles = (uint32_t)((max_blocks + kCopyBlock - 1) / kCopyBlock);
+  for (int32_t c = 0; c < p.caches; ++c) p.cache[c] = static_cast<unsigned char*>(caches[c]);
+  const int64_t copying = (int64_t)p.caches * num_requests * p.tiles;
+  const int64_t making = (int64_t)num_requests * p.table_tiles;
+  if (copying + making >= kInt) return TOPK_EINVAL;
+  const void* kernel = reorder_blocks_kernel_ptr(k <= 8 ? 8 : 32);
+  p.copying = copying > 0 ? 1 : 0;
+  // In place, given blocks take the place of the table entries that say where
+  // the parents' open blocks lie: copied first, then written.
+  if (in_place && tail_blocks && copying > 0) {
+    rc = launch(kernel, copying, kCopyBlock, &p, 0, stream);
+    if (rc != TOPK_OK) return rc;
+    p.copying = 0;
+  }
+  return launch(kernel, (p.copying ? copying : 0) + making, kCopyBlock, &p, 0, stream);
+}
+
+size_t topk_attend_workspace_bytes(int32_t num_groups, int32_t num_seqs, int32_t ragged, int32_t next_n,
+                                   int32_t num_heads, int32_t num_kv_heads, int32_t dim,
+                                   int64_t max_shared_len, int64_t max_own_len) {
+  if (num_groups < 0 || num_seqs < 1 || next_n < 1 || num_heads < 1 || num_kv_heads < 1 ||
+      num_heads % num_kv_heads || (dim != 64 && dim != 128) || max_shared_len < 0 || max_own_len < 0 ||
+      (int64_t)num_seqs * next_n >= kInt || (int64_t)num_seqs * next_n * num_heads >= kInt ||
+      max_shared_len > kInt || max_own_len > kInt)
+    return 0;
+  AttendPlan plan;
+  if (!attend_plan(num_groups, num_seqs, ragged != 0, next_n, num_heads, num_kv_heads, max_shared_len,
+                   max_own_len, plan))
+    return 0;
+  return attend_bytes(plan, (int64_t)num_seqs * next_n * num_heads, dim) + 16;
+}
+
+int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
+                int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
+                int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, const void* v_cache,
+                int64_t v_block_stride, int64_t v_slot_stride, int64_t v_head_stride, int64_t num_blocks,
+                int32_t block_size, const int32_t* shared_tables, int64_t shared_stride,
+                int32_t shared_width, const int32_t* shared_lens, const int32_t* group_starts,
+                int32_t num_groups, const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                const int32_t* own_lens, float scale, int64_t max_shared_len, int64_t max_own_len,
+                void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const AttendShape s{dtype, num_groups, num_seqs, next_n, num_heads, num_kv_heads, dim, block_size, num_blocks};
+  if (!attend_shape_ok(s, group_starts) || !(scale >= 0.0f) || isinf(scale) || q_stride < 0 || q_head_stride < 0 ||
+      max_shared_len < 0 || max_own_len < 0)
+    return TOPK_EINVAL;
+  if (num_seqs == 0) return TOPK_OK;
+  if (!q || !out || !pages_ok(k_cache, k_block_stride, k_slot_stride, k_head_stride, num_blocks) ||
+      !pages_ok(v_cache, v_block_stride, v_slot_stride, v_head_stride, num_blocks))
+    return TOPK_EINVAL;
+  if (!at(q, 16) || q_stride % 8 || q_head_stride % 8 || !at(out, 16) || !at(lse, 4) || !at(group_starts, 4) ||
+      !pages_at(k_cache, k_block_stride, k_slot_stride, k_head_stride) ||
+      !pages_at(v_cache, v_block_stride, v_slot_stride, v_head_stride) || !at(workspace, 16))
+    return TOPK_ELAYOUT;
+  int rc = tables_ok(shared_tables, shared_stride, shared_width, shared_lens, num_groups);
+  if (rc != TOPK_OK) return rc;
+  rc = tables_ok(own_tables, own_stride, own_width, own_lens, num_seqs);
+  if (rc != TOPK_OK) return rc;
+  const int64_t most_shared = longest_of(num_groups > 0 ? shared_width : 0, block_size, num_blocks, max_shared_len);
+  const int64_t most_own = longest_of(own_width, block_size, num_blocks, max_own_len);
+  AttendPlan plan;
+  if (most_shared < 0 || most_own < 0 ||
+      !attend_plan(num_groups, num_seqs, group_starts != nullptr, next_n, num_heads, num_kv_heads, most_shared,
+                   most_own, plan))
+    return TOPK_EINVAL;
+  const int64_t rows = (int64_t)num_seqs * next_n * num_heads;
+  const size_t bytes = attend_bytes(plan, rows, dim);
+  if (bytes > 0 && (!workspace || workspace_bytes < bytes)) return TOPK_EWORKSPACE;
+  rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  AttendParams p;
+  attend_params(p, s, q, q_stride, q_head_stride, k_cache, k_block_stride, k_slot_stride, k_head_stride,
+                shared_tables, shared_stride, shared_width, shared_lens, most_shared, group_starts, own_tables,
+                own_stride, own_width, own_lens, most_own, scale);
+  p.v = Pages{static_cast<const unsigned char*>(v_cache), v_block_stride * 2, v_slot_stride * 2, v_head_stride * 2};
+  p.shared_keys = (int32_t)plan.shared_keys;
+  p.shared_splits = (int32_t)plan.shared_splits;
+  p.shared_tiles = (int32_t)plan.shared_tiles;
+  p.own_keys = (int32_t)plan.own_keys;
+  p.own_splits = (int32_t)plan.own_splits;
+  p.own_tiles = (int32_t)plan.own_tiles;
+  p.shared_wgs = plan.shared_wgs;
+  p.parts = static_cast<float*>(workspace);
+  p.stats = reinterpret_cast<float2*>(p.parts + (plan.shared_splits + plan.own_splits) * rows * dim);
+  p.out = static_cast<unsigned char*>(out);
+  p.lse = lse;
+  if (plan.shared_wgs + plan.own_wgs > 0) {
+    rc = launch(attend_kernel_ptr(dtype, dim, plan.nt), plan.shared_wgs + plan.own_wgs, kAttendBlock, &p, 0, stream);
+    if (rc != TOPK_OK) return rc;
+  }
+  const int64_t per = 256 / (dim / 4);
+  return launch(attend_join_kernel_ptr(dtype, dim), (rows + per - 1) / per, 256, &p, 0, stream);
+}
+
+int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
+                     int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
+                     int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, int64_t num_blocks,
+                     int32_t block_size, const int32_t* shared_tables, int64_t shared_stride,
+                     int32_t shared_width, const int32_t* shared_lens, const int32_t* group_starts,
+                     int32_t num_groups, const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                     const int32_t* own_lens, float scale, const float* lse, float decay,
+                     const float* shared_mass, float* shared_out, int32_t shared_positions,
+                     const float* own_mass, float* own_out, int32_t own_positions, hipStream_t stream) {
+  const AttendShape s{dtype, num_groups, num_seqs, next_n, num_heads, num_kv_heads, dim, block_size, num_blocks};
+  if (!attend_shape_ok(s, group_starts) || !(scale >= 0.0f) || isinf(scale) || q_stride < 0 || q_head_stride < 0 ||
+      !isfinite(decay) || shared_positions < 0 || shared_positions > kMaxPositions || own_positions < 0 ||
+      own_positions > kMaxPositions)
+    return TOPK_EINVAL;
+  if (num_seqs > 0 && (!q || !lse)) return TOPK_EINVAL;
+  if (!pages_ok(k_cache, k_block_stride, k_slot_stride, k_head_stride, num_blocks)) return TOPK_EINVAL;
+  const uint64_t sb = (uint64_t)num_groups * num_kv_heads * shared_positions * 4;
+  const uint64_t ob = (uint64_t)num_seqs * num_kv_heads * own_positions * 4;
+  if ((sb > 0 && !shared_out) || (ob > 0 && !own_out)) return TOPK_EINVAL;
+  if (!at(q, 16) || q_stride % 8 || q_head_stride % 8 || !at(lse, 4) || !at(group_starts, 4) ||
+      !at(shared_mass, 4) || !at(shared_out, 4) || !at(own_mass, 4) || !at(own_out, 4) ||
+      !pages_at(k_cache, k_block_stride, k_slot_stride, k_head_stride))
+    return TOPK_ELAYOUT;
+  if ((shared_mass != shared_out && !clear_of(shared_mass, sb, shared_out, sb)) ||
+      (own_mass != own_out && !clear_of(own_mass, ob, own_out, ob)) || !clear_of(shared_out, sb, own_out, ob) ||
+      !clear_of(shared_out, sb, own_mass, ob) || !clear_of(own_out, ob, shared_mass, sb))
+    return TOPK_EINVAL;
+  int rc = tables_ok(shared_tables, shared_stride, shared_width, shared_lens, num_groups);
+  if (rc != TOPK_OK) return rc;
+  rc = tables_ok(own_tables, own_stride, own_width, own_lens, num_seqs);
+  if (rc != TOPK_OK) return rc;
+  const int64_t most_shared = longest_of(num_groups > 0 ? shared_width : 0, block_size, num_blocks, 0);
+  const int64_t most_own = longest_of(own_width, block_size, num_blocks, 0);
+  if (most_shared < 0 || most_own < 0) return TOPK_EINVAL;
+  const int64_t shared_tiles = ((int64_t)shared_positions + kAttendStep - 1) / kAttendStep;
+  const int64_t own_tiles = ((int64_t)own_positions + kAttendStep - 1) / kAttendStep;
+  const int64_t shared_wgs = shared_tiles * num_groups * num_kv_heads;
+  const int64_t own_wgs = own_tiles * num_seqs * num_kv_heads;
+  if (shared_wgs + own_wgs >= kInt) return TOPK_EINVAL;
+  if (shared_wgs + own_wgs == 0) return TOPK_OK;
+  rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  MassParams p;
+  attend_params(p.a, s, q, q_stride, q_head_stride, k_cache, k_block_stride, k_slot_stride, k_head_stride,
+                shared_tables, shared_stride, shared_width, shared_lens, most_shared, group_starts, own_tables,
+                own_stride, own_width, own_lens, most_own, scale);
+  p.lse = lse;
+  p.shared_in = shared_mass;
+  p.shared_out = shared_out;
+  p.shared_width = shared_positions;
+  p.own_in = own_mass;
+  p.own_out = own_out;
+  p.own_width = own_positions;
+  p.decay = decay;
+  p.shared_tiles = (int32_t)shared_tiles;
+  p.own_tiles = (int32_t)own_tiles;
+  p.shared_wgs = shared_wgs;
+  return launch(attend_mass_kernel_ptr(dtype, dim), shared_wgs + own_wgs, kAttendBlock, &p, 0, stream);
+}
+
+int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stride, int32_t positions,
+                    int32_t num_requests, int32_t num_heads, const int32_t* kv_lens, int32_t budget,
+                    int32_t sinks, int32_t recent, int32_t* kept, float* mass_out, int32_t out_positions,
+                    int32_t* new_lens, hipStream_t stream) {
+  if (num_requests < 0 || num_heads < 1 || positions < 0 || request_stride < 0 || head_stride < 0 ||
+      budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget ||
+      (mass_out && out_positions < budget) || positions > (1 << 30) || budget > (1 << 30) ||
+      (int64_t)num_requests * num_heads >= kInt)
+    return TOPK_EINVAL;
+  if (num_requests == 0) return TOPK_OK;
+  if ((!mass && positions > 0) || !kv_lens || !kept || !new_lens || kv_lens == new_lens) return TOPK_EINVAL;
+  if (!at(mass, 4) || !at(kv_lens, 4) || !at(kept, 4) || !at(mass_out, 4) || !at(new_lens, 4)) return TOPK_ELAYOUT;
+  const int64_t rows = (int64_t)num_requests * num_heads;
+  const uint64_t in = positions > 0 ? (uint64_t)((num_requests - 1) * request_stride + (num_heads - 1) * head_stride + positions) * 4 : 0;
+  const uint64_t kb = (uint64_t)rows * budget * 4, mb = (uint64_t)rows * out_positions * 4, nb = (uint64_t)num_requests * 4;
+  if (!clear_of(mass, in, kept, kb) || !clear_of(mass, in, mass_out, mb) || !clear_of(mass, in, new_lens, nb) ||
+      !clear_of(kv_lens, nb, kept, kb) || !clear_of(kv_lens, nb, mass_out, mb) || !clear_of(kv_lens, nb, new_lens, nb) ||
+      !clear_of(kept, kb, mass_out, mb) || !clear_of(kept, kb, new_lens, nb) || !clear_of(mass_out, mb, new_lens, nb))
+    return TOPK_EINVAL;
+  const int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  KeepParams p;
+  memset(&p, 0, sizeof(p));
+  p.mass = mass;
+  p.request_stride = request_stride;
+  p.head_stride = head_stride;
+  p.positions = positions;
+  p.requests = num_requests;
+  p.heads = num_heads;
+  p.kv_lens = kv_lens;
+  p.budget = budget;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.kept = kept;
+  p.mass_out = mass_out;
+  p.out_positions = out_positions;
+  p.new_lens = new_lens;
+  return launch(evict_keep_kernel_ptr(), rows, kKeepBlock, &p, 0, stream);
+}
+
+int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads, int32_t budget,
+                    const int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
+                    const int32_t* out_tables, int64_t out_stride, int32_t out_blocks, int32_t block_size,
+                    int32_t num_caches, void* const* caches, int64_t num_blocks, int64_t slot_bytes,
+                    hipStream_t stream) {
+  if (num_requests < 0 || num_heads < 1 || budget < 1 || budget > (1 << 30) || max_blocks < 0 || table_stride < max_blocks ||
+      out_blocks < 0 || out_stride < out_blocks || block_size < 1 || block_size > (1 << 20) || num_caches < 0 ||
+      num_caches > kMaxCaches || num_blocks < 0 || num_blocks > kInt || slot_bytes < 0 ||
+      slot_bytes > ((int64_t)1 << 31) || slot_bytes % num_heads || (slot_bytes / num_heads) % 16)
+    return TOPK_EINVAL;
+  if (num_requests == 0 || num_caches == 0 || slot_bytes == 0 || num_blocks == 0) return TOPK_OK;
+  if (!kept || !caches || (max_blocks > 0 && !block_tables) || (out_blocks > 0 && !out_tables)) return TOPK_EINVAL;
+  if (!at(kept, 4) || !at(block_tables, 4) || !at(out_tables, 4)) return TOPK_ELAYOUT;
+  for (int32_t c = 0; c < num_caches; ++c) {
+    if (!caches[c]) return TOPK_EINVAL;
+    if (!at(caches[c], 16)) return TOPK_ELAYOUT;
+  }
+  if (max_blocks == 0 || out_blocks == 0) return TOPK_OK;
+  const int rc = device_ok();
+  if (rc != TOPK_OK) return rc;
+  MoveParams p;
+  memset(&p, 0, sizeof(p));
+  p.kept = kept;
+  p.requests = num_requests;
+  p.heads = num_heads;
+  p.budget = budget;
+  p.tables = block_tables;
+  p.table_stride = table_stride;
+  p.max_blocks = max_blocks;
+  p.out_tables = out_tables;
+  p.out_stride = out_stride;
+  p.out_blocks = out_blocks;
+  p.by_block = divisor((uint32_t)block_size);
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.slot_bytes = slot_bytes;
+  p.row_bytes = slot_bytes / num_heads;
+  p.caches = num_caches;
+  for (int32_t c = 0; c < num_caches; ++c) p.cache[c] = static_cast<unsigned char*>(caches[c]);
+  // Other bytes of a row are another workgroup's, 256 of them at least; rows
+  // are split too where targets are not sources.
+  const int64_t rows = (int64_t)num_caches * num_requests * num_heads;
+  const int64_t pieces = p.row_bytes / 16;
+  int64_t columns = (pieces + 15) / 16;
+  while (columns > 1 && rows * columns > 4096) columns = (columns + 1) / 2;
+  p.columns = (int32_t)columns;
+  int64_t parts = 1;
+  if (block_tables != out_tables) {
+    parts = 2048 / (rows * columns);
+    const int64_t most = ((int64_t)budget + 127) / 128;
+    parts = parts < 1 ? 1 : (parts > most ? most : parts);
+  }
+  p.parts = (int32_t)parts;
+  return launch(evict_move_kernel_ptr(), rows * columns * parts, kMoveBlock, &p, 0, stream);
+}
+
+}  // extern "C"

@@ -521,6 +521,163 @@ int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_
                const int32_t* row_requests, int32_t next_n, int32_t block_size, void* slots,
                int32_t slots_64, hipStream_t stream);
 
+/* ---- A beam search's step over a paged cache -----------------------------------
+ * The choice across a request's rows, what it does to the rows' states and
+ * cache, attention over a cache whose prefix sequences share, and which cached
+ * positions stay.  The conventions of the row operators hold.  Block tables
+ * are int32 rows of max_blocks entries, table_stride apart; position p of a
+ * row lies in block table[p / block_size] at p % block_size. */
+
+/* The k best continuations of each request's beams.
+ *
+ * logits [num_requests * beams][vocab]; scores, ended, lengths
+ * [num_requests][beams].  Beam b offers each token i whose logit is neither
+ * NaN nor -inf with the total scores[b] + x_i - ln sum_j exp(x_j) (+inf logits
+ * share the whole weight); an ended beam offers end_token alone, with its
+ * score as it is, and its logits are not read; a beam whose score is not
+ * finite offers nothing.  A total's rank is total / n^length_penalty with n =
+ * lengths[b] + 1 (ended: lengths[b]; at least 1), or the total itself without
+ * lengths.  The k largest ranks are chosen in falling order, equal ones by
+ * beam, then token.
+ *  out_scores, parents, tokens: device float / int32 / int32
+ *      [num_requests][k]: total, beam and token; places without a candidate
+ *      hold -inf, -1, -1.
+ *  ended: device uint8 or NULL, lengths: device int32 or NULL.
+ * Sums are 64-bit, of weights that are whole multiples of 2^-43 of a 2048-score
+ * segment's largest: totals are off by at most vocab * 2^-43 of a weight sum
+ * and 2^-45 beside it, so only totals that near each other may come in either
+ * order; beams with equal scores and logits tie to the bit.
+ * vocab 1 .. 2^20, beams 1 .. 32, k 1 .. 64; workspace as for topk_sample, of
+ * topk_beams_workspace_bytes(...) bytes. */
+size_t topk_beams_workspace_bytes(int32_t num_requests, int32_t beams, int32_t k, int32_t vocab);
+
+int topk_beams(const void* logits, int32_t dtype, int64_t row_stride, int32_t vocab, int32_t num_requests,
+               int32_t beams, int32_t k, const float* scores, const uint8_t* ended, int32_t end_token,
+               const int32_t* lengths, float length_penalty, float* out_scores, int32_t* parents,
+               int32_t* tokens, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Rows by parent: for each array a, row r * k + j of targets[a] becomes row r *
+ * beams + parents[r][j] of sources[a] (device pointers in host arrays;
+ * strides and row_bytes in bytes, any alignment).  A target may be its source
+ * (same stride, beams == k): rows are then moved in place, whatever the
+ * parents; it overlaps nothing else.  Rows whose parent is not in [0, beams)
+ * are cleared (clear 1) or left (clear 0).  beams, k 1 .. 32. */
+int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* const* targets,
+                      const int64_t* source_strides, const int64_t* target_strides,
+                      const int64_t* row_bytes, const int32_t* parents, int32_t num_requests,
+                      int32_t beams, int32_t k, int32_t clear, hipStream_t stream);
+
+/* Paged rows by parent.  All beams of request r hold kv_lens[r] tokens: full =
+ * kv_lens[r] / block_size full blocks and, where kv_lens[r] % block_size > 0,
+ * an open one.  Child j's table row gets its parent's entries [0, full), and
+ * as entry `full` the child's own open block: tail_blocks[r][j] or, with
+ * tail_blocks NULL (beams == k), the entry its own row holds there; the open
+ * block's tokens are copied from the parent's to the child's own in every
+ * cache.  Further entries are those of the child's own row (beams == k), else
+ * -1.  So full blocks are shared and no block is ever taken or returned; the
+ * open blocks of a request's rows are distinct, and blocks written for one
+ * request are no other request's.  A child whose parent is not in [0, beams)
+ * keeps its own row (-1 where beams != k); blocks outside [0, num_blocks) are
+ * not copied.
+ *  out_tables: [num_requests * k][max_blocks], may be block_tables (same
+ *      stride, beams == k).
+ *  caches: num_caches (at most 64) device arrays [num_blocks][block_size] of
+ *      slot_bytes bytes each, contiguous, in a host array.
+ * beams, k 1 .. 32. */
+int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
+                        const int32_t* kv_lens, const int32_t* parents, int32_t num_requests,
+                        int32_t beams, int32_t k, int32_t block_size, const int32_t* tail_blocks,
+                        int32_t* out_tables, int64_t out_stride, int32_t num_caches, void* const* caches,
+                        int64_t num_blocks, int64_t slot_bytes, hipStream_t stream);
+
+/* Decode attention of sequences that share prefixes, bfloat16 or float16.
+ *
+ * q [num_seqs * next_n][num_heads][dim], next_n tokens a sequence, one after
+ * the other; caches [num_blocks][block_size][num_kv_heads][dim] by their
+ * strides (elements, multiples of 8); query head h reads key head h /
+ * (num_heads / num_kv_heads).  Group g, the sequences group_starts[g] ..
+ * group_starts[g + 1] - 1 (device int32[num_groups + 1], rising; NULL:
+ * num_groups equal groups), sees the first shared_lens[g] positions of
+ * shared_tables row g; then sequence s's token t sees the first own_lens[s] -
+ * next_n + t + 1 positions of own_tables row s.  Sequences in no group have no
+ * prefix.
+ *     out = sum_p softmax_p(scale q k_p) v_p,  lse = ln sum_p exp(scale q k_p)
+ * over all of them; a token that sees nothing gives 0 and -inf.  Lengths are
+ * cut to [0, what the table row holds] (and max_shared_len, max_own_len where
+ * those are > 0: bounds that the work is planned for).  Positions whose block
+ * is not in [0, num_blocks) are left out.  Slots behind the lengths may hold
+ * anything; values that some token of a sequence sees must be finite for all
+ * of its tokens.  scale >= 0.  Scores, sums and the weighted values are 32-bit;
+ * weights are rounded to the caches' type.
+ *  out: [num_seqs * next_n][num_heads][dim] in q's type, contiguous, 16-byte
+ *      aligned; lse: float [num_seqs * next_n][num_heads] or NULL.
+ *  workspace: topk_attend_workspace_bytes(...) bytes (ragged: group_starts is
+ *      given; the longest lengths as planned for), 16-byte aligned.
+ * dim 64 or 128, next_n 1 .. 1024, at most 2^30 positions a row. */
+size_t topk_attend_workspace_bytes(int32_t num_groups, int32_t num_seqs, int32_t ragged, int32_t next_n,
+                                   int32_t num_heads, int32_t num_kv_heads, int32_t dim,
+                                   int64_t max_shared_len, int64_t max_own_len);
+
+int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
+                int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
+                int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, const void* v_cache,
+                int64_t v_block_stride, int64_t v_slot_stride, int64_t v_head_stride, int64_t num_blocks,
+                int32_t block_size, const int32_t* shared_tables, int64_t shared_stride,
+                int32_t shared_width, const int32_t* shared_lens, const int32_t* group_starts,
+                int32_t num_groups, const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                const int32_t* own_lens, float scale, int64_t max_shared_len, int64_t max_own_len,
+                void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Attention mass of cached positions, from topk_attend's lse:
+ *     shared_out[g][h][p] = decay shared_mass[g][h][p] + sum of exp(scale q k_p
+ *         - lse) over the group's tokens and the query heads of key head h,
+ * and the same of own_out[s][h][p] over sequence s's tokens that see p.  Every
+ * position of the rows ([..][num_kv_heads][shared_positions] and
+ * [..][num_kv_heads][own_positions], contiguous float) is written; those that
+ * no token sees get the decayed mass alone.  A mass array may be NULL (zeros)
+ * or its output.  Tokens whose lse is -inf or NaN add nothing.  The rest as for
+ * topk_attend; sums have one order, so results repeat bit for bit. */
+int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
+                     int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
+                     int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, int64_t num_blocks,
+                     int32_t block_size, const int32_t* shared_tables, int64_t shared_stride,
+                     int32_t shared_width, const int32_t* shared_lens, const int32_t* group_starts,
+                     int32_t num_groups, const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                     const int32_t* own_lens, float scale, const float* lse, float decay,
+                     const float* shared_mass, float* shared_out, int32_t shared_positions,
+                     const float* own_mass, float* own_out, int32_t own_positions, hipStream_t stream);
+
+/* The cached positions that stay: of request r's n = kv_lens[r] positions (cut
+ * to [0, positions]) in each of num_heads rows of mass (strides in elements),
+ * all where n <= budget, else the first `sinks`, the last `recent`, and the
+ * budget - sinks - recent of the others with the largest mass (equal masses:
+ * the lower position first; NaN below all).
+ *  kept: int32 [num_requests][num_heads][budget], rising, then -1;
+ *  mass_out: float [num_requests][num_heads][out_positions] or NULL: the kept
+ *      positions' mass, then 0; out_positions >= budget;
+ *  new_lens: int32 [num_requests]: min(n, budget).
+ * budget >= 1, sinks + recent <= budget. */
+int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stride, int32_t positions,
+                    int32_t num_requests, int32_t num_heads, const int32_t* kv_lens, int32_t budget,
+                    int32_t sinks, int32_t recent, int32_t* kept, float* mass_out, int32_t out_positions,
+                    int32_t* new_lens, hipStream_t stream);
+
+/* Moves the kept positions' rows to the front: in every cache and of every head
+ * group, position j of out_tables row r becomes position kept[r][h][j] of
+ * block_tables row r (left as it is where kept is -1 or a block is not in [0,
+ * num_blocks)).  kept rises and kept[r][h][j] >= j, as topk_evict_keep gives
+ * it.  out_tables is block_tables (the same pointer: in place) or names blocks
+ * that block_tables does not; no block belongs to two requests.
+ *  caches: num_caches (at most 64) device arrays [num_blocks][block_size] of
+ *      slot_bytes bytes, contiguous and 16-byte aligned, in a host array; head
+ *      group h's share of a slot is the h-th of num_heads equal parts, a
+ *      multiple of 16 bytes. */
+int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads, int32_t budget,
+                    const int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
+                    const int32_t* out_tables, int64_t out_stride, int32_t out_blocks, int32_t block_size,
+                    int32_t num_caches, void* const* caches, int64_t num_blocks, int64_t slot_bytes,
+                    hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
