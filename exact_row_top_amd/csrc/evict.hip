@@ -20,11 +20,6 @@ namespace {
 constexpr int kKeepWaves = kKeepBlock / 64;
 constexpr int kDigitBins = 2048;
 
-// n / d for n < 2^31.
-__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& d) {
-  return (d.magic ? __umulhi(n, d.magic) : n) >> d.shift;
-}
-
 struct KeepShared {
   uint32_t count[kDigitBins];
   uint32_t wave[kKeepWaves];
@@ -195,7 +190,7 @@ __global__ void __launch_bounds__(kMoveBlock) evict_move_kernel(const MoveParams
   const int span = (((q.budget + q.parts - 1) / q.parts + step - 1) / step) * step;
   const int j1 = min(q.budget, (part + 1) * span);
   auto address = [&](const int32_t* table, int width, int p) -> unsigned char* {
-    const uint32_t e = quotient((uint32_t)p, q.by_block);
+    const uint32_t e = q.by_block((uint32_t)p);
     if (e >= (uint32_t)width) return nullptr;
     const int32_t b = table[e];
     if (b < 0 || b >= q.num_blocks) return nullptr;

@@ -19,11 +19,6 @@ namespace ert {
 
 namespace {
 
-// n / d for n < 2^31.
-__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& d) {
-  return (d.magic ? __umulhi(n, d.magic) : n) >> d.shift;
-}
-
 // The last bytes of a row, fewer than 16, in pieces of 8, 4, 2 and 1.
 __device__ __forceinline__ uint4 load_tail(const unsigned char* p, uint32_t n) {
   unsigned char b[16] = {};
@@ -120,7 +115,7 @@ __global__ void __launch_bounds__(kCopyBlock) reorder_blocks_kernel(const Reorde
   const int32_t* tables = q.tables + (int64_t)req * q.beams * q.table_stride;
   const int32_t* tail = q.tail ? q.tail + (int64_t)req * q.k : nullptr;
   const uint32_t len = (uint32_t)max(q.kv_lens[req], 0);
-  const uint32_t full = quotient(len, q.by_block), part = len - full * (uint32_t)q.block_size;
+  const uint32_t full = q.by_block(len), part = len - full * (uint32_t)q.block_size;
   const bool open = part > 0 && full < (uint32_t)q.max_blocks;
   // the block that child j's open one becomes
   auto own = [&](int j) { return tail ? tail[j] : tables[j * q.table_stride + full]; };

@@ -35,6 +35,13 @@ bool route_shape_ok(int32_t tokens, int32_t experts, int32_t top_k) {
          top_k <= experts;
 }
 
+Divisor divisor(uint32_t d) {
+  uint32_t log = 0;
+  while (((uint64_t)1 << log) < d) ++log;
+  if (((uint64_t)1 << log) == d) return Divisor{0, log};
+  return Divisor{(uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), log - 1};
+}
+
 // How a token's experts are spread: 16 lanes up to 256 experts (four tokens a
 // wave share each step of the selection), a whole wave above.
 struct Spread {

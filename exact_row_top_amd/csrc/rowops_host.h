@@ -9,7 +9,6 @@
 #include <string.h>
 
 #include "exact_row_top.h"
-#include "rowops.h"
 
 namespace ert {
 
@@ -49,13 +48,6 @@ inline int launch(const void* kernel, int64_t grid, int block, void* params, siz
     return TOPK_ELAUNCH;
   }
   return TOPK_OK;
-}
-
-inline Divisor divisor(uint32_t d) {
-  uint32_t log = 0;
-  while (((uint64_t)1 << log) < d) ++log;
-  if (((uint64_t)1 << log) == d) return Divisor{0, log};
-  return Divisor{(uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), log - 1};
 }
 
 }  // namespace ert

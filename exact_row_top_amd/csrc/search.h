@@ -7,6 +7,15 @@
 
 namespace ert {
 
+// Division by d of numbers below 2^31, without a branch: the high word of 2 n
+// ceil(2^(31 + L) / d), L = ceil(log2 d), shifted by L (the rounding adds less
+// than n 2^L / 2^(31 + L) < 1 to n / d scaled by d, so the quotient is exact).
+struct Quotient {
+  uint32_t magic;
+  uint32_t shift;
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return __umulhi(n << 1, magic) >> shift; }
+};
+
 // ---- the beams' choice ---------------------------------------------------------
 
 constexpr int kMaxBeams = 32;
@@ -83,7 +92,7 @@ struct ReorderBlocksParams {
   int64_t out_stride;
   const int32_t* kv_lens;   // [requests]
   const int32_t* tail;      // [requests * k] or null: each row's own open block
-  Divisor by_block;
+  Quotient by_block;
   int32_t block_size;
   int64_t num_blocks;
   int64_t slot_bytes;       // of the caches
@@ -97,9 +106,9 @@ struct ReorderBlocksParams {
 
 // ---- attention with a shared prefix ---------------------------------------------------
 
-constexpr int kAttendBlock = 256;
-constexpr int kKeyTile = 32;                               // keys of a wave's step
-constexpr int kAttendStep = kKeyTile * kAttendBlock / 64;  // keys of a workgroup's step
+constexpr int kKeyTile = 32;        // keys of a score tile
+constexpr int kMassBlock = 256;
+constexpr int kOwnSets = 4;         // waves that take turns at the keys of up to 32 queries
 
 // Pages of one cache: position p of a table row lies in block table[p / size]
 // at p % size.
@@ -125,7 +134,7 @@ struct AttendParams {
   Pages k, v;
   int64_t num_blocks;
   int32_t block_size;
-  Divisor by_block;
+  Quotient by_block;
   PageTables shared, own;    // [groups], [seqs]
   const int32_t* starts;     // [groups + 1]: a group's sequences; null: equal groups
   int32_t groups;
@@ -136,17 +145,22 @@ struct AttendParams {
   int32_t kv_heads;
   int32_t per;               // heads / kv_heads
   float scale;               // log2(e) times the scores' scale
-  // How keys are split over workgroups, and queries into tiles.
-  int32_t shared_keys;       // keys of a split
-  int32_t shared_splits;
-  int32_t shared_tiles;      // query tiles of all groups
-  int32_t own_keys;
+  // The shared kernel's work: `query_waves` waves of 32 queries to a workgroup,
+  // shared_wgs of them to a key head; own positions in own_splits.
+  int32_t query_waves;
+  int32_t shared_tile;       // keys of its step
+  int32_t shared_least;      // steps of a workgroup, at least
+  int32_t shared_wgs;
+  int32_t strips;            // query tiles of all groups, at most
   int32_t own_splits;
   int32_t own_tiles;         // query tiles of a sequence
-  int64_t shared_wgs;
+  int64_t shared_grid;       // workgroups of this launch on shared positions
   int64_t rows;              // seqs * next_n * heads
-  float* parts;              // [splits][rows][dim]: sums of the weighted values
-  float2* stats;             // [splits][rows]: largest score (log2), sum of weights
+  int4* group_at;            // [groups + 1]: first step, first strip; steps of all
+  float* shared_parts;       // [kv_heads][shared_wgs + strips][32 query_waves][dim]: weighted values
+  float2* shared_stats;      // the same rows: largest score (log2), sum of weights
+  float* own_parts;          // [own_splits][seqs][kv_heads][next_n * per][dim]
+  float2* own_stats;
   unsigned char* out;        // [rows][dim]
   float* lse;                // [rows] or null
 };
@@ -199,7 +213,7 @@ struct MoveParams {
   const int32_t* out_tables;
   int64_t out_stride;
   int32_t out_blocks;
-  Divisor by_block;
+  Quotient by_block;
   int32_t block_size;
   int64_t num_blocks;
   int64_t slot_bytes;        // of all heads

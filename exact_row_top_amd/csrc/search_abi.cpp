@@ -15,7 +15,7 @@ const void* beam_segment_kernel_ptr(int dtype);
 const void* beam_row_kernel_ptr(int dtype);
 const void* reorder_rows_kernel_ptr(int n);
 const void* reorder_blocks_kernel_ptr(int n);
-const void* attend_kernel_ptr(int dtype, int dim, int nt);
+const void* attend_kernel_ptr(int dtype, int dim, int query_waves);
 const void* attend_join_kernel_ptr(int dtype, int dim);
 const void* attend_mass_kernel_ptr(int dtype, int dim);
 const void* evict_keep_kernel_ptr();
@@ -26,7 +26,14 @@ using namespace ert;
 
 namespace {
 
+constexpr int64_t kMassStep = kKeyTile * kMassBlock / 64;  // positions of a workgroup
 constexpr int64_t kInt = ((int64_t)1 << 31) - 1;
+
+Quotient quotient_of(uint32_t d) {
+  uint32_t log = 0;
+  while (((uint64_t)1 << log) < d) ++log;
+  return Quotient{(uint32_t)((((uint64_t)1 << (31 + log)) + d - 1) / d), log};
+}
 
 // Whether [a, a + na) and [b, b + nb) share no byte (or one is not given).
 bool clear_of(const void* a, uint64_t na, const void* b, uint64_t nb) {
@@ -43,40 +50,50 @@ int64_t beam_cap(int64_t segments, int32_t k) {
 }
 
 struct AttendPlan {
-  int nt;
-  int64_t shared_keys, shared_splits, shared_tiles, own_keys, own_splits, own_tiles, shared_wgs, own_wgs;
+  int32_t query_waves, tile, least;
+  int64_t strips, shared_wgs, own_splits, own_tiles, own_wgs;
 };
 
-// How the work is cut up.  32 or 64 query columns a workgroup; a split's keys
-// so that about 1024 workgroups share the longest rows there may be, but at
-// least one step of a workgroup.
-void plan_kind(int64_t units, int64_t longest, int64_t& keys, int64_t& splits) {
-  const int64_t steps = (longest + kAttendStep - 1) / kAttendStep;
-  int64_t want = units > 0 ? (1024 + units - 1) / units : 1;
-  want = want < 1 ? 1 : (want > steps ? steps : want);
-  const int64_t per = want > 0 ? (steps + want - 1) / want : 1;
-  keys = per * kAttendStep;
-  splits = longest > 0 ? (longest + keys - 1) / keys : 0;
-}
-
+// How the work is cut up.  A group's prefix is read once for up to 256 of its
+// queries (8 waves of 32); groups of up to 32 have a wave for each fourth key
+// tile instead.  About 2048 waves in all, so that each of the chip's 1024
+// SIMDs has two.
 bool attend_plan(int32_t groups, int32_t seqs, bool ragged, int32_t next_n, int32_t heads,
                  int32_t kv_heads, int64_t max_shared, int64_t max_own, AttendPlan& p) {
   const int64_t per = heads / kv_heads, rows = (int64_t)next_n * per;
   const int64_t group_rows = groups > 0 ? (seqs + groups - 1) / groups * rows : 0;
-  p.nt = group_rows > 32 ? 2 : 1;
-  const int64_t cols = 32 * p.nt;
-  p.shared_tiles = ragged ? seqs * rows / cols + groups : groups * ((group_rows + cols - 1) / cols);
-  if (groups == 0 || max_shared == 0) p.shared_tiles = 0;
-  p.own_tiles = (rows + cols - 1) / cols;
-  plan_kind(p.shared_tiles * kv_heads, p.shared_tiles ? max_shared : 0, p.shared_keys, p.shared_splits);
-  plan_kind((int64_t)seqs * kv_heads * p.own_tiles, max_own, p.own_keys, p.own_splits);
-  p.shared_wgs = (p.shared_splits * kv_heads + 7) / 8 * 8 * p.shared_tiles;
-  p.own_wgs = (int64_t)seqs * p.own_splits * kv_heads * p.own_tiles;
-  return p.shared_wgs + p.own_wgs < kInt && p.shared_tiles < kInt;
+  p.query_waves = group_rows > 128 ? 8 : (group_rows > 64 ? 4 : (group_rows > 32 ? 2 : 1));
+  const int64_t cols = 32 * p.query_waves;
+  p.tile = p.query_waves == 8 ? 64 : 32;
+  p.least = p.query_waves == 1 ? kOwnSets : 1;
+  p.strips = ragged ? seqs * rows / cols + groups : groups * ((group_rows + cols - 1) / cols);
+  p.shared_wgs = 0;
+  if (groups > 0 && seqs > 0 && max_shared > 0) {
+    const int64_t steps = (max_shared + p.tile - 1) / p.tile * p.strips;
+    if (steps >= kInt) return false;
+    const int64_t most = (steps + p.least - 1) / p.least;
+    p.shared_wgs = 2048 / (p.query_waves == 1 ? kOwnSets : p.query_waves) / kv_heads;
+    p.shared_wgs = p.shared_wgs < 1 ? 1 : (p.shared_wgs > most ? most : p.shared_wgs);
+  }
+  p.own_tiles = (rows + 31) / 32;
+  p.own_splits = 0;
+  const int64_t units = (int64_t)seqs * kv_heads * p.own_tiles;
+  if (max_own > 0 && units > 0) {
+    const int64_t steps = (max_own + kKeyTile - 1) / kKeyTile, most = (steps + kOwnSets - 1) / kOwnSets;
+    p.own_splits = 2048 / kOwnSets / units;
+    p.own_splits = p.own_splits < 1 ? 1 : (p.own_splits > most ? most : p.own_splits);
+  }
+  p.own_wgs = units * p.own_splits;
+  return p.shared_wgs * kv_heads + p.own_wgs < kInt;
 }
 
-size_t attend_bytes(const AttendPlan& p, int64_t rows, int32_t dim) {
-  return (size_t)((p.shared_splits + p.own_splits) * rows) * ((size_t)dim * 4 + 8);
+int64_t shared_rows(const AttendPlan& p, int32_t kv_heads) {
+  return p.shared_wgs > 0 ? kv_heads * (p.shared_wgs + p.strips) * 32 * p.query_waves : 0;
+}
+
+size_t attend_bytes(const AttendPlan& p, int32_t groups, int32_t kv_heads, int64_t rows, int32_t dim) {
+  return (size_t)(shared_rows(p, kv_heads) + p.own_splits * rows) * ((size_t)dim * 4 + 8) +
+         (size_t)(groups + 1) * sizeof(int4);
 }
 
 // What attention and mass share.
@@ -120,7 +137,7 @@ void attend_params(AttendParams& p, const AttendShape& s, const void* q, int64_t
   p.k = Pages{static_cast<const unsigned char*>(k), k_block * 2, k_slot * 2, k_head * 2};
   p.num_blocks = s.num_blocks;
   p.block_size = s.block_size;
-  p.by_block = divisor((uint32_t)s.block_size);
+  p.by_block = quotient_of((uint32_t)s.block_size);
   p.shared = PageTables{shared_tables, shared_stride, shared_width, (int32_t)shared_limit, shared_lens};
   p.own = PageTables{own_tables, own_stride, own_width, (int32_t)own_limit, own_lens};
   p.starts = starts;
@@ -317,7 +334,7 @@ int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32
   p.out_stride = out_stride;
   p.kv_lens = kv_lens;
   p.tail = tail_blocks;
-  p.by_block = divisor((uint32_t)block_size);
+  p.by_block = quotient_of((uint32_t)block_size);
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   p.slot_bytes = slot_bytes;
@@ -354,7 +371,7 @@ size_t topk_attend_workspace_bytes(int32_t num_groups, int32_t num_seqs, int32_t
   if (!attend_plan(num_groups, num_seqs, ragged != 0, next_n, num_heads, num_kv_heads, max_shared_len,
                    max_own_len, plan))
     return 0;
-  return attend_bytes(plan, (int64_t)num_seqs * next_n * num_heads, dim) + 16;
+  return attend_bytes(plan, num_groups, num_kv_heads, (int64_t)num_seqs * next_n * num_heads, dim);
 }
 
 int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
@@ -390,8 +407,7 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
                    most_own, plan))
     return TOPK_EINVAL;
   const int64_t rows = (int64_t)num_seqs * next_n * num_heads;
-  const size_t bytes = attend_bytes(plan, rows, dim);
-  if (bytes > 0 && (!workspace || workspace_bytes < bytes)) return TOPK_EWORKSPACE;
+  if (!workspace || workspace_bytes < attend_bytes(plan, num_groups, num_kv_heads, rows, dim)) return TOPK_EWORKSPACE;
   rc = device_ok();
   if (rc != TOPK_OK) return rc;
   AttendParams p;
@@ -399,19 +415,32 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
                 shared_tables, shared_stride, shared_width, shared_lens, most_shared, group_starts, own_tables,
                 own_stride, own_width, own_lens, most_own, scale);
   p.v = Pages{static_cast<const unsigned char*>(v_cache), v_block_stride * 2, v_slot_stride * 2, v_head_stride * 2};
-  p.shared_keys = (int32_t)plan.shared_keys;
-  p.shared_splits = (int32_t)plan.shared_splits;
-  p.shared_tiles = (int32_t)plan.shared_tiles;
-  p.own_keys = (int32_t)plan.own_keys;
+  p.query_waves = plan.query_waves;
+  p.shared_tile = plan.tile;
+  p.shared_least = plan.least;
+  p.shared_wgs = (int32_t)plan.shared_wgs;
+  p.strips = (int32_t)plan.strips;
   p.own_splits = (int32_t)plan.own_splits;
   p.own_tiles = (int32_t)plan.own_tiles;
-  p.shared_wgs = plan.shared_wgs;
-  p.parts = static_cast<float*>(workspace);
-  p.stats = reinterpret_cast<float2*>(p.parts + (plan.shared_splits + plan.own_splits) * rows * dim);
+  const int64_t shared = shared_rows(plan, num_kv_heads), own = plan.own_splits * rows;
+  p.group_at = static_cast<int4*>(workspace);
+  p.shared_parts = reinterpret_cast<float*>(p.group_at + num_groups + 1);
+  p.own_parts = p.shared_parts + shared * dim;
+  p.shared_stats = reinterpret_cast<float2*>(p.own_parts + own * dim);
+  p.own_stats = p.shared_stats + shared;
   p.out = static_cast<unsigned char*>(out);
   p.lse = lse;
-  if (plan.shared_wgs + plan.own_wgs > 0) {
-    rc = launch(attend_kernel_ptr(dtype, dim, plan.nt), plan.shared_wgs + plan.own_wgs, kAttendBlock, &p, 0, stream);
+  p.shared_grid = plan.shared_wgs * num_kv_heads;
+  const bool together = plan.query_waves == 1;
+  const int64_t first = p.shared_grid + (together ? plan.own_wgs : 0);
+  if (first > 0) {
+    rc = launch(attend_kernel_ptr(dtype, dim, plan.query_waves), first,
+                64 * (together ? kOwnSets : plan.query_waves), &p, 0, stream);
+    if (rc != TOPK_OK) return rc;
+  }
+  if (!together && plan.own_wgs > 0) {
+    p.shared_grid = 0;
+    rc = launch(attend_kernel_ptr(dtype, dim, 1), plan.own_wgs, 64 * kOwnSets, &p, 0, stream);
     if (rc != TOPK_OK) return rc;
   }
   const int64_t per = 256 / (dim / 4);
@@ -452,8 +481,8 @@ int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_h
   const int64_t most_shared = longest_of(num_groups > 0 ? shared_width : 0, block_size, num_blocks, 0);
   const int64_t most_own = longest_of(own_width, block_size, num_blocks, 0);
   if (most_shared < 0 || most_own < 0) return TOPK_EINVAL;
-  const int64_t shared_tiles = ((int64_t)shared_positions + kAttendStep - 1) / kAttendStep;
-  const int64_t own_tiles = ((int64_t)own_positions + kAttendStep - 1) / kAttendStep;
+  const int64_t shared_tiles = ((int64_t)shared_positions + kMassStep - 1) / kMassStep;
+  const int64_t own_tiles = ((int64_t)own_positions + kMassStep - 1) / kMassStep;
   const int64_t shared_wgs = shared_tiles * num_groups * num_kv_heads;
   const int64_t own_wgs = own_tiles * num_seqs * num_kv_heads;
   if (shared_wgs + own_wgs >= kInt) return TOPK_EINVAL;
@@ -475,7 +504,7 @@ int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_h
   p.shared_tiles = (int32_t)shared_tiles;
   p.own_tiles = (int32_t)own_tiles;
   p.shared_wgs = shared_wgs;
-  return launch(attend_mass_kernel_ptr(dtype, dim), shared_wgs + own_wgs, kAttendBlock, &p, 0, stream);
+  return launch(attend_mass_kernel_ptr(dtype, dim), shared_wgs + own_wgs, kMassBlock, &p, 0, stream);
 }
 
 int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stride, int32_t positions,
@@ -550,7 +579,7 @@ int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads
   p.out_tables = out_tables;
   p.out_stride = out_stride;
   p.out_blocks = out_blocks;
-  p.by_block = divisor((uint32_t)block_size);
+  p.by_block = quotient_of((uint32_t)block_size);
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   p.slot_bytes = slot_bytes;
