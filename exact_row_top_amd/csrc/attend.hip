@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "search.h"
 
 namespace ert {
@@ -50,7 +52,14 @@ struct F16 {
 
 constexpr float kNone = -__builtin_inff();
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// The two halves' values of a lane and its counterpart.
+struct Pair {
+  float a, b;
+};
+__device__ __forceinline__ Pair both_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return Pair{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
 
 // A group's sequences.
 __device__ __forceinline__ void group_range(const AttendParams& q, int g, int& s0, int& s1) {
@@ -128,27 +137,76 @@ __device__ __forceinline__ int value_piece(int row, int piece) {
 
 }  // namespace
 
+namespace {
+
+// 16 bytes a lane from memory into 1 KB of LDS from `to` on (uniform), lane by
+// lane.  Written out so that reads of another part of LDS do not wait for it:
+// whoever reads waits for vmcnt first.
+__device__ __forceinline__ void load_to_lds(const unsigned char* from, const Piece* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const Piece*)to);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(at), "v"(from)
+      : "memory");
+}
+// The same from a uniform base and a lane's own offset.
+__device__ __forceinline__ void load_to_lds(const unsigned char* base, uint32_t lane_off, const Piece* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const Piece*)to);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(at), "v"(lane_off), "s"(base)
+      : "memory");
+}
+// Waits until all but the last N loads are done.
+template <int N>
+__device__ __forceinline__ void loads_but() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// Waits for this wave's LDS reads and writes.
+__device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+// A workgroup's LDS writes, and nothing on its way to LDS or registers.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+}  // namespace
+
 // ---------------------------------------------------------------------------
 // QW waves of 32 queries each share the keys and values of a step (KT of
 // them); KW such sets take turns at the steps, and are joined at the end.
 //
-// A step's keys and values are on their way to registers while the step
-// before is computed, and its block numbers one step ahead of that.
+// Steps go straight from memory to LDS.  With QW > 1 one is on its way while
+// the one before is computed; of eight waves, the second on each SIMD runs
+// half a step behind the first, so that one's products meet the other's
+// exponentials.  A wave alone (QW 1) has one buffer: the next step's keys are
+// fetched once the products with this one's are done, and its values likewise.
 //
 // Shared positions: the steps of all strips form one line, of which every
 // workgroup of a key head takes an equal share, whatever the lengths; pieces
 // of a strip are told apart by workgroup + strip, which no two pieces have in
 // common.
 // ---------------------------------------------------------------------------
-template <class T, int DIM, int QW, int KW, int KT>
-__global__ void __launch_bounds__(64 * QW * KW, QW == 1 ? 1 : 2) attend_kernel(const AttendParams q) {
+template <class T, int DIM, int QW, int KW, int KT, bool EVEN>
+__global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendParams q) {
   constexpr int STEPS = DIM / 16;          // products of 16 deep a score tile
   constexpr int MT = DIM / 32;             // tiles of the output
+  constexpr int SUBS = KT / kKeyTile;      // score tiles of a step
   constexpr int PIECES = DIM / 8;          // 16-byte pieces of a row
-  constexpr int ROWS = 64 * QW / PIECES;   // rows that a set's threads load at once
-  constexpr int PASSES = KT / ROWS;
-  constexpr int BUFFERS = QW == 1 ? 1 : 2; // a wave alone reads what it wrote
-  static_assert(KT % ROWS == 0 && (QW == 1 || KW == 1), "");
+  constexpr int ROWS = 64 / PIECES;        // rows that a wave loads at once
+  constexpr int PASSES = KT / (ROWS * QW);
+  constexpr bool LAG = QW == 8;
+  constexpr int BUFFERS = QW == 1 ? 1 : (LAG ? 3 : 2);
+  static_assert(PASSES * ROWS * QW == KT && (PASSES & (PASSES - 1)) == 0 && (QW == 1 || KW == 1), "");
   struct Stage {
     Piece key[KT * PIECES];
     Piece value[KT * PIECES];
@@ -159,11 +217,105 @@ __global__ void __launch_bounds__(64 * QW * KW, QW == 1 ? 1 : 2) attend_kernel(c
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int set = wave / QW, qw = wave % QW;
-  const int lt = (int)threadIdx.x - set * QW * 64;
-  const int lrow = lt / PIECES, lpiece = lt % PIECES;
+  const int lrow = lane / PIECES, lpiece = lane % PIECES;
+  const bool lag = LAG && qw >= QW / 2;
 
   auto run = [&](const Share& s, float* parts, float2* stats) {
     const int least = s.len - s.cut;    // positions that every query of the entry sees
+    // Steps that the waves load: pass i of wave qw is rows row0(i) on.  EVEN:
+    // blocks hold whole passes, so that a pass lies in one block; lane i < PASSES
+    // makes the address of pass i's keys, lane i + PASSES that of its values.
+    const unsigned char* kbase = q.k.base + s.head * q.k.head_stride;
+    const unsigned char* vbase = q.v.base + s.head * q.v.head_stride;
+    auto row0 = [&](int i) { return (i * QW + qw) * ROWS; };
+    auto entry = [&](int p) {
+      return s.table[min(q.by_block((uint32_t)min(p, s.len - 1)), (uint32_t)s.width - 1u)];
+    };
+    const bool for_values = lane & PASSES;
+    const uint32_t my_block_stride = for_values ? q.v.block_stride : q.k.block_stride;
+    const uint32_t my_slot_stride = for_values ? q.v.slot_stride : q.k.slot_stride;
+    const uint64_t my_base = (uint64_t)(for_values ? vbase : kbase);
+    int32_t ids = 0;     // table entries of the step to be fetched next
+    uint64_t from = 0;   // where its passes lie
+    auto find = [&](int t) {
+      if (EVEN) ids = entry(t * KT + row0(lane % PASSES));
+    };
+    // What is not there is read from the cache's first slot, and masked.
+    auto locate = [&](int t) {
+      if (!EVEN) return;
+      const uint32_t p = (uint32_t)(t * KT + row0(lane % PASSES));
+      const uint32_t ok = p < (uint32_t)s.len && (uint32_t)ids < (uint32_t)q.num_blocks ? ~0u : 0u;
+      const uint32_t off = (p - q.by_block(p) * (uint32_t)q.block_size) & ok;
+      from = my_base + (uint64_t)((uint32_t)ids & ok) * my_block_stride + (uint64_t)off * my_slot_stride;
+    };
+    auto fetch = [&](int t, int b, bool keys) {
+      const Pages& c = keys ? q.k : q.v;
+      Piece* to = keys ? stages[set][b].key : stages[set][b].value;
+      int r = lrow, x = lpiece;
+      asm("" : "+v"(r), "+v"(x));   // (offsets of all passes would fill the registers)
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int row = row0(i) + r;
+        const uint32_t piece = (uint32_t)(keys ? key_piece<DIM>(row, x) : value_piece<DIM>(row, x)) * 16;
+        Piece* at = to + (i * QW + qw) * 64;
+        if (EVEN) {
+          const int l = keys ? i : i + PASSES;
+          const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(from >> 32), l) << 32 |
+                                (uint32_t)__builtin_amdgcn_readlane((int)from, l);
+          load_to_lds(reinterpret_cast<const unsigned char*>(base), (uint32_t)r * c.slot_stride + piece, at);
+        } else {
+          const uint32_t p = (uint32_t)(t * KT + row), id = (uint32_t)entry((int)p);
+          const uint32_t ok = p < (uint32_t)s.len && id < (uint32_t)q.num_blocks ? ~0u : 0u;
+          load_to_lds((keys ? kbase : vbase) + (uint64_t)(id & ok) * c.block_stride +
+                          (uint64_t)((p - q.by_block(p) * (uint32_t)q.block_size) & ok) * c.slot_stride + piece,
+                      at);
+        }
+      }
+    };
+    // Steps before `full` hold KT positions that are there, those before `seen`
+    // no position that a query of the entry does not see.
+    int full = 0, seen = 0;
+    // For a step that lacks rows: marks them, and, once it has arrived, clears
+    // their values, which must not be NaN or infinite even without a weight.
+    auto mark = [&](int t, int b) {
+      for (int r = lane; r < KT; r += 64) {
+        const int p = t * KT + r;
+        valid[set][b][r] = p < s.len && (uint32_t)entry(p) < (uint32_t)q.num_blocks ? 1 : 0;
+      }
+      wave_sync();
+    };
+    auto clear = [&](int b) {
+#pragma unroll 1
+      for (int i = 0; i < PASSES; ++i) {
+        const int row = row0(i) + lrow;
+        if (!valid[set][b][row]) stages[set][b].value[row * PIECES + lpiece] = Piece{0, 0, 0, 0};
+      }
+      wave_sync();
+    };
+
+    // A step's own part has arrived.
+    auto settle = [&](int t, int b) {
+      loads_but<0>();
+      if (t >= full) {
+        mark(t, b);   // (each wave all of them, the same)
+        clear(b);
+      }
+    };
+
+    int t = s.step0 + set;
+    find(t);
+    bool clean = true;   // every block of this share is there
+    {
+      const uint32_t e1 = min(q.by_block((uint32_t)min(s.step1 * KT, s.len) - 1u) + 1u, (uint32_t)s.width);
+      for (uint32_t e = q.by_block((uint32_t)(s.step0 * KT)) + threadIdx.x; e < e1; e += 64 * QW * KW)
+        clean = clean && (uint32_t)s.table[e] < (uint32_t)q.num_blocks;
+    }
+    if (t < s.step1) {
+      locate(t);
+      fetch(t, 0, true);
+      fetch(t, 0, false);
+      find(t + KW);
+    }
     // this wave's queries, as right operands
     Piece query[STEPS];
     const int r = s.first + qw * 32 + col;
@@ -171,150 +323,249 @@ __global__ void __launch_bounds__(64 * QW * KW, QW == 1 ? 1 : 2) attend_kernel(c
     int sees;
     {
       const int rr = has ? r : 0;
-      const int tok = rr / q.per, sub = rr - tok * q.per;
+      const int tok = (int)((uint32_t)rr / (uint32_t)q.per), sub = rr - tok * q.per;
       sees = least + (s.cut ? tok % q.next_n : 0);
       const unsigned char* p = q.q + ((int64_t)s.seq0 * q.next_n + tok) * q.q_stride +
                                (s.head * q.per + sub) * q.q_head_stride + half * 16;
 #pragma unroll
-      for (int d = 0; d < STEPS; ++d)
-        query[d] = has ? *reinterpret_cast<const Piece*>(p + d * 32) : Piece{0, 0, 0, 0};
+      for (int d = 0; d < STEPS; ++d) {
+        query[d] = *reinterpret_cast<const Piece*>(p + d * 32);
+        if (!has) query[d] = Piece{0, 0, 0, 0};
+      }
     }
-    f32x16 acc[MT];
+    if (__syncthreads_and(clean)) {
+      full = s.len / KT;
+      seen = max(least, 0) / KT;
+    }
+
+    f32x16 acc[MT], sc[SUBS];
+    typename T::Vec w[2 * SUBS];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][i] = 0.0f;
     float top = kNone, sum = 0.0f;
 
-    const unsigned char* kbase = q.k.base + s.head * q.k.head_stride + lpiece * 16;
-    const unsigned char* vbase = q.v.base + s.head * q.v.head_stride + lpiece * 16;
-    Piece kreg[PASSES], vreg[PASSES];
-    int32_t block[PASSES];   // table entries of the step to be loaded next
-    uint32_t live_row[PASSES];  // all ones where a position is there, else zero
-    // (no branches around these loads: each would be waited for in its own)
-    auto find = [&](int t) {
+    // Matrix products: the scores of the step in buffer bk (QK) and the values
+    // of the one in buffer bv times its weights (PV), in turn; LDS reads run
+    // AHEAD steps of either before their products.
+    auto multiply = [&](auto qk, auto pv, int bk, int bv) {
+      constexpr bool QK = decltype(qk)::value, PV = decltype(pv)::value;
+      constexpr int AHEAD = PV ? 2 : 4, VALUES = 2 * SUBS * MT, VAHEAD = 4;
+      // (made anew in every step: kept, these addresses fill the registers)
+      int kcol = col, vlane = lane;
+      asm("" : "+v"(kcol), "+v"(vlane));
+      auto key = [&](int d, int n) {
+        return stages[set][bk].key[(n * kKeyTile + kcol) * PIECES + key_piece<DIM>(kcol, 2 * d + half)];
+      };
+      // four keys of a column a read: lane l gives the address of row l % 16 /
+      // 4, columns 4 (l % 4) on, of its 16 lanes' columns
+      auto value = [&](int j) {
+        const int row = 16 * (j / MT) + 4 * half + ((vlane & 15) >> 2);
+        const int piece = value_piece<DIM>((vlane & 15) >> 2, 4 * (j % MT) + 2 * ((vlane >> 4) & 1) + ((vlane & 3) >> 1));
+        s16x4 a[2];
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const uint32_t p = (uint32_t)min(t * KT + i * ROWS + lrow, s.len - 1);
-        block[i] = s.table[min(q.by_block(p), (uint32_t)s.width - 1u)];
+        for (int e = 0; e < 2; ++e)
+          a[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<unsigned char*>(&stages[set][bv].value[(row + 8 * e) * PIECES + piece]) + 8 * (vlane & 1)));
+        return __builtin_bit_cast(Piece, __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      Piece keys[AHEAD][SUBS], values[VAHEAD];
+      if (QK) {
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+#pragma unroll
+          for (int n = 0; n < SUBS; ++n) keys[d][n] = key(d, n);
+#pragma unroll
+        for (int n = 0; n < SUBS; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sc[n][i] = 0.0f;
       }
-    };
-    auto fetch = [&](int t) {
+      if (PV) {
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const uint32_t p = (uint32_t)(t * KT + i * ROWS + lrow);
-        live_row[i] = p < (uint32_t)s.len && (uint32_t)block[i] < (uint32_t)q.num_blocks ? ~0u : 0u;
-        // what is not there is read from the cache's first slot, and masked
-        const uint32_t off = (p - q.by_block(p) * (uint32_t)q.block_size) & live_row[i];
-        const uint32_t blk = (uint32_t)block[i] & live_row[i];
-        kreg[i] = *reinterpret_cast<const Piece*>(kbase + (int64_t)blk * q.k.block_stride + (int64_t)off * q.k.slot_stride);
-        vreg[i] = *reinterpret_cast<const Piece*>(vbase + (int64_t)blk * q.v.block_stride + (int64_t)off * q.v.slot_stride);
+        for (int j = 0; j < VAHEAD; ++j) values[j] = value(j);
       }
-    };
-
-    int t = s.step0 + set, b = 0;
-    find(t);
-    fetch(t);
-    find(t + KW);
-    for (; t < s.step1; t += KW, b ^= BUFFERS - 1) {
-      Stage& st = stages[set][b];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int row = i * ROWS + lrow;
-        st.key[row * PIECES + key_piece<DIM>(row, lpiece)] = kreg[i];
-        // values that no weight counts must not be NaN or infinite
-        st.value[row * PIECES + value_piece<DIM>(row, lpiece)] =
-            vreg[i] & live_row[i];
-        if (lpiece == 0) valid[set][b][row] = (int32_t)live_row[i];
-      }
-      fetch(t + KW);
-      find(t + 2 * KW);
-      if (QW > 1) {
-        // the writes are done; what is on its way to registers need not be
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-      } else {
-        wave_sync();
-      }
-      const uint64_t live = __ballot(valid[set][b][lane % KT] != 0);
-      const bool whole = live == ~0ull && (t + 1) * KT <= least;
-#pragma unroll 1
-      for (int k0 = 0; k0 < KT; k0 += kKeyTile) {
-        f32x16 sc;
+      for (int d = 0; d < STEPS; ++d) {
+        if (QK) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[i] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < STEPS; ++d)
-          sc = T::mfma(st.key[(k0 + col) * PIECES + key_piece<DIM>(col, 2 * d + half)], query[d], sc);
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = k0 + 8 * (i / 4) + 4 * half + i % 4;
-            sc[i] = (live >> j & 1) && t * KT + j < sees ? sc[i] : kNone;
+          for (int n = 0; n < SUBS; ++n) {
+            sc[n] = T::mfma(keys[d % AHEAD][n], query[d], sc[n]);
+            if (d + AHEAD < STEPS) keys[d % AHEAD][n] = key(d + AHEAD, n);
           }
         }
-        float mx = sc[0];
+        if (PV) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
-        mx = fmaxf(mx, other_half(mx)) * q.scale;
-        // The weights' reference follows the largest score only once that is
-        // over 2^8 times the reference's weight: weights of up to 2^8 lose
-        // nothing, and sums are seldom scaled again.
-        if (__ballot(mx > top + 8.0f)) {
-          const float now = fmaxf(mx, top);
-          const float f = now == kNone ? 0.0f : __builtin_amdgcn_exp2f(top - now);
-          top = now;
-          sum *= f;
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[m][i] *= f;
-        }
-        const float ref = top == kNone ? 0.0f : top;
-        float part = 0.0f;
-        typename T::Vec w[2];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], q.scale, -ref));
-          part += p;
-          w[i / 8][i % 8] = (typename T::Value)p;
-        }
-        sum += part;
-        // four keys of a column a read: lane l gives the address of row l % 16
-        // / 4, columns 4 (l % 4) on, of its 16 lanes' columns
-        const int vrow = k0 + 4 * half + ((lane & 15) >> 2);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            s16x4 a[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int row = vrow + 16 * u + 8 * e;
-              const int piece = value_piece<DIM>((lane & 15) >> 2, 4 * m + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1));
-              a[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<unsigned char*>(&st.value[row * PIECES + piece]) + 8 * (lane & 1)));
-            }
-            const s16x8 left = __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7);
-            acc[m] = T::mfma(__builtin_bit_cast(Piece, left), __builtin_bit_cast(Piece, w[u]), acc[m]);
+          for (int j = d * VALUES / STEPS; j < (d + 1) * VALUES / STEPS; ++j) {
+            acc[j % MT] = T::mfma(values[j % VAHEAD], __builtin_bit_cast(Piece, w[j / MT]), acc[j % MT]);
+            if (j + VAHEAD < VALUES) values[j % VAHEAD] = value(j + VAHEAD);
           }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (QW == 1) wave_sync();
-    }
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
 
-    sum += other_half(sum);
-    if (KW == 1) {
-      if (has) {
-        float* to = parts + (int64_t)(qw * 32 + col) * DIM + 4 * half;
+    // From a step's scores to its weights.
+    auto soften = [&](int t, int b) {
+      if (t >= seen) {
+        const uint64_t live = t < full ? ~0ull : __ballot(valid[set][b][lane % KT] != 0);
+#pragma unroll
+        for (int n = 0; n < SUBS; ++n) {
+          // this half's keys from its first on that are there, and seen
+          const int from = n * kKeyTile + 4 * half;
+          const int ahead = min(max(sees - (t * KT + from), 0), 31);
+          const uint32_t on = (uint32_t)(live >> from) & ((1u << ahead) - 1u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sc[n][i] = on >> (8 * (i / 4) + i % 4) & 1 ? sc[n][i] : kNone;
+        }
+      }
+      float mx = kNone;
+#pragma unroll
+      for (int n = 0; n < SUBS; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[n][i]);
+      {
+        const Pair h = both_halves(mx);
+        mx = fmaxf(h.a, h.b) * q.scale;
+      }
+      // The weights' reference follows the largest score only once that is
+      // over 2^8 times the reference's weight: weights of up to 2^8 lose
+      // nothing, and sums are seldom scaled again.
+      if (__ballot(mx > top + 8.0f)) {
+        const float now = fmaxf(mx, top);
+        const float f = now == kNone ? 0.0f : __builtin_amdgcn_exp2f(top - now);
+        top = now;
+        sum *= f;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(to + 32 * m + 2 * i) =
-                float4{acc[m][i], acc[m][i + 1], acc[m][i + 2], acc[m][i + 3]};
-        if (half == 0) stats[qw * 32 + col] = float2{top, sum};
+          for (int i = 0; i < 16; ++i) acc[m][i] *= f;
       }
+      const float ref = top == kNone ? 0.0f : top;
+      float part[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 2 * SUBS; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u / 2][u % 2 * 8 + i], q.scale, -ref));
+          part[i % 2] += p;
+          w[u][i] = (typename T::Value)p;
+        }
+      sum += part[0] + part[1];
+      if (LAG) {   // here, and not among the next phase's products
+#pragma unroll
+        for (int u = 0; u < 2 * SUBS; ++u) asm volatile("" : "+v"(w[u]));
+      }
+    };
+
+    if (QW == 1) {
+      for (; t < s.step1; t += KW) {
+        const bool more = t + KW < s.step1;
+        // all but the values have arrived, and the next step's table entries
+        loads_but<PASSES + 1>();
+        if (t >= full) mark(t, 0);
+        multiply(yes, no, 0, 0);
+        if (more) {
+          lds_done();   // the keys are read
+          locate(t + KW);
+          fetch(t + KW, 0, true);
+        }
+        soften(t, 0);
+        if (more) loads_but<PASSES>();
+        else loads_but<0>();
+        if (t >= full) clear(0);
+        multiply(no, yes, 0, 0);
+        if (more) {
+          lds_done();   // the values are read
+          fetch(t + KW, 0, false);
+          find(t + 2 * KW);
+        }
+      }
+    } else if (!LAG) {
+      int b = 0;
+      for (; t < s.step1; ++t) {
+        // the step has arrived, and the next one's table entries
+        settle(t, b);
+        lds_barrier();
+        if (t + 1 < s.step1) {
+          locate(t + 1);
+          fetch(t + 1, b ^ 1, true);
+          fetch(t + 1, b ^ 1, false);
+          find(t + 2);
+        }
+        multiply(yes, no, b, b);
+        soften(t, b);
+        multiply(no, yes, b, b);
+        b ^= 1;
+      }
+    } else {
+      // Two phases a step: in one the products of step t's keys and of step t
+      // - 1's values, in the other step t's weights.  The first four waves are
+      // a phase ahead of the others, so that each SIMD has one wave at either.
+      // All waves fetch step t + 1 in phase 2 t, and wait for it at the end of
+      // the next: of three buffers, t - 1 and t are read then.
+      int b = 0;
+      auto get = [&](int t, int b) {
+        if (t < s.step1) {
+          locate(t);
+          fetch(t, b, true);
+          fetch(t, b, false);
+          find(t + 1);
+        }
+      };
+      settle(t, 0);
+      lds_barrier();
+      if (lag) {
+        get(t + 1, 1);
+        lds_barrier();
+      }
+      for (; t < s.step1; ++t) {
+        const int after = b == 2 ? 0 : b + 1, last = b == 0 ? 2 : b - 1;
+        if (!lag) get(t + 1, after);
+        if (t > s.step0) multiply(yes, yes, b, last);
+        else multiply(yes, no, b, b);
+        if (lag && t + 1 < s.step1) settle(t + 1, after);
+        lds_barrier();
+        if (lag) get(t + 2, last);
+        soften(t, b);
+        if (!lag && t + 1 < s.step1) settle(t + 1, after);
+        lds_barrier();
+        b = after;
+      }
+      if (!lag) lds_barrier();
+      if (s.step1 > s.step0) multiply(no, yes, 0, b == 0 ? 2 : b - 1);
+    }
+
+    {
+      const Pair h = both_halves(sum);
+      sum = h.a + h.b;
+    }
+    if (KW == 1) {
+      // Rows leave through LDS, 128 bytes of each at a time: 16 bytes of 64
+      // rows, as the lanes hold them, would take several times as long.
+      constexpr int PITCH = 36;
+      static_assert(sizeof(stages) >= QW * 32 * PITCH * sizeof(float), "");
+      float* rows = reinterpret_cast<float*>(&stages[0][0]) + qw * 32 * PITCH;
+      const int r8 = lane >> 3, c8 = (lane & 7) * 4;
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(rows + col * PITCH + 2 * i + 4 * half) =
+              float4{acc[m][i], acc[m][i + 1], acc[m][i + 2], acc[m][i + 3]};
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          if (s.first + qw * 32 + i + r8 < s.rows)
+            *reinterpret_cast<float4*>(parts + (int64_t)(qw * 32 + i + r8) * DIM + 32 * m + c8) =
+                *reinterpret_cast<const float4*>(rows + (i + r8) * PITCH + c8);
+        wave_sync();
+      }
+      if (has && half == 0) stats[qw * 32 + col] = float2{top, sum};
       __syncthreads();   // before the next piece's first step is written
       return;
     }
@@ -405,13 +656,13 @@ __global__ void __launch_bounds__(64 * QW * KW, QW == 1 ? 1 : 2) attend_kernel(c
     return;
   }
   if (QW > 1) return;
-  int64_t id = (int64_t)blockIdx.x - q.shared_grid;
-  s.head = (int)(id % q.kv_heads);
-  id /= q.kv_heads;
-  const int tile = (int)(id % q.own_tiles);
-  id /= q.own_tiles;
-  const int split = (int)(id % q.own_splits);
-  s.seq0 = (int)(id / q.own_splits);
+  uint32_t id = blockIdx.x - (uint32_t)q.shared_grid;
+  s.head = (int)(id % (uint32_t)q.kv_heads);
+  id /= (uint32_t)q.kv_heads;
+  const int tile = (int)(id % (uint32_t)q.own_tiles);
+  id /= (uint32_t)q.own_tiles;
+  const int split = (int)(id % (uint32_t)q.own_splits);
+  s.seq0 = (int)(id / (uint32_t)q.own_splits);
   s.rows = q.next_n * q.per;
   s.first = tile * 32;
   s.table = q.own.tables + (int64_t)s.seq0 * q.own.stride;
@@ -428,13 +679,14 @@ __global__ void __launch_bounds__(64 * QW * KW, QW == 1 ? 1 : 2) attend_kernel(c
 }
 
 // ---------------------------------------------------------------------------
-// Joins a row's pieces: dim / 4 threads a row.
+// Joins a row's pieces: a wave a row, its lanes in 64 / (dim / 4) sets that
+// take turns at the pieces.
 // ---------------------------------------------------------------------------
 template <class T, int DIM>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) {
-  constexpr int LANES = DIM / 4;
-  const int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-  const int d = (int)(threadIdx.x % LANES) * 4;
+  constexpr int LANES = DIM / 4, SETS = 64 / LANES;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (row >= q.rows) return;
   const int tok = (int)(row / q.heads), head = (int)(row - (int64_t)tok * q.heads);
   const int seq = tok / q.next_n, kv = head / q.per, sub = head - kv * q.per;
@@ -445,26 +697,25 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) 
     int g = -1, s0 = 0, s1;
     if (!q.starts) {
       g = seq / q.members;
-      group_range(q, g, s0, s1);
     } else {
-      int lo = 0, hi = q.groups;  // the last group that starts at or before seq
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (q.starts[mid] <= seq) lo = mid;
-        else hi = mid;
+      for (int g0 = 0; g0 < q.groups; g0 += 64) {  // the last group that starts at or before seq
+        const uint64_t m = __ballot(g0 + lane < q.groups && q.starts[min(g0 + lane, q.groups)] <= seq);
+        if (m) g = g0 + 63 - __builtin_clzll(m);
+        if (m != ~0ull) break;
       }
-      group_range(q, lo, s0, s1);
-      if (seq >= s0 && seq < s1) g = lo;
     }
-    const int steps = g < 0 ? 0 : (min(max(q.shared.lens[g], 0), q.shared.limit) + q.shared_tile - 1) / q.shared_tile;
-    if (steps > 0 && q.group_at[q.groups].y <= q.strips) {
-      const int cols = 32 * q.query_waves;
-      const int r = (tok - s0 * q.next_n) * q.per + sub, tile = r / cols;
-      const int4 at = q.group_at[g];
-      const int share = share_of(q, q.group_at[q.groups].x);
-      const int a = at.x + tile * steps, first = a / share;
-      shared = (a + steps - 1) / share - first + 1;
-      shared_slot = ((int64_t)kv * (q.shared_wgs + q.strips) + first + at.y + tile) * cols + (r - tile * cols);
+    if (g >= 0) {
+      group_range(q, g, s0, s1);
+      const int4 at = q.group_at[g], all = q.group_at[q.groups];
+      const int steps = (min(max(q.shared.lens[g], 0), q.shared.limit) + q.shared_tile - 1) / q.shared_tile;
+      if (seq >= s0 && seq < s1 && steps > 0 && all.y <= q.strips) {
+        const int cols = 32 * q.query_waves;
+        const int r = (tok - s0 * q.next_n) * q.per + sub, tile = r / cols;
+        const int share = share_of(q, all.x);
+        const int a = at.x + tile * steps, first = a / share;
+        shared = (a + steps - 1) / share - first + 1;
+        shared_slot = ((int64_t)kv * (q.shared_wgs + q.strips) + first + at.y + tile) * cols + (r - tile * cols);
+      }
     }
   }
   const int own_rows = q.next_n * q.per;
@@ -473,35 +724,49 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) 
   const int own = q.own_splits > 0 ? (steps + share - 1) / share : 0;
   const int64_t own_slot = ((int64_t)seq * q.kv_heads + kv) * own_rows + (tok - seq * q.next_n) * q.per + sub;
   const int64_t own_stride = (int64_t)q.seqs * q.kv_heads * own_rows;
-
-  float top = kNone, total = 0.0f;
-  float4 v{0.0f, 0.0f, 0.0f, 0.0f};
-  auto add = [&](const float2 st, const float4 o) {
-    const float now = fmaxf(top, st.x), ref = now == kNone ? 0.0f : now;
-    const float f = __builtin_amdgcn_exp2f(top - ref), g = __builtin_amdgcn_exp2f(st.x - ref);
-    top = now;
-    total = total * f + st.y * g;
-    v.x = v.x * f + o.x * g;
-    v.y = v.y * f + o.y * g;
-    v.z = v.z * f + o.z * g;
-    v.w = v.w * f + o.w * g;
+  const int n = shared + own;
+  auto stat = [&](int i) {
+    return i < shared ? q.shared_stats[shared_slot + (int64_t)i * 32 * q.query_waves]
+                      : q.own_stats[own_slot + (i - shared) * own_stride];
   };
-  for (int i = 0; i < shared; ++i) {
-    const int64_t s = shared_slot + (int64_t)i * 32 * q.query_waves;
-    add(q.shared_stats[s], *reinterpret_cast<const float4*>(q.shared_parts + s * DIM + d));
+
+  float top = kNone;
+  for (int i = lane; i < n; i += 64) top = fmaxf(top, stat(i).x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float ref = top == kNone ? 0.0f : top;
+  const int set = lane / LANES, at = (lane % LANES) * 4;
+  float total = 0.0f;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = set; i < n; i += SETS) {
+    const float2 st = stat(i);
+    const float* o = (i < shared ? q.shared_parts + (shared_slot + (int64_t)i * 32 * q.query_waves) * DIM
+                                 : q.own_parts + (own_slot + (i - shared) * own_stride) * DIM) + at;
+    const float4 x = *reinterpret_cast<const float4*>(o);
+    const float f = __builtin_amdgcn_exp2f(st.x - ref);
+    total += st.y * f;
+    v[0] += x.x * f;
+    v[1] += x.y * f;
+    v[2] += x.z * f;
+    v[3] += x.w * f;
   }
-  for (int i = 0; i < own; ++i) {
-    const int64_t s = own_slot + i * own_stride;
-    add(q.own_stats[s], *reinterpret_cast<const float4*>(q.own_parts + s * DIM + d));
+#pragma unroll
+  for (int d = LANES; d < 64; d <<= 1) {
+    total += __shfl_xor(total, d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], d);
   }
+  if (set > 0) return;
   const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
   typedef typename T::Value Value;
-  Value* out = reinterpret_cast<Value*>(q.out) + row * DIM + d;
-  Value r[4] = {(Value)(v.x * inv), (Value)(v.y * inv), (Value)(v.z * inv), (Value)(v.w * inv)};
+  Value r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (Value)(v[i] * inv);
   uint2 w;
   __builtin_memcpy(&w, r, 8);
-  *reinterpret_cast<uint2*>(out) = w;
-  if (q.lse && d == 0)
+  *reinterpret_cast<uint2*>(reinterpret_cast<Value*>(q.out) + row * DIM + at) = w;
+  if (q.lse && lane == 0)
     q.lse[row] = total > 0.0f || total != total ? (top + __builtin_log2f(total)) * 0.69314718f : kNone;
 }
 
@@ -551,7 +816,7 @@ __global__ void __launch_bounds__(kMassBlock) attend_mass_kernel(const MassParam
     const int32_t b = p < s.len ? block_at(q, s.table, pt.width, p) : -1;
     const uint32_t off = (uint32_t)p - q.by_block((uint32_t)p) * (uint32_t)q.block_size;
     const unsigned char* a = q.k.base + s.head * q.k.head_stride + half * 16 +
-                             (b >= 0 ? b * q.k.block_stride + off * q.k.slot_stride : 0);
+                             (b >= 0 ? (uint64_t)b * q.k.block_stride + (uint64_t)off * q.k.slot_stride : 0);
 #pragma unroll
     for (int d = 0; d < STEPS; ++d) key[d] = *reinterpret_cast<const Piece*>(a + d * 32);
     const uint64_t live = __ballot(b >= 0);
@@ -571,6 +836,8 @@ __global__ void __launch_bounds__(kMassBlock) attend_mass_kernel(const MassParam
       const bool on = has && lse > kNone;
       lse = on ? lse * 1.44269504f : 0.0f;
       const int sees = s.len - s.cut + (s.cut ? tok % q.next_n : 0);
+      const int ahead = on ? min(max(sees - (p0 + 4 * half), 0), 31) : 0;
+      const uint32_t seen = (uint32_t)(live >> (4 * half)) & ((1u << ahead) - 1u);
       f32x16 sc;
 #pragma unroll
       for (int i = 0; i < 16; ++i) sc[i] = 0.0f;
@@ -578,9 +845,8 @@ __global__ void __launch_bounds__(kMassBlock) attend_mass_kernel(const MassParam
       for (int d = 0; d < STEPS; ++d) sc = T::mfma(key[d], query[d], sc);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int j = 8 * (i / 4) + 4 * half + i % 4;
         const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], q.scale, -lse));
-        acc[i] += on && (live >> j & 1) && p0 + j < sees ? w : 0.0f;
+        acc[i] += seen >> (8 * (i / 4) + i % 4) & 1 ? w : 0.0f;
       }
     }
 #pragma unroll
@@ -603,21 +869,27 @@ __global__ void __launch_bounds__(kMassBlock) attend_mass_kernel(const MassParam
 
 namespace {
 
-template <class T, int DIM>
+template <class T, int DIM, bool EVEN>
 const void* attend_ptr(int query_waves) {
   switch (query_waves) {
-    case 8: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 8, 1, 64>);
-    case 4: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 4, 1, 32>);
-    case 2: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 2, 1, 32>);
-    default: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 1, kOwnSets, kKeyTile>);
+    case 8: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 8, 1, 64, EVEN>);
+    case 4: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 4, 1, 64, EVEN>);
+    case 2: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 2, 1, 32, EVEN>);
+    default: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 1, kOwnSets, kKeyTile, EVEN>);
   }
+}
+template <class T>
+const void* attend_ptr(int dim, int query_waves, bool even) {
+  if (dim == 64) return even ? attend_ptr<T, 64, true>(query_waves) : attend_ptr<T, 64, false>(query_waves);
+  return even ? attend_ptr<T, 128, true>(query_waves) : attend_ptr<T, 128, false>(query_waves);
 }
 
 }  // namespace
 
-const void* attend_kernel_ptr(int dtype, int dim, int query_waves) {
-  if (dtype == 1) return dim == 64 ? attend_ptr<Bf16, 64>(query_waves) : attend_ptr<Bf16, 128>(query_waves);
-  return dim == 64 ? attend_ptr<F16, 64>(query_waves) : attend_ptr<F16, 128>(query_waves);
+const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int block_size) {
+  // rows that a wave loads at once
+  const bool even = block_size % (64 / (dim / 8)) == 0;
+  return dtype == 1 ? attend_ptr<Bf16>(dim, query_waves, even) : attend_ptr<F16>(dim, query_waves, even);
 }
 const void* attend_join_kernel_ptr(int dtype, int dim) {
   if (dtype == 1)

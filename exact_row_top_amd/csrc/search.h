@@ -114,8 +114,8 @@ constexpr int kOwnSets = 4;         // waves that take turns at the keys of up t
 // at p % size.
 struct Pages {
   const unsigned char* base;
-  int64_t block_stride;      // bytes
-  int64_t slot_stride;
+  uint32_t block_stride;     // bytes
+  uint32_t slot_stride;
   int64_t head_stride;
 };
 

@@ -15,7 +15,7 @@ const void* beam_segment_kernel_ptr(int dtype);
 const void* beam_row_kernel_ptr(int dtype);
 const void* reorder_rows_kernel_ptr(int n);
 const void* reorder_blocks_kernel_ptr(int n);
-const void* attend_kernel_ptr(int dtype, int dim, int query_waves);
+const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int block_size);
 const void* attend_join_kernel_ptr(int dtype, int dim);
 const void* attend_mass_kernel_ptr(int dtype, int dim);
 const void* evict_keep_kernel_ptr();
@@ -64,7 +64,7 @@ bool attend_plan(int32_t groups, int32_t seqs, bool ragged, int32_t next_n, int3
   const int64_t group_rows = groups > 0 ? (seqs + groups - 1) / groups * rows : 0;
   p.query_waves = group_rows > 128 ? 8 : (group_rows > 64 ? 4 : (group_rows > 32 ? 2 : 1));
   const int64_t cols = 32 * p.query_waves;
-  p.tile = p.query_waves == 8 ? 64 : 32;
+  p.tile = p.query_waves >= 4 ? 64 : 32;
   p.least = p.query_waves == 1 ? kOwnSets : 1;
   p.strips = ragged ? seqs * rows / cols + groups : groups * ((group_rows + cols - 1) / cols);
   p.shared_wgs = 0;
@@ -112,11 +112,16 @@ bool attend_shape_ok(const AttendShape& s, const int32_t* starts) {
 }
 
 bool pages_ok(const void* base, int64_t block, int64_t slot, int64_t head, int64_t num_blocks) {
-  return (base || num_blocks == 0) && block >= 0 && slot >= 0 && head >= 0;
+  return (base || num_blocks == 0) && block >= 0 && block < kInt && slot >= 0 && slot < (1 << 27) && head >= 0 &&
+         head < kInt;
 }
 
 bool pages_at(const void* base, int64_t block, int64_t slot, int64_t head) {
   return at(base, 16) && block % 8 == 0 && slot % 8 == 0 && head % 8 == 0;
+}
+
+Pages pages(const void* base, int64_t block, int64_t slot, int64_t head) {
+  return Pages{static_cast<const unsigned char*>(base), (uint32_t)block * 2, (uint32_t)slot * 2, head * 2};
 }
 
 int tables_ok(const int32_t* tables, int64_t stride, int32_t width, const int32_t* lens, int32_t rows) {
@@ -134,7 +139,7 @@ void attend_params(AttendParams& p, const AttendShape& s, const void* q, int64_t
   p.q = static_cast<const unsigned char*>(q);
   p.q_stride = q_stride * 2;
   p.q_head_stride = q_head_stride * 2;
-  p.k = Pages{static_cast<const unsigned char*>(k), k_block * 2, k_slot * 2, k_head * 2};
+  p.k = pages(k, k_block, k_slot, k_head);
   p.num_blocks = s.num_blocks;
   p.block_size = s.block_size;
   p.by_block = quotient_of((uint32_t)s.block_size);
@@ -414,7 +419,7 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
   attend_params(p, s, q, q_stride, q_head_stride, k_cache, k_block_stride, k_slot_stride, k_head_stride,
                 shared_tables, shared_stride, shared_width, shared_lens, most_shared, group_starts, own_tables,
                 own_stride, own_width, own_lens, most_own, scale);
-  p.v = Pages{static_cast<const unsigned char*>(v_cache), v_block_stride * 2, v_slot_stride * 2, v_head_stride * 2};
+  p.v = pages(v_cache, v_block_stride, v_slot_stride, v_head_stride);
   p.query_waves = plan.query_waves;
   p.shared_tile = plan.tile;
   p.shared_least = plan.least;
@@ -434,17 +439,16 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
   const bool together = plan.query_waves == 1;
   const int64_t first = p.shared_grid + (together ? plan.own_wgs : 0);
   if (first > 0) {
-    rc = launch(attend_kernel_ptr(dtype, dim, plan.query_waves), first,
+    rc = launch(attend_kernel_ptr(dtype, dim, plan.query_waves, block_size), first,
                 64 * (together ? kOwnSets : plan.query_waves), &p, 0, stream);
     if (rc != TOPK_OK) return rc;
   }
   if (!together && plan.own_wgs > 0) {
     p.shared_grid = 0;
-    rc = launch(attend_kernel_ptr(dtype, dim, 1), plan.own_wgs, 64 * kOwnSets, &p, 0, stream);
+    rc = launch(attend_kernel_ptr(dtype, dim, 1, block_size), plan.own_wgs, 64 * kOwnSets, &p, 0, stream);
     if (rc != TOPK_OK) return rc;
   }
-  const int64_t per = 256 / (dim / 4);
-  return launch(attend_join_kernel_ptr(dtype, dim), (rows + per - 1) / per, 256, &p, 0, stream);
+  return launch(attend_join_kernel_ptr(dtype, dim), (rows + 3) / 4, 256, &p, 0, stream);
 }
 
 int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
