@@ -33,6 +33,12 @@ def _flat(t, name, dtype, shape, device):
     """Pointer of a contiguous tensor of one shape, or None."""
     if t is None:
         return None
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == device.index):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _tensor(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -41,6 +47,30 @@ def _flat(t, name, dtype, shape, device):
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     return t.data_ptr()
+
+
+def _given(t, name, length, device):
+    """Pointer of an int32 vector that must be given."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return _vector(t, name, torch.int32, length, device)
+
+
+def _tables(t, name, rows, device):
+    """(pointer, row stride, width) of block tables; any number of rows for None."""
+    try:
+        (n, width), (stride, inner) = t.shape, t.stride()
+        if (t.dtype is torch.int32 and inner == 1 and stride >= width and n == rows and n < 1 << 31
+                and width < 1 << 31 and t.get_device() == device.index):
+            return t.data_ptr(), stride if n > 1 else width, width
+    except (AttributeError, TypeError, ValueError):
+        pass
+    n, width, stride = _tables_layout(t)
+    if rows is not None and n != rows:
+        raise ValueError(f"{name} must hold {rows} rows")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.data_ptr(), stride, width
 
 
 def select_beams(logits, scores, k, *, ended=None, end_token=0, lengths=None, length_penalty=0.0,
@@ -77,8 +107,8 @@ def select_beams(logits, scores, k, *, ended=None, end_token=0, lengths=None, le
     n = _flat(lengths, "lengths", torch.int32, (requests, beams), dev)
     if k < 1:
         raise ValueError("k must be at least 1")
-    found, parents, tokens = torch.empty((3, requests, k), dtype=torch.int32, device=dev).unbind(0)
-    found = found.view(torch.float32)
+    found = torch.empty((requests, k), dtype=torch.float32, device=dev)
+    parents, tokens = torch.empty((2, requests, k), dtype=torch.int32, device=dev).unbind(0)
     nbytes = lib.topk_beams_workspace_bytes(requests, beams, k, vocab)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(lib.topk_beams(logits.data_ptr(), code, stride, vocab, requests, beams, k, s, e, end_token, n,
@@ -88,6 +118,13 @@ def select_beams(logits, scores, k, *, ended=None, end_token=0, lengths=None, le
 
 
 def _parents(parents, device):
+    try:
+        shape = parents.shape
+        if (parents.dtype is torch.int32 and len(shape) == 2 and parents.is_contiguous()
+                and parents.get_device() == device.index):
+            return shape
+    except AttributeError:
+        pass
     _tensor(parents, "parents")
     if parents.dtype != torch.int32:
         raise TypeError(f"parents must be torch.int32, got {parents.dtype}")
@@ -100,6 +137,12 @@ def _parents(parents, device):
 
 def _rows_layout(t, name, rows, device):
     """(row stride, row size) in bytes of a tensor of contiguous rows."""
+    try:
+        if t.is_contiguous() and t.shape[0] == rows and rows and t.get_device() == device.index:
+            n = t.nbytes // rows
+            return n, n
+    except (AttributeError, IndexError):
+        pass
     _tensor(t, name)
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -147,39 +190,52 @@ def reorder_beams(states, parents, *, beams=None, out=None, stream=None):
     clear = out is None
     sources = [_rows_layout(t, "states", requests * beams, dev) for t in states]
     if clear:
-        out = [torch.empty((requests * k, *t.shape[1:]), dtype=t.dtype, device=dev) for t in states]
-    targets = [_rows_layout(t, "out", requests * k, dev) for t in out]
-    for a, b, s, o in zip(states, out, sources, targets):
-        if a.dtype != b.dtype or a.shape[1:] != b.shape[1:]:
-            raise ValueError("out must have its state's type and row shape")
+        out = [t.new_empty((requests * k, *t.shape[1:])) for t in states]
+        targets = [(n, n) for _, n in sources]
+    else:
+        targets = [_rows_layout(t, "out", requests * k, dev) for t in out]
+        for a, b in zip(states, out):
+            if a.dtype != b.dtype or a.shape[1:] != b.shape[1:]:
+                raise ValueError("out must have its state's type and row shape")
+    # one array: sources, targets, their strides, row sizes
     n = len(states)
-    pointers, sizes = ctypes.c_void_p * n, ctypes.c_int64 * n
-    _check(_lib().topk_reorder_rows(
-        n, pointers(*[t.data_ptr() for t in states]), pointers(*[t.data_ptr() for t in out]),
-        sizes(*[s[0] for s in sources]), sizes(*[s[0] for s in targets]), sizes(*[s[1] for s in sources]),
-        parents.data_ptr(), requests, beams, k, 1 if clear else 0, _raw_stream(dev)))
+    each = (ctypes.c_int64 * (5 * n))(*[t.data_ptr() for t in states], *[t.data_ptr() for t in out],
+                                      *[s for s, _ in sources], *[s for s, _ in targets],
+                                      *[b for _, b in sources])
+    at = ctypes.addressof(each)
+    _check(_lib().topk_reorder_rows(n, at, at + 8 * n, at + 16 * n, at + 24 * n, at + 32 * n,
+                                    parents.data_ptr(), requests, beams, k, 1 if clear else 0,
+                                    _raw_stream(dev)))
     return out[0] if single else out
 
 
 def _caches(caches, block_size, device):
     """(pointer array, caches, blocks, bytes of a slot) of caches of one shape."""
-    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    caches = [caches] if isinstance(caches, torch.Tensor) else caches
     if not caches:
         return None, 0, 0, 0
-    first = _tensor(caches[0], "caches")
-    for c in caches:
-        _tensor(c, "caches")
-        if c.device != device:
-            raise ValueError(f"caches must be on {device}")
-        if c.dim() < 2 or not c.is_contiguous() or c.shape != first.shape or c.dtype != first.dtype:
-            raise ValueError("caches must be contiguous [blocks, block_size, ...] tensors of one shape and type")
-        if c.shape[1] != block_size:
-            raise ValueError(f"caches must hold blocks of {block_size}")
-    slots = first.shape[0] * first.shape[1]
-    slot_bytes = first.numel() // slots * first.element_size() if slots else 0
-    if first.shape[0] >> 31 or slot_bytes >> 31:
+    try:
+        first = caches[0]
+        shape, dtype, nbytes = first.shape, first.dtype, first.nbytes
+        good = len(shape) >= 2 and shape[1] == block_size
+        for c in caches:
+            good = (good and c.is_contiguous() and c.shape == shape and c.dtype is dtype
+                    and c.get_device() == device.index)
+    except (AttributeError, TypeError):
+        good = False
+    if not good:
+        for c in caches:
+            _tensor(c, "caches")
+            if c.device != device:
+                raise ValueError(f"caches must be on {device}")
+            if c.dim() < 2 or not c.is_contiguous() or c.shape != shape or c.dtype != dtype:
+                raise ValueError("caches must be contiguous [blocks, block_size, ...] tensors of one shape and type")
+        raise ValueError(f"caches must hold blocks of {block_size}")
+    slots = shape[0] * shape[1]
+    slot_bytes = nbytes // slots if slots else 0
+    if shape[0] >> 31 or slot_bytes >> 31:
         raise ValueError("caches are too large: their sizes must fit 32 bits")
-    return ((ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches]), len(caches), first.shape[0],
+    return ((ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches]), len(caches), shape[0],
             slot_bytes)
 
 
@@ -205,26 +261,27 @@ def reorder_block_tables(block_tables, kv_lens, parents, block_size, *, caches=(
         with guard:
             return reorder_block_tables(block_tables, kv_lens, parents, block_size, caches=caches,
                                         tail_blocks=tail_blocks, out=out)
-    rows, width, stride = _tables_layout(block_tables)
     dev = block_tables.device
     requests, k = _parents(parents, dev)
+    rows = len(block_tables)
+    tables, stride, width = _tables(block_tables, "block_tables", rows, dev)
     beams = rows // requests if requests else k
     if requests * beams != rows:
         raise ValueError(f"block_tables must hold the rows of {requests} requests")
     block_size = _int32(block_size, "block_size")
-    lens = _vector(_tensor(kv_lens, "kv_lens"), "kv_lens", torch.int32, requests, dev)
+    lens = _given(kv_lens, "kv_lens", requests, dev)
     tail = _vector(tail_blocks, "tail_blocks", torch.int32, requests * k, dev)
     if tail is None and beams != k:
         raise ValueError("tail_blocks is needed where k differs from the beams of a request")
     pointers, count, blocks, slot_bytes = _caches(caches, block_size, dev)
     if out is None:
         out = torch.empty((requests * k, width), dtype=torch.int32, device=dev)
-    out_rows, out_width, out_stride = _tables_layout(out)
-    if (out_rows, out_width) != (requests * k, width) or out.device != dev:
-        raise ValueError(f"out must be an int32 [{requests * k}, {width}] tensor on {dev}")
+    to, out_stride, out_width = _tables(out, "out", requests * k, dev)
+    if out_width != width:
+        raise ValueError(f"out must be an int32 [{requests * k}, {width}] tensor")
     _check(_lib().topk_reorder_blocks(
-        block_tables.data_ptr(), stride, width, lens, parents.data_ptr(), requests, beams, k, block_size,
-        tail, out.data_ptr(), out_stride, count, pointers, blocks, slot_bytes, _raw_stream(dev)))
+        tables, stride, width, lens, parents.data_ptr(), requests, beams, k, block_size, tail, to, out_stride,
+        count, pointers, blocks, slot_bytes, _raw_stream(dev)))
     return out
 
 
@@ -232,59 +289,58 @@ def _attend_arguments(q, k_cache, prefix_tables, prefix_lens, block_tables, kv_l
                       next_n, scale):
     """The arguments that attention and mass share: (device, query arguments,
     key cache layout, blocks and their size, tables and scale, sizes)."""
-    code = TOPK_DT.get(q.dtype)
-    if code not in (1, 2):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    if q.dim() != 3 or (q.numel() and q.stride(2) != 1):
+    dtype, dev = q.dtype, q.device
+    code = TOPK_DT.get(dtype)
+    if code != 1 and code != 2:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    if q.dim() != 3:
         raise ValueError("q must be 3-D [tokens, heads, dim] with unit inner stride")
-    tokens, heads, dim = q.shape
+    (tokens, heads, dim), (token_stride, head_stride, inner) = q.shape, q.stride()
+    if inner != 1 and q.numel():
+        raise ValueError("q must be 3-D [tokens, heads, dim] with unit inner stride")
     next_n = _int32(next_n, "next_n")
     if next_n < 1 or tokens % next_n:
         raise ValueError("q must hold next_n tokens for each sequence")
-    dev, seqs = q.device, tokens // next_n
-    keys = _cache_layout(k_cache, "k_cache", q)
-    blocks, block_size, kv_heads = k_cache.shape[:3]
+    seqs = tokens // next_n
+    keys = _cache_layout(k_cache, "k_cache", dtype, dim, dev)
+    blocks, block_size, kv_heads, _ = k_cache.shape
     if kv_heads < 1 or heads % kv_heads:
         raise ValueError("q's heads must be a multiple of the cache's")
     if tokens >> 31 or blocks >> 31 or block_size >> 31:
         raise ValueError("sizes must fit 32 bits")
-    rows, width, stride = _tables_layout(block_tables)
-    if rows != seqs or block_tables.device != dev:
-        raise ValueError(f"block_tables must hold {seqs} rows on {dev}")
-    own = (block_tables.data_ptr(), stride, width,
-           _vector(_tensor(kv_lens, "kv_lens"), "kv_lens", torch.int32, seqs, dev))
+    own = (*_tables(block_tables, "block_tables", seqs, dev), _given(kv_lens, "kv_lens", seqs, dev))
     if prefix_tables is None:
         if prefix_lens is not None or group_starts is not None:
             raise ValueError("prefix_lens and group_starts need prefix_tables")
         groups, shared, starts = 0, (None, 0, 0, None), None
     else:
-        groups, width, stride = _tables_layout(prefix_tables)
-        if prefix_tables.device != dev:
-            raise ValueError(f"prefix_tables must be on {dev}")
-        shared = (prefix_tables.data_ptr(), stride, width,
-                  _vector(_tensor(prefix_lens, "prefix_lens"), "prefix_lens", torch.int32, groups, dev))
+        groups = len(prefix_tables)
+        shared = (*_tables(prefix_tables, "prefix_tables", groups, dev),
+                  _given(prefix_lens, "prefix_lens", groups, dev))
         starts = _vector(group_starts, "group_starts", torch.int32, groups + 1, dev)
         if starts is None and groups and seqs % groups:
             raise ValueError("without group_starts the sequences must form equal groups")
     scale = float(dim) ** -0.5 if scale is None else float(scale)
-    token_stride = q.stride(0) if tokens > 1 else heads * dim
-    head_stride = q.stride(1) if heads > 1 else dim
-    query = (q.data_ptr(), code, token_stride, head_stride, seqs, next_n, heads, kv_heads, dim)
+    query = (q.data_ptr(), code, token_stride if tokens > 1 else 0, head_stride if heads > 1 else 0, seqs,
+             next_n, heads, kv_heads, dim)
     return (dev, query, keys, (blocks, block_size), (*shared, starts, groups, *own, scale),
             (tokens, heads, kv_heads, dim, seqs, groups, next_n))
 
 
-def _cache_layout(cache, name, q):
+def _cache_layout(cache, name, dtype, dim, device):
+    """(pointer, block, slot and head strides) of a cache."""
+    try:
+        (blocks, size, heads, d), (b, s, h, inner) = cache.shape, cache.stride()
+        if cache.dtype is dtype and d == dim and inner == 1 and cache.get_device() == device.index:
+            return cache.data_ptr(), b if blocks > 1 else 0, s if size > 1 else 0, h if heads > 1 else 0
+    except (AttributeError, TypeError, ValueError):
+        pass
     _tensor(cache, name)
-    if cache.dtype != q.dtype:
-        raise TypeError(f"{name} must be {q.dtype}, got {cache.dtype}")
-    if cache.dim() != 4 or cache.shape[3] != q.shape[2] or (cache.numel() and cache.stride(3) != 1):
-        raise ValueError(f"{name} must be [blocks, block_size, heads, {q.shape[2]}] with unit inner stride")
-    if cache.device != q.device:
-        raise ValueError(f"{name} must be on {q.device}")
-    b, s, h, _ = cache.stride()
-    return cache.data_ptr(), b if cache.shape[0] > 1 else 0, s if cache.shape[1] > 1 else 0, \
-        h if cache.shape[2] > 1 else 0
+    if cache.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {cache.dtype}")
+    if cache.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    raise ValueError(f"{name} must be [blocks, block_size, heads, {dim}] with unit inner stride")
 
 
 def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_lens, block_tables, kv_lens, *,
@@ -316,24 +372,22 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_lens, block_tabl
     dev, query, keys, paging, tables, sizes = _attend_arguments(
         q, k_cache, prefix_tables, prefix_lens, block_tables, kv_lens, group_starts, next_n, scale)
     tokens, heads, kv_heads, dim, seqs, groups, next_n = sizes
-    values = _cache_layout(v_cache, "v_cache", q)
+    values = _cache_layout(v_cache, "v_cache", q.dtype, dim, dev)
     if v_cache.shape != k_cache.shape:
         raise ValueError("v_cache must have k_cache's shape")
-    bounds = []
-    for name, bound in (("max_prefix_len", max_prefix_len), ("max_len", max_len)):
-        bound = 0 if bound is None else _int32(bound, name)
-        if bound < 0:
-            raise ValueError(f"{name} must not be negative")
-        bounds.append(bound)
+    most = 0 if max_prefix_len is None else _int32(max_prefix_len, "max_prefix_len")
+    most_own = 0 if max_len is None else _int32(max_len, "max_len")
+    if most < 0 or most_own < 0:
+        raise ValueError("max_prefix_len and max_len must not be negative")
     out = _matrix(out, "out", q.dtype, (tokens, heads, dim), dev)
     lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
     lib = _lib()
-    blocks, block_size = paging
-    room = [min(w * block_size, b) if b else w * block_size for w, b in zip((tables[2], tables[8]), bounds)]
+    room, room_own = tables[2] * paging[1], tables[8] * paging[1]
     nbytes = lib.topk_attend_workspace_bytes(groups, seqs, tables[4] is not None, next_n, heads, kv_heads,
-                                             dim, room[0] if groups else 0, room[1])
+                                             dim, min(room, most) if most else room,
+                                             min(room_own, most_own) if most_own else room_own)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _check(lib.topk_attend(*query, *keys, *values, *paging, *tables, *bounds, out.data_ptr(),
+    _check(lib.topk_attend(*query, *keys, *values, *paging, *tables, most, most_own, out.data_ptr(),
                            lse.data_ptr() if lse is not None else None, ws.data_ptr(), nbytes,
                            _raw_stream(dev)))
     return (out, lse) if return_lse else out
@@ -419,46 +473,48 @@ def evict_cache(mass, kv_lens, budget, *, sinks=0, recent=0, block_tables=None, 
                                caches=caches, out_tables=out_tables, mass_out=mass_out)
     if mass.dtype != torch.float32:
         raise TypeError(f"mass must be torch.float32, got {mass.dtype}")
-    if mass.dim() != 3 or (mass.numel() and mass.shape[2] > 1 and mass.stride(2) != 1):
+    if mass.dim() != 3:
         raise ValueError("mass must be 3-D [requests, heads, positions] with unit inner stride")
     dev = mass.device
-    requests, heads, positions = mass.shape
+    (requests, heads, positions), (stride0, stride1, inner) = mass.shape, mass.stride()
+    if inner != 1 and positions > 1 and mass.numel():
+        raise ValueError("mass must be 3-D [requests, heads, positions] with unit inner stride")
     if requests >> 31 or heads >> 31 or positions >> 31:
         raise ValueError("mass is too large: its sizes must fit 32 bits")
-    lens = _vector(_tensor(kv_lens, "kv_lens"), "kv_lens", torch.int32, requests, dev)
+    lens = _given(kv_lens, "kv_lens", requests, dev)
     budget, sinks, recent = _int32(budget, "budget"), _int32(sinks, "sinks"), _int32(recent, "recent")
     if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("budget must be at least 1, and sinks and recent within it")
-    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    caches = [caches] if isinstance(caches, torch.Tensor) else caches
     if caches:
         if block_tables is None:
             raise ValueError("caches need block_tables")
-        if _tensor(caches[0], "caches").dim() < 3:
+        shape = _tensor(caches[0], "caches").shape
+        if len(shape) < 3:
             raise ValueError("caches must be [blocks, block_size, kv_heads, ...] tensors")
-        pointers, count, blocks, slot_bytes = _caches(caches, caches[0].shape[1], dev)
-        if heads < 1 or caches[0].shape[2] % heads:
+        pointers, count, blocks, slot_bytes = _caches(caches, shape[1], dev)
+        if heads < 1 or shape[2] % heads:
             raise ValueError("mass' heads must divide the caches' heads")
         if (slot_bytes // heads) % 16:
             raise ValueError("a head's share of a cache slot must be a multiple of 16 bytes")
-        rows, width, stride = _tables_layout(block_tables)
-        to = block_tables if out_tables is None else out_tables
-        to_rows, to_width, to_stride = _tables_layout(to)
-        if rows != requests or to_rows != requests or block_tables.device != dev or to.device != dev:
-            raise ValueError(f"tables must hold {requests} rows on {dev}")
+        tables = _tables(block_tables, "block_tables", requests, dev)
+        to = tables if out_tables is None else _tables(out_tables, "out_tables", requests, dev)
     kept = torch.empty((requests, heads, budget), dtype=torch.int32, device=dev)
     new_lens = torch.empty(requests, dtype=torch.int32, device=dev)
+    width = budget
     if mass_out is None:
         mass_out = torch.empty((requests, heads, budget), dtype=torch.float32, device=dev)
-    elif _tensor(mass_out, "mass_out").dim() != 3 or mass_out.shape[2] < budget:
-        raise ValueError("mass_out must be [requests, heads, budget or more]")
-    out = _flat(mass_out, "mass_out", torch.float32, (requests, heads, mass_out.shape[2]), dev)
+        out = mass_out.data_ptr()
+    else:
+        if _tensor(mass_out, "mass_out").dim() != 3 or mass_out.shape[2] < budget:
+            raise ValueError("mass_out must be [requests, heads, budget or more]")
+        width = mass_out.shape[2]
+        out = _flat(mass_out, "mass_out", torch.float32, (requests, heads, width), dev)
     lib, raw = _lib(), _raw_stream(dev)
-    _check(lib.topk_evict_keep(mass.data_ptr(), mass.stride(0) if requests > 1 else 0,
-                               mass.stride(1) if heads > 1 else 0, positions, requests, heads, lens, budget,
-                               sinks, recent, kept.data_ptr(), out, mass_out.shape[2], new_lens.data_ptr(),
-                               raw))
+    _check(lib.topk_evict_keep(mass.data_ptr(), stride0 if requests > 1 else 0, stride1 if heads > 1 else 0,
+                               positions, requests, heads, lens, budget, sinks, recent, kept.data_ptr(), out,
+                               width, new_lens.data_ptr(), raw))
     if caches:
-        _check(lib.topk_evict_move(kept.data_ptr(), requests, heads, budget, block_tables.data_ptr(), stride,
-                                   width, to.data_ptr(), to_stride, to_width, caches[0].shape[1], count,
+        _check(lib.topk_evict_move(kept.data_ptr(), requests, heads, budget, *tables, *to, shape[1], count,
                                    pointers, blocks, slot_bytes, raw))
     return kept, mass_out, new_lens
