@@ -124,49 +124,35 @@ __global__ void __launch_bounds__(256) beam_segment_kernel(const BeamParams q) {
 //
 // Of the chunks ordered by (largest score falling, position) the first k hold
 // the beam's k best: were one of those in another chunk, the k chunks before
-// that one would each hold a score before it.  A bound for the k-th chunk is
-// the k-th largest of the threads' own maxima; what lies above it goes to LDS
-// and is ranked by counting, as are the chosen chunks' scores from the k-th
-// chunk's largest up.  So equal scores cost no more than others.
+// that one would each hold a score before it.  The chunks' maxima sit in
+// registers; a bound for the k-th of them is the k-th largest of 128 sets' own
+// maxima, found to 16 bits of its key with ballots.  What reaches it goes to
+// LDS and is ranked by counting, as are the chosen chunks' scores from the
+// k-th chunk's largest up.  Where more reach it than fit (equal or nearly
+// equal maxima), the bound is the k-th largest of the 512 threads' maxima to
+// the bit: fewer than k threads hold any above it, and of those that equal it
+// each wave takes its first k.
 // ---------------------------------------------------------------------------
 
 namespace {
 
 constexpr int kBeamWaves = kBeamBlock / 64;
 
+struct ListEntry {
+  float x;
+  int32_t i;
+};
+
 struct BeamShared {
   uint32_t keys[kBeamBlock];
   int32_t chosen[kMaxBeamK];
-  float top[kMaxBeamK];
-  float redf[kBeamWaves];
-  double redd[kBeamWaves];
-  uint32_t n;
+  float least;
+  float best[kBeamWaves];
+  double lse;
+  uint32_t n[3];
   uint32_t turn;
   BeamCandidate out[kMaxBeamK];
 };
-
-__device__ __forceinline__ float block_max(float v, BeamShared& sh) {
-  float low = v;
-  wave_minmax(low, v);
-  if ((threadIdx.x & 63) == 0) sh.redf[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = sh.redf[0];
-#pragma unroll
-  for (int w = 1; w < kBeamWaves; ++w) v = fmaxf(v, sh.redf[w]);
-  return v;
-}
-
-// Added up in one fixed order.
-__device__ __forceinline__ double block_sum(double v, BeamShared& sh) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  if ((threadIdx.x & 63) == 0) sh.redd[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = sh.redd[0];
-#pragma unroll
-  for (int w = 1; w < kBeamWaves; ++w) v += sh.redd[w];
-  return v;
-}
 
 // Appends what is `in` to a list in LDS; returns the place.
 __device__ __forceinline__ uint32_t append(bool in, uint32_t* n) {
@@ -179,16 +165,55 @@ __device__ __forceinline__ uint32_t append(bool in, uint32_t* n) {
                                           __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
-// How many of the list's n entries come before (x, i).
-__device__ __forceinline__ int before(const float* lx, const int32_t* li, int n, float x, int i) {
-  int c = 0;
-  for (int j = 0; j < n; ++j) c += (lx[j] > x || (lx[j] == x && li[j] < i)) ? 1 : 0;
-  return c;
+// f(entry, how many of the list's n come before it) for each entry of which
+// fewer than k do: by one wave in registers where they fit one, else by all.
+template <class F>
+__device__ __forceinline__ void rank_list(const ListEntry* list, int n, int k, F&& f) {
+  const int t = threadIdx.x;
+  if (n <= 64) {
+    if (t >= 64) return;
+    const ListEntry e = t < n ? list[t] : ListEntry{-__builtin_inff(), 0x7FFFFFFF};
+    int c = 0;
+    for (int j = 0; j < n; ++j) {
+      const float x = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(e.x), j));
+      const int i = __builtin_amdgcn_readlane(e.i, j);
+      c += (x > e.x || (x == e.x && i < e.i)) ? 1 : 0;
+    }
+    if (t < n && c < k) f(e, c);
+    return;
+  }
+  for (int o = t; o < n; o += kBeamBlock) {
+    const ListEntry e = list[o];
+    int c = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const ListEntry b = list[j];
+      c += (b.x > e.x || (b.x == e.x && b.i < e.i)) ? 1 : 0;
+    }
+    if (c < k) f(e, c);
+  }
+}
+
+// The largest value whose lowest `low` bits are zero that at least k of the
+// wave's keys (N a lane) reach.
+template <int N>
+__device__ __forceinline__ uint32_t kth_key(const uint32_t (&key)[N], int k, int low) {
+  uint32_t thr = 0;
+#pragma unroll 1
+  for (int b = 31; b >= low; --b) {
+    const uint32_t at = thr | (1u << b);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= at));
+    if (n >= k) thr = at;
+  }
+  return thr;
 }
 
 }  // namespace
 
-template <class T>
+// NV: 16-byte pieces of chunk maxima that a thread holds.
+template <class T, int NV>
 __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q) {
   extern __shared__ __align__(16) unsigned char lds[];
   __shared__ BeamShared sh;
@@ -197,110 +222,132 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
   const int k = q.k, segs = q.segments;
   const float score = q.scores[row];
   const bool ended = q.ended && q.ended[row];
+  const bool reads = offers(score) && !ended;
   double norm = 1.0;
   if (q.lengths && q.penalty != 0.0)
     norm = pow((double)max((int64_t)q.lengths[row] + (ended ? 0 : 1), (int64_t)1), q.penalty);
   if (t < k) sh.out[t] = BeamCandidate{-__builtin_inf(), -__builtin_inff(), -1};
-  if (t == 0) sh.n = 0;
-  __syncthreads();
+  if (t < 3) sh.n[t] = 0;
 
-  if (offers(score)) {
-    if (ended) {
-      if (t == 0) sh.out[0] = BeamCandidate{(double)score / norm, score, q.end_token};
-    } else {
-      const float* bests = q.bests + (int64_t)row * segs;
-      const uint64_t* masses = q.masses + (int64_t)row * segs;
-      float m = -__builtin_inff();
-      for (int s = t; s < segs; s += kBeamBlock) m = fmaxf(m, bests[s]);
-      // the largest chunk of each thread's own
-      const float* chunks = q.chunks + (int64_t)row * segs * 64 + (int64_t)wv * (segs * 64 / kBeamWaves);
-      const int mine = segs * 64 / kBeamWaves;  // a wave's chunks
-      float top = -__builtin_inff();
-      for (int c = lane; c < mine; c += 64) top = fmaxf(top, chunks[c]);
-      sh.keys[t] = fkey(top);
-      m = block_max(m, sh);
-      if (m > -__builtin_inff()) {
+  ListEntry* list = reinterpret_cast<ListEntry*>(lds);
+  if (offers(score) && ended) {
+    __syncthreads();
+    if (t == 0) sh.out[0] = BeamCandidate{(double)score / norm, score, q.end_token};
+  } else if (reads) {
+    // a wave holds NV * 256 neighbouring chunks, a lane four in each piece
+    const int chunks = segs * 64, c0 = wv * NV * 256 + lane * 4;
+    const float* from = q.chunks + (int64_t)row * chunks;
+    float v[NV][4];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float4 x{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+      if (c0 + j * 256 < chunks) x = *reinterpret_cast<const float4*>(from + c0 + j * 256);
+      v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, v[j][e]);
+    float four = fmaxf(top, __shfl_xor(top, 1));
+    four = fmaxf(four, __shfl_xor(four, 2));
+    if ((lane & 3) == 0) sh.keys[t >> 2] = fkey(four);
+    float low = top, best = top;
+    wave_minmax(low, best);
+    if (lane == 0) sh.best[wv] = best;
+    __syncthreads();
+    float m = sh.best[0];
+#pragma unroll
+    for (int w = 1; w < kBeamWaves; ++w) m = fmaxf(m, sh.best[w]);
+    if (m > -__builtin_inff()) {
+      const uint32_t sets[2] = {sh.keys[lane], sh.keys[64 + lane]};
+      const uint32_t thr = max(kth_key(sets, k, 16), fkey(-__builtin_inff()) + 1u);
+      uint32_t room = (uint32_t)q.cap;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = fkey(v[j][e]) >= thr;
+          const uint32_t at = append(in, &sh.n[0]);
+          if (in && at < room) list[at] = ListEntry{v[j][e], c0 + j * 256 + e};
+        }
+      __syncthreads();
+      int n = (int)sh.n[0];
+      if (n > q.cap) {
+        // too many: to the bit, and of equal ones each wave's first k
+        sh.keys[t] = fkey(top);
+        __syncthreads();
+        uint32_t all[kBeamWaves];
+#pragma unroll
+        for (int i = 0; i < kBeamWaves; ++i) all[i] = sh.keys[i * 64 + lane];
+        const float floor = from_key(kth_key(all, k, 0));
+        int ties = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          uint64_t even[4];
+          int rank = ties;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            even[e] = __ballot(v[j][e] == floor && v[j][e] > -__builtin_inff());
+            rank += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(even[e] >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)even[e], 0u));
+            ties += __popcll(even[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool tie = even[e] >> lane & 1;
+            const bool in = v[j][e] > floor || (tie && rank < k);
+            rank += tie ? 1 : 0;
+            const uint32_t at = append(in, &sh.n[1]);
+            if (in) list[at] = ListEntry{v[j][e], c0 + j * 256 + e};
+          }
+        }
+        __syncthreads();
+        n = (int)sh.n[1];
+      }
+      const int picked = min(n, k);
+      rank_list(list, n, k, [&](const ListEntry& e, int r) {
+        sh.chosen[r] = e.i;
+        if (r == picked - 1) sh.least = n >= k ? e.x : -__builtin_inff();
+      });
+      if (wv == 1) {
+        // the row's sum, segment by segment in one order
+        const float* bests = q.bests + (int64_t)row * segs;
+        const uint64_t* masses = q.masses + (int64_t)row * segs;
         const Exp2Poly poly;
         double sum = 0.0;
-        for (int s = t; s < segs; s += kBeamBlock) {
+        for (int s = lane; s < segs; s += 64) {
           const float b = bests[s];
           const double w = b == m ? 1.0 : exp2_64(((double)b - (double)m) * kLog2e, poly);
           sum += (double)masses[s] * w;
         }
-        sum = block_sum(sum, sh) * 0x1p-43;
-        const double lse = m == __builtin_inff() ? log(sum) : (double)m + log(sum);
-
-        uint32_t key[kBeamWaves], thr = 0;
 #pragma unroll
-        for (int i = 0; i < kBeamWaves; ++i) key[i] = sh.keys[i * 64 + lane];
-#pragma unroll 1
-        for (int b = 31; b >= 0; --b) {
-          const uint32_t at = thr | (1u << b);
-          int n = 0;
-#pragma unroll
-          for (int i = 0; i < kBeamWaves; ++i) n += __popcll(__ballot(key[i] >= at));
-          if (n >= k) thr = at;
-        }
-        const float floor = from_key(thr);
-        float* lx = reinterpret_cast<float*>(lds);
-        int32_t* li = reinterpret_cast<int32_t*>(lx + q.cap);
-        int ties = 0;  // this wave's, in the order of the row
-        for (int c0 = 0; c0 < mine; c0 += 64) {
-          const float v = c0 + lane < mine ? chunks[c0 + lane] : -__builtin_inff();
-          const uint64_t even = __ballot(v == floor && v > -__builtin_inff());
-          const int rank = ties + (int)__builtin_amdgcn_mbcnt_hi(
-                                      (uint32_t)(even >> 32),
-                                      __builtin_amdgcn_mbcnt_lo((uint32_t)even, 0u));
-          const bool in = v > floor || ((even >> lane & 1) && rank < k);
-          ties += __popcll(even);
-          const uint32_t at = append(in, &sh.n);
-          if (in) {
-            lx[at] = v;
-            li[at] = wv * mine + c0 + lane;
-          }
-        }
-        __syncthreads();
-        const int n = (int)sh.n, picked = min(n, k);
-        for (int i = t; i < n; i += kBeamBlock) {
-          const int r = before(lx, li, n, lx[i], li[i]);
-          if (r < k) {
-            sh.chosen[r] = li[i];
-            sh.top[r] = lx[i];
-          }
-        }
-        __syncthreads();
-        if (t == 0) sh.n = 0;
-        const float least = n >= k ? sh.top[k - 1] : -__builtin_inff();
-        __syncthreads();
-        int32_t* gi = reinterpret_cast<int32_t*>(lx + k * kChunk);
-        const unsigned char* base = static_cast<const unsigned char*>(q.logits) +
-                                    (int64_t)row * q.row_stride * (int64_t)sizeof(T);
-        for (int i0 = 0; i0 < picked * kChunk; i0 += kBeamBlock) {
-          const int i = i0 + t;
-          float v = -__builtin_inff();
-          int pos = 0;
-          if (i < picked * kChunk) {
-            pos = sh.chosen[i / kChunk] * kChunk + i % kChunk;
-            if (pos < q.vocab) v = Elem<T>::load(base, pos);
-          }
-          const bool in = v > -__builtin_inff() && v >= least && (m < __builtin_inff() || v == m);
-          const uint32_t at = append(in, &sh.n);
-          if (in) {
-            lx[at] = v;
-            gi[at] = pos;
-          }
-        }
-        __syncthreads();
-        const int found = (int)sh.n;
-        for (int i = t; i < found; i += kBeamBlock) {
-          const float v = lx[i];
-          const int r = before(lx, gi, found, v, gi[i]);
-          if (r < k) {
-            const double total = (double)score + (m == __builtin_inff() ? -lse : (double)v - lse);
-            sh.out[r] = BeamCandidate{total / norm, (float)total, gi[i]};
-          }
-        }
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        sum = log(sum * 0x1p-43);
+        if (lane == 0) sh.lse = m == __builtin_inff() ? sum : (double)m + sum;
       }
+      __syncthreads();
+      const float least = sh.least;
+      const unsigned char* base = static_cast<const unsigned char*>(q.logits) +
+                                  (int64_t)row * q.row_stride * (int64_t)sizeof(T);
+      for (int i0 = 0; i0 < picked * kChunk; i0 += kBeamBlock) {
+        const int i = i0 + t;
+        float x = -__builtin_inff();
+        int pos = 0;
+        if (i < picked * kChunk) {
+          pos = sh.chosen[i / kChunk] * kChunk + i % kChunk;
+          if (pos < q.vocab) x = Elem<T>::load(base, pos);
+        }
+        const bool in = x > -__builtin_inff() && x >= least && (m < __builtin_inff() || x == m);
+        const uint32_t at = append(in, &sh.n[2]);
+        if (in) list[at] = ListEntry{x, pos};
+      }
+      __syncthreads();
+      const double lse = sh.lse;
+      rank_list(list, (int)sh.n[2], k, [&](const ListEntry& e, int r) {
+        const double total = (double)score + (m == __builtin_inff() ? -lse : (double)e.x - lse);
+        sh.out[r] = BeamCandidate{total / norm, (float)total, e.i};
+      });
     }
   }
   __syncthreads();
@@ -319,7 +366,7 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
   __syncthreads();
   if (t == 0) {
     sh.turn = __hip_atomic_fetch_add(q.arrived + req, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sh.n = 0;
+    sh.n[0] = 0;
   }
   __syncthreads();
   if (sh.turn != (uint32_t)q.beams - 1) return;
@@ -337,21 +384,29 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
     c.rank = rank[i];
     __builtin_memcpy(&c.total, &rest[i], 8);
     if (c.token < 0) continue;
-    atomicAdd(&sh.n, 1u);
+    atomicAdd(&sh.n[0], 1u);
     const int b = i / k;
     int place = i - b * k;
-    for (int o = 0; o < q.beams && place < k; ++o) {
-      if (o == b) continue;
-      // entries of beam o before c: in falling order, and the same from an
-      // earlier beam first
-      int lo = 0, hi = k;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        const double r = rank[o * k + mid];
-        if (r > c.rank || (r == c.rank && o < b)) lo = mid + 1;
-        else hi = mid;
+    if (all <= 512) {
+      // counted: those before it in the list that are not less, those behind
+      // it that are more (lists stand in falling order, ties by beam)
+      place = 0;
+#pragma unroll 8
+      for (int j = 0; j < all; ++j) place += (rank[j] > c.rank || (rank[j] == c.rank && j < i)) ? 1 : 0;
+    } else {
+      for (int o = 0; o < q.beams && place < k; ++o) {
+        if (o == b) continue;
+        // entries of beam o before c: in falling order, and the same from an
+        // earlier beam first
+        int lo = 0, hi = k;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          const double r = rank[o * k + mid];
+          if (r > c.rank || (r == c.rank && o < b)) lo = mid + 1;
+          else hi = mid;
+        }
+        place += lo;
       }
-      place += lo;
     }
     if (place < k) {
       const int64_t at = (int64_t)req * k + place;
@@ -361,7 +416,7 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
     }
   }
   __syncthreads();
-  for (int i = (int)sh.n + t; i < k; i += kBeamBlock) {
+  for (int i = (int)sh.n[0] + t; i < k; i += kBeamBlock) {
     const int64_t at = (int64_t)req * k + i;
     q.out_scores[at] = -__builtin_inff();
     q.parents[at] = -1;
@@ -369,15 +424,28 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
   }
 }
 
+namespace {
+
+template <class T>
+const void* beam_row_ptr(int pieces) {
+  switch (pieces) {
+    case 1: return reinterpret_cast<const void*>(&beam_row_kernel<T, 1>);
+    case 2: return reinterpret_cast<const void*>(&beam_row_kernel<T, 2>);
+    case 4: return reinterpret_cast<const void*>(&beam_row_kernel<T, 4>);
+    default: return reinterpret_cast<const void*>(&beam_row_kernel<T, 16>);
+  }
+}
+
+}  // namespace
+
 const void* beam_segment_kernel_ptr(int dtype) {
   return dtype == 0 ? reinterpret_cast<const void*>(&beam_segment_kernel<float>)
          : dtype == 1 ? reinterpret_cast<const void*>(&beam_segment_kernel<__hip_bfloat16>)
                       : reinterpret_cast<const void*>(&beam_segment_kernel<__half>);
 }
-const void* beam_row_kernel_ptr(int dtype) {
-  return dtype == 0 ? reinterpret_cast<const void*>(&beam_row_kernel<float>)
-         : dtype == 1 ? reinterpret_cast<const void*>(&beam_row_kernel<__hip_bfloat16>)
-                      : reinterpret_cast<const void*>(&beam_row_kernel<__half>);
+const void* beam_row_kernel_ptr(int dtype, int pieces) {
+  return dtype == 0 ? beam_row_ptr<float>(pieces)
+         : dtype == 1 ? beam_row_ptr<__hip_bfloat16>(pieces) : beam_row_ptr<__half>(pieces);
 }
 
 }  // namespace ert

@@ -26,6 +26,7 @@ struct KeepShared {
   uint32_t wave2[kKeepWaves];
   uint32_t digit;
   uint32_t need;
+  uint32_t whole;
 };
 
 }  // namespace
@@ -33,11 +34,15 @@ struct KeepShared {
 // ---------------------------------------------------------------------------
 // One workgroup a row: the key of the last position that stays, digit by
 // digit from the top (11, 11 and 10 bits, counted in LDS), then one pass that
-// writes what stays in order, each wave its own range.
+// writes what stays in order, each wave its own range.  The row's mass sits in
+// registers, HELD values a thread, and is read once; rows longer than 1024
+// HELD are read again in every pass (HELD 0).
 // ---------------------------------------------------------------------------
+template <int HELD>
 __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams q) {
   __shared__ KeepShared sh;
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  const int t = threadIdx.x, lane = t & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
   const int req = blockIdx.x / q.heads, head = blockIdx.x - req * q.heads;
   const float* mass = q.mass + req * q.request_stride + head * q.head_stride;
   const int n = min(max(q.kv_lens[req], 0), q.positions);
@@ -56,21 +61,46 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
     return;
   }
   const int lo = q.sinks, hi = n - q.recent;   // lo < hi: sinks + recent <= budget < n
+  const int span = ((n + kKeepBlock - 1) / kKeepBlock) * 64;  // a wave's positions
+  const int w0 = wv * span, steps = span / 64;
+  float held[HELD > 0 ? HELD : 1];
+  if (HELD > 0) {
+#pragma unroll
+    for (int s = 0; s < HELD; ++s) {
+      const int i = w0 + s * 64 + lane;
+      held[s] = s < steps && i < n ? mass[i] : 0.0f;
+    }
+  }
+  // f(position, its mass) for the wave's positions in order; the same number
+  // of calls in every lane
+  auto each = [&](auto&& f) {
+    if (HELD > 0) {
+#pragma unroll
+      for (int s = 0; s < HELD; ++s)
+        if (s < steps) f(w0 + s * 64 + lane, held[s]);
+    } else {
+      for (int s = 0; s < steps; ++s) {
+        const int i = w0 + s * 64 + lane;
+        f(i, i < n ? mass[i] : 0.0f);
+      }
+    }
+  };
   uint32_t need = (uint32_t)(q.budget - q.sinks - q.recent);
+  const bool any = need > 0;
   // prefix: the digits found so far, of `bits` bits
   uint32_t prefix = 0;
   int bits = 0;
-  if (need > 0) {
+  if (any) {
 #pragma unroll 1
     for (int level = 0; level < 3; ++level) {
       const int width = level < 2 ? 11 : 10, shift = 32 - bits - width;
       for (int b = t; b < kDigitBins; b += kKeepBlock) sh.count[b] = 0;
       __syncthreads();
-      for (int i = lo + t; i < hi; i += kKeepBlock) {
-        const uint32_t key = rkey(mass[i]);
-        if (bits == 0 || (key >> (32 - bits)) == prefix)
+      each([&](int i, float m) {
+        const uint32_t key = rkey(m);
+        if (i >= lo && i < hi && (bits == 0 || (key >> (32 - bits)) == prefix))
           atomicAdd(&sh.count[(key >> shift) & ((1u << width) - 1)], 1u);
-      }
+      });
       __syncthreads();
       // from the largest digit down: thread t holds digits 2047 - 2t and 2046 - 2t
       const uint32_t a = sh.count[kDigitBins - 1 - 2 * t], b = sh.count[kDigitBins - 2 - 2 * t];
@@ -83,61 +113,54 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
       if (above < need && need <= above + a) {
         sh.digit = (uint32_t)(kDigitBins - 1 - 2 * t);
         sh.need = need - above;
+        sh.whole = need == above + a;
       } else if (above + a < need && need <= sum) {
         sh.digit = (uint32_t)(kDigitBins - 2 - 2 * t);
         sh.need = need - above - a;
+        sh.whole = need == sum;
       }
       __syncthreads();
       prefix = (prefix << width) | sh.digit;
       need = sh.need;
       bits += width;
+      if (sh.whole) break;   // all that share these digits stay
     }
   }
-  // Now `prefix` is the last key that stays, `need` how many of its positions.
-  const bool any = q.budget > q.sinks + q.recent;
-  const int span = ((n + kKeepBlock - 1) / kKeepBlock) * 64;  // a wave's positions
-  const int w0 = wv * span, w1 = min(w0 + span, n);
-  uint32_t larger = 0, even = 0;   // of this wave's
-  for (int i0 = w0; i0 < w1; i0 += 64) {
-    const int i = i0 + lane;
-    bool gt = false, eq = false;
-    if (i < w1) {
-      if (i < lo || i >= hi) {
-        gt = true;
-      } else if (any) {
-        const uint32_t key = rkey(mass[i]);
-        gt = key > prefix;
-        eq = key == prefix;
-      }
+  // Now `prefix` are the first digits of the last keys that stay, `need` how
+  // many of their positions.
+  auto side = [&](int i, float m, bool& gt, bool& eq) {
+    gt = eq = false;
+    if (i >= n) return;
+    if (i < lo || i >= hi) {
+      gt = true;
+    } else if (any) {
+      const uint32_t key = rkey(m) >> (32 - bits);
+      gt = key > prefix;
+      eq = key == prefix;
     }
+  };
+  uint32_t larger = 0, even = 0;   // of this wave's
+  each([&](int i, float m) {
+    bool gt, eq;
+    side(i, m, gt, eq);
     larger += (uint32_t)__popcll(__ballot(gt));
     even += (uint32_t)__popcll(__ballot(eq));
-  }
+  });
   if (lane == 0) {
     sh.wave[wv] = larger;
     sh.wave2[wv] = even;
   }
   __syncthreads();
   uint32_t larger_before = 0, even_before = 0;
-  for (int w = 0; w < wv; ++w) {
-    larger_before += sh.wave[w];
-    even_before += sh.wave2[w];
+#pragma unroll
+  for (int w = 0; w < kKeepWaves; ++w) {
+    larger_before += w < wv ? sh.wave[w] : 0u;
+    even_before += w < wv ? sh.wave2[w] : 0u;
   }
   uint32_t at = larger_before + min(even_before, need);
-  for (int i0 = w0; i0 < w1; i0 += 64) {
-    const int i = i0 + lane;
-    bool gt = false, eq = false;
-    float m = 0.0f;
-    if (i < w1) {
-      m = mass[i];
-      if (i < lo || i >= hi) {
-        gt = true;
-      } else if (any) {
-        const uint32_t key = rkey(m);
-        gt = key > prefix;
-        eq = key == prefix;
-      }
-    }
+  each([&](int i, float m) {
+    bool gt, eq;
+    side(i, m, gt, eq);
     const uint64_t evens = __ballot(eq);
     const uint32_t turn = even_before + __builtin_amdgcn_mbcnt_hi(
                                             (uint32_t)(evens >> 32),
@@ -152,7 +175,7 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
     }
     at += (uint32_t)__popcll(ins);
     even_before += (uint32_t)__popcll(evens);
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -227,7 +250,11 @@ __global__ void __launch_bounds__(kMoveBlock) evict_move_kernel(const MoveParams
   }
 }
 
-const void* evict_keep_kernel_ptr() { return reinterpret_cast<const void*>(&evict_keep_kernel); }
+const void* evict_keep_kernel_ptr(int64_t positions) {
+  if (positions <= 8 * kKeepBlock) return reinterpret_cast<const void*>(&evict_keep_kernel<8>);
+  if (positions <= 32 * kKeepBlock) return reinterpret_cast<const void*>(&evict_keep_kernel<32>);
+  return reinterpret_cast<const void*>(&evict_keep_kernel<0>);
+}
 const void* evict_move_kernel_ptr() { return reinterpret_cast<const void*>(&evict_move_kernel); }
 
 }  // namespace ert

@@ -39,30 +39,34 @@ __device__ __forceinline__ void store_tail(unsigned char* p, uint32_t n, const u
   if (n & 1) *p = b[14];
 }
 
-// Moves this thread's piece of a request's rows: from(j) and to(j) are child
-// j's source and target (uniform; null: none), the loads of N children ahead
-// of their stores.  With k <= N everything is read before anything is
-// written.  A null source with a target clears.
-template <int N, class From, class To>
-__device__ __forceinline__ void move_rows(int k, int64_t bytes, int64_t off, From&& from, To&& to) {
+// A number that lane j holds, in all lanes.
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int j) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), j) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, j);
+}
+
+// Moves this thread's piece of a request's rows: lane j holds child j's source
+// and target (0: none; a target without a source is cleared).  With k <= N
+// everything is read before anything is written.
+template <int N>
+__device__ __forceinline__ void move_rows(int k, int64_t bytes, int64_t off, uint64_t src, uint64_t dst) {
   const int64_t left = bytes - off;
-  if (left <= 0) return;
-  const uint32_t tail = left < 16 ? (uint32_t)left : 0u;
+  const uint32_t tail = left < 16 ? (uint32_t)max(left, (int64_t)0) : 0u;
   for (int j0 = 0; j0 < k; j0 += N) {
     uint4 v[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       v[j] = uint4{0, 0, 0, 0};
-      const unsigned char* p = j0 + j < k ? from(j0 + j) : nullptr;
-      if (p) {
+      const unsigned char* p = reinterpret_cast<const unsigned char*>(of_lane(src, j0 + j));
+      if (p && left > 0) {
         if (!tail) __builtin_memcpy(&v[j], p + off, 16);
         else v[j] = load_tail(p + off, tail);
       }
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      unsigned char* p = j0 + j < k ? to(j0 + j) : nullptr;
-      if (p) {
+      unsigned char* p = reinterpret_cast<unsigned char*>(of_lane(dst, j0 + j));
+      if (p && left > 0) {
         if (!tail) __builtin_memcpy(p + off, &v[j], 16);
         else store_tail(p + off, tail, v[j]);
       }
@@ -82,21 +86,17 @@ __global__ void __launch_bounds__(kCopyBlock) reorder_rows_kernel(const ReorderP
   const uint32_t at = blockIdx.x - c.first;
   const uint32_t req = at / c.tiles;
   const int64_t off = ((int64_t)(at - req * c.tiles) * kCopyBlock + threadIdx.x) * 16;
-  const int32_t* parents = q.parents + (int64_t)req * q.k;
-  const unsigned char* src = c.src + (int64_t)req * q.beams * c.src_stride;
-  unsigned char* dst = c.dst + (int64_t)req * q.k * c.dst_stride;
-  auto from = [&](int j) -> const unsigned char* {
-    const int p = parents[j];
-    return (unsigned)p < (unsigned)q.beams ? src + p * c.src_stride : nullptr;
-  };
-  auto to = [&](int j) -> unsigned char* {
-    const bool has = (unsigned)parents[j] < (unsigned)q.beams;
-    unsigned char* d = dst + j * c.dst_stride;
+  const int j = (int)(threadIdx.x & 63);
+  uint64_t src = 0, dst = 0;
+  if (j < q.k) {
+    const int p = q.parents[(int64_t)req * q.k + j];
+    const bool has = (unsigned)p < (unsigned)q.beams;
+    if (has) src = (uint64_t)(c.src + ((int64_t)req * q.beams + p) * c.src_stride);
+    dst = (uint64_t)(c.dst + ((int64_t)req * q.k + j) * c.dst_stride);
     // nothing to do for a row that stays where it is
-    if (!has ? !q.clear : d == src + parents[j] * c.src_stride) return nullptr;
-    return d;
-  };
-  move_rows<N>(q.k, c.row_bytes, off, from, to);
+    if (has ? dst == src : !q.clear) src = dst = 0;
+  }
+  move_rows<N>(q.k, c.row_bytes, off, src, dst);
 }
 
 // Table rows and open blocks.  The launch's first workgroups copy: a request's
@@ -111,54 +111,51 @@ __global__ void __launch_bounds__(kCopyBlock) reorder_blocks_kernel(const Reorde
   const uint32_t unit = (copy ? w : w - copying) / per;
   const uint32_t tile = (copy ? w : w - copying) - unit * per;
   const uint32_t req = copy ? unit % (uint32_t)q.requests : unit;
-  const int32_t* parents = q.parents + (int64_t)req * q.k;
   const int32_t* tables = q.tables + (int64_t)req * q.beams * q.table_stride;
-  const int32_t* tail = q.tail ? q.tail + (int64_t)req * q.k : nullptr;
   const uint32_t len = (uint32_t)max(q.kv_lens[req], 0);
   const uint32_t full = q.by_block(len), part = len - full * (uint32_t)q.block_size;
   const bool open = part > 0 && full < (uint32_t)q.max_blocks;
-  // the block that child j's open one becomes
-  auto own = [&](int j) { return tail ? tail[j] : tables[j * q.table_stride + full]; };
+  // lane j: child j
+  const int j = (int)(threadIdx.x & 63);
+  const int parent = j < q.k ? q.parents[(int64_t)req * q.k + j] : -1;
+  const bool has = (unsigned)parent < (unsigned)q.beams;
   if (copy) {
     if (!open) return;
     unsigned char* cache = q.cache[unit / (uint32_t)q.requests];
-    auto block = [&](int32_t b) -> unsigned char* {
-      return b >= 0 && b < q.num_blocks ? cache + b * q.block_stride : nullptr;
-    };
-    auto from = [&](int j) -> const unsigned char* {
-      const int p = parents[j];
-      return (unsigned)p < (unsigned)q.beams ? block(tables[p * q.table_stride + full]) : nullptr;
-    };
-    auto to = [&](int j) -> unsigned char* {
-      const unsigned char* f = from(j);
-      unsigned char* d = f ? block(own(j)) : nullptr;
-      return d == f ? nullptr : d;
-    };
+    uint64_t src = 0, dst = 0;
+    if (has) {
+      const int32_t from = tables[parent * q.table_stride + full];
+      // the block that the child's open one becomes
+      const int32_t own = q.tail ? q.tail[(int64_t)req * q.k + j] : tables[j * q.table_stride + full];
+      if (from >= 0 && from < q.num_blocks && own >= 0 && own < q.num_blocks && own != from) {
+        src = (uint64_t)(cache + from * q.block_stride);
+        dst = (uint64_t)(cache + own * q.block_stride);
+      }
+    }
     const int64_t bytes = (int64_t)part * q.slot_bytes;
-    for (int64_t off = ((int64_t)tile * kCopyBlock + threadIdx.x) * 16; off < bytes;
-         off += (int64_t)q.tiles * kCopyBlock * 16)
-      move_rows<N>(q.k, bytes, off, from, to);
+    for (int64_t off = (int64_t)tile * kCopyBlock * 16; off < bytes; off += (int64_t)q.tiles * kCopyBlock * 16)
+      move_rows<N>(q.k, bytes, off + threadIdx.x * 16, src, dst);
     return;
   }
   const uint32_t e = tile * kCopyBlock + threadIdx.x;
-  if (e >= (uint32_t)q.max_blocks) return;
+  const int own = has && open && q.tail ? q.tail[(int64_t)req * q.k + j] : -1;
   int32_t* out = q.out + (int64_t)req * q.k * q.out_stride + e;
-  const bool rows_stay = q.beams == q.k;
+  const bool rows_stay = q.beams == q.k, inside = e < (uint32_t)q.max_blocks;
   for (int j0 = 0; j0 < q.k; j0 += N) {
     int32_t v[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v[j] = -1;
-      if (j0 + j >= q.k) continue;
-      const int p = parents[j0 + j];
-      const bool has = (unsigned)p < (unsigned)q.beams;
-      if (has && e < full) v[j] = tables[p * q.table_stride + e];
-      else if (has && open && e == full && tail) v[j] = tail[j0 + j];
-      else if (rows_stay) v[j] = tables[(j0 + j) * q.table_stride + e];
+    for (int i = 0; i < N; ++i) {
+      v[i] = -1;
+      const int p = __builtin_amdgcn_readlane(parent, j0 + i), tail = __builtin_amdgcn_readlane(own, j0 + i);
+      if (j0 + i >= q.k || !inside) continue;
+      const bool child = (unsigned)p < (unsigned)q.beams;
+      if (child && e < full) v[i] = tables[p * q.table_stride + e];
+      else if (child && open && e == full && q.tail) v[i] = tail;
+      else if (rows_stay) v[i] = tables[(j0 + i) * q.table_stride + e];
     }
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (j0 + j < q.k) out[(j0 + j) * q.out_stride] = v[j];
+    for (int i = 0; i < N; ++i)
+      if (j0 + i < q.k && inside) out[(j0 + i) * q.out_stride] = v[i];
   }
 }
 

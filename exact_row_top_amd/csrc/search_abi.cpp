@@ -12,13 +12,13 @@
 
 namespace ert {
 const void* beam_segment_kernel_ptr(int dtype);
-const void* beam_row_kernel_ptr(int dtype);
+const void* beam_row_kernel_ptr(int dtype, int pieces);
 const void* reorder_rows_kernel_ptr(int n);
 const void* reorder_blocks_kernel_ptr(int n);
 const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int block_size);
 const void* attend_join_kernel_ptr(int dtype, int dim);
 const void* attend_mass_kernel_ptr(int dtype, int dim);
-const void* evict_keep_kernel_ptr();
+const void* evict_keep_kernel_ptr(int64_t positions);
 const void* evict_move_kernel_ptr();
 }  // namespace ert
 
@@ -43,10 +43,17 @@ bool clear_of(const void* a, uint64_t na, const void* b, uint64_t nb) {
 
 int64_t beam_segments(int32_t vocab) { return ((int64_t)vocab + kSegment - 1) / kSegment; }
 
-// Chunks that a row's threads can find above the k-th largest of their own
-// maxima (fewer than k threads hold any), and each wave's first k that equal it.
+// Chunk maxima that a thread holds, in 16-byte pieces.
+int beam_pieces(int64_t segments) {
+  const int64_t n = (segments * 64 + 4 * kBeamBlock - 1) / (4 * kBeamBlock);
+  return n <= 1 ? 1 : (n <= 2 ? 2 : (n <= 4 ? 4 : 16));
+}
+
+// Chunks that a row can list: above the k-th largest of the threads' own
+// maxima lie those of fewer than k threads, and each wave lists its first k
+// that equal it.
 int64_t beam_cap(int64_t segments, int32_t k) {
-  return (int64_t)(k - 1) * ((segments * 64 / (kBeamBlock / 64) + 63) / 64) + (int64_t)k * (kBeamBlock / 64);
+  return (int64_t)(k - 1) * beam_pieces(segments) * 4 + (int64_t)k * (kBeamBlock / 64);
 }
 
 struct AttendPlan {
@@ -224,10 +231,10 @@ int topk_beams(const void* logits, int32_t dtype, int64_t row_stride, int32_t vo
   p.parents = parents;
   p.tokens = tokens;
   p.found = static_cast<BeamCandidate*>(workspace);
-  p.masses = reinterpret_cast<uint64_t*>(p.found + rows * k);
+  p.chunks = reinterpret_cast<float*>(p.found + rows * k);
+  p.masses = reinterpret_cast<uint64_t*>(p.chunks + rows * segments * 64);
   p.bests = reinterpret_cast<float*>(p.masses + rows * segments);
-  p.chunks = p.bests + rows * segments;
-  p.arrived = reinterpret_cast<uint32_t*>(p.chunks + rows * segments * 64);
+  p.arrived = reinterpret_cast<uint32_t*>(p.bests + rows * segments);
   p.cap = (int32_t)beam_cap(segments, k);
   rc = launch(beam_segment_kernel_ptr(dtype), (rows * segments + 3) / 4, 256, &p, 0, stream);
   if (rc != TOPK_OK) return rc;
@@ -235,7 +242,7 @@ int topk_beams(const void* logits, int32_t dtype, int64_t row_stride, int32_t vo
   const size_t gather = (size_t)k * kChunk * 8, merge = (size_t)beams * k * 16;
   lds = lds > gather ? lds : gather;
   lds = lds > merge ? lds : merge;
-  return launch(beam_row_kernel_ptr(dtype), rows, kBeamBlock, &p, lds, stream);
+  return launch(beam_row_kernel_ptr(dtype, beam_pieces(segments)), rows, kBeamBlock, &p, lds, stream);
 }
 
 int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* const* targets,
@@ -548,7 +555,7 @@ int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stri
   p.mass_out = mass_out;
   p.out_positions = out_positions;
   p.new_lens = new_lens;
-  return launch(evict_keep_kernel_ptr(), rows, kKeepBlock, &p, 0, stream);
+  return launch(evict_keep_kernel_ptr(positions), rows, kKeepBlock, &p, 0, stream);
 }
 
 int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads, int32_t budget,
