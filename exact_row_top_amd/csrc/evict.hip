@@ -179,15 +179,21 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
 }
 
 // ---------------------------------------------------------------------------
-// Moves the kept rows, 16 bytes a thread, a step of rows at a time: all of a
-// step's loads are done before its first store, and a later step reads
-// positions behind everything that was stored (kept[j] >= j), so source and
-// target may be the same blocks.  parts > 1 only where they are not.
+// Moves the kept rows, 16 bytes a thread, a step of rows at a time.  In place,
+// all of a step's loads are done before its first store, and a later step
+// reads positions behind everything that was stored (kept[j] >= j); between
+// different blocks nothing waits, and workgroups share a row's positions.
+//
+// Bound by memory: rows of 256 bytes from all over a cache.  Four rows in
+// flight a thread: 16 x 8192 positions to 1024, 8 heads of 256 bytes, two
+// caches, 134 MB from and to memory, 56 us with the choice; with 8 rows 68,
+// with 16 (fewer waves) 124.
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int kMoveRows = 8;   // rows in flight a thread
+constexpr int kMoveRows = 4;   // rows in flight a thread
 }
 
+template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveBlock) evict_move_kernel(const MoveParams q) {
   uint32_t id = blockIdx.x;
   const int part = (int)(id % (uint32_t)q.parts);
@@ -240,12 +246,14 @@ __global__ void __launch_bounds__(kMoveBlock) evict_move_kernel(const MoveParams
           }
         }
       }
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // the loads are done
-      __syncthreads();
+      if (IN_PLACE) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // the loads are done
+        __syncthreads();
+      }
 #pragma unroll
       for (int i = 0; i < kMoveRows; ++i)
         if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = v[i];
-      __syncthreads();
+      if (IN_PLACE) __syncthreads();
     }
   }
 }
@@ -255,6 +263,9 @@ const void* evict_keep_kernel_ptr(int64_t positions) {
   if (positions <= 32 * kKeepBlock) return reinterpret_cast<const void*>(&evict_keep_kernel<32>);
   return reinterpret_cast<const void*>(&evict_keep_kernel<0>);
 }
-const void* evict_move_kernel_ptr() { return reinterpret_cast<const void*>(&evict_move_kernel); }
+const void* evict_move_kernel_ptr(bool in_place) {
+  return in_place ? reinterpret_cast<const void*>(&evict_move_kernel<true>)
+                  : reinterpret_cast<const void*>(&evict_move_kernel<false>);
+}
 
 }  // namespace ert

@@ -19,7 +19,7 @@ const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int block_siz
 const void* attend_join_kernel_ptr(int dtype, int dim);
 const void* attend_mass_kernel_ptr(int dtype, int dim);
 const void* evict_keep_kernel_ptr(int64_t positions);
-const void* evict_move_kernel_ptr();
+const void* evict_move_kernel_ptr(bool in_place);
 }  // namespace ert
 
 using namespace ert;
@@ -605,13 +605,14 @@ int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads
   while (columns > 1 && rows * columns > 4096) columns = (columns + 1) / 2;
   p.columns = (int32_t)columns;
   int64_t parts = 1;
-  if (block_tables != out_tables) {
-    parts = 2048 / (rows * columns);
-    const int64_t most = ((int64_t)budget + 127) / 128;
+  const bool in_place = block_tables == out_tables;
+  if (!in_place) {
+    parts = 8192 / (rows * columns);
+    const int64_t most = ((int64_t)budget + 63) / 64;
     parts = parts < 1 ? 1 : (parts > most ? most : parts);
   }
   p.parts = (int32_t)parts;
-  return launch(evict_move_kernel_ptr(), rows * columns * parts, kMoveBlock, &p, 0, stream);
+  return launch(evict_move_kernel_ptr(in_place), rows * columns * parts, kMoveBlock, &p, 0, stream);
 }
 
 }  // extern "C"
