@@ -63,44 +63,56 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
   const int lo = q.sinks, hi = n - q.recent;   // lo < hi: sinks + recent <= budget < n
   const int span = ((n + kKeepBlock - 1) / kKeepBlock) * 64;  // a wave's positions
   const int w0 = wv * span, steps = span / 64;
+  // Keys: what always stays is above all masses (the largest of which is
+  // 0xFF800000); NaN and what is behind the last position are zero.
+  auto key_of = [&](int i, float m) { return i >= n ? 0u : (i < lo || i >= hi ? ~0u : rkey(m)); };
   float held[HELD > 0 ? HELD : 1];
+  uint32_t keys[HELD > 0 ? HELD : 1];
   if (HELD > 0) {
 #pragma unroll
     for (int s = 0; s < HELD; ++s) {
       const int i = w0 + s * 64 + lane;
       held[s] = s < steps && i < n ? mass[i] : 0.0f;
     }
+#pragma unroll
+    for (int s = 0; s < HELD; ++s) keys[s] = key_of(w0 + s * 64 + lane, held[s]);
   }
-  // f(position, its mass) for the wave's positions in order; the same number
-  // of calls in every lane
+  // f(position, its mass, its key) for the wave's positions in order; the same
+  // number of calls in every lane
   auto each = [&](auto&& f) {
     if (HELD > 0) {
 #pragma unroll
       for (int s = 0; s < HELD; ++s)
-        if (s < steps) f(w0 + s * 64 + lane, held[s]);
+        if (s < steps) f(w0 + s * 64 + lane, held[s], keys[s]);
     } else {
       for (int s = 0; s < steps; ++s) {
         const int i = w0 + s * 64 + lane;
-        f(i, i < n ? mass[i] : 0.0f);
+        const float m = i < n ? mass[i] : 0.0f;
+        f(i, m, key_of(i, m));
       }
     }
   };
   uint32_t need = (uint32_t)(q.budget - q.sinks - q.recent);
-  const bool any = need > 0;
-  // prefix: the digits found so far, of `bits` bits
-  uint32_t prefix = 0;
-  int bits = 0;
-  if (any) {
+  // prefix: the digits found so far, all but the lowest `below` bits
+  uint32_t prefix = need > 0 ? 0u : ~1u;
+  int below = need > 0 ? 32 : 0;
+  if (need > 0) {
 #pragma unroll 1
     for (int level = 0; level < 3; ++level) {
-      const int width = level < 2 ? 11 : 10, shift = 32 - bits - width;
+      const int width = level < 2 ? 11 : 10, shift = below - width;
       for (int b = t; b < kDigitBins; b += kKeepBlock) sh.count[b] = 0;
       __syncthreads();
-      each([&](int i, float m) {
-        const uint32_t key = rkey(m);
-        if (i >= lo && i < hi && (bits == 0 || (key >> (32 - bits)) == prefix))
-          atomicAdd(&sh.count[(key >> shift) & ((1u << width) - 1)], 1u);
+      // Positions without any mass count in registers first: their adds to one
+      // address would wait for each other.
+      uint32_t zeros = 0;
+      each([&](int i, float m, uint32_t key) {
+        if (i >= lo && i < hi && (level == 0 || (key >> (below & 31)) == prefix)) {
+          if (m == 0.0f) ++zeros;
+          else atomicAdd(&sh.count[(key >> shift) & ((1u << width) - 1)], 1u);
+        }
       });
+      zeros = wave_sum(zeros);
+      if (lane == 0 && zeros) atomicAdd(&sh.count[(rkey(0.0f) >> shift) & ((1u << width) - 1)], zeros);
       __syncthreads();
       // from the largest digit down: thread t holds digits 2047 - 2t and 2046 - 2t
       const uint32_t a = sh.count[kDigitBins - 1 - 2 * t], b = sh.count[kDigitBins - 2 - 2 * t];
@@ -122,30 +134,29 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
       __syncthreads();
       prefix = (prefix << width) | sh.digit;
       need = sh.need;
-      bits += width;
+      below = shift;
       if (sh.whole) break;   // all that share these digits stay
     }
   }
   // Now `prefix` are the first digits of the last keys that stay, `need` how
   // many of their positions.
-  auto side = [&](int i, float m, bool& gt, bool& eq) {
-    gt = eq = false;
-    if (i >= n) return;
-    if (i < lo || i >= hi) {
-      gt = true;
-    } else if (any) {
-      const uint32_t key = rkey(m) >> (32 - bits);
-      gt = key > prefix;
-      eq = key == prefix;
+  uint32_t counts = 0;   // this lane's larger ones, and from bit 16 on its even ones
+  uint32_t larger = 0, even = 0;
+  each([&](int i, float, uint32_t key) {
+    const uint32_t d = key >> below;
+    if (HELD > 0) {
+      counts += (d > prefix ? 1u : 0u) + (d == prefix && i < n ? 0x10000u : 0u);
+    } else {
+      larger += d > prefix ? 1u : 0u;
+      even += d == prefix && i < n ? 1u : 0u;
     }
-  };
-  uint32_t larger = 0, even = 0;   // of this wave's
-  each([&](int i, float m) {
-    bool gt, eq;
-    side(i, m, gt, eq);
-    larger += (uint32_t)__popcll(__ballot(gt));
-    even += (uint32_t)__popcll(__ballot(eq));
   });
+  if (HELD > 0) {
+    counts = wave_sum(counts);
+    larger = counts & 0xFFFFu, even = counts >> 16;
+  } else {
+    larger = wave_sum(larger), even = wave_sum(even);
+  }
   if (lane == 0) {
     sh.wave[wv] = larger;
     sh.wave2[wv] = even;
@@ -158,15 +169,19 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
     even_before += w < wv ? sh.wave2[w] : 0u;
   }
   uint32_t at = larger_before + min(even_before, need);
-  each([&](int i, float m) {
-    bool gt, eq;
-    side(i, m, gt, eq);
-    const uint64_t evens = __ballot(eq);
-    const uint32_t turn = even_before + __builtin_amdgcn_mbcnt_hi(
-                                            (uint32_t)(evens >> 32),
-                                            __builtin_amdgcn_mbcnt_lo((uint32_t)evens, 0u));
-    const bool in = gt || (eq && turn < need);
+  each([&](int i, float m, uint32_t key) {
+    const uint32_t d = key >> below;
+    bool in = d > prefix;
+    const uint64_t evens = __ballot(d == prefix && i < n);
+    if (evens) {
+      const uint32_t turn = even_before + __builtin_amdgcn_mbcnt_hi(
+                                              (uint32_t)(evens >> 32),
+                                              __builtin_amdgcn_mbcnt_lo((uint32_t)evens, 0u));
+      in = in || ((evens >> lane & 1) && turn < need);
+      even_before += (uint32_t)__popcll(evens);
+    }
     const uint64_t ins = __ballot(in);
+    if (!ins) return;
     const uint32_t j = at + __builtin_amdgcn_mbcnt_hi(
                                 (uint32_t)(ins >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)ins, 0u));
     if (in) {
@@ -174,7 +189,6 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
       if (out) out[j] = m;
     }
     at += (uint32_t)__popcll(ins);
-    even_before += (uint32_t)__popcll(evens);
   });
 }
 
