@@ -772,99 +772,153 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) 
 
 // ---------------------------------------------------------------------------
 // Attention mass: mass[h][p] = decay mass[h][p] + the weights of position p in
-// every query of key head h.  A wave holds 32 keys and runs over the entry's
-// queries, 32 at a time; each lane adds up its query column's weights, and the
-// 32 columns are added at the end, so sums have one order.
+// every query of key head h.  A wave holds two tiles of 32 keys and runs over
+// the entry's queries, 32 at a time; each lane adds up its query column's
+// weights, and the 32 columns are added at the end, so sums have one order.
+// The next tiles are on their way while these are added up and written.
 // ---------------------------------------------------------------------------
+namespace {
+
+// The sum over a half wave, in all its lanes.
+__device__ __forceinline__ float half_sum(float v) {
+  auto add = [&](auto ctl) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctl)::value, 0xf, 0xf, true));
+  };
+  add(std::integral_constant<int, 0xB1>{});    // neighbours: quad_perm 1 0 3 2
+  add(std::integral_constant<int, 0x4E>{});    // quad_perm 2 3 0 1
+  add(std::integral_constant<int, 0x141>{});   // row_half_mirror
+  add(std::integral_constant<int, 0x140>{});   // row_mirror
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+}  // namespace
+
 template <class T, int DIM>
-__global__ void __launch_bounds__(kMassBlock) attend_mass_kernel(const MassParams mp) {
-  constexpr int STEPS = DIM / 16;
+__global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassParams mp) {
+  constexpr int STEPS = DIM / 16, TILES = kMassTiles, PAIR = 2;
   const AttendParams& q = mp.a;
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t id = blockIdx.x;
-  const bool shared = id < mp.shared_wgs;
-  if (!shared) id -= mp.shared_wgs;
-  const int tiles = shared ? mp.shared_tiles : mp.own_tiles;
-  const int tile = (int)(id % tiles);
-  id /= tiles;
-  Share s;
-  s.head = (int)(id % q.kv_heads);
-  const int entry = (int)(id / q.kv_heads);
+  uint32_t id = blockIdx.x;
+  const bool shared = id < (uint32_t)mp.shared_wgs;
+  if (!shared) id -= (uint32_t)mp.shared_wgs;
+  const uint32_t parts = (uint32_t)(shared ? mp.shared_tiles : mp.own_tiles);
+  const int part = (int)(id % parts);
+  id /= parts;
+  const int head = (int)(id % (uint32_t)q.kv_heads);
+  const int entry = (int)(id / (uint32_t)q.kv_heads);
   const int row_len = shared ? mp.shared_width : mp.own_width;
   const PageTables& pt = shared ? q.shared : q.own;
-  s.table = pt.tables + (int64_t)entry * pt.stride;
-  s.len = min(max(pt.lens[entry], 0), pt.limit);
+  const int32_t* table = pt.tables + (int64_t)entry * pt.stride;
+  const int len = min(max(pt.lens[entry], 0), pt.limit);
+  int seq0 = entry, seqs = 1, cut = q.next_n - 1;
   if (shared) {
     int s1;
-    group_range(q, entry, s.seq0, s1);
-    s.rows = (s1 - s.seq0) * q.next_n * q.per;
-    s.cut = 0;
-  } else {
-    s.seq0 = entry;
-    s.rows = q.next_n * q.per;
-    s.cut = q.next_n - 1;
+    group_range(q, entry, seq0, s1);
+    seqs = s1 - seq0;
+    cut = 0;
   }
-  const int p0 = (tile * (kMassBlock / 64) + wv) * kKeyTile;
-  if (p0 >= row_len) return;
-  float acc[16];
+  const int rows = seqs * q.next_n * q.per;
+  // this wave's tiles: every fourth of the workgroup's
+  auto first_of = [&](int i) { return ((part * TILES + i) * (kMassBlock / 64) + wv) * kKeyTile; };
+  if (first_of(0) >= row_len) return;
+
+  int32_t block[TILES];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  if (p0 < s.len) {
-    Piece key[STEPS];
-    const int p = p0 + col;
-    const int32_t b = p < s.len ? block_at(q, s.table, pt.width, p) : -1;
-    const uint32_t off = (uint32_t)p - q.by_block((uint32_t)p) * (uint32_t)q.block_size;
-    const unsigned char* a = q.k.base + s.head * q.k.head_stride + half * 16 +
-                             (b >= 0 ? (uint64_t)b * q.k.block_stride + (uint64_t)off * q.k.slot_stride : 0);
+  for (int i = 0; i < TILES; ++i) {
+    const int p = first_of(i) + col;
+    block[i] = p < len ? block_at(q, table, pt.width, p) : -1;
+  }
+  Piece key[PAIR][STEPS], query[STEPS];
+  uint64_t live[PAIR];
+  auto load_keys = [&](int i0) {
 #pragma unroll
-    for (int d = 0; d < STEPS; ++d) key[d] = *reinterpret_cast<const Piece*>(a + d * 32);
-    const uint64_t live = __ballot(b >= 0);
-    for (int r0 = 0; r0 < s.rows; r0 += 32) {
-      const int r = r0 + col;
-      const bool has = r < s.rows;
-      const int rr = has ? r : 0;
-      const int tok = rr / q.per, sub = rr - tok * q.per;
-      const int64_t row = (int64_t)s.seq0 * q.next_n + tok;
-      const int head = s.head * q.per + sub;
-      const unsigned char* at = q.q + row * q.q_stride + head * q.q_head_stride + half * 16;
-      Piece query[STEPS];
+    for (int i = 0; i < PAIR; ++i) {
+      const int32_t b = block[i0 + i];
+      const uint32_t p = (uint32_t)(first_of(i0 + i) + col);
+      const uint32_t off = p - q.by_block(p) * (uint32_t)q.block_size;
+      const unsigned char* a = q.k.base + head * q.k.head_stride + half * 16 +
+                               (b >= 0 ? (uint64_t)b * q.k.block_stride + (uint64_t)off * q.k.slot_stride : 0);
+      live[i] = __ballot(b >= 0);
+      if (live[i]) {
 #pragma unroll
-      for (int d = 0; d < STEPS; ++d) query[d] = *reinterpret_cast<const Piece*>(at + d * 32);
-      // a row that saw nothing has a sum of nothing: its weights are none
-      float lse = mp.lse[row * q.heads + head];
-      const bool on = has && lse > kNone;
-      lse = on ? lse * 1.44269504f : 0.0f;
-      const int sees = s.len - s.cut + (s.cut ? tok % q.next_n : 0);
-      const int ahead = on ? min(max(sees - (p0 + 4 * half), 0), 31) : 0;
-      const uint32_t seen = (uint32_t)(live >> (4 * half)) & ((1u << ahead) - 1u);
-      f32x16 sc;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sc[i] = 0.0f;
-#pragma unroll
-      for (int d = 0; d < STEPS; ++d) sc = T::mfma(key[d], query[d], sc);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], q.scale, -lse));
-        acc[i] += seen >> (8 * (i / 4) + i % 4) & 1 ? w : 0.0f;
+        for (int d = 0; d < STEPS; ++d) key[i][d] = *reinterpret_cast<const Piece*>(a + d * 32);
       }
     }
+  };
+  // queries r0 .. r0 + 31: this lane's, its log-sum and the positions it sees
+  float lse = 0.0f;
+  int sees = 0;
+  auto load_queries = [&](int r0) {
+    const int r = r0 + col;
+    const uint32_t rr = r < rows ? (uint32_t)r : 0u;
+    const uint32_t tok = rr / (uint32_t)q.per, sub = rr - tok * (uint32_t)q.per;
+    const int64_t row = (int64_t)seq0 * q.next_n + tok;
+    const unsigned char* at = q.q + row * q.q_stride + (head * q.per + sub) * q.q_head_stride + half * 16;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) acc[i] += __shfl_xor(acc[i], d);
+    for (int d = 0; d < STEPS; ++d) query[d] = *reinterpret_cast<const Piece*>(at + d * 32);
+    lse = mp.lse[row * q.heads + head * q.per + sub];
+    // a row that saw nothing has a sum of nothing: its weights are none
+    const bool on = r < rows && lse > kNone;
+    lse = on ? lse * 1.44269504f : 0.0f;
+    sees = on ? len - cut + (cut ? (int)(tok % (uint32_t)q.next_n) : 0) : 0;
+  };
+  if (rows > 0 && first_of(0) < len) {
+    load_keys(0);
+    load_queries(0);
   }
-  // lane j of the first 32 writes position j
-  const int64_t base = ((int64_t)entry * q.kv_heads + s.head) * row_len + p0;
   const float* in = shared ? mp.shared_in : mp.own_in;
   float* out = shared ? mp.shared_out : mp.own_out;
-  float mine = 0.0f;
-  // position j = 8 (i / 4) + 4 h + i % 4 is held by half h: lane c of half h
-  // takes register c % 16 if c < 16
+  const int64_t base = ((int64_t)entry * q.kv_heads + head) * row_len;
+  // register i of a half is position 8 (i / 4) + 4 half + i % 4: lane i of the
+  // half writes it
+  const int mine = 8 * (col / 4) + 4 * half + col % 4;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) mine = col == i ? acc[i] : mine;
-  const int j = 8 * (col / 4) + 4 * half + col % 4;
-  if (col < 16 && p0 + j < row_len) out[base + j] = (in ? in[base + j] * mp.decay : 0.0f) + mine;
+  for (int i0 = 0; i0 < TILES; i0 += PAIR) {
+    if (first_of(i0) >= row_len) break;
+    float old[PAIR], acc[PAIR][16];
+#pragma unroll
+    for (int i = 0; i < PAIR; ++i) {
+      const int p = first_of(i0 + i) + mine;
+      old[i] = in && col < 16 && p < row_len ? in[base + p] : 0.0f;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) acc[i][x] = 0.0f;
+    }
+    if (rows > 0 && first_of(i0) < len) {
+      for (int r0 = 0; r0 < rows; r0 += 32) {
+        if (r0 > 0 || (i0 > 0 && rows > 32)) load_queries(r0);
+#pragma unroll
+        for (int i = 0; i < PAIR; ++i) {
+          if (!live[i]) continue;
+          const int ahead = min(max(sees - (first_of(i0 + i) + 4 * half), 0), 31);
+          const uint32_t seen = (uint32_t)(live[i] >> (4 * half)) & ((1u << ahead) - 1u);
+          f32x16 sc;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) sc[x] = 0.0f;
+#pragma unroll
+          for (int d = 0; d < STEPS; ++d) sc = T::mfma(key[i][d], query[d], sc);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x], q.scale, -lse));
+            acc[i][x] += seen >> (8 * (x / 4) + x % 4) & 1 ? w : 0.0f;
+          }
+        }
+      }
+      if (i0 + PAIR < TILES && first_of(i0 + PAIR) < len) load_keys(i0 + PAIR);
+    }
+#pragma unroll
+    for (int i = 0; i < PAIR; ++i) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float v = half_sum(acc[i][x]);
+        sum = col == x ? v : sum;
+      }
+      const int p = first_of(i0 + i) + mine;
+      if (col < 16 && p < row_len) out[base + p] = old[i] * mp.decay + sum;
+    }
+  }
 }
 
 namespace {

@@ -108,6 +108,7 @@ struct ReorderBlocksParams {
 
 constexpr int kKeyTile = 32;        // keys of a score tile
 constexpr int kMassBlock = 256;
+constexpr int kMassTiles = 4;       // key tiles of a wave of the mass kernel
 constexpr int kOwnSets = 4;         // waves that take turns at the keys of up to 32 queries
 
 // Pages of one cache: position p of a table row lies in block table[p / size]

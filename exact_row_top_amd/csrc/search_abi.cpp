@@ -26,7 +26,7 @@ using namespace ert;
 
 namespace {
 
-constexpr int64_t kMassStep = kKeyTile * kMassBlock / 64;  // positions of a workgroup
+constexpr int64_t kMassStep = kKeyTile * kMassTiles * kMassBlock / 64;  // positions of a workgroup
 constexpr int64_t kInt = ((int64_t)1 << 31) - 1;
 
 Quotient quotient_of(uint32_t d) {
