@@ -7,10 +7,9 @@
 // the order is that of the logits, so its own k best logits are all that can
 // be chosen, and the sum of exponentials is one number a beam.
 //
-// The sum's weights are whole multiples of 2^-43 of a segment's largest, added
-// up exactly, and segments are counted from the row's own start whatever its
-// alignment: rows with the same scores have the same sum to the bit, and ties
-// between them go to the lower index.
+// The sum is made in 64 bits, in one order that is counted from the row's own
+// start whatever its alignment: rows with the same scores have the same sum to
+// the bit, and ties between them go to the lower index.
 //
 // Two launches: the segment kernel reads the logits once, the row kernel finds
 // each beam's k best and, in a request's last workgroup, the request's.
@@ -31,6 +30,38 @@ __device__ __forceinline__ uint4 load16(const unsigned char* p) {
   __builtin_memcpy(&v, p, 16);
   return v;
 }
+
+// 2^s for s <= 0 (-1000 and less, and NaN, as 2^-1000): interpolation of 2^f at the
+// nine Chebyshev nodes of [-1/2, 1/2], relative error at most 2^-39.7, and 1
+// for s = 0.  Adding 1.5 * 2^52 rounds s to a whole n, which then stands in the
+// sum's low bits and is added to the result's exponent.  (The coefficients in
+// scalar registers, as in Exp2Poly.)
+struct Exp2Short {
+  double k1, k2, k3, k4, k5, k6, k7, k8;
+  __device__ __forceinline__ Exp2Short()
+      : k1(0x1.62e42fef84cf0p-1), k2(0x1.ebfbdff823cedp-3), k3(0x1.c6b08dd6fd234p-5),
+        k4(0x1.3b2ab7181b755p-7), k5(0x1.5d8745a728441p-10), k6(0x1.4308ac85aa947p-13),
+        k7(0x1.00dc4a532fb8ep-16), k8(0x1.63d136366db24p-20) {
+    asm("" : "+s"(k1), "+s"(k2), "+s"(k3), "+s"(k4));
+    asm("" : "+s"(k5), "+s"(k6), "+s"(k7), "+s"(k8));
+  }
+  __device__ __forceinline__ double operator()(double s) const {
+    const double magic = 6755399441055744.0;
+    s = __builtin_fmax(s, -1000.0);
+    const double sm = s + magic, f = s - (sm - magic);
+    double p = __builtin_fma(f, k8, k7);
+    p = __builtin_fma(p, f, k6);
+    p = __builtin_fma(p, f, k5);
+    p = __builtin_fma(p, f, k4);
+    p = __builtin_fma(p, f, k3);
+    p = __builtin_fma(p, f, k2);
+    p = __builtin_fma(p, f, k1);
+    p = __builtin_fma(p, f, 1.0);
+    const uint64_t bits = (uint64_t)__double_as_longlong(p);
+    return __hiloint2double((int)((uint32_t)(bits >> 32) + ((uint32_t)__double_as_longlong(sm) << 20)),
+                            (int)(uint32_t)bits);
+  }
+};
 
 __device__ __forceinline__ bool offers(float score) { return __builtin_fabsf(score) < __builtin_inff(); }
 
@@ -89,29 +120,30 @@ __global__ void __launch_bounds__(256) beam_segment_kernel(const BeamParams q) {
   wave_minmax(low, best);
   q.chunks[(int64_t)id * 64 + (lane & (L - 1)) * (64 / L) + lane / L] = mine;
 
-  uint64_t mass = 0;
+  double mass = 0.0;
   if (best == __builtin_inff()) {
     uint32_t n = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int e = 0; e < V; ++e) n += x[g][e] == best ? 1u : 0u;
-    mass = wave_sum((uint64_t)n * kOne);
+    mass = (double)wave_sum(n);
   } else if (best > -__builtin_inff()) {
     // (four scores at a time: with more in flight the registers leave room
     // for fewer waves)
-    const Weigher w(best, kLog2e);
+    const Exp2Short exp2;
+    const double base = -(double)best * kLog2e;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        mass += w.raw(x[g][e]);
+        mass += exp2(__builtin_fma((double)x[g][e], kLog2e, base));
         if (e % 4 == 3) {
           asm("" : "+v"(mass));
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-    mass = wave_sum(mass - (uint64_t)(G * V) * kRaw);
+    mass = wave_sum(mass);
   }
   if (lane == 0) {
     q.bests[id] = best;
@@ -313,17 +345,17 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
       if (wv == 1) {
         // the row's sum, segment by segment in one order
         const float* bests = q.bests + (int64_t)row * segs;
-        const uint64_t* masses = q.masses + (int64_t)row * segs;
+        const double* masses = q.masses + (int64_t)row * segs;
         const Exp2Poly poly;
         double sum = 0.0;
         for (int s = lane; s < segs; s += 64) {
           const float b = bests[s];
           const double w = b == m ? 1.0 : exp2_64(((double)b - (double)m) * kLog2e, poly);
-          sum += (double)masses[s] * w;
+          sum += w > 0.0 ? masses[s] * w : 0.0;
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-        sum = log(sum * 0x1p-43);
+        sum = log(sum);
         if (lane == 0) sh.lse = m == __builtin_inff() ? sum : (double)m + sum;
       }
       __syncthreads();

@@ -46,7 +46,7 @@ struct BeamParams {
   float* out_scores;         // [requests][k]
   int32_t* parents;
   int32_t* tokens;
-  uint64_t* masses;          // [rows][segments]: a segment's weights against its best
+  double* masses;            // [rows][segments]: a segment's weights against its best
   float* bests;              // [rows][segments]
   float* chunks;             // [rows][segments * 64]: the largest of 32 neighbours
   BeamCandidate* found;      // [rows][k]

@@ -72,7 +72,9 @@ bool attend_plan(int32_t groups, int32_t seqs, bool ragged, int32_t next_n, int3
   p.query_waves = group_rows > 128 ? 8 : (group_rows > 64 ? 4 : (group_rows > 32 ? 2 : 1));
   const int64_t cols = 32 * p.query_waves;
   p.tile = p.query_waves >= 4 ? 64 : 32;
-  p.least = p.query_waves == 1 ? kOwnSets : 1;
+  // (four steps a workgroup at least, where there are: 36 us instead of 40 for
+  // one group of 32 sequences over a prefix of 8000; 8 and 16 are slower again)
+  p.least = 4;
   p.strips = ragged ? seqs * rows / cols + groups : groups * ((group_rows + cols - 1) / cols);
   p.shared_wgs = 0;
   if (groups > 0 && seqs > 0 && max_shared > 0) {
@@ -232,7 +234,7 @@ int topk_beams(const void* logits, int32_t dtype, int64_t row_stride, int32_t vo
   p.tokens = tokens;
   p.found = static_cast<BeamCandidate*>(workspace);
   p.chunks = reinterpret_cast<float*>(p.found + rows * k);
-  p.masses = reinterpret_cast<uint64_t*>(p.chunks + rows * segments * 64);
+  p.masses = reinterpret_cast<double*>(p.chunks + rows * segments * 64);
   p.bests = reinterpret_cast<float*>(p.masses + rows * segments);
   p.arrived = reinterpret_cast<uint32_t*>(p.bests + rows * segments);
   p.cap = (int32_t)beam_cap(segments, k);

@@ -543,10 +543,9 @@ int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_
  *      [num_requests][k]: total, beam and token; places without a candidate
  *      hold -inf, -1, -1.
  *  ended: device uint8 or NULL, lengths: device int32 or NULL.
- * Sums are 64-bit, of weights that are whole multiples of 2^-43 of a 2048-score
- * segment's largest: totals are off by at most vocab * 2^-43 of a weight sum
- * and 2^-45 beside it, so only totals that near each other may come in either
- * order; beams with equal scores and logits tie to the bit.
+ * Sums are 64-bit, of exponentials good to 2^-39 of themselves, in one order:
+ * only totals that near each other may come in either order, and beams with
+ * equal scores and logits tie to the bit.  -inf and NaN logits add nothing.
  * vocab 1 .. 2^20, beams 1 .. 32, k 1 .. 64; workspace as for topk_sample, of
  * topk_beams_workspace_bytes(...) bytes. */
 size_t topk_beams_workspace_bytes(int32_t num_requests, int32_t beams, int32_t k, int32_t vocab);
