@@ -610,15 +610,20 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
     s.cut = 0;
     s.width = q.shared.width;
     int all = 0, strips = 0;
+    uint64_t falls = 0;
     for (int g0 = 0; g0 < q.groups; g0 += 64) {
+      const int g = g0 + lane;
+      falls |= __ballot(q.starts && g < q.groups && q.starts[min(g, q.groups - 1) + 1] < q.starts[min(g, q.groups - 1)]);
       const GroupScan c = scan_groups(q, g0, 32 * QW, KT, all, strips);
       if (blockIdx.x == 0 && threadIdx.x < 64 && g0 + (int)threadIdx.x < q.groups)
         q.group_at[g0 + threadIdx.x] = int4{c.step_end - c.steps, c.strip_end - c.strips, 0, 0};
       all = __builtin_amdgcn_readlane(c.step_end, 63);
       strips = __builtin_amdgcn_readlane(c.strip_end, 63);
     }
+    // (starts that fall may have more strips than there is room for: no shared
+    // positions then, which the join learns from here)
+    if (falls) strips = q.strips + 1;
     if (blockIdx.x == 0 && threadIdx.x == 0) q.group_at[q.groups] = int4{all, strips, 0, 0};
-    // (more strips than rising starts can have: the shared positions are left out)
     if (strips > q.strips) return;
     const int share = share_of(q, all);
     const int64_t from = (int64_t)wg * share;

@@ -62,20 +62,29 @@ struct AttendPlan {
 };
 
 // How the work is cut up.  A group's prefix is read once for up to 256 of its
-// queries (8 waves of 32); groups of up to 32 have a wave for each fourth key
-// tile instead.  About 2048 waves in all, so that each of the chip's 1024
-// SIMDs has two.
+// queries (8 waves of 32).  Groups of up to 32 queries, and all where prefixes
+// take up to 2^27 products of a query's 32 (the strips of 32 queries times
+// positions, key heads and dim), have a wave for each fourth key tile instead:
+// prefixes and own positions are then one launch.  Groups of 70 queries over
+// 5001 positions (2^25) take 22 us so and 28 the other way, 8 of 256 over 2000
+// (2^27) 130 and 133, 64 of 64 over 2000 (2^28) 296 and 240.  About 2048 waves
+// in all, so that each of the chip's 1024 SIMDs has two.
+constexpr int64_t kSetProducts = (int64_t)1 << 27;
 bool attend_plan(int32_t groups, int32_t seqs, bool ragged, int32_t next_n, int32_t heads,
-                 int32_t kv_heads, int64_t max_shared, int64_t max_own, AttendPlan& p) {
+                 int32_t kv_heads, int32_t dim, int64_t max_shared, int64_t max_own, AttendPlan& p) {
   const int64_t per = heads / kv_heads, rows = (int64_t)next_n * per;
   const int64_t group_rows = groups > 0 ? (seqs + groups - 1) / groups * rows : 0;
-  p.query_waves = group_rows > 128 ? 8 : (group_rows > 64 ? 4 : (group_rows > 32 ? 2 : 1));
-  const int64_t cols = 32 * p.query_waves;
+  auto strips = [&](int64_t cols) {
+    return ragged ? seqs * rows / cols + groups : groups * ((group_rows + cols - 1) / cols);
+  };
+  p.query_waves = group_rows > 128 ? 8 : (group_rows > 64 ? 4 : 2);
+  const int64_t positions = max_shared * kv_heads;  // (below 2^62)
+  if (group_rows <= 32 || positions <= kSetProducts / dim / strips(32)) p.query_waves = 1;
   p.tile = p.query_waves >= 4 ? 64 : 32;
   // (four steps a workgroup at least, where there are: 36 us instead of 40 for
   // one group of 32 sequences over a prefix of 8000; 8 and 16 are slower again)
   p.least = 4;
-  p.strips = ragged ? seqs * rows / cols + groups : groups * ((group_rows + cols - 1) / cols);
+  p.strips = strips(32 * p.query_waves);
   p.shared_wgs = 0;
   if (groups > 0 && seqs > 0 && max_shared > 0) {
     const int64_t steps = (max_shared + p.tile - 1) / p.tile * p.strips;
@@ -382,7 +391,7 @@ size_t topk_attend_workspace_bytes(int32_t num_groups, int32_t num_seqs, int32_t
       max_shared_len > kInt || max_own_len > kInt)
     return 0;
   AttendPlan plan;
-  if (!attend_plan(num_groups, num_seqs, ragged != 0, next_n, num_heads, num_kv_heads, max_shared_len,
+  if (!attend_plan(num_groups, num_seqs, ragged != 0, next_n, num_heads, num_kv_heads, dim, max_shared_len,
                    max_own_len, plan))
     return 0;
   return attend_bytes(plan, num_groups, num_kv_heads, (int64_t)num_seqs * next_n * num_heads, dim);
@@ -417,8 +426,8 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
   const int64_t most_own = longest_of(own_width, block_size, num_blocks, max_own_len);
   AttendPlan plan;
   if (most_shared < 0 || most_own < 0 ||
-      !attend_plan(num_groups, num_seqs, group_starts != nullptr, next_n, num_heads, num_kv_heads, most_shared,
-                   most_own, plan))
+      !attend_plan(num_groups, num_seqs, group_starts != nullptr, next_n, num_heads, num_kv_heads, dim,
+                   most_shared, most_own, plan))
     return TOPK_EINVAL;
   const int64_t rows = (int64_t)num_seqs * next_n * num_heads;
   if (!workspace || workspace_bytes < attend_bytes(plan, num_groups, num_kv_heads, rows, dim)) return TOPK_EWORKSPACE;
@@ -478,6 +487,7 @@ int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_h
   if (!pages_ok(k_cache, k_block_stride, k_slot_stride, k_head_stride, num_blocks)) return TOPK_EINVAL;
   const uint64_t sb = (uint64_t)num_groups * num_kv_heads * shared_positions * 4;
   const uint64_t ob = (uint64_t)num_seqs * num_kv_heads * own_positions * 4;
+  const uint64_t lb = (uint64_t)num_seqs * next_n * num_heads * 4;
   if ((sb > 0 && !shared_out) || (ob > 0 && !own_out)) return TOPK_EINVAL;
   if (!at(q, 16) || q_stride % 8 || q_head_stride % 8 || !at(lse, 4) || !at(group_starts, 4) ||
       !at(shared_mass, 4) || !at(shared_out, 4) || !at(own_mass, 4) || !at(own_out, 4) ||
@@ -485,7 +495,8 @@ int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_h
     return TOPK_ELAYOUT;
   if ((shared_mass != shared_out && !clear_of(shared_mass, sb, shared_out, sb)) ||
       (own_mass != own_out && !clear_of(own_mass, ob, own_out, ob)) || !clear_of(shared_out, sb, own_out, ob) ||
-      !clear_of(shared_out, sb, own_mass, ob) || !clear_of(own_out, ob, shared_mass, sb))
+      !clear_of(shared_out, sb, own_mass, ob) || !clear_of(own_out, ob, shared_mass, sb) ||
+      !clear_of(shared_out, sb, lse, lb) || !clear_of(own_out, ob, lse, lb))
     return TOPK_EINVAL;
   int rc = tables_ok(shared_tables, shared_stride, shared_width, shared_lens, num_groups);
   if (rc != TOPK_OK) return rc;
@@ -571,7 +582,9 @@ int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads
       slot_bytes > ((int64_t)1 << 31) || slot_bytes % num_heads || (slot_bytes / num_heads) % 16)
     return TOPK_EINVAL;
   if (num_requests == 0 || num_caches == 0 || slot_bytes == 0 || num_blocks == 0) return TOPK_OK;
-  if (!kept || !caches || (max_blocks > 0 && !block_tables) || (out_blocks > 0 && !out_tables)) return TOPK_EINVAL;
+  if (!kept || !caches || (max_blocks > 0 && !block_tables) || (out_blocks > 0 && !out_tables) ||
+      (block_tables == out_tables && table_stride != out_stride && num_requests > 1))
+    return TOPK_EINVAL;
   if (!at(kept, 4) || !at(block_tables, 4) || !at(out_tables, 4)) return TOPK_ELAYOUT;
   for (int32_t c = 0; c < num_caches; ++c) {
     if (!caches[c]) return TOPK_EINVAL;

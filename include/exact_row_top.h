@@ -599,7 +599,7 @@ int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32
  * num_groups equal groups), sees the first shared_lens[g] positions of
  * shared_tables row g; then sequence s's token t sees the first own_lens[s] -
  * next_n + t + 1 positions of own_tables row s.  Sequences in no group have no
- * prefix.
+ * prefix, and starts that fall leave out all prefixes.
  *     out = sum_p softmax_p(scale q k_p) v_p,  lse = ln sum_p exp(scale q k_p)
  * over all of them; a token that sees nothing gives 0 and -inf.  Lengths are
  * cut to [0, what the table row holds] (and max_shared_len, max_own_len where
@@ -612,7 +612,8 @@ int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32
  *      aligned; lse: float [num_seqs * next_n][num_heads] or NULL.
  *  workspace: topk_attend_workspace_bytes(...) bytes (ragged: group_starts is
  *      given; the longest lengths as planned for), 16-byte aligned.
- * dim 64 or 128, next_n 1 .. 1024, at most 2^30 positions a row. */
+ * dim 64 or 128, next_n 1 .. 1024, at most 2^30 positions a row, block_size
+ * 1 .. 2^20, block and head strides below 2^31, slot strides below 2^27. */
 size_t topk_attend_workspace_bytes(int32_t num_groups, int32_t num_seqs, int32_t ragged, int32_t next_n,
                                    int32_t num_heads, int32_t num_kv_heads, int32_t dim,
                                    int64_t max_shared_len, int64_t max_own_len);
@@ -665,7 +666,7 @@ int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stri
  * group, position j of out_tables row r becomes position kept[r][h][j] of
  * block_tables row r (left as it is where kept is -1 or a block is not in [0,
  * num_blocks)).  kept rises and kept[r][h][j] >= j, as topk_evict_keep gives
- * it.  out_tables is block_tables (the same pointer: in place) or names blocks
+ * it.  out_tables is block_tables (pointer and stride: in place) or names blocks
  * that block_tables does not; no block belongs to two requests.
  *  caches: num_caches (at most 64) device arrays [num_blocks][block_size] of
  *      slot_bytes bytes, contiguous and 16-byte aligned, in a host array; head

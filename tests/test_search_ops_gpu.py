@@ -339,10 +339,12 @@ class Case:
                  self.sees(s, t, limit, own)[1]) for s in range(self.S) for t in range(self.next_n)]
 
 
-def _check_attend(ert, c, what, scale=None, limit=None, own=None, equal=False):
+def _check_attend(ert, c, what, scale=None, limit=None, own=None, equal=False, room=0):
     import torch
     log(f"[attend] {what}")
     pt, pl, tab, lens = c.dev()
+    if room:   # prefix tables for as many positions as `room`
+        pt = torch.nn.functional.pad(pt, (0, (room + c.bs - 1) // c.bs - pt.shape[1]), value=-1)
     out, lse = ert.prefix_attention(c.q, c.k, c.v, pt, pl, tab, lens, next_n=c.next_n, scale=scale,
                                     group_starts=_cuda(c.starts) if c.G and not equal else None,
                                     max_prefix_len=limit, max_len=own, return_lse=True)
@@ -369,6 +371,36 @@ def test_attention_sizes(ert, dtype, dim, bs):
         c = Case(dtype, dim, bs, members, prefix, suffix, heads, kv, next_n, seed=n)
         _check_attend(ert, c, f"{dtype} dim={dim} bs={bs} members={members} prefix={prefix} suffix={suffix} "
                               f"heads={heads}/{kv} next_n={next_n}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bs", [1, 7, 16, 64])
+def test_attention_where_queries_share_a_read(ert, dtype, dim, bs):
+    # room for 2^21 positions: waves of 32 queries share the prefix, 2, 4 and 8 of them
+    for n, (members, prefix, suffix, heads, kv, next_n) in enumerate([
+            ([20, 13], 130, 33, 4, 2, 1), ([9, 0, 30, 1], 333, 40, 6, 2, 2), ([33], 700, 50, 8, 2, 1),
+            ([40, 3, 90], 100, 10, 4, 1, 1), ([60], 257, 20, 8, 1, 1), ([70, 129], 65, 5, 6, 2, 1)]):
+        c = Case(dtype, dim, bs, members, prefix, suffix, heads, kv, next_n, seed=n)
+        _check_attend(ert, c, f"{dtype} dim={dim} bs={bs} members={members} prefix={prefix} suffix={suffix} "
+                              f"heads={heads}/{kv} next_n={next_n}", room=1 << 21)
+
+
+def test_attention_long_prefixes_of_many_queries(ert):
+    for dtype, dim, members, prefix, heads, kv in (("bf16", 64, [33], 17000, 2, 2), ("fp16", 128, [20, 5], 9001, 8, 2),
+                                                   ("bf16", 128, [2, 40, 30], 5000, 8, 1)):
+        c = Case(dtype, dim, 64, members, prefix, 20, heads, kv, plens=[prefix - 7 * g for g in range(len(members))])
+        _check_attend(ert, c, f"{dtype} {dim} {members} {prefix}", room=1 << 23)
+        c = Case(dtype, dim, 64, members, prefix // 2, 20, heads, kv, spread=8.0)
+        _check_attend(ert, c, f"{dtype} {dim} {members} spread 8", room=1 << 23)
+
+
+@pytest.mark.parametrize("members,room", [([3, 2], 0), ([70, 40], 1 << 21)])
+def test_attention_leaves_out_prefixes_of_falling_starts(ert, members, room):
+    c = Case("bf16", 64, 16, members, 200, 50, 8, 2)
+    c.starts = c.starts[::-1].copy()
+    c.group = lambda s: None
+    _check_attend(ert, c, f"falling starts {members}", room=room)
 
 
 def test_attention_long_rows_and_many_splits(ert):

@@ -99,7 +99,8 @@ REFUSALS = [
     (_attend, ELAYOUT, SHAPES_AT + [dict(vc=_at(2) + 8), dict(vb=4100), dict(out=_at(8) + 8), dict(ws=_at(10) + 4)]),
     (_attend, EWORKSPACE, [dict(ws=None), dict(ws_bytes=100)]),
     (_mass, EINVAL, SHAPES + [dict(lse=None), dict(decay=float("nan")), dict(pn=-1), dict(on=-1), dict(po=None), dict(oo=None),
-                              dict(po=_at(10) + 4), dict(oo=_at(12) + 4), dict(oo=_at(11)), dict(po=_at(12)), dict(oo=_at(10))]),
+                              dict(po=_at(10) + 4), dict(oo=_at(12) + 4), dict(oo=_at(11)), dict(po=_at(12)), dict(oo=_at(10)),
+                              dict(po=_at(9)), dict(oo=_at(9) + 4)]),
     (_mass, ELAYOUT, SHAPES_AT + [dict(pm=_at(10) + 2), dict(po=_at(11) + 2), dict(om=_at(12) + 2), dict(oo=_at(13) + 1)]),
     (_keep, EINVAL, [dict(requests=-1), dict(heads=0), dict(n=-1), dict(rs=-1), dict(hs=-1), dict(budget=0), dict(sinks=-1),
                      dict(recent=-1), dict(sinks=41), dict(width=49), dict(mass=None), dict(lens=None), dict(kept=None),
@@ -109,7 +110,7 @@ REFUSALS = [
                       dict(new=_at(4) + 1)]),
     (_move, EINVAL, [dict(requests=-1), dict(heads=0), dict(budget=0), dict(width=-1), dict(stride=7), dict(to_width=-1),
                      dict(to_stride=3), dict(bs=0), dict(n=-1), dict(n=65), dict(blocks=-1), dict(slot=-16), dict(slot=513),
-                     dict(slot=48), dict(kept=None), dict(tables=None), dict(to=None), dict(cache=None)]),
+                     dict(slot=48), dict(to=_at(1)), dict(kept=None), dict(tables=None), dict(to=None), dict(cache=None)]),
     (_move, ELAYOUT, [dict(kept=_at(0) + 2), dict(tables=_at(1) + 2), dict(to=_at(2) + 2), dict(cache=_at(3) + 8)]),
 ]
 
