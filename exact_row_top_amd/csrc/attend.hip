@@ -784,16 +784,27 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) 
 // ---------------------------------------------------------------------------
 namespace {
 
-// The sum over a half wave, in all its lanes.
-__device__ __forceinline__ float half_sum(float v) {
-  auto add = [&](auto ctl) {
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctl)::value, 0xf, 0xf, true));
-  };
-  add(std::integral_constant<int, 0xB1>{});    // neighbours: quad_perm 1 0 3 2
-  add(std::integral_constant<int, 0x4E>{});    // quad_perm 2 3 0 1
-  add(std::integral_constant<int, 0x141>{});   // row_half_mirror
-  add(std::integral_constant<int, 0x140>{});   // row_mirror
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+// Sums over a half wave: lane l of it gets that of value l % 16.  Lanes that
+// differ in one more bit of l exchange the half of their values that the other
+// keeps, so each step adds half as many.
+template <int CTL>
+__device__ __forceinline__ float from_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTL, 0xf, 0xf, true));
+}
+template <int CTL, int N>
+__device__ __forceinline__ void halve(float (&v)[16], bool upper) {
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    const float keep = upper ? v[x + N] : v[x], send = upper ? v[x] : v[x + N];
+    v[x] = keep + from_lane<CTL>(send);
+  }
+}
+__device__ __forceinline__ float half_sums(float (&v)[16], int lane) {
+  halve<0x140, 8>(v, lane & 8);   // row_mirror: lane ^ 15
+  halve<0x141, 4>(v, lane & 4);   // row_half_mirror: lane ^ 7
+  halve<0x1B, 2>(v, lane & 2);    // quad_perm 3 2 1 0
+  halve<0xB1, 1>(v, lane & 1);    // quad_perm 1 0 3 2
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[0]), __float_as_uint(v[0]), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
@@ -802,6 +813,8 @@ __device__ __forceinline__ float half_sum(float v) {
 template <class T, int DIM>
 __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassParams mp) {
   constexpr int STEPS = DIM / 16, TILES = kMassTiles, PAIR = 2;
+  constexpr int PIECES = DIM / 8, ROWS = 64 / PIECES, PASSES = kKeyTile / ROWS;
+  __shared__ Piece tiles[kMassBlock / 64][PAIR][kKeyTile * PIECES];
   const AttendParams& q = mp.a;
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -837,20 +850,35 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
   }
   Piece key[PAIR][STEPS], query[STEPS];
   uint64_t live[PAIR];
-  auto load_keys = [&](int i0) {
+  const int lrow = lane / PIECES, lpiece = lane % PIECES;
+  // two tiles to LDS: whole rows, side by side; what is not there is read from
+  // the cache's first slot, and masked
+  auto fetch = [&](int i0) {
 #pragma unroll
     for (int i = 0; i < PAIR; ++i) {
       const int32_t b = block[i0 + i];
+      if (!__ballot(b >= 0)) continue;
       const uint32_t p = (uint32_t)(first_of(i0 + i) + col);
       const uint32_t off = p - q.by_block(p) * (uint32_t)q.block_size;
-      const unsigned char* a = q.k.base + head * q.k.head_stride + half * 16 +
-                               (b >= 0 ? (uint64_t)b * q.k.block_stride + (uint64_t)off * q.k.slot_stride : 0);
-      live[i] = __ballot(b >= 0);
-      if (live[i]) {
+      const uint64_t from = b >= 0 ? (uint64_t)b * q.k.block_stride + (uint64_t)off * q.k.slot_stride : 0;
 #pragma unroll
-        for (int d = 0; d < STEPS; ++d) key[i][d] = *reinterpret_cast<const Piece*>(a + d * 32);
+      for (int s = 0; s < PASSES; ++s) {
+        const int row = s * ROWS + lrow;
+        const uint32_t low = (uint32_t)__shfl((int)(uint32_t)from, row), high = (uint32_t)__shfl((int)(from >> 32), row);
+        load_to_lds(q.k.base + head * q.k.head_stride + ((uint64_t)high << 32 | low) + key_piece<DIM>(row, lpiece) * 16,
+                    &tiles[wv][i][s * 64]);
       }
     }
+  };
+  auto take = [&](int i0) {
+    loads_but<0>();
+#pragma unroll
+    for (int i = 0; i < PAIR; ++i) {
+      live[i] = __ballot(block[i0 + i] >= 0);
+#pragma unroll
+      for (int d = 0; d < STEPS; ++d) key[i][d] = tiles[wv][i][col * PIECES + key_piece<DIM>(col, 2 * d + half)];
+    }
+    lds_done();
   };
   // queries r0 .. r0 + 31: this lane's, its log-sum and the positions it sees
   float lse = 0.0f;
@@ -870,7 +898,7 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
     sees = on ? len - cut + (cut ? (int)(tok % (uint32_t)q.next_n) : 0) : 0;
   };
   if (rows > 0 && first_of(0) < len) {
-    load_keys(0);
+    fetch(0);
     load_queries(0);
   }
   const float* in = shared ? mp.shared_in : mp.own_in;
@@ -891,18 +919,29 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
       for (int x = 0; x < 16; ++x) acc[i][x] = 0.0f;
     }
     if (rows > 0 && first_of(i0) < len) {
+      take(i0);
       for (int r0 = 0; r0 < rows; r0 += 32) {
         if (r0 > 0 || (i0 > 0 && rows > 32)) load_queries(r0);
+        if (r0 + 32 >= rows && i0 + PAIR < TILES && first_of(i0 + PAIR) < min(len, row_len)) {
+          loads_but<0>();   // (the queries: in order, they would wait for the keys as well)
+          fetch(i0 + PAIR);
+        }
 #pragma unroll
         for (int i = 0; i < PAIR; ++i) {
           if (!live[i]) continue;
-          const int ahead = min(max(sees - (first_of(i0 + i) + 4 * half), 0), 31);
-          const uint32_t seen = (uint32_t)(live[i] >> (4 * half)) & ((1u << ahead) - 1u);
           f32x16 sc;
 #pragma unroll
           for (int x = 0; x < 16; ++x) sc[x] = 0.0f;
 #pragma unroll
           for (int d = 0; d < STEPS; ++d) sc = T::mfma(key[i][d], query[d], sc);
+          if (live[i] == ~0ull && __ballot(sees >= first_of(i0 + i) + kKeyTile) == ~0ull) {   // all is seen
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              acc[i][x] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x], q.scale, -lse));
+            continue;
+          }
+          const int ahead = min(max(sees - (first_of(i0 + i) + 4 * half), 0), 31);
+          const uint32_t seen = (uint32_t)(live[i] >> (4 * half)) & ((1u << ahead) - 1u);
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x], q.scale, -lse));
@@ -910,16 +949,10 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
           }
         }
       }
-      if (i0 + PAIR < TILES && first_of(i0 + PAIR) < len) load_keys(i0 + PAIR);
     }
 #pragma unroll
     for (int i = 0; i < PAIR; ++i) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const float v = half_sum(acc[i][x]);
-        sum = col == x ? v : sum;
-      }
+      const float sum = half_sums(acc[i], lane);
       const int p = first_of(i0 + i) + mine;
       if (col < 16 && p < row_len) out[base + p] = old[i] * mp.decay + sum;
     }
