@@ -198,13 +198,15 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
 // reads positions behind everything that was stored (kept[j] >= j); between
 // different blocks nothing waits, and workgroups share a row's positions.
 //
-// Bound by memory: rows of 256 bytes from all over a cache.  Four rows in
-// flight a thread: 16 x 8192 positions to 1024, 8 heads of 256 bytes, two
-// caches, 134 MB from and to memory, 56 us with the choice; with 8 rows 68,
-// with 16 (fewer waves) 124.
+// Bound by memory: rows of 256 bytes from all over a cache.  16 x 8192 positions
+// to 1024, 8 heads of 256 bytes, two caches, 134 MB from and to memory, take 44
+// us with the choice (27 at a copy's rate); 48 without the stores' hint, which
+// keeps what is moved out of the caches' way.  Four rows in flight a thread:
+// with 8 the same took 68 where four took 56, with 16 (fewer waves) 124.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kMoveRows = 4;   // rows in flight a thread
+typedef uint32_t Four __attribute__((ext_vector_type(4)));
 }
 
 template <bool IN_PLACE>
@@ -242,20 +244,20 @@ __global__ void __launch_bounds__(kMoveBlock) evict_move_kernel(const MoveParams
   };
   for (int j0 = part * span; j0 < j1; j0 += step) {
     for (int x0 = 0; x0 < mine; x0 += across) {
-      uint4 v[kMoveRows];
+      Four v[kMoveRows];
       unsigned char* dst[kMoveRows];
 #pragma unroll
       for (int i = 0; i < kMoveRows; ++i) {
         const int j = j0 + i * down + y;
         dst[i] = nullptr;
-        v[i] = uint4{0, 0, 0, 0};
+        v[i] = Four{0, 0, 0, 0};
         if (y < down && j < j1 && x0 + x < mine) {
           const int p = kept[j];
           const unsigned char* src = p >= 0 ? address(from, q.max_blocks, p) : nullptr;
           dst[i] = src ? address(to, q.out_blocks, j) : nullptr;
           if (dst[i] == src) dst[i] = nullptr;
           if (dst[i]) {
-            v[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(x0 + x) * 16);
+            v[i] = *reinterpret_cast<const Four*>(src + (int64_t)(x0 + x) * 16);
             dst[i] += (int64_t)(x0 + x) * 16;
           }
         }
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kMoveBlock) evict_move_kernel(const MoveParams
       }
 #pragma unroll
       for (int i = 0; i < kMoveRows; ++i)
-        if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = v[i];
+        if (dst[i]) __builtin_nontemporal_store(v[i], reinterpret_cast<Four*>(dst[i]));
       if (IN_PLACE) __syncthreads();
     }
   }
