@@ -195,6 +195,15 @@ __device__ __forceinline__ void lds_barrier() {
 // workgroup of a key head takes an equal share, whatever the lengths; pieces
 // of a strip are told apart by workgroup + strip, which no two pieces have in
 // common.
+//
+// Bound, with eight waves, by the matrix products and the LDS reads that feed
+// them, which take about as long: 2 groups of 256 queries a key head (8 of them,
+// dim 128) over some 24 thousand positions each, 51 GFLOP, take 80 us, 640
+// TFLOP/s, of them about 20 for the first loads and the 33 MB of pieces.
+// Bound, alone (QW 1), by memory and the waits for it: 64 sequences' own 1 to
+// 512 positions, 67 MB, take 21 us (3.2 TB/s, the longest sequences last); four
+// queries' 1000 positions take 8, the launch and the waits for lengths, tables,
+// keys, values and the join of the four sets.
 // ---------------------------------------------------------------------------
 template <class T, int DIM, int QW, int KW, int KT, bool EVEN>
 __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendParams q) {
@@ -685,7 +694,9 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
 
 // ---------------------------------------------------------------------------
 // Joins a row's pieces: a wave a row, its lanes in 64 / (dim / 4) sets that
-// take turns at the pieces.
+// take turns at the pieces.  Bound by reading them: 4096 rows of about 18
+// pieces, 38 MB, take 11.4 us (3.3 TB/s), 128 rows 4.8, where the waits for
+// what says where the pieces lie are the whole.
 // ---------------------------------------------------------------------------
 template <class T, int DIM>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) {
@@ -780,7 +791,14 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) 
 // every query of key head h.  A wave holds two tiles of 32 keys and runs over
 // the entry's queries, 32 at a time; each lane adds up its query column's
 // weights, and the 32 columns are added at the end, so sums have one order.
-// The next tiles are on their way while these are added up and written.
+// The next tiles are on their way to LDS while the last queries are computed
+// and these are written.
+//
+// Bound by memory and by the exponentials, one a (position, query): 8 groups of
+// 64 queries a key head over some 6 thousand positions each, and 64 sequences'
+// own 128 to 256, 122 MB, take 31 us (3.9 TB/s), of them about 14 exponentials
+// and sums if nothing ran beside them.  Four tiles a wave: two take 36, for
+// their first loads, eight the same and 15 instead of 9 where there are few.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -962,26 +980,27 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
 namespace {
 
 template <class T, int DIM, bool EVEN>
-const void* attend_ptr(int query_waves) {
+const void* attend_ptr(int query_waves, int sets) {
   switch (query_waves) {
     case 8: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 8, 1, 64, EVEN>);
     case 4: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 4, 1, 64, EVEN>);
     case 2: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 2, 1, 32, EVEN>);
-    default: return reinterpret_cast<const void*>(&attend_kernel<T, DIM, 1, kOwnSets, kKeyTile, EVEN>);
   }
+  return sets == 1 ? reinterpret_cast<const void*>(&attend_kernel<T, DIM, 1, 1, kKeyTile, EVEN>)
+                   : reinterpret_cast<const void*>(&attend_kernel<T, DIM, 1, kOwnSets, kKeyTile, EVEN>);
 }
 template <class T>
-const void* attend_ptr(int dim, int query_waves, bool even) {
-  if (dim == 64) return even ? attend_ptr<T, 64, true>(query_waves) : attend_ptr<T, 64, false>(query_waves);
-  return even ? attend_ptr<T, 128, true>(query_waves) : attend_ptr<T, 128, false>(query_waves);
+const void* attend_ptr(int dim, int query_waves, int sets, bool even) {
+  if (dim == 64) return even ? attend_ptr<T, 64, true>(query_waves, sets) : attend_ptr<T, 64, false>(query_waves, sets);
+  return even ? attend_ptr<T, 128, true>(query_waves, sets) : attend_ptr<T, 128, false>(query_waves, sets);
 }
 
 }  // namespace
 
-const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int block_size) {
+const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int sets, int block_size) {
   // rows that a wave loads at once
   const bool even = block_size % (64 / (dim / 8)) == 0;
-  return dtype == 1 ? attend_ptr<Bf16>(dim, query_waves, even) : attend_ptr<F16>(dim, query_waves, even);
+  return dtype == 1 ? attend_ptr<Bf16>(dim, query_waves, sets, even) : attend_ptr<F16>(dim, query_waves, sets, even);
 }
 const void* attend_join_kernel_ptr(int dtype, int dim) {
   if (dtype == 1)

@@ -72,7 +72,6 @@ struct RowCopy {
 
 struct ReorderParams {
   const int32_t* parents;   // [requests][k]
-  int32_t requests;
   int32_t beams;
   int32_t k;
   int32_t copies;
@@ -191,7 +190,6 @@ struct KeepParams {
   int64_t request_stride;    // elements
   int64_t head_stride;
   int32_t positions;
-  int32_t requests;
   int32_t heads;
   const int32_t* kv_lens;    // [requests]
   int32_t budget;

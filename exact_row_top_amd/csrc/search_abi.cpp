@@ -15,7 +15,7 @@ const void* beam_segment_kernel_ptr(int dtype);
 const void* beam_row_kernel_ptr(int dtype, int pieces);
 const void* reorder_rows_kernel_ptr(int n);
 const void* reorder_blocks_kernel_ptr(int n);
-const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int block_size);
+const void* attend_kernel_ptr(int dtype, int dim, int query_waves, int sets, int block_size);
 const void* attend_join_kernel_ptr(int dtype, int dim);
 const void* attend_mass_kernel_ptr(int dtype, int dim);
 const void* evict_keep_kernel_ptr(int64_t positions);
@@ -57,7 +57,7 @@ int64_t beam_cap(int64_t segments, int32_t k) {
 }
 
 struct AttendPlan {
-  int32_t query_waves, tile, least;
+  int32_t query_waves, tile, least, own_sets;
   int64_t strips, shared_wgs, own_splits, own_tiles, own_wgs;
 };
 
@@ -96,6 +96,10 @@ bool attend_plan(int32_t groups, int32_t seqs, bool ragged, int32_t next_n, int3
   p.own_tiles = (rows + 31) / 32;
   p.own_splits = 0;
   const int64_t units = (int64_t)seqs * kv_heads * p.own_tiles;
+  // (enough sequences fill the chip with a wave each: 1024 of up to 100
+  // positions and 8 key heads, in groups of 16, took 242 us with four waves each
+  // and take 201)
+  p.own_sets = units >= 2048 ? 1 : kOwnSets;
   if (max_own > 0 && units > 0) {
     const int64_t steps = (max_own + kKeyTile - 1) / kKeyTile, most = (steps + kOwnSets - 1) / kOwnSets;
     p.own_splits = 2048 / kOwnSets / units;
@@ -286,7 +290,6 @@ int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* cons
   ReorderParams p;
   memset(&p, 0, sizeof(p));
   p.parents = parents;
-  p.requests = num_requests;
   p.beams = beams;
   p.k = k;
   p.clear = clear;
@@ -454,16 +457,18 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
   p.out = static_cast<unsigned char*>(out);
   p.lse = lse;
   p.shared_grid = plan.shared_wgs * num_kv_heads;
-  const bool together = plan.query_waves == 1;
+  const bool together = plan.query_waves == 1 && plan.own_sets == kOwnSets;
   const int64_t first = p.shared_grid + (together ? plan.own_wgs : 0);
   if (first > 0) {
-    rc = launch(attend_kernel_ptr(dtype, dim, plan.query_waves, block_size), first,
-                64 * (together ? kOwnSets : plan.query_waves), &p, 0, stream);
+    const int sets = plan.query_waves == 1 ? kOwnSets : 1;
+    rc = launch(attend_kernel_ptr(dtype, dim, plan.query_waves, sets, block_size), first,
+                64 * plan.query_waves * sets, &p, 0, stream);
     if (rc != TOPK_OK) return rc;
   }
   if (!together && plan.own_wgs > 0) {
     p.shared_grid = 0;
-    rc = launch(attend_kernel_ptr(dtype, dim, 1, block_size), plan.own_wgs, 64 * kOwnSets, &p, 0, stream);
+    rc = launch(attend_kernel_ptr(dtype, dim, 1, plan.own_sets, block_size), plan.own_wgs, 64 * plan.own_sets, &p, 0,
+                stream);
     if (rc != TOPK_OK) return rc;
   }
   return launch(attend_join_kernel_ptr(dtype, dim), (rows + 3) / 4, 256, &p, 0, stream);
@@ -558,7 +563,6 @@ int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stri
   p.request_stride = request_stride;
   p.head_stride = head_stride;
   p.positions = positions;
-  p.requests = num_requests;
   p.heads = num_heads;
   p.kv_lens = kv_lens;
   p.budget = budget;

@@ -536,8 +536,8 @@ int topk_slots(const int32_t* indices, int64_t num_rows, int32_t k, const int32_
  * share the whole weight); an ended beam offers end_token alone, with its
  * score as it is, and its logits are not read; a beam whose score is not
  * finite offers nothing.  A total's rank is total / n^length_penalty with n =
- * lengths[b] + 1 (ended: lengths[b]; at least 1), or the total itself without
- * lengths.  The k largest ranks are chosen in falling order, equal ones by
+ * lengths[b] + 1 (ended: lengths[b]; at least 1) and the power kept within
+ * 2^-500 and 2^500, or the total itself without lengths.  The k largest ranks are chosen in falling order, equal ones by
  * beam, then token.
  *  out_scores, parents, tokens: device float / int32 / int32
  *      [num_requests][k]: total, beam and token; places without a candidate

@@ -386,6 +386,13 @@ def test_attention_where_queries_share_a_read(ert, dtype, dim, bs):
                               f"heads={heads}/{kv} next_n={next_n}", room=1 << 21)
 
 
+@pytest.mark.parametrize("dtype,dim,bs,next_n", [("bf16", 64, 16, 1), ("fp16", 128, 7, 1), ("bf16", 128, 64, 2), ("fp16", 64, 1, 2)])
+def test_attention_of_many_short_sequences(ert, dtype, dim, bs, next_n):
+    for members, prefix in (([300, 0, 220], 40), ([], 0)):   # a wave a sequence and key head
+        c = Case(dtype, dim, bs, members, prefix, 70, 8, 4, next_n, outside=2 if members else 256)
+        _check_attend(ert, c, f"{dtype} dim={dim} bs={bs} many {members}")
+
+
 def test_attention_long_prefixes_of_many_queries(ert):
     for dtype, dim, members, prefix, heads, kv in (("bf16", 64, [33], 17000, 2, 2), ("fp16", 128, [20, 5], 9001, 8, 2),
                                                    ("bf16", 128, [2, 40, 30], 5000, 8, 1)):
