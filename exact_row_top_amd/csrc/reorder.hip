@@ -83,7 +83,7 @@ __device__ __forceinline__ void move_rows(int k, int64_t bytes, int64_t off, uin
 
 // Rows of up to kMaxCopies arrays in one launch; a workgroup takes 4 KB of
 // every row of a request.  Bound by memory: 256 rows of 260 KB, 68 MB written
-// and, by the children's parents, up to as much read, take 17.5 us where the
+// and, by the children's parents, up to as much read, take 20 us where the
 // last-level cache holds them; 8 small rows 3.3, the launch and the wait for
 // the parents.
 template <int N>
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kCopyBlock) reorder_rows_kernel(const ReorderP
 // open blocks in one cache each, 4 KB of a block at a time; the others make
 // its table rows, a thread an entry of every row.  Bound by memory: 32 requests
 // of 8 beams, blocks of 64 slots of 2 KB about half full, four caches, 67 MB
-// written, take 19.5 us where the last-level cache holds what is read; 8 rows 4.
+// written, take 20 us where the last-level cache holds what is read; 8 rows 4.
 template <int N>
 __global__ void __launch_bounds__(kCopyBlock) reorder_blocks_kernel(const ReorderBlocksParams q) {
   const uint32_t copying = q.copying ? (uint32_t)q.caches * q.requests * q.tiles : 0u;
