@@ -41,6 +41,26 @@ bool clear_of(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return !a || !b || x + na <= y || y + nb <= x;
 }
 
+// Whether rows of na bytes, a stride apart from a on, and rows of nb bytes share
+// no byte: side by side in rows of one stride, or apart.
+bool rows_clear(const void* a, int64_t na, int64_t sa, int64_t ra, const void* b, int64_t nb, int64_t sb, int64_t rb) {
+  if (clear_of(a, (uint64_t)((ra - 1) * sa + na), b, (uint64_t)((rb - 1) * sb + nb))) return true;
+  if (sa != sb) return false;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const int64_t at = ((d % sa) + sa) % sa;   // b's first byte in a's rows
+  return at >= na && sa - at >= nb;
+}
+
+// Whether caches of one size share no byte.
+bool caches_apart(void* const* caches, int32_t n, int64_t blocks, int32_t block_size, int64_t slot_bytes) {
+  const unsigned __int128 all = (unsigned __int128)blocks * (unsigned)block_size * (uint64_t)slot_bytes;
+  const uint64_t bytes = all >> 62 ? (uint64_t)1 << 62 : (uint64_t)all;
+  for (int32_t a = 1; a < n; ++a)
+    for (int32_t b = 0; b < a; ++b)
+      if (!clear_of(caches[a], bytes, caches[b], bytes)) return false;
+  return true;
+}
+
 int64_t beam_segments(int32_t vocab) { return ((int64_t)vocab + kSegment - 1) / kSegment; }
 
 // Chunk maxima that a thread holds, in 16-byte pieces.
@@ -274,8 +294,8 @@ int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* cons
   for (int32_t a = 0; a < num_arrays; ++a) {
     const int64_t n = row_bytes[a], ss = source_strides[a], ts = target_strides[a];
     const int64_t rows = (int64_t)num_requests * beams, outs = (int64_t)num_requests * k;
-    if (n < 0 || n > ((int64_t)1 << 40) || ss < n || ts < n || ss > ((int64_t)1 << 40) ||
-        ts > ((int64_t)1 << 40))
+    if (n < 0 || n > ((int64_t)1 << 40) || ss < n || ts < n || ss > ((int64_t)1 << 62) / rows ||
+        ts > ((int64_t)1 << 62) / outs)
       return TOPK_EINVAL;
     if (n == 0) continue;
     if (!sources[a] || !targets[a]) return TOPK_EINVAL;
@@ -284,6 +304,16 @@ int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* cons
     if (!in_place && !clear_of(sources[a], sb, targets[a], tb)) return TOPK_EINVAL;
     if (!clear_of(parents, (uint64_t)outs * 4, targets[a], tb)) return TOPK_EINVAL;
     if ((n + 16 * kCopyBlock - 1) / (16 * kCopyBlock) * num_requests >= kInt) return TOPK_EINVAL;
+    // what one array's rows are moved to is no other's source or target
+    for (int32_t b = 0; b < num_arrays; ++b) {
+      const int64_t m = row_bytes[b];
+      if (b == a || m <= 0 || source_strides[b] < m || source_strides[b] > ((int64_t)1 << 62) / rows ||
+          target_strides[b] < m || target_strides[b] > ((int64_t)1 << 62) / outs)
+        continue;
+      if (!rows_clear(sources[b], m, source_strides[b], rows, targets[a], n, ts, outs) ||
+          !rows_clear(targets[b], m, target_strides[b], outs, targets[a], n, ts, outs))
+        return TOPK_EINVAL;
+    }
   }
   int rc = device_ok();
   if (rc != TOPK_OK) return rc;
@@ -334,6 +364,8 @@ int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32
     return TOPK_ELAYOUT;
   for (int32_t c = 0; c < num_caches; ++c)
     if (!caches[c] && num_blocks > 0 && slot_bytes > 0) return TOPK_EINVAL;
+  if (num_caches > 1 && !caches_apart(caches, num_caches, num_blocks, block_size, slot_bytes))
+    return TOPK_EINVAL;
   const int64_t rows = (int64_t)num_requests * beams, outs = (int64_t)num_requests * k;
   const bool in_place = block_tables == out_tables && table_stride == out_stride && beams == k;
   const uint64_t out_bytes = max_blocks > 0 ? (uint64_t)((outs - 1) * out_stride + max_blocks) * 4 : 0;
@@ -594,6 +626,7 @@ int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads
     if (!caches[c]) return TOPK_EINVAL;
     if (!at(caches[c], 16)) return TOPK_ELAYOUT;
   }
+  if (!caches_apart(caches, num_caches, num_blocks, block_size, slot_bytes)) return TOPK_EINVAL;
   if (max_blocks == 0 || out_blocks == 0) return TOPK_OK;
   const int rc = device_ok();
   if (rc != TOPK_OK) return rc;

@@ -559,7 +559,8 @@ int topk_beams(const void* logits, int32_t dtype, int64_t row_stride, int32_t vo
  * beams + parents[r][j] of sources[a] (device pointers in host arrays;
  * strides and row_bytes in bytes, any alignment).  A target may be its source
  * (same stride, beams == k): rows are then moved in place, whatever the
- * parents; it overlaps nothing else.  Rows whose parent is not in [0, beams)
+ * parents; it overlaps nothing else, but arrays may lie side by side in rows of
+ * one stride.  Rows whose parent is not in [0, beams)
  * are cleared (clear 1) or left (clear 0).  beams, k 1 .. 32. */
 int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* const* targets,
                       const int64_t* source_strides, const int64_t* target_strides,
@@ -581,7 +582,7 @@ int topk_reorder_rows(int32_t num_arrays, const void* const* sources, void* cons
  *  out_tables: [num_requests * k][max_blocks], may be block_tables (same
  *      stride, beams == k).
  *  caches: num_caches (at most 64) device arrays [num_blocks][block_size] of
- *      slot_bytes bytes each, contiguous, in a host array.
+ *      slot_bytes bytes each, contiguous and apart, in a host array.
  * beams, k 1 .. 32. */
 int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32_t max_blocks,
                         const int32_t* kv_lens, const int32_t* parents, int32_t num_requests,
@@ -669,7 +670,7 @@ int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stri
  * it.  out_tables is block_tables (pointer and stride: in place) or names blocks
  * that block_tables does not; no block belongs to two requests.
  *  caches: num_caches (at most 64) device arrays [num_blocks][block_size] of
- *      slot_bytes bytes, contiguous and 16-byte aligned, in a host array; head
+ *      slot_bytes bytes, contiguous, apart and 16-byte aligned, in a host array; head
  *      group h's share of a slot is the h-th of num_heads equal parts, a
  *      multiple of 16 bytes. */
 int topk_evict_move(const int32_t* kept, int32_t num_requests, int32_t num_heads, int32_t budget,

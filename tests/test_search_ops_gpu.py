@@ -212,6 +212,35 @@ def test_reorder_rows_strided_other_width_and_single(ert):
     assert ert.reorder_beams(torch.empty(0, 5, device="cuda"), torch.empty(0, 3, dtype=torch.int32, device="cuda")).shape == (0, 5)
 
 
+def test_reorder_rows_side_by_side_and_crossed(ert):
+    import torch
+    rng = np.random.default_rng(4)
+    R, W = 3, 5
+    p = _parents(rng, R, W, W)
+    idx = _cuda((np.arange(R)[:, None] * W + p).reshape(-1))
+    wide = torch.randn(R * W, 53, device="cuda")
+    want = wide.clone()
+    want[:, :48] = wide[idx][:, :48]
+    parts = [wide[:, :20], wide[:, 20:41], wide[:, 41:48]]
+    ert.reorder_beams(parts, _cuda(p), out=parts)
+    assert torch.equal(wide, want)
+    a, b = torch.randn(R * W, 9, device="cuda"), torch.randn(R * W, 9, device="cuda")
+    for states, out in (([a, b], [b, a]), ([a, a], [a, a]), ([a, b], [a, a]), ([wide[:, :20], wide[:, 19:30]],) * 2):
+        with pytest.raises((ValueError, RuntimeError)):
+            ert.reorder_beams(states, _cuda(p), out=out)
+
+
+def test_same_cache_twice_is_refused(ert):
+    import torch
+    c = torch.zeros(12, 4, 2, 8, device="cuda")
+    tab, lens = torch.arange(12, device="cuda", dtype=torch.int32).view(6, 2), torch.full((2,), 5, dtype=torch.int32, device="cuda")
+    p = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    with pytest.raises((ValueError, RuntimeError)):
+        ert.reorder_block_tables(tab, lens, p, 4, caches=[c, c])
+    with pytest.raises((ValueError, RuntimeError)):
+        ert.evict_cache(torch.zeros(2, 1, 8, device="cuda"), lens, 3, block_tables=tab[:2], caches=[c, c])
+
+
 def test_reorder_rows_beyond_32_bit_offsets(ert):
     import torch
     x = torch.zeros(6, 1 << 30, dtype=torch.uint8, device="cuda")
@@ -664,6 +693,16 @@ def _search(seed):
 def _same(a, b):
     import torch
     return all(torch.equal(torch.nan_to_num(x.float()), torch.nan_to_num(y.float())) for x, y in zip(a, b))
+
+
+def test_ranks_stay_numbers_at_any_penalty(ert):
+    import torch
+    logits, scores = torch.zeros(6, 1, device="cuda"), torch.zeros(2, 3, device="cuda")
+    lengths = torch.tensor([[9, 1, 2 ** 31 - 1]] * 2, dtype=torch.int32, device="cuda")
+    for penalty in (-3e38, -400.0, 400.0, 3e38):   # totals of zero over powers of 0 and infinity
+        s, b, t = ert.select_beams(logits, scores, 4, lengths=lengths, length_penalty=penalty)
+        assert s.tolist() == [[0.0] * 3 + [NINF]] * 2 and t.tolist() == [[0] * 3 + [-1]] * 2
+        assert b.tolist() == [[0, 1, 2, -1]] * 2
 
 
 def test_step_on_another_stream_and_repeated(ert):

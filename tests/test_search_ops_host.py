@@ -86,13 +86,14 @@ REFUSALS = [
     (_rows, EINVAL, [dict(n=-1), dict(requests=-1), dict(beams=0), dict(beams=33), dict(k=0), dict(k=33), dict(clear=2),
                      dict(parents=None), dict(src=None), dict(dst=None), dict(size=-1), dict(ss=63), dict(ds=63),
                      dict(dst=_at(0) + 64), dict(dst=_at(0), ds=128), dict(dst=_at(0), k=3), dict(dst=_at(2)),
-                     dict(size=1 << 41, ss=1 << 41, ds=1 << 41)]),
+                     dict(size=1 << 41, ss=1 << 41, ds=1 << 41), dict(ss=1 << 60), dict(ds=1 << 60),
+                     dict(n=2), dict(n=3, dst=_at(0))]),
     (_rows, ELAYOUT, [dict(parents=_at(2) + 2)]),
     (_blocks, EINVAL, [dict(requests=-1), dict(beams=0), dict(beams=33), dict(k=0), dict(k=33), dict(width=-1), dict(stride=9),
                        dict(out_stride=9), dict(bs=0), dict(n=-1), dict(n=65), dict(blocks=-1), dict(slot=-1),
                        dict(tail=None, k=3), dict(lens=None), dict(parents=None), dict(tables=None), dict(out=None),
                        dict(cache=None), dict(out=_at(0) + 16), dict(out=_at(0), out_stride=12), dict(out=_at(1)),
-                       dict(out=_at(2)), dict(out=_at(3))]),
+                       dict(out=_at(2)), dict(out=_at(3)), dict(n=2)]),
     (_blocks, ELAYOUT, [dict(tables=_at(0) + 2), dict(lens=_at(1) + 2), dict(parents=_at(2) + 1), dict(tail=_at(3) + 2),
                         dict(out=_at(4) + 2)]),
     (_attend, EINVAL, SHAPES + [dict(out=None), dict(vc=None), dict(vs=-8), dict(ms=-1), dict(mo=-1)]),
@@ -110,7 +111,7 @@ REFUSALS = [
                       dict(new=_at(4) + 1)]),
     (_move, EINVAL, [dict(requests=-1), dict(heads=0), dict(budget=0), dict(width=-1), dict(stride=7), dict(to_width=-1),
                      dict(to_stride=3), dict(bs=0), dict(n=-1), dict(n=65), dict(blocks=-1), dict(slot=-16), dict(slot=513),
-                     dict(slot=48), dict(to=_at(1)), dict(kept=None), dict(tables=None), dict(to=None), dict(cache=None)]),
+                     dict(slot=48), dict(to=_at(1)), dict(n=2), dict(kept=None), dict(tables=None), dict(to=None), dict(cache=None)]),
     (_move, ELAYOUT, [dict(kept=_at(0) + 2), dict(tables=_at(1) + 2), dict(to=_at(2) + 2), dict(cache=_at(3) + 8)]),
 ]
 
