@@ -107,8 +107,10 @@ def select_beams(logits, scores, k, *, ended=None, end_token=0, lengths=None, le
     n = _flat(lengths, "lengths", torch.int32, (requests, beams), dev)
     if k < 1:
         raise ValueError("k must be at least 1")
-    found = torch.empty((requests, k), dtype=torch.float32, device=dev)
-    parents, tokens = torch.empty((2, requests, k), dtype=torch.int32, device=dev).unbind(0)
+    # (sizes one by one, and not in a tuple: a third of a microsecond less each)
+    found = torch.empty(requests, k, dtype=torch.float32, device=dev)
+    parents = torch.empty(requests, k, dtype=torch.int32, device=dev)
+    tokens = torch.empty(requests, k, dtype=torch.int32, device=dev)
     nbytes = lib.topk_beams_workspace_bytes(requests, beams, k, vocab)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(lib.topk_beams(logits.data_ptr(), code, stride, vocab, requests, beams, k, s, e, end_token, n,
@@ -190,7 +192,7 @@ def reorder_beams(states, parents, *, beams=None, out=None, stream=None):
     clear = out is None
     sources = [_rows_layout(t, "states", requests * beams, dev) for t in states]
     if clear:
-        out = [t.new_empty((requests * k, *t.shape[1:])) for t in states]
+        out = [torch.empty(requests * k, *t.shape[1:], dtype=t.dtype, device=dev) for t in states]
         targets = [(n, n) for _, n in sources]
     else:
         targets = [_rows_layout(t, "out", requests * k, dev) for t in out]
@@ -275,7 +277,7 @@ def reorder_block_tables(block_tables, kv_lens, parents, block_size, *, caches=(
         raise ValueError("tail_blocks is needed where k differs from the beams of a request")
     pointers, count, blocks, slot_bytes = _caches(caches, block_size, dev)
     if out is None:
-        out = torch.empty((requests * k, width), dtype=torch.int32, device=dev)
+        out = torch.empty(requests * k, width, dtype=torch.int32, device=dev)
     to, out_stride, out_width = _tables(out, "out", requests * k, dev)
     if out_width != width:
         raise ValueError(f"out must be an int32 [{requests * k}, {width}] tensor")
@@ -379,8 +381,11 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_lens, block_tabl
     most_own = 0 if max_len is None else _int32(max_len, "max_len")
     if most < 0 or most_own < 0:
         raise ValueError("max_prefix_len and max_len must not be negative")
-    out = _matrix(out, "out", q.dtype, (tokens, heads, dim), dev)
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
+    if out is None:
+        out = torch.empty(tokens, heads, dim, dtype=q.dtype, device=dev)
+    else:
+        out = _matrix(out, "out", q.dtype, (tokens, heads, dim), dev)
+    lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev) if return_lse else None
     lib = _lib()
     room, room_own = tables[2] * paging[1], tables[8] * paging[1]
     nbytes = lib.topk_attend_workspace_bytes(groups, seqs, tables[4] is not None, next_n, heads, kv_heads,
@@ -395,8 +400,9 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_lens, block_tabl
 
 def _mass(mass, out, name, entries, kv_heads, positions, device):
     """(positions, given mass' pointer, result) of one kind of mass rows."""
-    for t, what in ((mass, name), (out, f"{name}'s out")):
+    for t in (mass, out):
         if t is not None:
+            what = name if t is mass else f"{name}'s out"
             if _tensor(t, what).dim() != 3:
                 raise ValueError(f"{what} must be 3-D")
             positions = t.shape[2]
@@ -404,7 +410,11 @@ def _mass(mass, out, name, entries, kv_heads, positions, device):
         raise ValueError(f"{name} is too large: its sizes must fit 32 bits")
     shape = (entries, kv_heads, positions)
     given = _flat(mass, name, torch.float32, shape, device)
-    return positions, given, _matrix(out, f"{name}'s out", torch.float32, shape, device)
+    if out is None:
+        out = torch.empty(entries, kv_heads, positions, dtype=torch.float32, device=device)
+    else:
+        out = _matrix(out, f"{name}'s out", torch.float32, shape, device)
+    return positions, given, out
 
 
 def attention_mass(q, k_cache, lse, prefix_tables, prefix_lens, block_tables, kv_lens, *,
@@ -499,11 +509,11 @@ def evict_cache(mass, kv_lens, budget, *, sinks=0, recent=0, block_tables=None, 
             raise ValueError("a head's share of a cache slot must be a multiple of 16 bytes")
         tables = _tables(block_tables, "block_tables", requests, dev)
         to = tables if out_tables is None else _tables(out_tables, "out_tables", requests, dev)
-    kept = torch.empty((requests, heads, budget), dtype=torch.int32, device=dev)
+    kept = torch.empty(requests, heads, budget, dtype=torch.int32, device=dev)
     new_lens = torch.empty(requests, dtype=torch.int32, device=dev)
     width = budget
     if mass_out is None:
-        mass_out = torch.empty((requests, heads, budget), dtype=torch.float32, device=dev)
+        mass_out = torch.empty(requests, heads, budget, dtype=torch.float32, device=dev)
         out = mass_out.data_ptr()
     else:
         if _tensor(mass_out, "mass_out").dim() != 3 or mass_out.shape[2] < budget:
