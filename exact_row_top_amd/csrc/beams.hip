@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) beam_segment_kernel(const BeamParams q) {
 // each wave takes its first k.
 //
 // Bound by the waits between these steps, a few microseconds whatever the
-// sizes: 4 rows of 32768 take 8 us, 240 of 50001 9, 256 of 131072 13.
+// sizes: 4 rows of 32768 take 7.3 us, 240 of 50001 8.7, 256 of 131072 12.6.
 // ---------------------------------------------------------------------------
 
 namespace {
@@ -214,12 +214,19 @@ __device__ __forceinline__ void rank_list(const ListEntry* list, int n, int k, F
   const int t = threadIdx.x;
   if (n <= 64) {
     if (t >= 64) return;
-    const ListEntry e = t < n ? list[t] : ListEntry{-__builtin_inff(), 0x7FFFFFFF};
+    const ListEntry e = t < n ? list[t] : ListEntry{0.0f, 0};
+    const uint64_t mine = t < n ? (uint64_t)fkey(e.x) << 32 | (0xFFFFFFFFu - (uint32_t)e.i) : 0u;
     int c = 0;
-    for (int j = 0; j < n; ++j) {
-      const float x = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(e.x), j));
-      const int i = __builtin_amdgcn_readlane(e.i, j);
-      c += (x > e.x || (x == e.x && i < e.i)) ? 1 : 0;
+    // (lanes by number: eight at a time take what one did with a running index)
+#pragma unroll
+    for (int j0 = 0; j0 < 64; j0 += 8) {
+      if (j0 >= n) break;
+#pragma unroll
+      for (int j = j0; j < j0 + 8; ++j) {
+        const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), j) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)mine, j);
+        c += other > mine ? 1 : 0;
+      }
     }
     if (t < n && c < k) f(e, c);
     return;
@@ -237,17 +244,18 @@ __device__ __forceinline__ void rank_list(const ListEntry* list, int n, int k, F
 }
 
 // The largest value whose lowest `low` bits are zero that at least k of the
-// wave's keys (N a lane) reach.
+// wave's keys (N a lane) reach: two bits at a time.
 template <int N>
 __device__ __forceinline__ uint32_t kth_key(const uint32_t (&key)[N], int k, int low) {
   uint32_t thr = 0;
 #pragma unroll 1
-  for (int b = 31; b >= low; --b) {
-    const uint32_t at = thr | (1u << b);
-    int n = 0;
+  for (int b = 30; b >= low; b -= 2) {
+    int n[3] = {0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= at));
-    if (n >= k) thr = at;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int d = 0; d < 3; ++d) n[d] += __popcll(__ballot(key[i] >= (thr | ((uint32_t)(d + 1) << b))));
+    thr |= (uint32_t)((n[0] >= k) + (n[1] >= k) + (n[2] >= k)) << b;
   }
   return thr;
 }
@@ -262,6 +270,17 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
   const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
   const int row = blockIdx.x, req = row / q.beams, beam = row - req * q.beams;
   const int k = q.k, segs = q.segments;
+  // a wave holds NV * 256 neighbouring chunks, a lane four in each piece (asked
+  // for before it is known whether the beam reads them)
+  const int chunks = segs * 64, c0 = wv * NV * 256 + lane * 4;
+  const float* maxima = q.chunks + (int64_t)row * chunks;
+  float v[NV][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float4 x{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+    if (c0 + j * 256 < chunks) x = *reinterpret_cast<const float4*>(maxima + c0 + j * 256);
+    v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+  }
   const float score = q.scores[row];
   const bool ended = q.ended && q.ended[row];
   const bool reads = offers(score) && !ended;
@@ -278,17 +297,7 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
     __syncthreads();
     if (t == 0) sh.out[0] = BeamCandidate{(double)score / norm, score, q.end_token};
   } else if (reads) {
-    // a wave holds NV * 256 neighbouring chunks, a lane four in each piece
-    const int chunks = segs * 64, c0 = wv * NV * 256 + lane * 4;
-    const float* from = q.chunks + (int64_t)row * chunks;
-    float v[NV][4];
     float top = -__builtin_inff();
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float4 x{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
-      if (c0 + j * 256 < chunks) x = *reinterpret_cast<const float4*>(from + c0 + j * 256);
-      v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
-    }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -306,15 +315,28 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
     if (m > -__builtin_inff()) {
       const uint32_t sets[2] = {sh.keys[lane], sh.keys[64 + lane]};
       const uint32_t thr = max(kth_key(sets, k, 16), fkey(-__builtin_inff()) + 1u);
-      uint32_t room = (uint32_t)q.cap;
+      const uint32_t room = (uint32_t)q.cap;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        // the four of a piece together: one count of the list's entries
+        uint64_t in[4];
+        uint32_t all = 0, at = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool in = fkey(v[j][e]) >= thr;
-          const uint32_t at = append(in, &sh.n[0]);
-          if (in && at < room) list[at] = ListEntry{v[j][e], c0 + j * 256 + e};
+          in[e] = __ballot(fkey(v[j][e]) >= thr);
+          all += (uint32_t)__popcll(in[e]);
         }
+        if (all == 0) continue;
+        if (lane == 0) at = atomicAdd(&sh.n[0], all);
+        at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t mine = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(in[e] >> 32),
+                                                               __builtin_amdgcn_mbcnt_lo((uint32_t)in[e], 0u));
+          if ((in[e] >> lane & 1) && mine < room) list[mine] = ListEntry{v[j][e], c0 + j * 256 + e};
+          at += (uint32_t)__popcll(in[e]);
+        }
+      }
       __syncthreads();
       int n = (int)sh.n[0];
       if (n > q.cap) {
@@ -423,21 +445,28 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
     rest[i] = agent_load(from + 2 * i + 1);
   }
   __syncthreads();
-  for (int i = t; i < all; i += kBeamBlock) {
+  // up to 512 are counted: those before one in the list that are not less, those
+  // behind it that are more (lists stand in falling order, ties by beam), by up
+  // to 32 neighbouring threads each
+  int sharers = 1;
+  while (sharers < 32 && 2 * sharers * all <= kBeamBlock) sharers *= 2;
+  for (int n = t; n < all * sharers; n += kBeamBlock) {
+    const int i = n / sharers, first = n - i * sharers;
     BeamCandidate c;
     c.rank = rank[i];
     __builtin_memcpy(&c.total, &rest[i], 8);
-    if (c.token < 0) continue;
-    atomicAdd(&sh.n[0], 1u);
     const int b = i / k;
-    int place = i - b * k;
-    if (all <= 512) {
-      // counted: those before it in the list that are not less, those behind
-      // it that are more (lists stand in falling order, ties by beam)
-      place = 0;
-#pragma unroll 8
-      for (int j = 0; j < all; ++j) place += (rank[j] > c.rank || (rank[j] == c.rank && j < i)) ? 1 : 0;
-    } else {
+    int place = 0;
+    if (all <= kBeamBlock) {
+#pragma unroll 4
+      for (int j = first; j < all; j += sharers)
+        place += (rank[j] > c.rank || (rank[j] == c.rank && j < i)) ? 1 : 0;
+      for (int d = 1; d < sharers; d <<= 1) place += __shfl_xor(place, d);
+    }
+    if (first > 0 || c.token < 0) continue;
+    atomicAdd(&sh.n[0], 1u);
+    if (all > kBeamBlock) {
+      place = i - b * k;
       for (int o = 0; o < q.beams && place < k; ++o) {
         if (o == b) continue;
         // entries of beam o before c: in falling order, and the same from an
