@@ -38,6 +38,7 @@ __device__ __forceinline__ uint4 load16(const unsigned char* p) {
 // in scalar registers, as in Exp2Poly.)  Ranks need totals far better than
 // 32-bit sums would make them, and this is a third cheaper than weights that
 // are whole numbers, which add up exactly in any order.
+constexpr double kShift = 6755399441055744.0;
 struct Exp2Short {
   double k1, k2, k3, k4, k5, k6, k7, k8;
   __device__ __forceinline__ Exp2Short()
@@ -48,9 +49,12 @@ struct Exp2Short {
     asm("" : "+s"(k5), "+s"(k6), "+s"(k7), "+s"(k8));
   }
   __device__ __forceinline__ double operator()(double s) const {
-    const double magic = 6755399441055744.0;
     s = __builtin_fmax(s, -1000.0);
-    const double sm = s + magic, f = s - (sm - magic);
+    const double sm = s + kShift;
+    return scaled(s - (sm - kShift), sm);
+  }
+  // 2^f times 2 to the power of the whole number in sm's low bits.
+  __device__ __forceinline__ double scaled(double f, double sm) const {
     double p = __builtin_fma(f, k8, k7);
     p = __builtin_fma(p, f, k6);
     p = __builtin_fma(p, f, k5);
@@ -114,10 +118,7 @@ __global__ void __launch_bounds__(256) beam_segment_kernel(const BeamParams q) {
   for (int g = 0; g < G; ++g) {
     float m = -__builtin_inff();
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      x[g][e] = x[g][e] > -__builtin_inff() ? x[g][e] : -__builtin_inff();  // NaN too
-      m = fmaxf(m, x[g][e]);
-    }
+    for (int e = 0; e < V; ++e) m = fmaxf(m, x[g][e]);  // (passes over NaN)
 #pragma unroll
     for (int d = 1; d < L; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
     top = fmaxf(top, m);
@@ -139,18 +140,33 @@ __global__ void __launch_bounds__(256) beam_segment_kernel(const BeamParams q) {
     // (four scores at a time: with more in flight the registers leave room
     // for fewer waves)
     const Exp2Short exp2;
-    const double base = -(double)best * kLog2e;
+    auto add_all = [&](auto&& weight) {
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+      for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        mass += exp2(__builtin_fma((double)x[g][e], kLog2e, base));
-        if (e % 4 == 3) {
-          asm("" : "+v"(mass));
-          __builtin_amdgcn_sched_barrier(0);
+        for (int e = 0; e < V; ++e) {
+          mass += weight(x[g][e]);
+          if (e % 4 == 3) {
+            asm("" : "+v"(mass));
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
-      }
-    mass = wave_sum(mass);
+      mass = wave_sum(mass);
+    };
+    if (__builtin_fabsf(best) < 0x1p20f) {
+      // 2^((x - best) log2(e)) as 2^(x log2(e) + whole) times the rest of -best
+      // log2(e), once for all; what is 690 below the largest weighs nothing
+      const float low = best - 690.0f;
+      const double whole = __builtin_rint(-(double)best * kLog2e), shift = kShift + whole;
+      add_all([&](float v) {
+        const double d = (double)fmaxf(v, low), sm = __builtin_fma(d, kLog2e, shift);
+        return exp2.scaled(__builtin_fma(d, kLog2e, -(sm - shift)), sm);
+      });
+      mass *= exp2(__builtin_fma(-(double)best, kLog2e, -whole));
+    } else {
+      // (too large for products apart: the difference first)
+      add_all([&](float v) { return exp2(((double)v - (double)best) * kLog2e); });
+    }
   }
   if (lane == 0) {
     q.bests[id] = best;
@@ -190,7 +206,7 @@ struct BeamShared {
   int32_t chosen[kMaxBeamK];
   float least;
   float best[kBeamWaves];
-  double lse;
+  double weight;   // ln of the row's weights' sum against its largest score
   uint32_t n[3];
   uint32_t turn;
   BeamCandidate out[kMaxBeamK];
@@ -389,8 +405,7 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-        sum = log(sum);
-        if (lane == 0) sh.lse = m == __builtin_inff() ? sum : (double)m + sum;
+        if (lane == 0) sh.weight = log(sum);
       }
       __syncthreads();
       const float least = sh.least;
@@ -409,9 +424,10 @@ __global__ void __launch_bounds__(kBeamBlock) beam_row_kernel(const BeamParams q
         if (in) list[at] = ListEntry{x, pos};
       }
       __syncthreads();
-      const double lse = sh.lse;
+      const double weight = sh.weight;
       rank_list(list, (int)sh.n[2], k, [&](const ListEntry& e, int r) {
-        const double total = (double)score + (m == __builtin_inff() ? -lse : (double)e.x - lse);
+        // (differences first: the largest score may be far larger than they are)
+        const double total = (double)score + ((m == __builtin_inff() ? 0.0 : (double)e.x - (double)m) - weight);
         sh.out[r] = BeamCandidate{total / norm, (float)total, e.i};
       });
     }

@@ -28,7 +28,8 @@ def beams(x, scores, k, ended=None, end_token=0, lengths=None, penalty=0.0):
             live = np.flatnonzero(row == np.inf)
             lse, base = float(np.log(LD(live.size))), np.zeros(row.size)
         else:
-            lse, base = float(LD(top) + np.log(np.exp((row[live] - top).astype(LD)).sum())), row
+            # (against the largest: its own size would swallow the sum's logarithm)
+            lse, base = float(np.log(np.exp((row[live] - top).astype(LD)).sum())), row - top
         for i in live[np.argsort(-base[live], kind="stable")[:k]]:
             total = s + (base[i] - lse)
             found.append((total / norm, b, int(i), total))

@@ -100,6 +100,21 @@ def test_beam_ended_lengths_and_dead_beams(ert):
                              lengths=n, penalty=penalty, end_token=7)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_beam_scores_far_from_zero(ert, dtype):
+    rng = np.random.default_rng(8)
+    R, W, V = 2, 4, 5003
+    for at in (300.0, 6e4, 2.0 ** 20 - 3, 2.0 ** 20 + 3, 3e7, 1e12, 1e17, 1e30, 3e38):
+        if dtype == "fp16" and at > 6e4:
+            continue
+        for sign in (1.0, -1.0):
+            row = sign * at + rng.normal(0, 2, (R * W, V))
+            row[:, ::7] -= rng.exponential(1.0, (R * W, (V + 6) // 7)) * at * 0.1
+            row[:, 5], row[:, 6] = NINF, NAN
+            x = _cuda(np.clip(row, -3.38e38, 3.38e38).astype(np.float32), _dt(dtype))
+            _check_beams(ert, x, rng.uniform(-9, -1, (R, W)), 6, f"{dtype} around {sign * at}")
+
+
 def test_beam_first_step(ert):
     # all beams hold the same row; only the first has a score
     rng = np.random.default_rng(6)
