@@ -695,9 +695,9 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
 // ---------------------------------------------------------------------------
 // Joins a row's pieces: a wave a row, its lanes in 64 / (dim / 4) sets that
 // take turns at the pieces.  Bound by reading them: 4096 rows of about 18
-// pieces, 38 MB, take 11.2 us (3.4 TB/s), 128 rows 4.8, where the waits for
+// pieces, 38 MB, take 10.7 us (3.6 TB/s), 128 rows 4.3, where the waits for
 // what says where the pieces lie are the whole; a small row's pieces are asked
-// for before its largest score is known (1120 rows 4.9 instead of 6.3).
+// for before its largest score is known (1120 rows 4.8 instead of 6.3).
 // ---------------------------------------------------------------------------
 template <class T, int DIM>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) {
@@ -815,8 +815,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) 
 //
 // Bound by memory and by the exponentials, one a (position, query): 8 groups of
 // 64 queries a key head over some 6 thousand positions each, and 64 sequences'
-// own 128 to 256, 122 MB, take 31 us (3.9 TB/s), of them about 14 exponentials
-// and sums if nothing ran beside them.  Four tiles a wave: two take 36, for
+// own 1 to 256, 122 MB, take 31 us (3.9 TB/s): 28 for the reading alone, 22 for
+// the products and exponentials alone.  Four tiles a wave: two take 36, for
 // their first loads, eight the same and 15 instead of 9 where there are few.
 // ---------------------------------------------------------------------------
 namespace {

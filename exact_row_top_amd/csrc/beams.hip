@@ -78,8 +78,8 @@ __device__ __forceinline__ bool offers(float score) { return __builtin_fabsf(sco
 // the weights' sum against it, and the largest of each 32 neighbours.
 //
 // Bound by the 64-bit exponentials where the scores are 16 bits wide: 240 rows
-// of 50001, 24 MB, take 13.5 us (1.8 TB/s); and nearly by memory where they
-// are 32: 256 rows of 131072, a tenth of them ended, 121 MB, take 28 us (4.3
+// of 50001, 24 MB, take 13.9 us (1.7 TB/s); and nearly by memory where they
+// are 32: 256 rows of 131072, a tenth of them ended, 121 MB, take 27 us (4.5
 // TB/s).
 // ---------------------------------------------------------------------------
 template <class T>

@@ -39,7 +39,7 @@ struct KeepShared {
 // HELD are read again in every pass (HELD 0).
 //
 // Bound by the passes' waits and by the counting: 128 rows of 8192, which leave
-// half of the compute units idle, take 11.7 us, one row of 1000 positions 8.
+// half of the compute units idle, take 11 us, one row of 5003 positions 8.
 // ---------------------------------------------------------------------------
 template <int HELD>
 __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams q) {
