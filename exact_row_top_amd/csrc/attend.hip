@@ -72,6 +72,13 @@ __device__ __forceinline__ void group_range(const AttendParams& q, int g, int& s
   }
 }
 
+// Which of the groups g0 .. g0 + 63 end before they start: groups could overlap
+// without bound then, and no group has a prefix.  (All lanes of a wave together.)
+__device__ __forceinline__ uint64_t falling_starts(const AttendParams& q, int g0) {
+  const int g = g0 + (int)(threadIdx.x & 63);
+  return __ballot(q.starts && g < q.groups && q.starts[g + 1] < q.starts[g]);
+}
+
 // Sums over a wave's lanes up to each, and steps and strips of groups.
 struct GroupScan {
   int steps, strips;      // of this lane's group
@@ -621,8 +628,7 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
     int all = 0, strips = 0;
     uint64_t falls = 0;
     for (int g0 = 0; g0 < q.groups; g0 += 64) {
-      const int g = g0 + lane;
-      falls |= __ballot(q.starts && g < q.groups && q.starts[min(g, q.groups - 1) + 1] < q.starts[min(g, q.groups - 1)]);
+      falls |= falling_starts(q, g0);
       const GroupScan c = scan_groups(q, g0, 32 * QW, KT, all, strips);
       if (blockIdx.x == 0 && threadIdx.x < 64 && g0 + (int)threadIdx.x < q.groups)
         q.group_at[g0 + threadIdx.x] = int4{c.step_end - c.steps, c.strip_end - c.strips, 0, 0};
@@ -871,7 +877,9 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
   if (shared) {
     int s1;
     group_range(q, entry, seq0, s1);
-    seqs = s1 - seq0;
+    uint64_t falls = 0;
+    for (int g0 = 0; g0 < q.groups; g0 += 64) falls |= falling_starts(q, g0);
+    seqs = falls ? 0 : s1 - seq0;   // (the log-sums then lack all prefixes)
     cut = 0;
   }
   const int rows = seqs * q.next_n * q.per;

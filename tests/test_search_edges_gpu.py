@@ -1,0 +1,48 @@
+"""A beam search's operators where their other tests do not reach: group starts
+that fall in part, bounds of zero, bounds that cut, scores of any size, small
+weights in float16, more rows than a tile holds, long rows, refusals that leave
+everything as it was, and the documented loop over several steps."""
+import numpy as np
+import pytest
+
+from gpu_helpers import log
+from test_search_ops_gpu import (HALF, NINF, Case, _check_attend, _check_beams, _check_evict, _check_mass, _cuda, _dt,
+                                 ert)  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# group starts that fall in part: groups that overlap
+# ---------------------------------------------------------------------------
+
+FALLS = [([2, 2, 2], [0, 6, 2, 6]), ([2, 2, 2], [0, 4, 1, 6]), ([40, 30, 40], [0, 110, 2, 110]),
+         ([1, 0, 2, 1], [0, 3, 2, 2, 4])]
+
+
+@pytest.mark.parametrize("members,starts", FALLS)
+@pytest.mark.parametrize("room", [0, 1 << 21])
+def test_attention_leaves_out_prefixes_of_overlapping_groups(ert, members, starts, room):
+    c = Case("bf16", 64, 16, members, 200, 50, 8, 2, plens=[200, 150, 100, 50][:len(members)])
+    c.starts = np.array(starts, dtype=np.int32)
+    c.group = lambda s: None
+    _check_attend(ert, c, f"starts {starts} room {room}", room=room)
+
+
+@pytest.mark.parametrize("members,starts", FALLS)
+def test_mass_leaves_out_prefixes_of_overlapping_groups(ert, members, starts):
+    c = Case("bf16", 64, 16, members, 200, 50, 8, 2, plens=[200, 150, 100, 50][:len(members)])
+    c.starts = np.array(starts, dtype=np.int32)
+    c.group = lambda s: None
+    _check_mass(ert, c, f"starts {starts}")
+
+
+def test_mass_of_more_groups_than_a_wave_with_starts_that_fall_late(ert):
+    members = [1] * 150
+    c = Case("fp16", 64, 16, members, 40, 20, 4, 2)
+    _check_mass(ert, c, "150 groups")
+    c.starts[140:] = 130
+    c.group = lambda s: None
+    _check_mass(ert, c, "150 groups, falling at the 140th")
+
+
