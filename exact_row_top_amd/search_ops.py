@@ -329,6 +329,23 @@ def _attend_arguments(q, k_cache, prefix_tables, prefix_lens, block_tables, kv_l
             (tokens, heads, kv_heads, dim, seqs, groups, next_n))
 
 
+def _bounds(tables, block_size, max_prefix_len, max_len):
+    """(tables, bounds, positions that the rows hold within them): the C calls
+    take a bound of 0 for none, so a bound of zero takes the table's width."""
+    tables = list(tables)
+    bounds, room = [], []
+    for at, name, bound in ((2, "max_prefix_len", max_prefix_len), (8, "max_len", max_len)):
+        if bound is not None:
+            bound = _int32(bound, name)
+            if bound < 0:
+                raise ValueError(f"{name} must not be negative")
+            if bound == 0:
+                tables[at] = 0
+        bounds.append(bound or 0)
+        room.append(min(tables[at] * block_size, bound or tables[at] * block_size))
+    return tables, bounds, room
+
+
 def _cache_layout(cache, name, dtype, dim, device):
     """(pointer, block, slot and head strides) of a cache."""
     try:
@@ -358,8 +375,8 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_lens, block_tabl
     [groups, max_blocks]; None: no prefixes); token t of sequence s then sees
     the first kv_lens[s] - next_n + t + 1 positions of block_tables[s], its
     own.  scale: dim ** -0.5 unless given, never negative.  max_prefix_len and
-    max_len bound the lengths (which are cut to them) where the tables have
-    room for far more: the work is planned for the longest rows there can be.
+    max_len (0 and up) bound the lengths (which are cut to them) where the tables
+    have room for far more: the work is planned for the longest rows there can be.
 
     Returns out, [sequences * next_n, heads, dim] in q's type, or (out, lse)
     with the float32 log-sums [sequences * next_n, heads], which attention_mass
@@ -377,22 +394,19 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_lens, block_tabl
     values = _cache_layout(v_cache, "v_cache", q.dtype, dim, dev)
     if v_cache.shape != k_cache.shape:
         raise ValueError("v_cache must have k_cache's shape")
-    most = 0 if max_prefix_len is None else _int32(max_prefix_len, "max_prefix_len")
-    most_own = 0 if max_len is None else _int32(max_len, "max_len")
-    if most < 0 or most_own < 0:
-        raise ValueError("max_prefix_len and max_len must not be negative")
+    bounds, room = (0, 0), (tables[2] * paging[1], tables[8] * paging[1])
+    if max_prefix_len is not None or max_len is not None:
+        tables, bounds, room = _bounds(tables, paging[1], max_prefix_len, max_len)
     if out is None:
         out = torch.empty(tokens, heads, dim, dtype=q.dtype, device=dev)
     else:
         out = _matrix(out, "out", q.dtype, (tokens, heads, dim), dev)
     lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev) if return_lse else None
     lib = _lib()
-    room, room_own = tables[2] * paging[1], tables[8] * paging[1]
     nbytes = lib.topk_attend_workspace_bytes(groups, seqs, tables[4] is not None, next_n, heads, kv_heads,
-                                             dim, min(room, most) if most else room,
-                                             min(room_own, most_own) if most_own else room_own)
+                                             dim, *room)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _check(lib.topk_attend(*query, *keys, *values, *paging, *tables, most, most_own, out.data_ptr(),
+    _check(lib.topk_attend(*query, *keys, *values, *paging, *tables, *bounds, out.data_ptr(),
                            lse.data_ptr() if lse is not None else None, ws.data_ptr(), nbytes,
                            _raw_stream(dev)))
     return (out, lse) if return_lse else out

@@ -46,3 +46,13 @@ def test_mass_of_more_groups_than_a_wave_with_starts_that_fall_late(ert):
     _check_mass(ert, c, "150 groups, falling at the 140th")
 
 
+# ---------------------------------------------------------------------------
+# bounds
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("limit,own", [(0, None), (None, 0), (0, 0), (0, 31), (100, 0), (1, 1)])
+def test_attention_bounds_of_zero(ert, limit, own):
+    c = Case("bf16", 64, 16, [3, 2], 333, 77, 8, 2, next_n=2)
+    _check_attend(ert, c, f"limits {limit} {own}", limit=limit, own=own)
+
+
