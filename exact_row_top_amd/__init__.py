@@ -144,6 +144,9 @@ def load_library():
     lib.topk_attend_mass.argtypes = (heads + [P, I64, I64, I64, I64, I32] + tables
                                      + [P, F32, P, P, I32, P, P, I32, P])
     lib.topk_attend_mass.restype = ctypes.c_int
+    lib.topk_attend_mass_bounded.argtypes = (heads + [P, I64, I64, I64, I64, I32] + tables
+                                             + [I64, I64, P, F32, P, P, I32, P, P, I32, P])
+    lib.topk_attend_mass_bounded.restype = ctypes.c_int
     lib.topk_evict_keep.argtypes = [P, I64, I64, I32, I32, I32, P, I32, I32, I32, P, P, I32, P, P]
     lib.topk_evict_keep.restype = ctypes.c_int
     lib.topk_evict_move.argtypes = [P, I32, I32, I32, P, I64, I32, P, I64, I32, I32, I32, P, I64, I64, P]

@@ -506,18 +506,19 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
   return launch(attend_join_kernel_ptr(dtype, dim), (rows + 3) / 4, 256, &p, 0, stream);
 }
 
-int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
-                     int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
-                     int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, int64_t num_blocks,
-                     int32_t block_size, const int32_t* shared_tables, int64_t shared_stride,
-                     int32_t shared_width, const int32_t* shared_lens, const int32_t* group_starts,
-                     int32_t num_groups, const int32_t* own_tables, int64_t own_stride, int32_t own_width,
-                     const int32_t* own_lens, float scale, const float* lse, float decay,
-                     const float* shared_mass, float* shared_out, int32_t shared_positions,
-                     const float* own_mass, float* own_out, int32_t own_positions, hipStream_t stream) {
+int topk_attend_mass_bounded(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
+                             int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
+                             int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, int64_t num_blocks,
+                             int32_t block_size, const int32_t* shared_tables, int64_t shared_stride,
+                             int32_t shared_width, const int32_t* shared_lens, const int32_t* group_starts,
+                             int32_t num_groups, const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                             const int32_t* own_lens, float scale, int64_t max_shared_len, int64_t max_own_len,
+                             const float* lse, float decay, const float* shared_mass, float* shared_out,
+                             int32_t shared_positions, const float* own_mass, float* own_out, int32_t own_positions,
+                             hipStream_t stream) {
   const AttendShape s{dtype, num_groups, num_seqs, next_n, num_heads, num_kv_heads, dim, block_size, num_blocks};
   if (!attend_shape_ok(s, group_starts) || !(scale >= 0.0f) || isinf(scale) || q_stride < 0 || q_head_stride < 0 ||
-      !isfinite(decay) || shared_positions < 0 || shared_positions > kMaxPositions || own_positions < 0 ||
+      max_shared_len < 0 || max_own_len < 0 || !isfinite(decay) || shared_positions < 0 || shared_positions > kMaxPositions || own_positions < 0 ||
       own_positions > kMaxPositions)
     return TOPK_EINVAL;
   if (num_seqs > 0 && (!q || !lse)) return TOPK_EINVAL;
@@ -539,8 +540,8 @@ int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_h
   if (rc != TOPK_OK) return rc;
   rc = tables_ok(own_tables, own_stride, own_width, own_lens, num_seqs);
   if (rc != TOPK_OK) return rc;
-  const int64_t most_shared = longest_of(num_groups > 0 ? shared_width : 0, block_size, num_blocks, 0);
-  const int64_t most_own = longest_of(own_width, block_size, num_blocks, 0);
+  const int64_t most_shared = longest_of(num_groups > 0 ? shared_width : 0, block_size, num_blocks, max_shared_len);
+  const int64_t most_own = longest_of(own_width, block_size, num_blocks, max_own_len);
   if (most_shared < 0 || most_own < 0) return TOPK_EINVAL;
   const int64_t shared_tiles = ((int64_t)shared_positions + kMassStep - 1) / kMassStep;
   const int64_t own_tiles = ((int64_t)own_positions + kMassStep - 1) / kMassStep;
@@ -566,6 +567,22 @@ int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_h
   p.own_tiles = (int32_t)own_tiles;
   p.shared_wgs = shared_wgs;
   return launch(attend_mass_kernel_ptr(dtype, dim), shared_wgs + own_wgs, kMassBlock, &p, 0, stream);
+}
+
+int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
+                     int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
+                     int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, int64_t num_blocks,
+                     int32_t block_size, const int32_t* shared_tables, int64_t shared_stride,
+                     int32_t shared_width, const int32_t* shared_lens, const int32_t* group_starts,
+                     int32_t num_groups, const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                     const int32_t* own_lens, float scale, const float* lse, float decay,
+                     const float* shared_mass, float* shared_out, int32_t shared_positions,
+                     const float* own_mass, float* own_out, int32_t own_positions, hipStream_t stream) {
+  return topk_attend_mass_bounded(q, dtype, q_stride, q_head_stride, num_seqs, next_n, num_heads, num_kv_heads, dim,
+                                  k_cache, k_block_stride, k_slot_stride, k_head_stride, num_blocks, block_size,
+                                  shared_tables, shared_stride, shared_width, shared_lens, group_starts, num_groups,
+                                  own_tables, own_stride, own_width, own_lens, scale, 0, 0, lse, decay, shared_mass,
+                                  shared_out, shared_positions, own_mass, own_out, own_positions, stream);
 }
 
 int topk_evict_keep(const float* mass, int64_t request_stride, int64_t head_stride, int32_t positions,

@@ -433,12 +433,13 @@ def _mass(mass, out, name, entries, kv_heads, positions, device):
 
 def attention_mass(q, k_cache, lse, prefix_tables, prefix_lens, block_tables, kv_lens, *,
                    group_starts=None, next_n=1, scale=None, prefix_mass=None, mass=None, decay=1.0,
-                   prefix_out=None, out=None, stream=None):
+                   prefix_out=None, out=None, max_prefix_len=None, max_len=None, stream=None):
     """Accumulated attention mass of cached positions: decay times the mass
     given, plus the weights that the step's tokens gave each position, added up
     over the tokens and the query heads of a key head.
 
-    q to scale as in the prefix_attention call that gave lse.  prefix_mass:
+    q to scale, max_prefix_len and max_len as in the prefix_attention call that
+    gave lse: positions behind the bounds have no part in it.  prefix_mass:
     float32 [groups, kv_heads, positions], mass: float32 [sequences, kv_heads,
     positions] (None: zeros, as many positions as the tables hold).  prefix_out
     and out: where the results go, may be prefix_mass and mass.  Returns
@@ -449,7 +450,8 @@ def attention_mass(q, k_cache, lse, prefix_tables, prefix_lens, block_tables, kv
             return attention_mass(q, k_cache, lse, prefix_tables, prefix_lens, block_tables, kv_lens,
                                   group_starts=group_starts, next_n=next_n, scale=scale,
                                   prefix_mass=prefix_mass, mass=mass, decay=decay,
-                                  prefix_out=prefix_out, out=out)
+                                  prefix_out=prefix_out, out=out, max_prefix_len=max_prefix_len,
+                                  max_len=max_len)
     dev, query, keys, paging, tables, sizes = _attend_arguments(
         q, k_cache, prefix_tables, prefix_lens, block_tables, kv_lens, group_starts, next_n, scale)
     tokens, heads, kv_heads, dim, seqs, groups, next_n = sizes
@@ -464,9 +466,12 @@ def attention_mass(q, k_cache, lse, prefix_tables, prefix_lens, block_tables, kv
         shared, given_shared, prefix_out = _mass(prefix_mass, prefix_out, "prefix_mass", groups, kv_heads,
                                                  tables[2] * paging[1], dev)
     own, given_own, out = _mass(mass, out, "mass", seqs, kv_heads, tables[8] * paging[1], dev)
-    _check(_lib().topk_attend_mass(*query, *keys, *paging, *tables, weights, float(decay), given_shared,
-                                   prefix_out.data_ptr() if prefix_out is not None else None, shared,
-                                   given_own, out.data_ptr(), own, _raw_stream(dev)))
+    bounds = (0, 0)
+    if max_prefix_len is not None or max_len is not None:
+        tables, bounds, _ = _bounds(tables, paging[1], max_prefix_len, max_len)
+    _check(_lib().topk_attend_mass_bounded(*query, *keys, *paging, *tables, *bounds, weights, float(decay),
+                                           given_shared, prefix_out.data_ptr() if prefix_out is not None else None,
+                                           shared, given_own, out.data_ptr(), own, _raw_stream(dev)))
     return prefix_out, out
 
 

@@ -649,6 +649,20 @@ int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_h
                      const float* shared_mass, float* shared_out, int32_t shared_positions,
                      const float* own_mass, float* own_out, int32_t own_positions, hipStream_t stream);
 
+/* The same with the bounds that the topk_attend call was given: it cut lengths to
+ * them (0: none), and its log-sums hold no position behind. */
+int topk_attend_mass_bounded(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride,
+                             int32_t num_seqs, int32_t next_n, int32_t num_heads, int32_t num_kv_heads,
+                             int32_t dim, const void* k_cache, int64_t k_block_stride, int64_t k_slot_stride,
+                             int64_t k_head_stride, int64_t num_blocks, int32_t block_size,
+                             const int32_t* shared_tables, int64_t shared_stride, int32_t shared_width,
+                             const int32_t* shared_lens, const int32_t* group_starts, int32_t num_groups,
+                             const int32_t* own_tables, int64_t own_stride, int32_t own_width,
+                             const int32_t* own_lens, float scale, int64_t max_shared_len,
+                             int64_t max_own_len, const float* lse, float decay, const float* shared_mass,
+                             float* shared_out, int32_t shared_positions, const float* own_mass,
+                             float* own_out, int32_t own_positions, hipStream_t stream);
+
 /* The cached positions that stay: of request r's n = kv_lens[r] positions (cut
  * to [0, positions]) in each of num_heads rows of mass (strides in elements),
  * all where n <= budget, else the first `sinks`, the last `recent`, and the

@@ -56,3 +56,23 @@ def test_attention_bounds_of_zero(ert, limit, own):
     _check_attend(ert, c, f"limits {limit} {own}", limit=limit, own=own)
 
 
+@pytest.mark.parametrize("limit,own", [(None, None), (100, None), (None, 31), (100, 31), (0, 31), (100, 0), (0, 0), (5000, 5000)])
+def test_mass_within_the_bounds_of_its_attention(ert, limit, own):
+    import torch
+    c = Case("fp16", 64, 16, [3, 2], 333, 77, 8, 2, next_n=2, plens=[333, 90], lens=[77, 20, 33, 0, 60])
+    pt, pl, tab, lens = c.dev()
+    starts = _cuda(c.starts)
+    log(f"[mass] bounds {limit} {own}")
+    kw = dict(next_n=2, group_starts=starts)
+    bounds = dict(max_prefix_len=limit, max_len=own)
+    out, lse = ert.prefix_attention(c.q, c.k, c.v, pt, pl, tab, lens, return_lse=True, **kw, **bounds)
+    got = ert.attention_mass(c.q, c.k, lse, pt, pl, tab, lens, **kw, **bounds)
+    cut = [x if b is None else x.clamp(max=b) for x, b in ((pl, limit), (lens, own))]
+    want = ert.attention_mass(c.q, c.k, lse, pt, cut[0], tab, cut[1], **kw)
+    assert all(a.shape == b.shape and torch.equal(a, b) for a, b in zip(got, want))
+    # a token's weights sum to one: 64 bits over what the call wrote, heads of a key head together
+    rows = (lse > NINF).sum().item()
+    # (each weight to 2^-11 by its log-sum and score, sums in 32 bits)
+    assert abs(sum(float(m.double().sum()) for m in got) - rows) <= 2.0 ** -10 * max(rows, 1)
+
+

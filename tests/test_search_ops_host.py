@@ -251,3 +251,17 @@ def test_binding_refusals_on_the_device():
         with pytest.raises((ert.TopKError, ValueError)):
             f()
             pytest.fail(f"call {i} was taken")
+
+
+def test_c_refusals_of_bounded_mass():
+    """The bounds, and the checks that it shares with the call without them."""
+    f = ert.load_library().topk_attend_mass_bounded
+
+    def call(ms=0, mo=0, dim=128, lse=_at(9), po=_at(11), q=_at(0), scale=1.0, seqs=6):
+        return f(q, 1, 1024, 128, seqs, 1, 8, 2, dim, _at(1), 4096, 256, 128, 100, 16, _at(3), 8, 8, _at(4), _at(5), 3,
+                 _at(6), 4, 4, _at(7), scale, ms, mo, lse, 1.0, _at(10), po, 128, _at(12), _at(13), 64, None)
+
+    for change in (dict(ms=-1), dict(mo=-1), dict(dim=96), dict(lse=None), dict(po=None), dict(q=None), dict(scale=-1.0)):
+        assert call(**change) == EINVAL, change
+    for change in (dict(q=_at(0) + 8), dict(lse=_at(9) + 2), dict(po=_at(11) + 2)):
+        assert call(**change) == ELAYOUT, change
