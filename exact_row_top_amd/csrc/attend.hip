@@ -33,8 +33,12 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// kLift: the largest weights lie 2^kLift above 1 in the second product.  float16
+// loses bits below 2^-14 and everything below 2^-25: with it, below 2^-21 and
+// 2^-32 of the largest.  (With the 2^8 that the reference may lag, 2^15 at most.)
 struct Bf16 {
   typedef bf16x8 Vec;
+  static constexpr float kLift = 0.0f;
   static __device__ __forceinline__ f32x16 mfma(const Piece& a, const Piece& b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -43,6 +47,7 @@ struct Bf16 {
 };
 struct F16 {
   typedef f16x8 Vec;
+  static constexpr float kLift = 7.0f;
   static __device__ __forceinline__ f32x16 mfma(const Piece& a, const Piece& b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -447,11 +452,11 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
         const Pair h = both_halves(mx);
         mx = fmaxf(h.a, h.b) * q.scale;
       }
-      // The weights' reference follows the largest score only once that is
-      // over 2^8 times the reference's weight: weights of up to 2^8 lose
+      // The weights' reference, the largest score less kLift, follows it only
+      // once that is over 2^8 times what it was: weights of up to 2^8 more lose
       // nothing, and sums are seldom scaled again.
-      if (__ballot(mx > top + 8.0f)) {
-        const float now = fmaxf(mx, top);
+      if (__ballot(mx > top + (8.0f + T::kLift))) {
+        const float now = fmaxf(mx - T::kLift, top);
         const float f = now == kNone ? 0.0f : __builtin_amdgcn_exp2f(top - now);
         top = now;
         sum *= f;
@@ -468,6 +473,8 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
         for (int i = 0; i < 8; ++i) {
           const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u / 2][u % 2 * 8 + i], q.scale, -ref));
           part[i % 2] += p;
+          // (to the cache's type, as the matrix instructions take them; the sum, which
+          // the log-sum is made of, keeps 32 bits)
           w[u][i] = (typename T::Value)p;
         }
       sum += part[0] + part[1];

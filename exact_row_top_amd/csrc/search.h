@@ -158,7 +158,7 @@ struct AttendParams {
   int64_t rows;              // seqs * next_n * heads
   int4* group_at;            // [groups + 1]: first step, first strip; steps of all
   float* shared_parts;       // [kv_heads][shared_wgs + strips][32 query_waves][dim]: weighted values
-  float2* shared_stats;      // the same rows: largest score (log2), sum of weights
+  float2* shared_stats;      // the same rows: the weights' reference (log2), their sum
   float* own_parts;          // [own_splits][seqs][kv_heads][next_n * per][dim]
   float2* own_stats;
   unsigned char* out;        // [rows][dim]

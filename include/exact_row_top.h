@@ -608,8 +608,8 @@ int topk_reorder_blocks(const int32_t* block_tables, int64_t table_stride, int32
  * is not in [0, num_blocks) are left out.  Slots behind the lengths may hold
  * anything; values that some token of a sequence sees must be finite for all
  * of its tokens.  scale >= 0.  Scores, sums and the weighted values are 32-bit;
- * weights are rounded to the caches' type (float16: values whose weight is below
- * 2^-24 of the row's largest lose bits or vanish).
+ * weights are rounded to the caches' type for them (float16: weights below 2^-21
+ * of the row's largest lose bits there, those below 2^-32 vanish).
  *  out: [num_seqs * next_n][num_heads][dim] in q's type, contiguous, 16-byte
  *      aligned; lse: float [num_seqs * next_n][num_heads] or NULL.
  *  workspace: topk_attend_workspace_bytes(...) bytes (ragged: group_starts is

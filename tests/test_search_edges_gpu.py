@@ -76,3 +76,30 @@ def test_mass_within_the_bounds_of_its_attention(ert, limit, own):
     assert abs(sum(float(m.double().sum()) for m in got) - rows) <= 2.0 ** -10 * max(rows, 1)
 
 
+# ---------------------------------------------------------------------------
+# scores of any size, small weights
+# ---------------------------------------------------------------------------
+
+def test_attention_float16_keeps_the_weights_of_a_long_tail(ert):
+    """One key of weight 1 and 2^17 - 1 of 2^-25.5, which together are a 362nd of
+    the row, one wave over all of them."""
+    import torch
+    S, H, D, bs, n = 1024, 2, 64, 64, 1 << 17
+    blocks = n // bs
+    k = torch.zeros(blocks, bs, H, D, dtype=torch.float16, device="cuda")
+    v = torch.ones_like(k)
+    k[0, 0, :, 0], v[0, 0] = 17.6875, 0.0
+    q = torch.zeros(S, H, D, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1.0
+    tab = torch.arange(blocks, dtype=torch.int32, device="cuda").expand(S, blocks).contiguous()
+    lens = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    log("[attend] a tail of small weights")
+    out = ert.prefix_attention(q, k, v, None, None, tab, lens, scale=1.0).double()
+    tail = (n - 1) * np.exp(-17.6875)
+    want = tail / (1 + tail)
+    # each weight to half a step of float16's smallest, 2^-25, where the largest weighs 2^7 at least; the
+    # additions in 32 bits; out's own rounding
+    off = n * 2.0 ** -32 + want * (n * 2.0 ** -24 + 2.0 ** -11 + 2.0 ** -20)
+    assert float((out - want).abs().max()) <= off < want / 4
+
+
