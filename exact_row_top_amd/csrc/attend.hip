@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
       // The weights' reference, the largest score less kLift, follows it only
       // once that is over 2^8 times what it was: weights of up to 2^8 more lose
       // nothing, and sums are seldom scaled again.
-      if (__ballot(mx > top + (8.0f + T::kLift))) {
+      if (__ballot(mx - top > 8.0f + T::kLift)) {   // (the difference is exact where it counts)
         const float now = fmaxf(mx - T::kLift, top);
         const float f = now == kNone ? 0.0f : __builtin_amdgcn_exp2f(top - now);
         top = now;
@@ -465,13 +465,24 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[m][i] *= f;
       }
-      const float ref = top == kNone ? 0.0f : top;
+      float ref = top == kNone ? 0.0f : top, factor = q.scale;
+      // The reference is a rounded score.  Of scores beyond 2^16 the rounding
+      // would outgrow the lag, and from 2^28 on overflow the weights: both are
+      // rounded alike then, and none weighs more than the reference allows.
+      if (__ballot(__builtin_fabsf(mx) > 0x1p16f && mx > kNone)) {
+#pragma unroll
+        for (int n = 0; n < SUBS; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sc[n][i] = sc[n][i] * q.scale - ref;
+        factor = 1.0f;
+        ref = 0.0f;
+      }
       float part[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int u = 0; u < 2 * SUBS; ++u)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u / 2][u % 2 * 8 + i], q.scale, -ref));
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u / 2][u % 2 * 8 + i], factor, -ref));
           part[i % 2] += p;
           // (to the cache's type, as the matrix instructions take them; the sum, which
           // the log-sum is made of, keeps 32 bits)

@@ -80,6 +80,76 @@ def test_mass_within_the_bounds_of_its_attention(ert, limit, own):
 # scores of any size, small weights
 # ---------------------------------------------------------------------------
 
+@pytest.mark.parametrize("dtype,scale", [("fp16", 1.0), ("fp16", 64.0), ("bf16", 1.0), ("bf16", 2.0 ** 10)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("room", [0, 1 << 21])
+def test_attention_to_one_of_far_scores(ert, dtype, scale, sign, room):
+    """Scores whose last bits weigh more than their gaps' exponents: products are
+    exact, gaps are far, so all weight is the largest score's."""
+    import torch
+    rng = np.random.default_rng([3, sign + 1, room])
+    D, bs, G, W, H = 64, 16, 2, 140 if room else 5, 2
+    P, L = 320, 64
+    N = G * P // bs + G * W * L // bs
+    k, q = torch.zeros(N, bs, H, D, device="cuda"), torch.zeros(G * W, H, D, device="cuda")
+    # whole numbers of eight bits times a power of two: exact in both types, all of a row's distinct
+    v = torch.randn(N, bs, H, D, device="cuda").to(_dt(dtype))
+    pt = np.arange(G * P // bs, dtype=np.int32).reshape(G, -1)
+    tab = (np.arange(G * W * L // bs, dtype=np.int32) + G * P // bs).reshape(G * W, -1)
+    q[:, :, 0] = 1.375 * 2.0 ** 14
+    q[:, 1, 0] = 1.625 * 2.0 ** 14
+    kn = np.zeros((N, bs))
+    for g in range(G):
+        kn[pt[g]] = sign * rng.integers(1, 200, (P // bs, bs))
+    for s in range(G * W):
+        kn[tab[s]] = sign * rng.integers(1, 200, (L // bs, bs))
+    # one key of each sequence, or of its prefix, beyond all others
+    best = 250.0 if sign > 0 else 0.25
+    want = torch.zeros(G * W, H, D, dtype=torch.float64, device="cuda")
+    for s in range(G * W):
+        g = s // W
+        if g == 0:      # in the prefix, the same for the group
+            b, o = pt[0, 7], 5
+        else:
+            b, o = tab[s, s % (L // bs)], (3 * s) % bs
+        kn[b, o] = sign * best
+        want[s] = v[b, o].double()
+    k[:, :, :, 0] = torch.from_numpy(kn).cuda().float()[:, :, None] * 128.0
+    k, q = k.to(_dt(dtype)), q.to(_dt(dtype))
+    log(f"[attend] far scores {dtype} scale={scale} sign={sign} room={room}")
+    tables = torch.nn.functional.pad(_cuda(pt), (0, room // bs), value=-1)
+    out, lse = ert.prefix_attention(q, k, v, tables, _cuda(np.full(G, P, np.int32)), _cuda(tab),
+                                    _cuda(np.full(G * W, L, np.int32)), scale=scale, return_lse=True)
+    # one weight: the value times a power of two and back, rounded once
+    assert bool(((out.double() - want).abs() <= HALF[dtype] * want.abs()).all())
+    z = scale * q[:, :, 0].double() * sign * best * 128.0
+    assert bool(((lse.double() - z).abs() <= 2.0 ** -22 * z.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_attention_to_scores_a_step_of_their_type_apart(ert, dtype):
+    """Scores of 1.5 * 2^27, whose neighbours lie 16 apart: a later tile's weigh
+    2^16 times the first ones', just beyond what float16 holds."""
+    import torch
+    D, bs, n, S = 64, 32, 320, 2048   # (so many that a wave takes all of a row)
+    k, v = torch.zeros(n // bs, bs, 1, D, device="cuda"), torch.zeros(n // bs, bs, 1, D, device="cuda")
+    q = torch.zeros(S, 1, D, device="cuda")
+    q[:, 0, 0], q[:, 0, 1] = 1.5 * 2.0 ** 12, 4.0
+    k[..., 0] = 2.0 ** 15
+    k[4, :, 0, 1], v[4] = 4.0, 1.0
+    tab = torch.arange(n // bs, dtype=torch.int32, device="cuda").expand(S, n // bs).contiguous()
+    lens = _cuda(np.array([n, 160] * (S // 2), np.int32))
+    q, k, v = (x.to(_dt(dtype)) for x in (q, k, v))
+    log(f"[attend] scores 16 apart {dtype}")
+    out, lse = ert.prefix_attention(q, k, v, None, None, tab, lens, scale=float(np.log(2)), return_lse=True)
+    top = 2.0 ** 16 * 32
+    for s, others in ((0, n - 32), (1, 128)):
+        # weights and out rounded to the type
+        assert float((out[s].double() - top / (top + others)).abs().max()) <= 2 * HALF[dtype]
+        z = np.log(2) * (1.5 * 2.0 ** 27 + 16) + np.log(32 + others / 2.0 ** 16)
+        assert abs(float(lse[s, 0]) - z) <= 2.0 ** -22 * z
+
+
 def test_attention_float16_keeps_the_weights_of_a_long_tail(ert):
     """One key of weight 1 and 2^17 - 1 of 2^-25.5, which together are a 362nd of
     the row, one wave over all of them."""
