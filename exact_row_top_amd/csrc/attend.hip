@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][i] = 0.0f;
     float top = kNone, sum = 0.0f;
+    bool far = false;   // some query's reference lies beyond 2^16
 
     // Matrix products: the scores of the step in buffer bk (QK) and the values
     // of the one in buffer bv times its weights (PV), in turn; LDS reads run
@@ -464,12 +465,13 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[m][i] *= f;
+        far = __ballot(__builtin_fabsf(top) > 0x1p16f && top > kNone) != 0;
       }
       float ref = top == kNone ? 0.0f : top, factor = q.scale;
-      // The reference is a rounded score.  Of scores beyond 2^16 the rounding
-      // would outgrow the lag, and from 2^28 on overflow the weights: both are
-      // rounded alike then, and none weighs more than the reference allows.
-      if (__ballot(__builtin_fabsf(mx) > 0x1p16f && mx > kNone)) {
+      // The reference is a rounded score.  Beyond 2^16 its rounding would outgrow
+      // the lag, and from 2^27 on overflow the weights: the scores are rounded
+      // alike then, and none weighs more than the reference allows.
+      if (__builtin_expect(far, 0)) {
 #pragma unroll
         for (int n = 0; n < SUBS; ++n)
 #pragma unroll
