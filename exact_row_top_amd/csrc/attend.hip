@@ -165,13 +165,16 @@ __device__ __forceinline__ void load_to_lds(const unsigned char* from, const Pie
       : "s"(at), "v"(from)
       : "memory");
 }
-// The same from a uniform base and a lane's own offset.
+// The same from a uniform base and a lane's own offset.  The base may come
+// straight from v_readlane: a memory instruction that reads a scalar register
+// which a vector instruction wrote needs five wait states between them, and the
+// compiler puts none before inline assembly.
 __device__ __forceinline__ void load_to_lds(const unsigned char* base, uint32_t lane_off, const Piece* to) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const Piece*)to);
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
+      "s_nop 3\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(at), "v"(lane_off), "s"(base)
