@@ -153,16 +153,16 @@ namespace {
 
 // 16 bytes a lane from memory into 1 KB of LDS from `to` on (uniform), lane by
 // lane.  Written out so that reads of another part of LDS do not wait for it:
-// whoever reads waits for vmcnt first.
+// whoever reads waits for vmcnt first.  m0, which holds where in LDS, is an
+// operand, so that the compiler knows what is in it.
 __device__ __forceinline__ void load_to_lds(const unsigned char* from, const Piece* to) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const Piece*)to);
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
       "global_load_lds_dwordx4 %1, off"
       :
-      : "s"(at), "v"(from)
+      : "{m0}"(at), "v"(from)
       : "memory");
 }
 // The same from a uniform base and a lane's own offset.  The base may come
@@ -173,11 +173,10 @@ __device__ __forceinline__ void load_to_lds(const unsigned char* base, uint32_t 
   const uint32_t at = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const Piece*)to);
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 3\n\t"
+      "s_nop 4\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
-      : "s"(at), "v"(lane_off), "s"(base)
+      : "{m0}"(at), "v"(lane_off), "s"(base)
       : "memory");
 }
 // Waits until all but the last N loads are done.

@@ -265,3 +265,19 @@ def test_c_refusals_of_bounded_mass():
         assert call(**change) == EINVAL, change
     for change in (dict(q=_at(0) + 8), dict(lse=_at(9) + 2), dict(po=_at(11) + 2)):
         assert call(**change) == ELAYOUT, change
+
+
+def test_inline_assembly_that_uses_m0_says_so():
+    """A load to LDS takes its place there from m0: as an operand, or the
+    compiler may keep something of its own in it."""
+    import glob
+    import os
+    import re
+    found = 0
+    for path in glob.glob(os.path.join(os.path.dirname(ert.__file__), "csrc", "*")):
+        src = re.sub(r"//[^\n]*", "", open(path).read())
+        for text in re.findall(r"\basm\b(?:\s+volatile)?\s*\((.*?)\);", src, flags=re.S):
+            if re.search(r"\bm0\b|_load_lds|_lds_d", text):
+                found += 1
+                assert '"{m0}"' in text or '"m0"' in text, (os.path.basename(path), text)
+    assert found
