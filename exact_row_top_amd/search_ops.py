@@ -522,12 +522,22 @@ def evict_cache(mass, kv_lens, budget, *, sinks=0, recent=0, block_tables=None, 
         if len(shape) < 3:
             raise ValueError("caches must be [blocks, block_size, kv_heads, ...] tensors")
         pointers, count, blocks, slot_bytes = _caches(caches, shape[1], dev)
+        # (all that the move could refuse, before the choice writes anything)
+        if count > 64 or shape[1] > 1 << 20:
+            raise ValueError("at most 64 caches with blocks of at most 2 ** 20 positions")
+        size, free = blocks * shape[1] * slot_bytes, 0
+        for p in sorted(pointers) if size else ():
+            if p & 15 or p < free:
+                raise ValueError("caches must be aligned to 16 bytes and must not overlap")
+            free = p + size
         if heads < 1 or shape[2] % heads:
             raise ValueError("mass' heads must divide the caches' heads")
         if (slot_bytes // heads) % 16:
             raise ValueError("a head's share of a cache slot must be a multiple of 16 bytes")
         tables = _tables(block_tables, "block_tables", requests, dev)
         to = tables if out_tables is None else _tables(out_tables, "out_tables", requests, dev)
+        if to[0] == tables[0] and to[1] != tables[1] and requests > 1:
+            raise ValueError("out_tables must be block_tables or lie apart from them")
     kept = torch.empty(requests, heads, budget, dtype=torch.int32, device=dev)
     new_lens = torch.empty(requests, dtype=torch.int32, device=dev)
     width = budget

@@ -173,3 +173,28 @@ def test_attention_float16_keeps_the_weights_of_a_long_tail(ert):
     assert float((out - want).abs().max()) <= off < want / 4
 
 
+# ---------------------------------------------------------------------------
+# refusals, and the loop
+# ---------------------------------------------------------------------------
+
+def test_evict_refuses_caches_before_anything_is_written(ert):
+    import torch
+    def half(*shape):
+        return torch.zeros(*shape, dtype=torch.float16, device="cuda")
+    mass, lens = torch.rand(2, 1, 64, device="cuda"), torch.tensor([64, 20], dtype=torch.int32, device="cuda")
+    tab = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    c, n = half(12, 16, 2, 8), 12 * 16 * 2 * 8
+    odd, wide = half(n + 4)[4:].view(12, 16, 2, 8), half(n + 64)
+    calls = {"the same cache twice": dict(caches=[c, c]), "a cache not at 16 bytes": dict(caches=[c, odd]),
+             "caches that overlap": dict(caches=[wide[:n].view(12, 16, 2, 8), wide[64:].view(12, 16, 2, 8)]),
+             "more caches than a call takes": dict(caches=[half(1, 16, 2, 8) for _ in range(65)]),
+             "blocks too long": dict(caches=[half(1, (1 << 20) + 1, 1, 8)]),
+             "tables of two strides at one place": dict(caches=[c], out_tables=tab.as_strided((2, 2), (2, 1)))}
+    for what, kw in calls.items():
+        log(f"[evict] refuses {what}")
+        out = torch.full((2, 1, 8), 9.0, device="cuda")
+        with pytest.raises((ValueError, RuntimeError)):
+            ert.evict_cache(mass, lens, 8, block_tables=tab, mass_out=out, **kw)
+        assert bool((out == 9).all()), what
+
+
