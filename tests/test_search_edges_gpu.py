@@ -174,6 +174,51 @@ def test_attention_float16_keeps_the_weights_of_a_long_tail(ert):
 
 
 # ---------------------------------------------------------------------------
+# more query rows of a key head than a tile, long rows, crowded rows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,dim,bs", [("bf16", 64, 16), ("fp16", 64, 7), ("bf16", 128, 7), ("fp16", 128, 64)])
+def test_more_own_query_rows_than_a_tile(ert, dtype, dim, bs):
+    for n, (members, prefix, suffix, heads, kv, next_n) in enumerate([
+            ([2], 100, 90, 8, 1, 5), ([1, 2], 70, 130, 4, 2, 33), ([1], 40, 300, 2, 1, 65), ([], 0, 80, 6, 2, 32)]):
+        c = Case(dtype, dim, bs, members, prefix, suffix, heads, kv, next_n, seed=n, outside=0 if members else 1)
+        what = f"{dtype} dim={dim} bs={bs} members={members} heads={heads}/{kv} next_n={next_n}"
+        _check_attend(ert, c, what)
+        _check_mass(ert, c, what, seed=n)
+
+
+@pytest.mark.parametrize("positions", [8192, 8193, 32768, 32769, 70001])
+def test_evict_rows_held_in_registers_and_longer(ert, positions):
+    rng = np.random.default_rng(positions)
+    R, H = 4, 2
+    lens = np.array([positions, positions - 1, 33000, positions + 9], dtype=np.int32)
+    special = rng.choice([np.nan, np.inf, -np.inf, -0.0, 1e-42], (R, H, positions))
+    kinds = {"normal": rng.normal(0, 1, (R, H, positions)), "zeros": np.zeros((R, H, positions)),
+             "few": rng.integers(0, 3, (R, H, positions)).astype(float),
+             "half": np.where(rng.random((R, H, positions)) < 0.5, 0.0, np.exp(rng.normal(0, 9, (R, H, positions)))),
+             "masked": np.where(rng.random((R, H, positions)) < 0.3, special, rng.normal(0, 1, (R, H, positions))),
+             "nan": np.full((R, H, positions), np.nan)}
+    for name, m in kinds.items():
+        mass = _cuda(m.astype(np.float32))
+        for budget, sinks, recent in ((1, 0, 0), (1000, 4, 64), (1000, 400, 600), (positions // 2, 0, 7), (positions - 1, 3, 0)):
+            _check_evict(ert, mass, lens, budget, sinks, recent,
+                         f"{name} positions={positions} budget={budget} sinks={sinks} recent={recent}")
+
+
+@pytest.mark.parametrize("vocab", [131073, 262145, 1 << 20])
+def test_beams_of_crowded_rows_with_several_pieces_a_thread(ert, vocab):
+    rng = np.random.default_rng(vocab)
+    rows = [np.zeros(vocab), np.where(rng.random(vocab) < 0.5, 1.0, -1.0), np.where(rng.random(vocab) < 0.999, NINF, 2.0),
+            rng.integers(-3, 3, vocab).astype(float), np.sort(rng.normal(0, 1, vocab)),
+            np.where(np.arange(vocab) < vocab - 70, 0.5, 0.5 + (np.arange(vocab) % 3) * 0.25)]
+    x = _cuda(np.array(rows, dtype=np.float32))
+    for k in (1, 7, 64):
+        for r in range(len(rows)):
+            _check_beams(ert, x[r:r + 1], np.array([[-1.5]]), k, f"vocab={vocab} row {r} alone k={k}")
+        _check_beams(ert, x, rng.uniform(-9, -1, (2, 3)), k, f"vocab={vocab} together k={k}")
+
+
+# ---------------------------------------------------------------------------
 # refusals, and the loop
 # ---------------------------------------------------------------------------
 
