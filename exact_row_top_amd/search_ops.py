@@ -5,15 +5,15 @@ share, the attention mass of cached positions, and eviction by it.
 Thin bindings of the C calls declared in ``include/exact_row_top.h``, whose
 comments hold the definitions.
 
-    scores, parents, tokens = select_beams(logits, scores, k)
-    reorder_beams([history, state], parents, out=[history, state])
-    reorder_block_tables(tables, kv_lens, parents, block_size, caches=[k_cache, v_cache], out=tables)
     out, lse = prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_lens, tables, lens,
                                 return_lse=True)
     prefix_mass, mass = attention_mass(q, k_cache, lse, prefix_tables, prefix_lens, tables, lens,
                                        prefix_mass=prefix_mass, mass=mass)
-    kept, kept_mass, lens = evict_cache(prefix_mass, prefix_lens, budget, sinks=4, recent=64,
-                                        block_tables=prefix_tables, caches=[k_cache, v_cache])
+    scores, parents, tokens = select_beams(logits, scores, k)
+    reorder_beams([history, state, mass], parents, out=[history, state, mass])
+    reorder_block_tables(tables, kv_lens, parents, block_size, caches=[k_cache, v_cache], out=tables)
+    kept, prefix_mass, prefix_lens = evict_cache(prefix_mass, prefix_lens, budget, sinks=4, recent=64,
+                                                 block_tables=prefix_tables, caches=[k_cache, v_cache])
 
 Tensors must share one device, which need not be the current one.  The work
 runs on the current stream of that device, or on ``stream``, whose pool then
@@ -492,8 +492,9 @@ def evict_cache(mass, kv_lens, budget, *, sinks=0, recent=0, block_tables=None, 
     With caches (contiguous [blocks, block_size, kv_heads, ...] tensors of one
     shape, rows of block_tables, int32 [requests, max_blocks]) the kept
     positions' rows move to the front: position j of head h comes from position
-    kept[r, h, j].  heads divides kv_heads; with one, all heads keep the same
-    positions.  out_tables: the rows' new blocks, none of them in block_tables;
+    kept[r, h, j], and from then on has kept mass[r, h, j]: the mass given no
+    longer fits the cache.  heads divides kv_heads; with one, all heads keep the
+    same positions.  out_tables: the rows' new blocks, none of them in block_tables;
     None: in place."""
     guard = _elsewhere(mass, "mass", stream)
     if guard is not None:

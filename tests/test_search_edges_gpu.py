@@ -243,3 +243,88 @@ def test_evict_refuses_caches_before_anything_is_written(ert):
         assert bool((out == 9).all()), what
 
 
+def test_documented_loop_over_several_steps(ert):
+    """The step that the documentation shows, as often as a search takes it:
+    mass, ends and tables follow the beams, the prompt's cache and its mass are
+    cut together.  Against a search without paging that masks what was evicted."""
+    import torch
+    R, W, bs, H, per, D, V, steps, sinks, recent, eos = 2, 3, 4, 2, 2, 64, 301, 9, 2, 3, 5
+    g = torch.Generator(device="cuda").manual_seed(21)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    wq, wk, wv = rnd(V, H * per, D).bfloat16(), rnd(V, H, D).bfloat16(), rnd(V, H, D).bfloat16()
+    proj = rnd(H * per * D, V) * 0.5
+    prompt = torch.randint(0, V, (R, 23), device="cuda", generator=g)
+    N = R * 6 + R * W * 4
+    k_cache, v_cache = (torch.zeros(N, bs, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    prompt_tables = torch.arange(R * 6, device="cuda", dtype=torch.int32).view(R, 6)
+    for r in range(R):
+        at = prompt_tables[r].long().repeat_interleave(bs)[:23], (torch.arange(23, device="cuda") % bs)
+        k_cache[at], v_cache[at] = wk[prompt[r]], wv[prompt[r]]
+    prompt_lens = torch.tensor([23, 17], dtype=torch.int32, device="cuda")
+    tables = torch.full((R * W, 4), -1, dtype=torch.int32, device="cuda")
+    free, taken = torch.arange(R * 6, N, device="cuda", dtype=torch.int32), torch.zeros(1, dtype=torch.int32, device="cuda")
+    scores = torch.tensor([[0.0] + [NINF] * (W - 1)] * R, device="cuda")
+    ended = torch.zeros(R, W, dtype=torch.bool, device="cuda")
+    tokens = torch.zeros(R, W, dtype=torch.int32, device="cuda")
+    history = torch.zeros(R * W, steps, dtype=torch.int32, device="cuda")
+    prompt_mass = mass = None
+    # the same search kept apart: which prompt positions are left for each head, and the masses by position
+    left = [[np.arange(int(n)) for _ in range(H)] for n in prompt_lens.tolist()]
+    p_mass, o_mass = np.zeros((R, H, 23)), np.zeros((R * W, H, steps))
+    k64, v64, q64 = (x.double().cpu().numpy() for x in (wk, wv, wq))
+    host_prompt = prompt.cpu().numpy()
+    for step in range(steps):
+        lens = torch.full((R * W,), step + 1, dtype=torch.int32, device="cuda")
+        _, _, _, slots, taken = ert.extend_block_tables(tables, lens, torch.ones_like(lens), free, taken, bs, R * W)
+        history[:, step] = tokens.view(-1)
+        last = tokens.view(-1).long()
+        k_cache.view(-1, H, D)[slots.long()], v_cache.view(-1, H, D)[slots.long()] = wk[last], wv[last]
+        q = wq[last]
+        out, lse = ert.prefix_attention(q, k_cache, v_cache, prompt_tables, prompt_lens, tables, lens, return_lse=True)
+        prompt_mass, mass = ert.attention_mass(q, k_cache, lse, prompt_tables, prompt_lens, tables, lens,
+                                               prefix_mass=prompt_mass, mass=mass, decay=0.99)
+        # what it has to be
+        hist = history.cpu().numpy()
+        p_mass, o_mass = p_mass * np.float32(0.99), o_mass * np.float32(0.99)
+        for s in range(R * W):
+            r = s // W
+            for h in range(H):
+                seen, own = host_prompt[r][left[r][h]], hist[s, :step + 1]
+                ks = np.concatenate([k64[seen, h], k64[own, h]])
+                vs = np.concatenate([v64[seen, h], v64[own, h]])
+                for i in range(per):
+                    a = ks @ q64[hist[s, step], h * per + i] * D ** -0.5
+                    w = np.exp(a - a.max())
+                    w /= w.sum()
+                    p_mass[r, h, left[r][h]] += w[:seen.size]
+                    o_mass[s, h, :step + 1] += w[seen.size:]
+                    want, spread = w @ vs, w @ np.abs(vs)
+                    # weights and result rounded to bfloat16 (2^-8 each), the rest in 32 bits
+                    assert (np.abs(out[s, h * per + i].double().cpu().numpy() - want) <= 2.0 ** -7 * 1.05 * spread + 1e-5).all()
+        # (32-bit scores: 72 roundings of sums of products of about 8, 2^-14.8, in the weight and in its log-sum)
+        for r in range(R):
+            for h in range(H):
+                m = prompt_mass[r, h, :left[r][h].size].double().cpu().numpy()
+                assert (np.abs(m - p_mass[r, h, left[r][h]]) <= 2.0 ** -13 * p_mass[r, h, left[r][h]] + 1e-9).all(), (step, r, h)
+        m = mass[:, :, :step + 1].double().cpu().numpy()
+        assert (np.abs(m - o_mass[:, :, :step + 1]) <= 2.0 ** -13 * o_mass[:, :, :step + 1] + 1e-9).all(), step
+        logits = out.float().view(R * W, -1) @ proj
+        scores, parents, tokens = ert.select_beams(logits, scores, W, ended=ended, end_token=eos)
+        ended = ended.gather(1, parents.long().clamp(min=0)) | (tokens == eos)
+        history, mass = ert.reorder_beams([history, mass], parents)
+        tables = ert.reorder_block_tables(tables, lens.view(R, W)[:, 0].contiguous(), parents, bs,
+                                          caches=[k_cache, v_cache], out=tables)
+        src = (parents.cpu().numpy() + np.arange(R)[:, None] * W).reshape(-1)
+        assert (parents >= 0).all()
+        o_mass = o_mass[src]
+        n, budget = prompt_lens.tolist(), 14 - 3 * (step // 3)
+        kept, prompt_mass, prompt_lens = ert.evict_cache(prompt_mass, prompt_lens, budget, sinks=sinks, recent=recent,
+                                                         block_tables=prompt_tables, caches=[k_cache, v_cache])
+        for r in range(R):
+            for h in range(H):
+                # (masses next to each other at the border may come in either order: what the call kept stands,
+                # and is what its own mass says)
+                stay = kept[r, h].cpu().numpy()
+                stay = stay[stay >= 0]
+                assert stay.size == min(n[r], budget) and set(range(min(sinks, n[r]))) <= set(stay.tolist())
+                left[r][h] = left[r][h][stay]
