@@ -212,10 +212,10 @@ __device__ __forceinline__ void lds_barrier() {
 //
 // Bound, with eight waves, by the matrix products and the LDS reads that feed
 // them, which take about as long: 2 groups of 256 queries a key head (8 of them,
-// dim 128) over some 24 thousand positions each, 51 GFLOP, take 80 us, 640
+// dim 128) over some 24 thousand positions each, 51 GFLOP, take 84 us, 610
 // TFLOP/s, of them about 20 for the first loads and the 33 MB of pieces.
 // Bound, alone (QW 1), by memory and the waits for it: 64 sequences' own 1 to
-// 512 positions, 67 MB, take 21 us (3.2 TB/s, the longest sequences last); four
+// 512 positions, 67 MB, take 22 us (3.1 TB/s, the longest sequences last); four
 // queries' 1000 positions take 8, the launch and the waits for lengths, tables,
 // keys, values and the join of the four sets.
 // ---------------------------------------------------------------------------
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
 // ---------------------------------------------------------------------------
 // Joins a row's pieces: a wave a row, its lanes in 64 / (dim / 4) sets that
 // take turns at the pieces.  Bound by reading them: 4096 rows of about 18
-// pieces, 38 MB, take 10.7 us (3.6 TB/s), 128 rows 4.3, where the waits for
+// pieces, 38 MB, take 10.8 us (3.5 TB/s), 128 rows 4.5, where the waits for
 // what says where the pieces lie are the whole; a small row's pieces are asked
 // for before its largest score is known (1120 rows 4.8 instead of 6.3).
 // ---------------------------------------------------------------------------
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams q) 
 //
 // Bound by memory and by the exponentials, one a (position, query): 8 groups of
 // 64 queries a key head over some 6 thousand positions each, and 64 sequences'
-// own 1 to 256, 122 MB, take 31 us (3.9 TB/s): 28 for the reading alone, 22 for
+// own 1 to 256, 122 MB, take 32 us (3.8 TB/s): 28 for the reading alone, 22 for
 // the products and exponentials alone.  Four tiles a wave: two take 36, for
 // their first loads, eight the same and 15 instead of 9 where there are few.
 // ---------------------------------------------------------------------------

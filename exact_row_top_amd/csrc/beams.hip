@@ -188,8 +188,10 @@ __global__ void __launch_bounds__(256) beam_segment_kernel(const BeamParams q) {
 // the bit: fewer than k threads hold any above it, and of those that equal it
 // each wave takes its first k.
 //
-// Bound by the waits between these steps, a few microseconds whatever the
-// sizes: 4 rows of 32768 take 7.3 us, 240 of 50001 8.7, 256 of 131072 12.6.
+// Bound by the waits between these steps, and in a batch by its rankings, which
+// grow with k: 4 rows of 32768, best 8, take 7.1 us, 240 of 50001, best 10, 8.7,
+// 256 of 131072 9.1, 11.7 and 19.1 for the best 4, 16 and 32 of 8 beams each, 9.7
+// for the best 16 of 4 beams; the vocabulary adds little (256 rows of 32768 10.6).
 // ---------------------------------------------------------------------------
 
 namespace {

@@ -39,7 +39,9 @@ struct KeepShared {
 // HELD are read again in every pass (HELD 0).
 //
 // Bound by the passes' waits and by the counting: 128 rows of 8192, which leave
-// half of the compute units idle, take 11 us, one row of 5003 positions 8.
+// half of the compute units idle, take 11 us, one row of 5003 positions 8.  Rows
+// in memory, four passes by one workgroup each: one of 65536 takes 67 us, 128 of
+// them 98, one of 131072 126.
 // ---------------------------------------------------------------------------
 template <int HELD>
 __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams q) {
@@ -205,7 +207,9 @@ __global__ void __launch_bounds__(kKeepBlock) evict_keep_kernel(const KeepParams
 // to 1024, 8 heads of 256 bytes, two caches, 134 MB from and to memory, take 44
 // us with the choice (27 at a copy's rate); 48 without the stores' hint, which
 // keeps what is moved out of the caches' way.  Four rows in flight a thread:
-// with 8 the same took 68 where four took 56, with 16 (fewer waves) 124.
+// with 8 the same took 68 where four took 56, with 16 (fewer waves) 124.  In place
+// a workgroup takes all of a row's positions, and its next loads wait for the last
+// stores: the same move, 64 us.
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kMoveRows = 4;   // rows in flight a thread

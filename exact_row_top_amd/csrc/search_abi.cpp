@@ -85,10 +85,15 @@ struct AttendPlan {
 // queries (8 waves of 32).  Groups of up to 32 queries, and all where prefixes
 // take up to 2^27 products of a query's 32 (the strips of 32 queries times
 // positions, key heads and dim), have a wave for each fourth key tile instead:
-// prefixes and own positions are then one launch.  Groups of 70 queries over
-// 5001 positions (2^25) take 22 us so and 28 the other way, 8 of 256 over 2000
-// (2^27) 130 and 133, 64 of 64 over 2000 (2^28) 296 and 240.  About 2048 waves
-// in all, so that each of the chip's 1024 SIMDs has two.
+// prefixes and own positions are then one launch.  Kernel times of the two forms
+// at 2^26, 2^27 and 2^28 products, 8 key heads, 100 own positions: dim 128, 4
+// groups of 128 queries 55 / 60, 74 / 71 and 111 / 92 us, 8 of 64 queries 62 / 73,
+// 83 / 95 and 137 / 145; dim 64, where exponentials weigh twice as much, 4 groups
+// of 128 46 / 46 and 71 / 57 (2^26, 2^27).  With 2048 sequences times key heads or
+// more, own positions are a launch of their own either way, and the shared reads
+// are ahead from 2^26 on: 32 groups of 128 queries, dim 128, 84 / 77 and 102 / 86
+// (2^26, 2^27), dim 64 73 / 63 and 103 / 77.  About 2048 waves in all, so that
+// each of the chip's 1024 SIMDs has two.
 constexpr int64_t kSetProducts = (int64_t)1 << 27;
 bool attend_plan(int32_t groups, int32_t seqs, bool ragged, int32_t next_n, int32_t heads,
                  int32_t kv_heads, int32_t dim, int64_t max_shared, int64_t max_own, AttendPlan& p) {
