@@ -77,13 +77,6 @@ __device__ __forceinline__ void group_range(const AttendParams& q, int g, int& s
   }
 }
 
-// Which of the groups g0 .. g0 + 63 end before they start: groups could overlap
-// without bound then, and no group has a prefix.  (All lanes of a wave together.)
-__device__ __forceinline__ uint64_t falling_starts(const AttendParams& q, int g0) {
-  const int g = g0 + (int)(threadIdx.x & 63);
-  return __ballot(q.starts && g < q.groups && q.starts[g + 1] < q.starts[g]);
-}
-
 // Sums over a wave's lanes up to each, and steps and strips of groups.
 struct GroupScan {
   int steps, strips;      // of this lane's group
@@ -650,7 +643,8 @@ __global__ void __launch_bounds__(64 * QW * KW, 2) attend_kernel(const AttendPar
     int all = 0, strips = 0;
     uint64_t falls = 0;
     for (int g0 = 0; g0 < q.groups; g0 += 64) {
-      falls |= falling_starts(q, g0);
+      const int g = g0 + lane;
+      falls |= __ballot(q.starts && g < q.groups && q.starts[g + 1] < q.starts[g]);
       const GroupScan c = scan_groups(q, g0, 32 * QW, KT, all, strips);
       if (blockIdx.x == 0 && threadIdx.x < 64 && g0 + (int)threadIdx.x < q.groups)
         q.group_at[g0 + threadIdx.x] = int4{c.step_end - c.steps, c.strip_end - c.strips, 0, 0};
@@ -899,15 +893,12 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
   if (shared) {
     int s1;
     group_range(q, entry, seq0, s1);
-    uint64_t falls = 0;
-    for (int g0 = 0; g0 < q.groups; g0 += 64) falls |= falling_starts(q, g0);
-    seqs = falls ? 0 : s1 - seq0;   // (the log-sums then lack all prefixes)
+    seqs = s1 - seq0;
     cut = 0;
   }
-  const int rows = seqs * q.next_n * q.per;
   // this wave's tiles: every fourth of the workgroup's
   auto first_of = [&](int i) { return ((part * TILES + i) * (kMassBlock / 64) + wv) * kKeyTile; };
-  if (first_of(0) >= row_len) return;
+  int rows = seqs * q.next_n * q.per;
 
   int32_t block[TILES];
 #pragma unroll
@@ -964,10 +955,34 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
     lse = on ? lse * 1.44269504f : 0.0f;
     sees = on ? len - cut + (cut ? (int)(tok % (uint32_t)q.next_n) : 0) : 0;
   };
-  if (rows > 0 && first_of(0) < len) {
+  if (rows > 0 && first_of(0) < min(len, row_len)) {
     fetch(0);
     load_queries(0);
   }
+  // Where starts fall, the log-sums lack all prefixes.  A lane looks at three
+  // pairs of neighbours, a wave at 192 a load; the waves share what is more
+  // (4096 groups of a sequence over 128 positions: 230 us without looking, 290
+  // so, 680 with a wave's pairs one load after the other; 64 groups the same).
+  constexpr int PAIRS = 3 * 64;
+  const bool among = q.groups > PAIRS;
+  if (shared && q.starts && rows > 0 && (among || first_of(0) < min(len, row_len))) {
+    bool fall = false;
+    if (q.groups < 3) {
+      for (int g = 0; g < q.groups; ++g) fall |= q.starts[g + 1] < q.starts[g];
+    } else {
+#pragma unroll 4
+      for (int g = among ? wv * PAIRS : 0; g < q.groups; g += among ? PAIRS * (kMassBlock / 64) : PAIRS) {
+        int4 s;
+        __builtin_memcpy(&s, q.starts + min(g + 3 * lane, q.groups - 3), 16);
+        fall |= s.y < s.x || s.z < s.y || s.w < s.z;
+      }
+    }
+    if (among ? __syncthreads_or(fall) != 0 : __ballot(fall) != 0) {
+      rows = 0;
+      loads_but<0>();   // (nothing takes the keys)
+    }
+  }
+  if (first_of(0) >= row_len) return;
   const float* in = shared ? mp.shared_in : mp.own_in;
   float* out = shared ? mp.shared_out : mp.own_out;
   const int64_t base = ((int64_t)entry * q.kv_heads + head) * row_len;

@@ -46,6 +46,31 @@ def test_mass_of_more_groups_than_a_wave_with_starts_that_fall_late(ert):
     _check_mass(ert, c, "150 groups, falling at the 140th")
 
 
+@pytest.mark.parametrize("groups", [1, 2, 3, 4, 5, 63, 64, 200, 1007, 1008, 1009, 2300])
+def test_mass_finds_a_fall_wherever_it_is(ert, groups):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(groups)
+    q = torch.randn(groups, 2, 64, device="cuda", generator=g).half()
+    k = torch.randn(groups + 1, 16, 1, 64, device="cuda", generator=g).half()
+    pt = torch.arange(groups, device="cuda", dtype=torch.int32).view(-1, 1)
+    pl = torch.full((groups,), 16, dtype=torch.int32, device="cuda")
+    tab, lens = torch.full((groups, 1), groups, dtype=torch.int32, device="cuda"), torch.zeros(groups, dtype=torch.int32, device="cuda")
+    lse, mass = torch.full((groups, 2), 3.0, device="cuda"), torch.rand(groups, 1, 700, device="cuda", generator=g)
+
+    def run(starts):
+        return ert.attention_mass(q, k, lse, pt, pl, tab, lens, group_starts=_cuda(starts), prefix_mass=mass, decay=0.5)[0]
+
+    log(f"[mass] {groups} groups, a fall at each of some places")
+    rising = np.arange(groups + 1, dtype=np.int32)
+    seen = run(rising)
+    assert torch.equal(seen[:, :, 16:], mass[:, :, 16:] * 0.5) and bool((seen[:, :, :16] > mass[:, :, :16] * 0.5).all())
+    for at in {0, 1, 14, 15, 30, 31, 61, 62, 63, 64, 125, 126, 250, 251, 252, 253, 254, 1007, 1008, 2015, groups // 2, groups - 5, groups - 4, groups - 3, groups - 2, groups - 1}:
+        if 0 <= at < groups:
+            starts = rising.copy()
+            starts[at], starts[at + 1] = starts[at + 1], starts[at]
+            assert torch.equal(run(starts), mass * 0.5), at
+
+
 # ---------------------------------------------------------------------------
 # bounds
 # ---------------------------------------------------------------------------
