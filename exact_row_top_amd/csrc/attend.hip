@@ -893,7 +893,9 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
   if (shared) {
     int s1;
     group_range(q, entry, seq0, s1);
-    seqs = s1 - seq0;
+    // where starts fall, the log-sums lack all prefixes
+    const bool falls = q.starts && q.groups <= 64 && lane < q.groups && q.starts[lane + 1] < q.starts[lane];
+    seqs = __ballot(falls) ? 0 : s1 - seq0;
     cut = 0;
   }
   // this wave's tiles: every fourth of the workgroup's
@@ -959,25 +961,19 @@ __global__ void __launch_bounds__(kMassBlock, 2) attend_mass_kernel(const MassPa
     fetch(0);
     load_queries(0);
   }
-  // Where starts fall, the log-sums lack all prefixes.  A lane looks at three
-  // pairs of neighbours, a wave at 192 a load; the waves share what is more
-  // (4096 groups of a sequence over 128 positions: 230 us without looking, 290
-  // so, 680 with a wave's pairs one load after the other; 64 groups the same).
-  constexpr int PAIRS = 3 * 64;
-  const bool among = q.groups > PAIRS;
-  if (shared && q.starts && rows > 0 && (among || first_of(0) < min(len, row_len))) {
+  // More groups than a wave has lanes: three pairs of neighbours a lane, the
+  // workgroup's waves in turn, once the keys are on their way (4096 groups of a
+  // sequence over 128 positions: 230 us without looking, 280 so, 680 with a
+  // wave's pairs one load after the other).
+  if (shared && q.starts && q.groups > 64 && rows > 0) {
     bool fall = false;
-    if (q.groups < 3) {
-      for (int g = 0; g < q.groups; ++g) fall |= q.starts[g + 1] < q.starts[g];
-    } else {
 #pragma unroll 4
-      for (int g = among ? wv * PAIRS : 0; g < q.groups; g += among ? PAIRS * (kMassBlock / 64) : PAIRS) {
-        int4 s;
-        __builtin_memcpy(&s, q.starts + min(g + 3 * lane, q.groups - 3), 16);
-        fall |= s.y < s.x || s.z < s.y || s.w < s.z;
-      }
+    for (int g = wv * 192; g < q.groups; g += 192 * (kMassBlock / 64)) {
+      int4 s;
+      __builtin_memcpy(&s, q.starts + min(g + 3 * lane, q.groups - 3), 16);
+      fall |= s.y < s.x || s.z < s.y || s.w < s.z;
     }
-    if (among ? __syncthreads_or(fall) != 0 : __ballot(fall) != 0) {
+    if (__syncthreads_or(fall)) {
       rows = 0;
       loads_but<0>();   // (nothing takes the keys)
     }

@@ -46,7 +46,7 @@ def test_mass_of_more_groups_than_a_wave_with_starts_that_fall_late(ert):
     _check_mass(ert, c, "150 groups, falling at the 140th")
 
 
-@pytest.mark.parametrize("groups", [1, 2, 3, 4, 5, 63, 64, 200, 1007, 1008, 1009, 2300])
+@pytest.mark.parametrize("groups", [1, 2, 3, 5, 63, 64, 65, 66, 200, 768, 769, 2300])
 def test_mass_finds_a_fall_wherever_it_is(ert, groups):
     import torch
     g = torch.Generator(device="cuda").manual_seed(groups)
@@ -64,7 +64,7 @@ def test_mass_finds_a_fall_wherever_it_is(ert, groups):
     rising = np.arange(groups + 1, dtype=np.int32)
     seen = run(rising)
     assert torch.equal(seen[:, :, 16:], mass[:, :, 16:] * 0.5) and bool((seen[:, :, :16] > mass[:, :, :16] * 0.5).all())
-    for at in {0, 1, 14, 15, 30, 31, 61, 62, 63, 64, 125, 126, 250, 251, 252, 253, 254, 1007, 1008, 2015, groups // 2, groups - 5, groups - 4, groups - 3, groups - 2, groups - 1}:
+    for at in {0, 1, 14, 15, 30, 31, 61, 62, 63, 64, 125, 126, 250, 251, 252, 253, 254, 190, 191, 192, 193, 766, 767, 768, groups // 2, groups - 5, groups - 4, groups - 3, groups - 2, groups - 1}:
         if 0 <= at < groups:
             starts = rising.copy()
             starts[at], starts[at + 1] = starts[at + 1], starts[at]
