@@ -637,8 +637,10 @@ int topk_attend(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_s
  * position of the rows ([..][num_kv_heads][shared_positions] and
  * [..][num_kv_heads][own_positions], contiguous float) is written; those that
  * no token sees get the decayed mass alone, as all of shared_out does where
- * group_starts fall.  A mass array may be NULL (zeros) or its output.  Tokens whose lse is -inf or NaN add nothing.  The rest as for
- * topk_attend; sums have one order, so results repeat bit for bit. */
+ * group_starts fall.  A mass array may be NULL (zeros) or its output.  Tokens
+ * whose lse is -inf or NaN add nothing.  A weight is as good as its score and its
+ * 32-bit lse: 2^-23 of |lse|.  The rest as for topk_attend; sums have one order,
+ * so results repeat bit for bit. */
 int topk_attend_mass(const void* q, int32_t dtype, int64_t q_stride, int64_t q_head_stride, int32_t num_seqs,
                      int32_t next_n, int32_t num_heads, int32_t num_kv_heads, int32_t dim, const void* k_cache,
                      int64_t k_block_stride, int64_t k_slot_stride, int64_t k_head_stride, int64_t num_blocks,
